@@ -89,7 +89,8 @@ def draw(rng):
         ld += 64 if ld == 3072 else 0
         banned = rng.choice([0, 0, rng.randrange(1, 9)])
         prompt = rng.choice([0.0, 0.25, 0.5])
-        most = {"logps": 8192 * 50257 * 2, "policy": 6144 * 131072 * 2, "preference": 8192 * 50257 * 2}[op]
+        # the listed cases' bytes, whose prompts are not scored
+        most = {"logps": 6144 * 50257 * 2, "policy": 5632 * 131072 * 2, "preference": 6016 * 50257 * 2}[op]
         rows = max(1, min(8192, most // (vocab * BYTES[dtype])))
         if op == "logps":
             return dict(op=op, tokens=_log_int(rng, 1, rows), vocab=vocab, ld=ld, dtype=dtype, prompt=prompt,
