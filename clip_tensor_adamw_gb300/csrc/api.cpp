@@ -32,7 +32,7 @@ static thread_local std::string t_detail;
 
 void set_error_detail(const char* msg) { t_detail = msg; }
 
-static mica_status fail(mica_status s, const char* fmt, ...) {
+mica_status fail(mica_status s, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -42,7 +42,7 @@ static mica_status fail(mica_status s, const char* fmt, ...) {
     return s;
 }
 
-static mica_status ok() {
+mica_status ok() {
     t_detail.clear();
     return MICA_OK;
 }
@@ -72,7 +72,7 @@ static mica_status check_device_status(const char* what) {
     return MICA_OK;
 }
 
-static mica_status after_launch(int err, void* stream, const char* what) {
+mica_status after_launch(int err, void* stream, const char* what) {
     if (err != (int)cudaSuccess) return cuda_fail((cudaError_t)err, what);
     if (sync_debug()) {
         const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
@@ -270,7 +270,7 @@ static uint64_t mix(uint64_t h, uint64_t x) {
     return h * 0xFF51AFD7ED558CCDull;
 }
 
-static int sm_count(int device) {
+int sm_count(int device) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) {
         cudaGetLastError();
@@ -807,7 +807,7 @@ static mica_status check_list(int32_t T, const int64_t* n, std::initializer_list
     return MICA_OK;
 }
 
-static mica_status current_device(int* dev) {
+mica_status current_device(int* dev) {
     const cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) {
         cudaGetLastError();
