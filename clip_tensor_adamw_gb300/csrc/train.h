@@ -17,7 +17,9 @@ struct LogitRows {
     int32_t dtype;
     int32_t wide_targets;  // int64 targets
     float inv_t;           // 1 / temperature
-    float inv_t_log2e;     // log2(e) / temperature: exp(x - max) = 2^((z - zmax) * inv_t_log2e)
+    double wide_inv_t;
+    // log2(e) / temperature, rounded, and as a_hi + a_lo with a_lo > 0: exp(x - max) = 2^((z - zmax) * (a_hi + a_lo))
+    float a, a_hi, a_lo;
 };
 
 // A row's softmax statistics: the largest logit and 1 / sum exp.
@@ -36,8 +38,9 @@ struct PolicyTerms {
     float grad_factor;  // grad_scale / (denom * temperature)
 };
 
-// logps, and where not null entropies and softmax statistics, of every row
-int launch_row_logps(const LogitRows& L, float* logps, float* entropy, RowStat* stat, void* stream);
+// logps, and where not null entropies, of every row; without entropies also, where not null, the logps before they are
+// rounded and the softmax statistics
+int launch_row_logps(const LogitRows& L, float* logps, double* wide_logps, float* entropy, RowStat* stat, void* stream);
 // dz = coef * ((j == target) - p): coef[row] * factor given, the softmax computed here
 int launch_row_softmax_grad(const LogitRows& L, const float* coef, float factor, void* dz, int64_t ld_d, void* stream);
 // the same with the coefficient of the policy loss, from the log-probability found on the way (also written)
@@ -56,7 +59,7 @@ struct PairTerms {
     double grad_factor;  // grad_scale / (pairs * temperature)
 };
 // loss, rewards (or null) and, where coef is not null, each row's coefficient; sums: 2 * pairs doubles of workspace
-int launch_pairs(const LogitRows& L, const PairTerms& P, const float* logps, double* sums, float* loss, float* rewards,
+int launch_pairs(const LogitRows& L, const PairTerms& P, const double* logps, double* sums, float* loss, float* rewards,
                  float* coef, void* stream);
 
 int launch_act_pack(const void* x, int64_t ld_x, const mica_packed& p, int32_t act, bool gated, void* y, int64_t ld_y,

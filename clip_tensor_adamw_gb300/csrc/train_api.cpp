@@ -109,13 +109,15 @@ mica_status check_logits(const mica_logits* z, LogitRows* L) {
     if (z->target_bytes != 4 && z->target_bytes != 8) return fail(MICA_ERR_DTYPE, "targets must be int32 or int64");
     if (!std::isfinite(z->temperature) || !(z->temperature > 0.0))
         return fail(MICA_ERR_HYPER, "temperature %g is not finite and > 0", z->temperature);
+    if (!(z->temperature >= 1e-30 && z->temperature <= 1e30))
+        return fail(MICA_ERR_HYPER, "temperature %g is outside [1e-30, 1e30]", z->temperature);
     const double a = 1.4426950408889634074 / z->temperature;
-    if (!std::isfinite((float)a) || (float)a < 1.17549435e-38f)
-        return fail(MICA_ERR_HYPER, "temperature %g: its reciprocal is not a normal float32", z->temperature);
+    float a_hi = (float)a;  // the largest float32 below a, so that the rest is positive
+    if (a_hi >= a) a_hi = std::nextafter(a_hi, 0.0f);
     MICA_TRY(check_extent(z->rows, z->vocab, 1, "logits"));
     MICA_TRY(check_stride(z->ld, 0, "logits"));
     *L = LogitRows{z->logits, z->targets, z->rows, z->ld, (int32_t)z->vocab, z->dtype, z->target_bytes == 8,
-                   (float)(1.0 / z->temperature), (float)a};
+                   (float)(1.0 / z->temperature), 1.0 / z->temperature, (float)a, a_hi, (float)(a - a_hi)};
     return MICA_OK;
 }
 
@@ -174,7 +176,7 @@ extern "C" mica_status mica_token_logps(const mica_logits* z, float* logps, floa
     MICA_TRY(b.vec(logps, z->rows, 4, true, "logps"));
     if (entropy) MICA_TRY(b.vec(entropy, z->rows, 4, true, "entropy"));
     MICA_TRY(b.disjoint());
-    return after_launch(launch_row_logps(L, logps, entropy, nullptr, stream), stream, "token log-probabilities launch");
+    return after_launch(launch_row_logps(L, logps, nullptr, entropy, nullptr, stream), stream, "token log-probabilities launch");
 }
 
 extern "C" mica_status mica_token_logps_grad(const mica_logits* z, const float* dlogps, void* dlogits, int64_t ld_d,
@@ -194,10 +196,10 @@ extern "C" mica_status mica_token_logps_grad(const mica_logits* z, const float* 
                         "log-probabilities' gradient launch");
 }
 
-// workspace: a double per sequence | a RowStat per row | a coefficient per row
+// workspace: a sum per sequence | a log-probability, a RowStat and a coefficient per row
 extern "C" int64_t mica_preference_workspace(int64_t rows, int32_t pairs) {
     if (rows < 0 || rows > MICA_MAX_ROWS || pairs < 0 || pairs > (1 << 24)) return 0;
-    return (int64_t)(round16((size_t)pairs * 2 * sizeof(double)) + round16((size_t)rows * sizeof(RowStat)) +
+    return (int64_t)((size_t)pairs * 2 * sizeof(double) + round16((size_t)rows * (sizeof(double) + sizeof(RowStat))) +
                      round16((size_t)rows * sizeof(float)));
 }
 
@@ -238,16 +240,16 @@ extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t*
 
     char* w = static_cast<char*>(workspace);
     double* sums = reinterpret_cast<double*>(w);
-    w += round16((size_t)pairs * 2 * sizeof(double));
-    RowStat* stat = reinterpret_cast<RowStat*>(w);
-    w += round16((size_t)z->rows * sizeof(RowStat));
+    double* wide = sums + 2 * (size_t)pairs;
+    RowStat* stat = reinterpret_cast<RowStat*>(wide + z->rows);
+    w += (size_t)pairs * 2 * sizeof(double) + round16((size_t)z->rows * (sizeof(double) + sizeof(RowStat)));
     float* coef = reinterpret_cast<float*>(w);
     const PairTerms P{cu_seqlens, ref_logps, pairs, hp->kind, (hp->flags & MICA_PREF_LENGTH_NORM) != 0, hp->beta,
                       hp->label_smoothing, pairs ? hp->grad_scale / pairs / z->temperature : 0.0};
     if (z->rows)
-        MICA_TRY(after_launch(launch_row_logps(L, logps, nullptr, dlogits ? stat : nullptr, stream), stream,
+        MICA_TRY(after_launch(launch_row_logps(L, logps, wide, nullptr, dlogits ? stat : nullptr, stream), stream,
                               "log-probabilities launch"));
-    MICA_TRY(after_launch(launch_pairs(L, P, logps, sums, loss, rewards, dlogits ? coef : nullptr, stream), stream,
+    MICA_TRY(after_launch(launch_pairs(L, P, wide, sums, loss, rewards, dlogits ? coef : nullptr, stream), stream,
                           "preference pairs launch"));
     if (!dlogits || z->rows == 0) return ok();
     return after_launch(launch_row_grad(L, stat, coef, dlogits, ld_d, stream), stream, "preference gradient launch");
@@ -285,7 +287,7 @@ extern "C" mica_status mica_policy_loss(const mica_logits* z, const float* old_l
                         (float)(hp->grad_scale / hp->denom / z->temperature)};
     if (z->rows)
         MICA_TRY(after_launch(dlogits ? launch_row_policy_grad(L, P, logps, dlogits, ld_d, stream)
-                                      : launch_row_logps(L, logps, nullptr, nullptr, stream),
+                                      : launch_row_logps(L, logps, nullptr, nullptr, nullptr, stream),
                               stream, "policy loss launch"));
     return after_launch(launch_policy_sums(L, P, logps, stats, stream), stream, "policy sums launch");
 }

@@ -56,7 +56,7 @@ typedef struct {
     int64_t rows;         /* [0, MICA_MAX_ROWS] */
     int64_t vocab;        /* [1, MICA_MAX_COLS] */
     int64_t ld;
-    double temperature;   /* finite, > 0 */
+    double temperature;   /* [1e-30, 1e30] */
     int32_t dtype;        /* MICA_F32, MICA_F16 or MICA_BF16 */
     int32_t target_bytes; /* 4 or 8 */
 } mica_logits;
