@@ -165,8 +165,6 @@ struct Vec {
         return v;
     }
 };
-    }
-};
 
 // Where a row's 16-byte vectors lie: vector k holds elements [k * n - lead, k * n - lead + n). Of a CTA's vectors those in
 // [lo, hi) lie inside the row; the row's first or last, where it reaches outside, is `edge` of thread 0 or 1 (else -1).
@@ -182,7 +180,7 @@ __device__ __forceinline__ RowVectors row_vectors(const T* z, int vocab) {
     const int end = min(first + per, total), open = lead > 0, closed = (lead + vocab) / n;  // whole ones: [open, closed)
     int edge = -1;
     if (threadIdx.x == 0 && open && first == 0) edge = 0;
-    if (threadIdx.x == 1 && closed < total && total <= end && !(open && total == 1)) edge = total - 1;
+    if (threadIdx.x == 1 && closed < total && first < total && end == total && !(open && total == 1)) edge = total - 1;
     return RowVectors{lead, max(first, open), min(end, closed), edge};
 }
 
