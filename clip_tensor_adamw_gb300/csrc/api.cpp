@@ -18,6 +18,7 @@
 #include "host.h"
 #include "mica_optim.h"
 #include "plan.h"
+#include "train.h"
 
 namespace mica {
 
@@ -64,6 +65,9 @@ static mica_status check_device_status(const char* what) {
     unsigned int st = 0, fst = 0;
     int e = read_device_status(&st);
     if (e == (int)cudaSuccess) e = read_fused_status(&fst);
+    unsigned int more = 0;
+    if (e == (int)cudaSuccess) e = read_logits_status(&more);
+    st |= more;
     if (e != (int)cudaSuccess) return cuda_fail((cudaError_t)e, what);
     if (fst) return fail(MICA_ERR_CUDA, "%s: a fused kernel's grid-wide wait gave up (status 0x%x); its results are "
                          "not valid, and the list's table must be released (mica_release_cache)", what, fst);

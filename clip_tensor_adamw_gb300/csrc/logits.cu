@@ -6,6 +6,7 @@
 
 #include "elem.cuh"
 #include "mica_optim.h"
+#include "pipe.cuh"
 #include "plan.h"
 #include "stream.cuh"
 #include "train.h"
@@ -18,10 +19,10 @@ constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMostCluster = 8;  // CTAs of a portable cluster
 constexpr int kBatch = 4;        // vectors of a thread in flight
 constexpr int64_t kFewCtas = 304;
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr double kLn2 = 0.693147180559945309;
 constexpr float kFarBelow = -1000.0f;  // an exponent of 2 whose power is 0, and finite (0 * it is 0)
 // ex2.approx's relative error averages -4.9e-8 over every unit interval (measured on GB300; 2^0 is exact), and so does that
-// of a sum of its values past the largest one's 1: a log-probability that is to be summed over a sequence takes it out.
+// of a sum of its values past the origin's 1: a log-probability that is to be summed over a sequence takes it out.
 constexpr double kExp2Bias = 4.9e-8;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -41,8 +42,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // joins its threads', and one barrier joins the warps'. Where there are few rows, a cluster of CTAs shares each, and its
 // CTAs read one another's shared memory.
 //
-// Measured on GB300, 8,192 rows of 50,257 bfloat16 logits of which 6,144 count: log-probabilities and entropies 116 us
-// (5.3 TB/s), 138 us with CTAs of 512 threads. Rows held in the registers of a cluster, read once from L2 too, took 295 us:
+// This serves few rows and short ones; see the ring below for the others. Rows held in the registers of a cluster, read once from L2 too, took 295 us:
 // the share of a thread was so small that the joins were most of its work.
 //
 // Vectors start at 16-byte addresses, whatever the row's alignment (an odd vocabulary puts each row elsewhere): the first
@@ -90,7 +90,8 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
 // A part that has seen nothing but -inf counts from 0, so that no difference of two infinities makes its zero weight a NaN.
 __device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// The softmax of part of a row: the largest logit, s = sum 2^x and u = sum x 2^x, x the exponents.
+// The softmax of part of a row: the logit that the weights are counted from (-inf: nothing above that yet), s = sum 2^x and
+// u = sum x 2^x, x the exponents.
 struct Running {
     float m, s, u;
 };
@@ -221,7 +222,7 @@ enum RowKind { kLogps, kEntropy, kGiven, kPolicy };
 
 struct RowOut {
     float* logps;         // kLogps, kEntropy, kPolicy
-    double* wide_logps;   // kLogps, or null: the log-probabilities before they are rounded
+    float* rest_logps;    // kLogps, or null: what rounding took from the log-probabilities
     float* entropy;       // kEntropy
     RowStat* stat;        // kLogps, or null
     const float* coef;    // kGiven
@@ -311,28 +312,30 @@ __device__ __forceinline__ void grad_row(const LogitRows& L, const T* z, const R
     }
 }
 
-// Adds a vector's weights, counted from o, to s (and their moments to u).
-template <typename T, bool kMoment>
-__device__ __forceinline__ void add_vector(const LogitRows& L, const Vec<T>& v, float o, float& s, float& u) {
+// The sum of some vectors' weights, counted from o, and of their moments. kAnything: with banned tokens among them (whose
+// zero weights would make a moment of 0 * -inf).
+template <typename T, bool kMoment, bool kAnything, int kCount>
+__device__ __forceinline__ void sum_weights(const LogitRows& L, const Vec<T> (&v)[kCount], float o, float& s, float& u) {
     const Two away = two(-o, -o), hi = two(L.a_hi, L.a_hi), lo = two(L.a_lo, L.a_lo);
     Two sv = two(0.0f, 0.0f), uv = two(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < Vec<T>::n / 2; ++i) {
-        const Two d = v.pair(i) + away;
-        const float2 x = each(fma2(d, hi, d * lo));
-        const Two e = two(exp2_fast(x.x), exp2_fast(x.y));
-        sv = sv + e;
-        if (kMoment) uv = fma2(e, two(fmaxf(x.x, kFarBelow), fmaxf(x.y, kFarBelow)), uv);
-    }
-    const float2 t = each(sv);
-    s += t.x + t.y;
-    if (kMoment) {
-        const float2 w = each(uv);
-        u += w.x + w.y;
-    }
+    for (int j = 0; j < kCount; ++j)
+#pragma unroll
+        for (int i = 0; i < Vec<T>::n / 2; ++i) {
+            const Two d = v[j].pair(i) + away;
+            Two xx = fma2(d, hi, d * lo);
+            float2 x = each(xx);
+            const Two e = two(exp2_fast(x.x), exp2_fast(x.y));
+            sv = sv + e;
+            if (kMoment && kAnything) xx = two(fmaxf(x.x, kFarBelow), fmaxf(x.y, kFarBelow));
+            if (kMoment) uv = fma2(e, xx, uv);
+        }
+    const float2 t = each(sv), w = each(uv);
+    s = t.x + t.y;
+    u = w.x + w.y;
 }
 
-// Counts a part from `m`, a larger maximum.
+// Counts a part from `m` instead, a larger origin.
 template <bool kMoment>
 __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
     const float x = fmaxf(exponent(L, r.m, m), kFarBelow), f = exp2_fast(x);
@@ -341,10 +344,27 @@ __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
     r.m = m;
 }
 
+// Adds some vectors to a thread's part. Weights are counted from an origin that need not be the maximum: any will do as long
+// as one weight of the row is at least 1 and none comes near 2^128. So the target's logit serves, until a sum passes 2^60;
+// the elements are compared only then (and where the target is banned, or an infinity or a NaN is among them).
+template <typename T, bool kMoment, int kCount>
+__device__ __forceinline__ void add_vectors(const LogitRows& L, const Vec<T> (&v)[kCount], Running& r) {
+    float s, u;
+    sum_weights<T, kMoment, false>(L, v, r.m, s, u);
+    if (!(s < 0x1p60f) || (kMoment && !(fabsf(u) < 0x1p100f))) {
+        float m = v[0].max();
+#pragma unroll
+        for (int j = 1; j < kCount; ++j) m = fmaxf(m, v[j].max());
+        if (!(s < 0x1p60f) && m > r.m) raise<kMoment>(L, r, m);
+        sum_weights<T, kMoment, true>(L, v, origin(r.m), s, u);
+    }
+    r.s += s;
+    if (kMoment) r.u += u;
+}
+
 struct Parts {
     Running warp[kRowWarps];
     Running cta;
-    float c;
 };
 
 // The lanes' parts as one, in all lanes alike.
@@ -387,30 +407,43 @@ __device__ __forceinline__ void leave_cluster() {
     if (cluster_size() > 1) cluster_wait();
 }
 
-// Writes a row's results and returns the gradient's coefficient (c itself where it was given). zy: the target's logit, in
-// thread 0.
+// A row that does not count.
+template <RowKind kKind>
+__device__ __forceinline__ void skip_outputs(const RowOut& out, int64_t row) {
+    if (kKind == kGiven || threadIdx.x != 0 || cluster_rank() != 0) return;
+    out.logps[row] = 0.0f;
+    if (kKind == kLogps && out.rest_logps) out.rest_logps[row] = 0.0f;
+    if (kKind == kEntropy) out.entropy[row] = 0.0f;
+}
+
+// log(s) to some 2^-25 absolutely: the exponent's part in float64, and that of the fraction, which is below 0.7, in
+// float32. (float64's own log took 3 us of a row's 12: this chip has next to no float64.)
+__device__ __forceinline__ double wide_log(float s) {
+    const uint32_t bits = __float_as_uint(s);
+    if (!(s >= 0x1p-126f && s < INFINITY)) return logf(s);
+    return ((int)(bits >> 23) - 127) * kLn2 + logf(__uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u));
+}
+
+// Writes a row's results (one thread, `head`) and returns the gradient's coefficient, c itself where it was given, in every
+// thread alike. zy: the target's logit.
 template <RowKind kKind>
 __device__ __forceinline__ float finish_row(const LogitRows& L, const PolicyTerms& P, const RowOut& out, int64_t row,
-                                            int64_t y, float zy, const Running& r, float c, Parts& parts) {
+                                            int64_t y, float zy, const Running& r, float c, bool head) {
     const float o = origin(r.m);
-    const bool head = threadIdx.x == 0 && cluster_rank() == 0;
     if constexpr (kKind == kLogps || kKind == kEntropy) {
         if (head) {
-            const double lp = y < L.vocab ? ((double)zy - o) * L.wide_inv_t - (log((double)r.s) + kExp2Bias * (1.0 - 1.0 / r.s)) : NAN;
+            const double log_sum = wide_log(r.s) + kExp2Bias * (1.0f - 1.0f / r.s);
+            const double lp = y < L.vocab ? ((double)zy - o) * L.wide_inv_t - log_sum : NAN;
             out.logps[row] = (float)lp;
-            if (kKind == kLogps && out.wide_logps) out.wide_logps[row] = lp;
-            if (kKind == kEntropy) out.entropy[row] = logf(r.s) - kLn2 * r.u / r.s;
+            if (kKind == kLogps && out.rest_logps) out.rest_logps[row] = isfinite(lp) ? (float)(lp - (float)lp) : 0.0f;
+            if (kKind == kEntropy) out.entropy[row] = (float)(log_sum - kLn2 * (r.u / r.s));
             if (kKind == kLogps && out.stat) out.stat[row] = RowStat{r.m, 1.0f / r.s};
         }
     }
     if constexpr (kKind == kPolicy) {
-        if (threadIdx.x == 0) {
-            const float lp = y < L.vocab ? fmaf(zy - o, L.inv_t, -logf(r.s)) : NAN;
-            parts.c = policy_coef(P, row, lp);
-            if (head) out.logps[row] = lp;
-        }
-        __syncthreads();
-        c = parts.c;
+        const float lp = y < L.vocab ? fmaf(zy - o, L.inv_t, -logf(r.s)) : NAN;
+        c = policy_coef(P, row, lp);
+        if (head) out.logps[row] = lp;
     }
     return y < L.vocab ? c : NAN;
 }
@@ -431,15 +464,11 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(
     float c = kKind == kGiven && y >= 0 ? out.coef[row] * out.factor : 0.0f;
     if (y < 0 || (kKind == kGiven && c == 0.0f)) {  // a row that does not count is not read (every CTA of the cluster alike)
         if (kGrad) zero_row<T, kThreads>(g, L.vocab, dz, same);
-        if (kKind != kGiven && threadIdx.x == 0 && cluster_rank() == 0) {
-            out.logps[row] = 0.0f;
-            if (kKind == kLogps && out.wide_logps) out.wide_logps[row] = 0.0;
-            if (kKind == kEntropy) out.entropy[row] = 0.0f;
-        }
+        skip_outputs<kKind>(out, row);
         return;
     }
-    const float zy = threadIdx.x == 0 && y < L.vocab ? widen(z[y]) : 0.0f;  // (dz may be written over z after the join)
-    Running r{-INFINITY, 0.0f, 0.0f};
+    const float zy = y < L.vocab ? widen(z[y]) : -INFINITY;  // (read before the join, after which dz may be written over z)
+    Running r{zy, 0.0f, 0.0f};
     int k = g.lo + (int)threadIdx.x;
     for (; k + (kBatch - 1) * kThreads < g.hi; k += kBatch * kThreads) {
         const T* at = z + (k * n - g.lead);
@@ -447,29 +476,295 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             v[u] = Vec<T>{kGrad ? ld16_again(at + u * kThreads * n) : ld16_stream(at + u * kThreads * n)};
-        float m = v[0].max();
-#pragma unroll
-        for (int u = 1; u < kBatch; ++u) m = fmaxf(m, v[u].max());
-        if (m > r.m) raise<kMoment>(L, r, m);
-        const float o = origin(r.m);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) add_vector<T, kMoment>(L, v[u], o, r.s, r.u);
+        add_vectors<T, kMoment>(L, v, r);
     }
-    auto add_one = [&](const Vec<T>& v) {
-        const float m = v.max();
-        if (m > r.m) raise<kMoment>(L, r, m);
-        add_vector<T, kMoment>(L, v, origin(r.m), r.s, r.u);
-    };
-    for (; k < g.hi; k += kThreads) add_one(Vec<T>{kGrad ? ld16_again(z + (k * n - g.lead)) : ld16_stream(z + (k * n - g.lead))});
-    if (g.edge >= 0) add_one(load_edge(z, g.edge * n - g.lead, L.vocab));
+    for (; k < g.hi; k += kThreads) {
+        const Vec<T> v[1] = {{kGrad ? ld16_again(z + (k * n - g.lead)) : ld16_stream(z + (k * n - g.lead))}};
+        add_vectors<T, kMoment>(L, v, r);
+    }
+    if (g.edge >= 0) {
+        const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
+        add_vectors<T, kMoment>(L, v, r);
+    }
     r = join_parts<kMoment>(L, parts, r);
-    c = finish_row<kKind>(L, P, out, row, y, zy, r, c, parts);
+    c = finish_row<kKind>(L, P, out, row, y, zy, r, c, threadIdx.x == 0 && cluster_rank() == 0);
     if constexpr (kGrad) {
         const RowGrad q{origin(r.m), c, 1.0f / r.s, y < L.vocab ? (int)y : -16};
         if (c == 0.0f) zero_row<T, kThreads>(g, L.vocab, dz, same);
         else grad_row<T, kThreads>(L, z, g, q, dz, same);
     }
     leave_cluster();
+}
+
+// ----------------------------------------------------------------------------------------------------------------------
+// many long rows: a ring of shared memory
+// ----------------------------------------------------------------------------------------------------------------------
+//
+// Where there are more rows than CTAs, what a CTA per row loses is its start and its joins: the loads stop there. Here a
+// CTA takes row after row. One producer thread keeps a ring of kStages stages filled with bulk copies, the row's vectors
+// once for the statistics and, for a gradient, once more for it (from L2), and goes on to the next row while the consumers
+// join this one's parts: the loads depend on nothing that they compute. Eight consumer warps take a stage each together.
+// Rows are handed out by the hardware: the grid has a CTA for each row, and a CTA that is at work cancels one that has not
+// begun and takes its row, so that rows that do not count leave no CTA idle. Every wait is bounded.
+// A CTA's consumer threads, its ring, and the CTAs of an SM.
+template <int kThreads, int kVectors, int kCount, int kCtas>
+struct RingShape {
+    static constexpr int consumers = kThreads, warps = kThreads / 32, vectors = kVectors, stages = kCount, ctas = kCtas;
+    static constexpr int threads = kThreads + 32, stage_bytes = kVectors * 16, bytes = kCount * stage_bytes;
+    static constexpr int per_thread = kVectors / kThreads;
+};
+// Reading only: three CTAs, so that others compute while one joins a row (8,192 rows of 50,257 bfloat16 logits, of which
+// 6,144 count: 106 us, 5.8 TB/s; with two 123 us, with one of 512 threads 178 us).
+using ReadRing = RingShape<256, 2048, 2, 3>;
+// A gradient reads its row again, which has to be in L2 still: of long rows one at a time on an SM (6,144 rows of 131,072:
+// 502 us, 6.0 TB/s, against 535 us with two CTAs and 625 us with three), of others two (6,144 rows of 50,257: 217 us
+// against 261 us with one).
+using GradRing = RingShape<256, 2048, 3, 2>;
+using LongGradRing = RingShape<512, 2048, 6, 1>;
+constexpr int64_t kLongRowBytes = 160 << 10;
+constexpr int kEntries = 2;
+constexpr int64_t kRingRows = 608;
+
+// Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_logits_status).
+__device__ unsigned int g_logits_status;
+enum : unsigned int { kStatusRowProducer = 0x20u, kStatusRowConsumer = 0x40u };
+
+// A row handed to the consumers; row < 0: no more.
+struct RowEntry {
+    int64_t row, y;
+    float c;   // the coefficient where it was given
+    float zy;  // the target's logit; -inf for a target past the vocabulary
+};
+
+template <typename S>
+struct Ring {
+    alignas(16) uint4 answer;  // of the hardware, about the next row
+    uint64_t asked;
+    uint64_t full[S::stages], empty[S::stages];
+    uint64_t entry_full[kEntries], entry_empty[kEntries];
+    uint64_t joined;
+    RowEntry entry[kEntries];
+    Running part[2][S::warps];  // by the row's parity: a warp is at most one row ahead
+};
+
+template <typename S>
+__device__ __forceinline__ void ask_next_row(Ring<S>& ring) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last answer has been read
+    mbar_arrive_expect_tx(&ring.asked, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(&ring.answer)),
+                 "r"(smem_u32(&ring.asked))
+                 : "memory");
+}
+
+// The row of the CTA that was cancelled, or -1 when every CTA has begun.
+template <typename S>
+__device__ __forceinline__ int64_t next_row(const Ring<S>& ring) {
+    uint32_t got, row;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
+        "ld.shared.v2.b64 {lo, hi}, [%2];\n\t"
+        "mov.b128 r, {lo, hi};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(row)
+        : "r"(smem_u32(&ring.answer))
+        : "memory");
+    return got ? (int64_t)row : -1;
+}
+
+template <typename T>
+__device__ __forceinline__ Vec<T> stage_vector(const unsigned char* stage, int i) {
+    return Vec<T>{*reinterpret_cast<const uint4*>(stage + i * 16)};
+}
+
+// kStream: the gradient with the statistics given (`stat`, out.coef the whole coefficient): no first pass.
+template <typename T, RowKind kKind, bool kStream, typename S>
+__global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, PolicyTerms P, RowOut out) {
+    constexpr int n = Vec<T>::n;
+    constexpr bool kGrad = kKind == kGiven || kKind == kPolicy, kMoment = kKind == kEntropy;
+    constexpr int kPasses = kGrad && !kStream ? 2 : 1;
+    extern __shared__ __align__(128) unsigned char stages[];
+    constexpr int kStages = S::stages, kStageVectors = S::vectors, kStageBytes = S::stage_bytes;
+    constexpr int kConsumers = S::consumers, kPerThread = S::per_thread;
+    __shared__ Ring<S> ring;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        mbar_init(&ring.asked, 1);
+        mbar_init(&ring.joined, kConsumers / 32);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&ring.full[i], 1);
+            mbar_init(&ring.empty[i], kConsumers / 32);
+        }
+        for (int i = 0; i < kEntries; ++i) {
+            mbar_init(&ring.entry_full[i], 1);
+            mbar_init(&ring.entry_empty[i], kConsumers / 32);
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
+    wait_prerequisite();
+    const T* logits = reinterpret_cast<const T*>(L.z);
+
+    if (warp == kConsumers / 32) {  // the producer
+        if (lane != 0) return;
+        auto head = [&](int64_t row, int64_t* y, float* c) {
+            *y = target_of(L, row);
+            *c = kKind == kGiven ? out.coef[row] * out.factor : 1.0f;
+        };
+        uint64_t keep, drop;
+        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
+        int64_t row = blockIdx.x, y, slot = 0;
+        float c;
+        head(row, &y, &c);
+        ask_next_row(ring);
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+            if (!mbar_wait(&ring.asked, r & 1)) {
+                ok = false;
+                break;
+            }
+            const int64_t next = next_row(ring);
+            int64_t next_y = -1;
+            float next_c = 0.0f;
+            if (next >= 0) {
+                ask_next_row(ring);
+                head(next, &next_y, &next_c);  // (arrives while this row's copies are queued)
+            }
+            const int e = r % kEntries;
+            if (r >= kEntries && !(ok = mbar_wait(&ring.entry_empty[e], (r / kEntries - 1) & 1))) break;
+            const float zy = !kStream && y >= 0 && y < L.vocab ? widen(logits[row * L.ld + y]) : -INFINITY;
+            ring.entry[e] = RowEntry{row, y, c, zy};
+            mbar_arrive(&ring.entry_full[e]);
+            if (y >= 0 && c != 0.0f) {
+                const T* z = logits + row * L.ld;
+                const int lead = (int)(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+                const int lo = lead > 0, hi = (lead + L.vocab) / n;
+                for (int pass = 0; pass < kPasses && ok; ++pass)
+                    for (int k = lo; k < hi; k += kStageVectors, ++slot) {
+                        const int s = (int)(slot % kStages);
+                        if (slot >= kStages && !(ok = mbar_wait(&ring.empty[s], (uint32_t)(slot / kStages - 1) & 1))) break;
+                        const uint32_t bytes = (uint32_t)min(kStageVectors, hi - k) * 16;
+                        mbar_arrive_expect_tx(&ring.full[s], bytes);
+                        if (kPasses == 1) bulk_copy_g2s(stages + s * kStageBytes, z + (k * n - lead), bytes, &ring.full[s]);
+                        else bulk_copy_g2s_hint(stages + s * kStageBytes, z + (k * n - lead), bytes, &ring.full[s], pass == 0 ? keep : drop);
+                    }
+            }
+            row = next, y = next_y, c = next_c;
+            if (row < 0 && ok) {  // the end: an entry of its own
+                ++r;
+                const int last = r % kEntries;
+                if (r >= kEntries && !(ok = mbar_wait(&ring.entry_empty[last], (r / kEntries - 1) & 1))) break;
+                ring.entry[last] = RowEntry{-1, -1, 0.0f, 0.0f};
+                mbar_arrive(&ring.entry_full[last]);
+                break;
+            }
+        }
+        if (!ok) atomicOr(&g_logits_status, kStatusRowProducer);
+        // no copy is left in flight when the CTA ends
+        for (int64_t j = slot < kStages ? 0 : slot - kStages; j < slot; ++j) mbar_wait(&ring.full[j % kStages], (j / kStages) & 1);
+        return;
+    }
+
+    int64_t slot = 0;
+    int joins = 0;
+    auto give_up = [&] { atomicOr(&g_logits_status, kStatusRowConsumer); };
+    for (int r = 0;; ++r) {
+        const int e = r % kEntries;
+        if (!mbar_wait(&ring.entry_full[e], (r / kEntries) & 1)) return give_up();
+        const RowEntry at = ring.entry[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.entry_empty[e]);
+        const int64_t row = at.row, y = at.y;
+        if (row < 0) return;
+        const T* z = logits + row * L.ld;
+        T* dz = kGrad ? reinterpret_cast<T*>(out.dz) + row * out.ld_d : nullptr;
+        const bool same = kGrad && (reinterpret_cast<uintptr_t>(dz) - reinterpret_cast<uintptr_t>(z)) % 16 == 0;
+        const RowVectors g = row_vectors(z, L.vocab);
+        float c = kKind == kGiven ? at.c : 0.0f;
+        if (y < 0 || (kKind == kGiven && c == 0.0f)) {
+            if (kGrad) zero_row<T, kConsumers>(g, L.vocab, dz, same);
+            skip_outputs<kKind>(out, row);
+            continue;
+        }
+        const float zy = at.zy;
+        Running q{zy, 0.0f, 0.0f};
+        if constexpr (!kStream) {
+            for (int k = g.lo; k < g.hi; k += kStageVectors, ++slot) {
+                const int s = (int)(slot % kStages), left = g.hi - k;
+                if (!mbar_wait(&ring.full[s], (uint32_t)(slot / kStages) & 1)) return give_up();
+                const unsigned char* stage = stages + s * kStageBytes;
+                if (left >= kStageVectors) {
+                    Vec<T> v[kPerThread];
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u) v[u] = stage_vector<T>(stage, (int)threadIdx.x + u * kConsumers);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ring.empty[s]);
+#pragma unroll
+                    for (int u = 0; u < kPerThread; u += 2) {
+                        const Vec<T> two_of[2] = {v[u], v[u + 1]};
+                        add_vectors<T, kMoment>(L, two_of, q);
+                    }
+                } else {
+                    for (int i = (int)threadIdx.x; i < left; i += kConsumers) {
+                        const Vec<T> v[1] = {stage_vector<T>(stage, i)};
+                        add_vectors<T, kMoment>(L, v, q);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ring.empty[s]);
+                }
+            }
+            if (g.edge >= 0) {
+                const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
+                add_vectors<T, kMoment>(L, v, q);
+            }
+            q = join_warp<kMoment>(L, q);
+            Running* part = ring.part[joins & 1];
+            if (lane == 0) {
+                part[warp] = q;
+                mbar_arrive(&ring.joined);
+            }
+            if (!mbar_wait(&ring.joined, joins & 1)) return give_up();
+            ++joins;
+            q = join_warp<kMoment>(L, lane < kConsumers / 32 ? part[lane] : Running{-INFINITY, 0.0f, 0.0f});
+            c = finish_row<kKind>(L, P, out, row, y, zy, q, c, threadIdx.x == 0);
+        } else {
+            const RowStat st = out.stat[row];
+            q = Running{st.zmax, 1.0f / st.inv_sum, 0.0f};
+            if (y >= L.vocab) c = NAN;
+        }
+        if constexpr (kGrad) {
+            const RowGrad grad{origin(q.m), c, kStream ? out.stat[row].inv_sum : 1.0f / q.s, y < L.vocab ? (int)y : -16};
+            if (g.edge >= 0) {
+                const int j0 = g.edge * n - g.lead;
+                float d[n];
+                grad_values(L, load_edge(z, j0, L.vocab), grad, j0, d);
+                store_some(dz, j0, L.vocab, d);
+            }
+            for (int k = g.lo; k < g.hi; k += kStageVectors, ++slot) {
+                const int s = (int)(slot % kStages), left = g.hi - k, j0 = (k + (int)threadIdx.x) * n - g.lead;
+                if (!mbar_wait(&ring.full[s], (uint32_t)(slot / kStages) & 1)) return give_up();
+                const unsigned char* stage = stages + s * kStageBytes;
+                if (left >= kStageVectors) {
+                    Vec<T> v[kPerThread];
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u) v[u] = stage_vector<T>(stage, (int)threadIdx.x + u * kConsumers);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ring.empty[s]);
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u) grad_vector(L, v[u], grad, j0 + u * kConsumers * n, dz, same);
+                } else {
+                    for (int i = (int)threadIdx.x; i < left; i += kConsumers)
+                        grad_vector(L, stage_vector<T>(stage, i), grad, (k + i) * n - g.lead, dz, same);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ring.empty[s]);
+                }
+            }
+        }
+    }
 }
 
 // The gradient with the rows' statistics and coefficients given: a stream, a cluster of CTAs per row for few rows.
@@ -497,121 +792,170 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_grad_ke
 // per-token and per-pair terms
 // ----------------------------------------------------------------------------------------------------------------------
 
-constexpr int kSumThreads = 1024;
+constexpr int kSumThreads = 1024, kSumWarps = kSumThreads / 32;
 
-__device__ __forceinline__ double warp_sum(double x) {
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-    return x;
-}
+// A sum in two float32, hi + lo, to some 2^-45 of its terms: what each addition rounds away is added up too. (This chip has
+// next to no float64: 96 tokens' sums in it took 37 us.) hi alone once it is infinite or a NaN.
+struct Sum {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float t = hi + x, z = t - hi;
+        lo += (hi - (t - z)) + (x - z);
+        hi = t;
+    }
+    __device__ __forceinline__ void add(const Sum& o) {
+        add(o.hi);
+        lo += o.lo;
+    }
+    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
 
-__device__ double block_sum_ordered(double x, double* shared) {
-    x = warp_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x / 32] = x;
-    __syncthreads();
-    double s = 0.0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += shared[w];
+// The lanes' sums in order, in lane 0.
+__device__ __forceinline__ Sum warp_total(Sum s) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const Sum o{__shfl_down_sync(~0u, s.hi, d), __shfl_down_sync(~0u, s.lo, d)};
+        s.add(o);
+    }
     return s;
 }
 
 __global__ void __launch_bounds__(kSumThreads) policy_sums_kernel(LogitRows L, PolicyTerms P, const float* logps,
                                                                   float* stats) {
-    __shared__ double shared[kSumThreads / 32];
+    __shared__ Sum part[3][kSumWarps];
     wait_prerequisite();
     allow_dependents();
-    double sl = 0.0, sk = 0.0, sc = 0.0;
-    for (int64_t row = threadIdx.x; row < L.rows; row += blockDim.x) {
-        if (target_of(L, row) < 0) continue;
-        const float lp = logps[row], A = P.advantages[row], r = expf(lp - P.old_logps[row]);
-        const float plain = r * A, held = fminf(fmaxf(r, P.lo), P.hi) * A;
-        const double w = P.weights ? P.weights[row] : 1.0;
-        sl -= w * (held < plain ? held : plain);
-        sc += held < plain ? w : 0.0;
-        if (P.ref_logps) {
-            const float q = P.ref_logps[row] - lp;
-            sk += w * (double)(expm1f(q) - q);
-        }
+    Sum sum[3] = {};  // surrogate, KL, clipped
+    for (int64_t row = threadIdx.x; row < L.rows; row += kSumThreads) {
+        const int64_t y = target_of(L, row);
+        const float lp = logps[row], A = P.advantages[row], old = P.old_logps[row];
+        const float w = P.weights ? P.weights[row] : 1.0f, ref = P.ref_logps ? P.ref_logps[row] : 0.0f;
+        if (y < 0) continue;
+        const float r = expf(lp - old), plain = r * A, held = fminf(fmaxf(r, P.lo), P.hi) * A;
+        sum[0].add(-w * (held < plain ? held : plain));
+        if (P.ref_logps) sum[1].add(w * (expm1f(ref - lp) - (ref - lp)));
+        sum[2].add(held < plain ? w : 0.0f);
     }
-    sl = block_sum_ordered(sl, shared) * P.inv_denom;
-    sk = block_sum_ordered(sk, shared) * P.inv_denom;
-    sc = block_sum_ordered(sc, shared) * P.inv_denom;
-    if (threadIdx.x == 0) {
-        stats[0] = (float)(P.ref_logps ? sl + P.kl_coef * sk : sl);
-        stats[1] = (float)sl;
-        stats[2] = (float)sk;
-        stats[3] = (float)sc;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const Sum s = warp_total(sum[i]);
+        if (lane == 0) part[i][warp] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        float v[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] = warp_total(part[i][lane]).value() * P.inv_denom;
+        if (lane == 0) {
+            stats[0] = P.ref_logps ? fmaf(P.kl_coef, v[1], v[0]) : v[0];
+            stats[1] = v[0];
+            stats[2] = v[1];
+            stats[3] = v[2];
+        }
     }
 }
 
-__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
 __device__ __forceinline__ int64_t clamp_row(int64_t x, int64_t rows) { return x < 0 ? 0 : x > rows ? rows : x; }
 
-// One CTA: each warp sums its sequences; then the threads take the pairs' losses and slopes; then each warp writes its
-// sequences' coefficients. sums[s] holds a sequence's sum, then its rows' coefficient.
-__global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTerms P, const double* logps, double* sums,
-                                                            float* loss, float* rewards, float* coef) {
-    __shared__ double shared[kSumThreads / 32];
+// One CTA. Teams of warps sum the sequences (as many teams as sequences, at most one a warp); then the threads take the
+// pairs' losses and slopes; then the teams write their sequences' coefficients. sums[s]: a sequence's sum, then its rows'
+// coefficient.
+__global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTerms P, const float* logps,
+                                                            const float* rest, float* sums, float* loss, float* rewards,
+                                                            float* coef) {
+    __shared__ Sum part[kSumWarps];
+    __shared__ int count[kSumWarps];
     wait_prerequisite();
     allow_dependents();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = 2 * P.pairs;
+    int team = kSumWarps;  // warps of a team
+    while (team > 1 && kSumWarps / team < n) team /= 2;
+    const int first = warp / team, step = kSumWarps / team, rank = (warp % team) * 32 + lane, stride = team * 32;
     if (coef)
-        for (int64_t row = threadIdx.x; row < L.rows; row += blockDim.x) coef[row] = 0.0f;
-    auto count_of = [&](int64_t a, int64_t b) {
-        int n = 0;
-        for (int64_t row = a + lane; row < b; row += 32) n += target_of(L, row) >= 0;
-        return __reduce_add_sync(~0u, n);
-    };
-    for (int s = warp; s < 2 * P.pairs; s += warps) {
-        const int64_t a = clamp_row(P.cu_seqlens[s], L.rows), b = clamp_row(P.cu_seqlens[s + 1], L.rows);
-        double d = 0.0;
-        for (int64_t row = a + lane; row < b; row += 32)
-            if (target_of(L, row) >= 0) d += logps[row] - (P.ref_logps ? (double)P.ref_logps[row] : 0.0);
-        d = warp_sum(d);
-        if (P.length_norm) {
-            const int n = count_of(a, b);
-            d /= n > 0 ? n : 1;
+        for (int64_t row = threadIdx.x; row < L.rows; row += kSumThreads) coef[row] = 0.0f;
+    const int rounds = (n + step - 1) / step;
+    for (int i = 0; i < rounds; ++i) {
+        const int s = first + i * step;
+        Sum d{};
+        int scored = 0;
+        if (s < n) {
+            const int64_t a = clamp_row(P.cu_seqlens[s], L.rows), b = clamp_row(P.cu_seqlens[s + 1], L.rows);
+#pragma unroll 4
+            for (int64_t row = a + rank; row < b; row += stride) {
+                const bool on = target_of(L, row) >= 0;
+                const float hi = logps[row], lo = rest[row], ref = P.ref_logps ? P.ref_logps[row] : 0.0f;
+                d.add(on ? hi : 0.0f);
+                d.add(on ? -ref : 0.0f);
+                d.lo += lo;
+                scored += on;
+            }
         }
+        d = warp_total(d);
+        scored = __reduce_add_sync(~0u, scored);
+        __syncthreads();  // the last round's parts have been read
         if (lane == 0) {
-            sums[s] = d;
-            if (rewards) rewards[s] = (float)(P.beta * d);
+            part[warp] = d;
+            count[warp] = scored;
+        }
+        __syncthreads();
+        if (rank == 0 && s < n) {
+            for (int w = 1; w < team; ++w) {
+                d.add(part[warp + w]);
+                scored += count[warp + w];
+            }
+            const float share = P.length_norm ? 1.0f / (float)(scored > 0 ? scored : 1) : 1.0f;
+            sums[s] = P.length_norm ? d.value() / (float)(scored > 0 ? scored : 1) : d.value();
+            sums[n + s] = share;
+            if (rewards) rewards[s] = P.beta * sums[s];
         }
     }
     __syncthreads();
-    double mine = 0.0;
-    for (int p = threadIdx.x; p < P.pairs; p += blockDim.x) {
-        const double d = sums[2 * p] - sums[2 * p + 1], h = P.beta * d;
-        double l, slope;  // the pair's loss and its derivative by d
+    Sum mine{};
+    for (int p = threadIdx.x; p < P.pairs; p += kSumThreads) {
+        const float d = sums[2 * p] - sums[2 * p + 1], h = P.beta * d;
+        float l, slope;  // the pair's loss and its derivative by d
         if (P.kind == MICA_PREF_SIGMOID) {
-            l = (1.0 - P.smoothing) * softplus(-h) + (P.smoothing > 0.0 ? P.smoothing * softplus(h) : 0.0);
-            slope = P.beta * (-(1.0 - P.smoothing) / (1.0 + exp(h)) + P.smoothing / (1.0 + exp(-h)));
+            l = (1.0f - P.smoothing) * softplus(-h) + (P.smoothing > 0.0f ? P.smoothing * softplus(h) : 0.0f);
+            slope = P.beta * (P.smoothing / (1.0f + expf(-h)) - (1.0f - P.smoothing) / (1.0f + expf(h)));
         } else if (P.kind == MICA_PREF_HINGE) {
-            l = h < 1.0 ? 1.0 - h : (h >= 1.0 ? 0.0 : h);  // (a NaN stays one)
-            slope = h < 1.0 ? -P.beta : (h >= 1.0 ? 0.0 : h);
+            l = h < 1.0f ? 1.0f - h : (h >= 1.0f ? 0.0f : h);  // (a NaN stays one)
+            slope = h < 1.0f ? -P.beta : (h >= 1.0f ? 0.0f : h);
         } else {
-            const double gap = d - 0.5 / P.beta;
+            const float gap = d - 0.5f / P.beta;
             l = gap * gap;
-            slope = 2.0 * gap;
+            slope = 2.0f * gap;
         }
-        mine += l;
+        mine.add(l);
         sums[2 * p] = slope * P.grad_factor;
         sums[2 * p + 1] = -slope * P.grad_factor;
     }
-    const double total = block_sum_ordered(mine, shared);
-    if (threadIdx.x == 0) *loss = P.pairs ? (float)(total / P.pairs) : 0.0f;
+    mine = warp_total(mine);
+    if (lane == 0) part[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+        const Sum total = warp_total(part[lane]);
+        if (lane == 0) *loss = P.pairs ? total.value() / (float)P.pairs : 0.0f;
+    }
     if (!coef) return;
-    for (int s = warp; s < 2 * P.pairs; s += warps) {
+    for (int s = first; s < n; s += step) {
         const int64_t a = clamp_row(P.cu_seqlens[s], L.rows), b = clamp_row(P.cu_seqlens[s + 1], L.rows);
-        double c = sums[s];
-        if (P.length_norm) {
-            const int n = count_of(a, b);
-            c /= n > 0 ? n : 1;
-        }
-        for (int64_t row = a + lane; row < b; row += 32) coef[row] = (float)c;
+        const float c = sums[s] * sums[n + s];
+        for (int64_t row = a + rank; row < b; row += stride) coef[row] = c;
     }
 }
 
-// How a row is cut: C CTAs of `threads` threads.
+// Many long rows go through the ring. Measured both ways, in us, the ring first: log-probabilities of 8,192 rows of 8,192
+// bfloat16 logits 42 and 36, 16,384: 51 and 52, 32,768: 73 and 95; policy gradients of 6,144 rows of 16,384: 95 and 79,
+// 50,257: 217 and 267; of 600 rows of 131,072: 59 and 74, of 300: 38 and 39.
+bool takes_ring(const LogitRows& L, bool grad) {
+    const int64_t bytes = L.vocab * (L.dtype == MICA_F32 ? 4 : 2);
+    return L.rows >= kRingRows && bytes >= (grad ? 64 << 10 : 32 << 10);
+}
+
+// How a row is cut otherwise: C CTAs of `threads` threads.
 struct RowShape {
     int C, threads;
 };
@@ -625,10 +969,11 @@ RowShape row_shape(const LogitRows& L) {
 }
 
 template <typename K, typename... A>
-cudaError_t launch_clusters(K kernel, int64_t ctas, int C, int threads, void* stream, A... args) {
+cudaError_t launch_clusters(K kernel, int64_t ctas, int C, int threads, size_t shared, void* stream, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -642,13 +987,27 @@ cudaError_t launch_clusters(K kernel, int64_t ctas, int C, int threads, void* st
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <typename T, RowKind kKind, bool kStream>
+cudaError_t launch_ring(const LogitRows& L, const PolicyTerms& P, const RowOut& out, void* stream) {
+    auto go = [&](auto shape) {
+        using S = decltype(shape);
+        const auto kernel = ring_kernel<T, kKind, kStream, S>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
+        return e != cudaSuccess ? e : launch_clusters(kernel, L.rows, 1, S::threads, S::bytes, stream, L, P, out);
+    };
+    if constexpr (kKind == kLogps || kKind == kEntropy) return go(ReadRing{});
+    else if constexpr (kStream) return go(GradRing{});
+    else return L.vocab * (int64_t)sizeof(T) > kLongRowBytes ? go(LongGradRing{}) : go(GradRing{});
+}
+
 template <RowKind kKind, typename T>
 cudaError_t launch_rows_of(const LogitRows& L, const PolicyTerms& P, const RowOut& out, void* stream) {
+    if (takes_ring(L, kKind == kGiven || kKind == kPolicy)) return launch_ring<T, kKind, false>(L, P, out, stream);
     const RowShape s = row_shape(L);
     const int64_t ctas = L.rows * s.C;
     return s.threads == kShortThreads
-               ? launch_clusters(row_kernel<T, kShortThreads, kKind>, ctas, s.C, s.threads, stream, L, P, out)
-               : launch_clusters(row_kernel<T, kRowThreads, kKind>, ctas, s.C, s.threads, stream, L, P, out);
+               ? launch_clusters(row_kernel<T, kShortThreads, kKind>, ctas, s.C, s.threads, 0, stream, L, P, out)
+               : launch_clusters(row_kernel<T, kRowThreads, kKind>, ctas, s.C, s.threads, 0, stream, L, P, out);
 }
 
 template <RowKind kKind>
@@ -660,18 +1019,21 @@ int launch_rows(const LogitRows& L, const PolicyTerms& P, const RowOut& out, voi
 
 template <typename T>
 int launch_row_grad_of(const LogitRows& L, const RowStat* stat, const float* coef, void* dz, int64_t ld_d, void* stream) {
+    if (takes_ring(L, true))
+        return (int)launch_ring<T, kGiven, true>(
+            L, PolicyTerms{}, RowOut{nullptr, nullptr, nullptr, const_cast<RowStat*>(stat), coef, 1.0f, dz, ld_d}, stream);
     const RowShape s = row_shape(L);
     T* out = static_cast<T*>(dz);
-    return (int)(s.threads == kShortThreads ? launch_clusters(row_grad_kernel<T, kShortThreads>, L.rows * s.C, s.C, s.threads,
+    return (int)(s.threads == kShortThreads ? launch_clusters(row_grad_kernel<T, kShortThreads>, L.rows * s.C, s.C, s.threads, 0,
                                                               stream, L, stat, coef, out, ld_d)
-                                            : launch_clusters(row_grad_kernel<T, kRowThreads>, L.rows * s.C, s.C, s.threads,
+                                            : launch_clusters(row_grad_kernel<T, kRowThreads>, L.rows * s.C, s.C, s.threads, 0,
                                                               stream, L, stat, coef, out, ld_d));
 }
 
 }  // namespace
 
-int launch_row_logps(const LogitRows& L, float* logps, double* wide_logps, float* entropy, RowStat* stat, void* stream) {
-    const RowOut out{logps, wide_logps, entropy, stat, nullptr, 0.0f, nullptr, 0};
+int launch_row_logps(const LogitRows& L, float* logps, float* rest_logps, float* entropy, RowStat* stat, void* stream) {
+    const RowOut out{logps, rest_logps, entropy, stat, nullptr, 0.0f, nullptr, 0};
     return entropy ? launch_rows<kEntropy>(L, PolicyTerms{}, out, stream) : launch_rows<kLogps>(L, PolicyTerms{}, out, stream);
 }
 
@@ -690,12 +1052,24 @@ int launch_row_grad(const LogitRows& L, const RowStat* stat, const float* coef, 
 }
 
 int launch_policy_sums(const LogitRows& L, const PolicyTerms& P, const float* logps, float* stats, void* stream) {
-    return (int)launch_clusters(policy_sums_kernel, 1, 1, kSumThreads, stream, L, P, logps, stats);
+    return (int)launch_clusters(policy_sums_kernel, 1, 1, kSumThreads, 0, stream, L, P, logps, stats);
 }
 
-int launch_pairs(const LogitRows& L, const PairTerms& P, const double* logps, double* sums, float* loss, float* rewards,
-                 float* coef, void* stream) {
-    return (int)launch_clusters(pairs_kernel, 1, 1, kSumThreads, stream, L, P, logps, sums, loss, rewards, coef);
+int launch_pairs(const LogitRows& L, const PairTerms& P, const float* logps, const float* rest, float* sums, float* loss,
+                 float* rewards, float* coef, void* stream) {
+    return (int)launch_clusters(pairs_kernel, 1, 1, kSumThreads, 0, stream, L, P, logps, rest, sums, loss, rewards, coef);
+}
+
+int read_logits_status(unsigned int* status) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_logits_status, sizeof v);
+    if (e != cudaSuccess) return (int)e;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_logits_status, &zero, sizeof zero);
+    }
+    *status = v;
+    return (int)e;
 }
 
 }  // namespace mica

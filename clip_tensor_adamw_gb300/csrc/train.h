@@ -33,14 +33,13 @@ struct PolicyTerms {
     const float* advantages;
     const float* ref_logps;  // or null
     const float* weights;    // or null
-    float lo, hi, kl_coef;
-    double inv_denom;
+    float lo, hi, kl_coef, inv_denom;
     float grad_factor;  // grad_scale / (denom * temperature)
 };
 
-// logps, and where not null entropies, of every row; without entropies also, where not null, the logps before they are
-// rounded and the softmax statistics
-int launch_row_logps(const LogitRows& L, float* logps, double* wide_logps, float* entropy, RowStat* stat, void* stream);
+// logps, and where not null entropies, of every row; without entropies also, where not null, what rounding took from the
+// logps, and the softmax statistics
+int launch_row_logps(const LogitRows& L, float* logps, float* rest_logps, float* entropy, RowStat* stat, void* stream);
 // dz = coef * ((j == target) - p): coef[row] * factor given, the softmax computed here
 int launch_row_softmax_grad(const LogitRows& L, const float* coef, float factor, void* dz, int64_t ld_d, void* stream);
 // the same with the coefficient of the policy loss, from the log-probability found on the way (also written)
@@ -55,12 +54,13 @@ struct PairTerms {
     int32_t pairs;
     int32_t kind;
     int32_t length_norm;
-    double beta, smoothing;
-    double grad_factor;  // grad_scale / (pairs * temperature)
+    float beta, smoothing;
+    float grad_factor;  // grad_scale / (pairs * temperature)
 };
-// loss, rewards (or null) and, where coef is not null, each row's coefficient; sums: 2 * pairs doubles of workspace
-int launch_pairs(const LogitRows& L, const PairTerms& P, const double* logps, double* sums, float* loss, float* rewards,
-                 float* coef, void* stream);
+// loss, rewards (or null) and, where coef is not null, each row's coefficient, from the logps and their rests; sums: 4 * pairs
+// floats of workspace
+int launch_pairs(const LogitRows& L, const PairTerms& P, const float* logps, const float* rest, float* sums, float* loss,
+                 float* rewards, float* coef, void* stream);
 
 int launch_act_pack(const void* x, int64_t ld_x, const mica_packed& p, int32_t act, bool gated, void* y, int64_t ld_y,
                     void* stream);
@@ -80,6 +80,9 @@ struct Wgrad {
     void* dw;
     int64_t ld_dw;
 };
+// The status words of these kernels' bounded waits, as read_device_status (plan.h).
+int read_logits_status(unsigned int* status);
+
 int64_t wgrad_workspace(int64_t tokens, int64_t features, int64_t n, int sms);
 int launch_wgrad(const Wgrad& w, void* workspace, int sms, void* stream);
 

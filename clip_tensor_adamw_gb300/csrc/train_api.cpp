@@ -196,11 +196,10 @@ extern "C" mica_status mica_token_logps_grad(const mica_logits* z, const float* 
                         "log-probabilities' gradient launch");
 }
 
-// workspace: a sum per sequence | a log-probability, a RowStat and a coefficient per row
+// workspace: two floats per sequence | a RowStat, the rest of a log-probability and a coefficient per row
 extern "C" int64_t mica_preference_workspace(int64_t rows, int32_t pairs) {
     if (rows < 0 || rows > MICA_MAX_ROWS || pairs < 0 || pairs > (1 << 24)) return 0;
-    return (int64_t)((size_t)pairs * 2 * sizeof(double) + round16((size_t)rows * (sizeof(double) + sizeof(RowStat))) +
-                     round16((size_t)rows * sizeof(float)));
+    return (int64_t)((size_t)pairs * 4 * sizeof(float) + round16((size_t)rows * (sizeof(RowStat) + 2 * sizeof(float))));
 }
 
 extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t* cu_seqlens, int32_t pairs,
@@ -238,18 +237,17 @@ extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t*
     MICA_TRY(b.matrix(workspace, 1, need, need, 1, 16, true, "workspace"));
     MICA_TRY(b.disjoint());
 
-    char* w = static_cast<char*>(workspace);
-    double* sums = reinterpret_cast<double*>(w);
-    double* wide = sums + 2 * (size_t)pairs;
-    RowStat* stat = reinterpret_cast<RowStat*>(wide + z->rows);
-    w += (size_t)pairs * 2 * sizeof(double) + round16((size_t)z->rows * (sizeof(double) + sizeof(RowStat)));
-    float* coef = reinterpret_cast<float*>(w);
-    const PairTerms P{cu_seqlens, ref_logps, pairs, hp->kind, (hp->flags & MICA_PREF_LENGTH_NORM) != 0, hp->beta,
-                      hp->label_smoothing, pairs ? hp->grad_scale / pairs / z->temperature : 0.0};
+    float* sums = static_cast<float*>(workspace);
+    RowStat* stat = reinterpret_cast<RowStat*>(sums + 4 * (size_t)pairs);
+    float* rest = reinterpret_cast<float*>(stat + z->rows);
+    float* coef = rest + z->rows;
+    const PairTerms P{cu_seqlens, ref_logps, pairs, hp->kind, (hp->flags & MICA_PREF_LENGTH_NORM) != 0,
+                      (float)hp->beta, (float)hp->label_smoothing,
+                      pairs ? (float)(hp->grad_scale / pairs / z->temperature) : 0.0f};
     if (z->rows)
-        MICA_TRY(after_launch(launch_row_logps(L, logps, wide, nullptr, dlogits ? stat : nullptr, stream), stream,
+        MICA_TRY(after_launch(launch_row_logps(L, logps, rest, nullptr, dlogits ? stat : nullptr, stream), stream,
                               "log-probabilities launch"));
-    MICA_TRY(after_launch(launch_pairs(L, P, wide, sums, loss, rewards, dlogits ? coef : nullptr, stream), stream,
+    MICA_TRY(after_launch(launch_pairs(L, P, logps, rest, sums, loss, rewards, dlogits ? coef : nullptr, stream), stream,
                           "preference pairs launch"));
     if (!dlogits || z->rows == 0) return ok();
     return after_launch(launch_row_grad(L, stat, coef, dlogits, ld_d, stream), stream, "preference gradient launch");
@@ -283,7 +281,7 @@ extern "C" mica_status mica_policy_loss(const mica_logits* z, const float* old_l
     MICA_TRY(b.disjoint());
 
     const PolicyTerms P{old_logps, advantages, ref_logps, weights, (float)(1.0 - hp->clip_low),
-                        (float)(1.0 + hp->clip_high), (float)hp->kl_coef, 1.0 / hp->denom,
+                        (float)(1.0 + hp->clip_high), (float)hp->kl_coef, (float)(1.0 / hp->denom),
                         (float)(hp->grad_scale / hp->denom / z->temperature)};
     if (z->rows)
         MICA_TRY(after_launch(dlogits ? launch_row_policy_grad(L, P, logps, dlogits, ld_d, stream)

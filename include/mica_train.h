@@ -22,7 +22,7 @@
  *     whose size a call of its own gives; its contents need not be set and are not read by a later call.
  *   - Results do not depend on the order in which CTAs run: no floating-point atomics.
  *   - Every call can be captured into a CUDA graph.
- *   - Sums, maxima and statistics are held in float32 or float64; results are rounded once, to nearest-even.
+ *   - Sums, maxima and statistics are held in float32, pairs of float32 or float64; results are rounded once, to nearest-even.
  *   - Where the inputs give an infinity or a NaN, the formula's value comes out, never an error.
  */
 #ifndef MICA_TRAIN_H
@@ -104,7 +104,7 @@ typedef struct {
  *   logps     [rows]: the policy's log-probabilities
  *   dlogits   the gradient of grad_scale * loss, as in mica_token_logps_grad; NULL for the loss alone
  * workspace: mica_preference_workspace(rows, pairs) bytes, 16-byte aligned.
- * A sequence's log-ratios are summed in float64. 0 <= pairs <= 2^24.
+ * A sequence's log-ratios are summed unrounded, in pairs of float32 (some 45 bits). 0 <= pairs <= 2^24.
  * Errors: NULL / COUNT (also a workspace too small) / DTYPE / HYPER / ADDRESS / OVERLAP / DEVICE / CUDA.
  */
 MICA_API mica_status mica_preference_loss(const mica_logits* z, const int32_t* cu_seqlens, int32_t pairs,
@@ -133,7 +133,7 @@ typedef struct {
  *   logps   [rows]
  *   dlogits the gradient of grad_scale * loss, as in mica_token_logps_grad; NULL for the loss alone
  * old_logps, advantages, ref_logps and weights are [rows] float32; those of rows that do not count are not read. The
- * four sums are taken in float64. No workspace.
+ * sums are taken in pairs of float32 (some 45 bits). No workspace.
  * Errors: as mica_preference_loss.
  */
 MICA_API mica_status mica_policy_loss(const mica_logits* z, const float* old_logps, const float* advantages,

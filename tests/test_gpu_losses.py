@@ -426,3 +426,71 @@ def test_streams_graphs_and_repeats():
     torch.cuda.synchronize()
     for a, b in zip(both(), held):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,vocab,ld,offset", [(700, 20011, 20011, 1), (640, 32768, 32768, 0), (1300, 16411, 16416, 3)])
+def test_many_long_rows(rows, vocab, ld, offset, dtype):
+    """Every operator over more long rows than there are CTAs, at every alignment: runs of rows that do not count,
+    masked values, the gradient in place and elsewhere."""
+    z, y = make(rows, vocab, dtype, seed=rows, ld=ld, offset=offset)
+    y[100:300] = -1
+    y[5] = vocab + 3
+    z[7, 10:] = -math.inf
+    y[7] = 4
+    z[8] = torch.finfo(dtype).min
+    inside = y.clamp(max=vocab - 1)
+    want, want_h, p = reference(z, inside, 0.9)
+    lp, h = mica.mica_token_logps(z, y, temperature=0.9, entropy=True)
+    fine = torch.arange(rows, device="cuda") != 5
+    tol = rel(vocab) + 6 * U * want.abs() + 64 * U
+    close(lp[fine], want[fine], tol[fine])
+    close(h[fine], want_h[fine], 30 * rel(vocab))
+    assert lp[5].isnan()
+    assert torch.equal(lp[fine], mica.mica_token_logps(z, y, temperature=0.9)[fine])
+    y[5] = 3
+    want, _, p = reference(z, y, 0.9)
+    c = torch.randn(rows, generator=gen(5), device="cuda")
+    c[::5] = 0.0
+    k = torch.where(y >= 0, c.double() / 0.9, 0.0)
+    d = mica.mica_token_logps_grad(z, y, c, temperature=0.9)
+    close_grad(d, grad_of(p, y, k), p, k, vocab)
+    elsewhere = torch.full((rows * (vocab + 3) + 9,), 7.0, dtype=dtype, device="cuda")
+    out = elsewhere[2:].as_strided((rows, vocab), (vocab + 3, 1))
+    mica.mica_token_logps_grad(z, y, c, temperature=0.9, out=out)
+    assert torch.equal(out, d)
+    out.fill_(7.0)
+    assert (elsewhere == 7.0).all()
+    # preference: pairs of 40 rows, one sequence empty
+    cu = torch.arange(0, rows + 1, 20, dtype=torch.int32, device="cuda")[:31].clone()
+    cu[4] = cu[5]
+    ref = (reference(z, y)[0] + 0.1 * c).float()
+    r = mica.mica_preference_loss(z, y, cu, ref, beta=0.1)
+    lp64, _, p1 = reference(z, y)
+    loss, rewards, dlp = preference_reference(lp64, y >= 0, cu.tolist(), ref.double(), 0.1, "sigmoid", 0.0, False)
+    lp_tol = float((rel(vocab) + 6 * U * lp64.abs() + 64 * U).max())
+    close(r.rewards, rewards, 0.1 * 40 * lp_tol + 2 * U * rewards.abs())
+    close(r.loss, loss.reshape(1), 80 * 0.1 * lp_tol + 4 * U * loss)
+    c_tol = torch.where(y >= 0, 80 * lp_tol * 0.0025 / 15 + 8 * U * dlp.abs(), 0.0)
+    close_grad(r.dlogits, grad_of(p1, y, dlp), p1, dlp, vocab, c_tol)
+    # policy, then both gradients in place: the same bits
+    old = (lp64 + 0.05 * c).float()
+    adv = torch.randn(rows, generator=gen(9), device="cuda")
+    q = mica.mica_policy_loss(z, y, old, adv, denom=100.0, ref_logps=ref, kl_coef=0.1, clip_low=1.0, clip_high=math.inf)
+    x = lp64.clone().requires_grad_()
+    ratio, kq = torch.exp(x - old.double()), ref.double() - x
+    each = torch.where(y >= 0, -ratio * adv + 0.1 * (torch.exp(kq) - kq - 1), 0.0)
+    k = torch.autograd.grad(each.sum() / 100, x)[0]
+    size = (torch.where(y >= 0, (ratio * adv).abs() + 0.1 * (torch.exp(kq) + 1), 0.0) / 100).detach()
+    each_tol = size * 2 * (lp_tol + 8 * U * (1 + old.abs()))
+    close(q.stats[0], (each.sum() / 100).detach(), float(each_tol.sum()) + 1e-6 * float(size.sum()))
+    close_grad(q.dlogits, grad_of(p1, y, k), p1, k, vocab, each_tol + 8 * U * k.abs())
+    copy = z.clone() if ld == vocab else None
+    again = mica.mica_policy_loss(z, y, old, adv, denom=100.0, ref_logps=ref, kl_coef=0.1, clip_low=1.0,
+                                  clip_high=math.inf, out=z)
+    assert torch.equal(again.dlogits, q.dlogits) and torch.equal(again.stats, q.stats)
+    if copy is not None:
+        z.copy_(copy)
+        again = mica.mica_preference_loss(z, y, cu, ref, beta=0.1, out=z)
+        assert torch.equal(again.dlogits, r.dlogits)
+    mica.mica_sync()
