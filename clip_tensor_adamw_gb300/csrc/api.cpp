@@ -65,9 +65,10 @@ static mica_status check_device_status(const char* what) {
     unsigned int st = 0, fst = 0;
     int e = read_device_status(&st);
     if (e == (int)cudaSuccess) e = read_fused_status(&fst);
-    unsigned int more = 0;
-    if (e == (int)cudaSuccess) e = read_logits_status(&more);
-    st |= more;
+    unsigned int rows = 0, wgrad = 0;
+    if (e == (int)cudaSuccess) e = read_logits_status(&rows);
+    if (e == (int)cudaSuccess) e = read_wgrad_status(&wgrad);
+    st |= rows | wgrad;
     if (e != (int)cudaSuccess) return cuda_fail((cudaError_t)e, what);
     if (fst) return fail(MICA_ERR_CUDA, "%s: a fused kernel's grid-wide wait gave up (status 0x%x); its results are "
                          "not valid, and the list's table must be released (mica_release_cache)", what, fst);

@@ -82,8 +82,9 @@ struct Wgrad {
 };
 // The status words of these kernels' bounded waits, as read_device_status (plan.h).
 int read_logits_status(unsigned int* status);
+int read_wgrad_status(unsigned int* status);
 
-int64_t wgrad_workspace(int64_t tokens, int64_t features, int64_t n, int sms);
+int64_t wgrad_workspace(int64_t tokens, int64_t features, int64_t n, const void* dy, int64_t ld_dy, int sms);
 int launch_wgrad(const Wgrad& w, void* workspace, int sms, void* stream);
 
 }  // namespace mica

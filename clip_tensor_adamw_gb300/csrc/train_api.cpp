@@ -344,15 +344,10 @@ extern "C" mica_status mica_act_grad(const mica_packed* p, int32_t act, int32_t 
                         "activation gradient launch");
 }
 
-extern "C" int64_t mica_packed_wgrad_workspace(int64_t tokens, int64_t features, int64_t n) {
-    if (tokens < 0 || tokens > MICA_MAX_ROWS || features < 0 || features > MICA_MAX_COLS || n < 0 || n > MICA_MAX_COLS)
-        return 0;
+extern "C" int64_t mica_packed_wgrad_workspace(const mica_packed* x, const void* dy, int64_t ld_dy, int64_t n) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return wgrad_workspace(tokens, features, n, sm_count(dev));
+    if (check_packed(x, "the checkpoint") != MICA_OK || n < 0 || n > MICA_MAX_COLS || current_device(&dev) != MICA_OK) return 0;
+    return wgrad_workspace(x->rows, x->cols, n, dy, ld_dy, sm_count(dev));
 }
 
 extern "C" mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, int64_t ld_dy, int32_t dy_dtype, int64_t n,
@@ -371,7 +366,7 @@ extern "C" mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, i
     int dev = 0;
     MICA_TRY(current_device(&dev));
     const int sms = sm_count(dev);
-    const int64_t need = wgrad_workspace(x->rows, x->cols, n, sms);
+    const int64_t need = wgrad_workspace(x->rows, x->cols, n, dy, ld_dy, sms);
     if (need && !workspace) return fail(MICA_ERR_NULL, "workspace is NULL");
     if (workspace_bytes < need)
         return fail(MICA_ERR_COUNT, "the workspace has %lld bytes of %lld", (long long)workspace_bytes, (long long)need);

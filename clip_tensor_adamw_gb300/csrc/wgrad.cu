@@ -1,70 +1,549 @@
-// A linear layer's weight gradient from its input's 8-bit checkpoint: dw = add + x^T dy.
+// A linear layer's weight gradient from its input's 8-bit checkpoint: dw = add + x^T dy, on the tensor cores.
+//
+// A pair of CTAs takes a tile of 256 outputs (dy's columns, the rows of the accumulator) x 256 features (the checkpoint's
+// columns), 64 tokens at a time. Each CTA holds 128 of the outputs and decodes 128 of the features; tcgen05.mma of the pair
+// multiplies both halves with one another, so that dy and the codes come from L2 once for two SMs (one CTA alone would
+// take 80 bytes a clock, more than an SM gets).
+//
+// A code times its block's power of two is exact in bfloat16 (7 bits), and by the format in binary16 too, so decoding adds
+// no rounding and the products are exact. The tensor cores' additions are not rounded to nearest: their sums leave TMEM
+// every kChunk tokens and are added in registers, which keeps a float32 gradient as exact as a float32 product's.
+//
+// Both operands are MN-major: a stage is [64 tokens][64 columns] boxes with 128-byte swizzle, as dy lies in memory and as
+// the codes do, so nothing is transposed. dy comes by TMA; the codes come by TMA into a stage of their own, from which
+// eight warps decode them into the operand. The same warps empty TMEM, a chunk behind.
+//
+// Whole tiles are dealt to the pairs in turn; what remains for the last round is split along the tokens so that every pair
+// has a share, whose sums a second kernel joins in a fixed order.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "packed.cuh"
+#include "pipe.cuh"
 #include "plan.h"
+#include "stream.cuh"
 #include "train.h"
 
 namespace mica {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kSimpleThreads = 256;
+constexpr int kHalf = 128, kTile = 2 * kHalf;  // outputs, and features: of a CTA, of a pair
+constexpr int kDepth = 64;                     // tokens of a stage
+constexpr int kDepths = 5;                     // stages
+constexpr int kChunkStages = 4;                // stages between two visits to the accumulator
+constexpr int kWorkers = 256, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 64;
+constexpr int kOperandBytes = kDepth * kHalf * 2, kCodeBytes = kDepth * kHalf, kBoxBytes = kDepth * 128;
+constexpr int kSharedBytes = 1024 + kDepths * (2 * kOperandBytes + kCodeBytes);
 
-// One CTA per 64 x 64 tile of dw, each thread 4 x 4 of it, 16 tokens at a time through shared memory.
-template <typename T, typename O>
-__global__ void __launch_bounds__(kSimpleThreads) wgrad_simple_kernel(Wgrad w) {
-    __shared__ float xs[kDepth][kTile], ys[kDepth][kTile];
-    const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
-    const T* dy = static_cast<const T*>(w.dy);
-    float acc[4][4] = {};
-    for (int64_t t0 = 0; t0 < w.x.rows; t0 += kDepth) {
-        for (int k = threadIdx.x; k < kDepth * kTile; k += kSimpleThreads) {
-            const int64_t t = t0 + k / kTile, i = i0 + k % kTile, j = j0 + k % kTile;
-            float x = 0.0f, y = 0.0f;
-            if (t < w.x.rows && i < w.x.cols)
-                x = (float)reinterpret_cast<const int8_t*>(w.x.codes)[t * w.x.ld + i] *
-                    step_value(reinterpret_cast<const uint8_t*>(w.x.steps)[t * w.x.ld_s + i / kBlock]);
-            if (t < w.x.rows && j < w.n) y = widen(dy[t * w.ld_dy + j]);
-            xs[k / kTile][k % kTile] = x;
-            ys[k / kTile][k % kTile] = y;
-        }
-        __syncthreads();
-        for (int k = 0; k < kDepth; ++k)
-            for (int a = 0; a < 4; ++a)
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(xs[k][ti + a], ys[k][tj + b], acc[a][b]);
-        __syncthreads();
+// Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_wgrad_status).
+__device__ unsigned int g_wgrad_status;
+enum : unsigned int { kStatusWgrad = 0x80u };
+
+// How the work is dealt: `whole` tiles one after another, then `split` tiles in `parts` along the tokens.
+struct Deal {
+    int pairs, feature_tiles, tiles, whole, parts, stages;
+};
+
+// A pair's i-th piece of work: a tile's stages [from, to); piece >= 0: part of a split tile, whose sums go to the workspace.
+struct Piece {
+    int tile, from, to, piece;
+};
+
+__host__ __device__ inline int pieces_of(const Deal& d) { return d.whole + (d.tiles - d.whole) * d.parts; }
+
+__device__ __forceinline__ Piece piece_at(const Deal& d, int i) {
+    if (i < d.whole) return Piece{i, 0, d.stages, -1};
+    const int k = i - d.whole, part = k % d.parts;
+    return Piece{d.whole + k / d.parts, (int)((int64_t)d.stages * part / d.parts),
+                 (int)((int64_t)d.stages * (part + 1) / d.parts), d.parts > 1 ? k : -1};
+}
+
+struct Barriers {
+    uint64_t codes_full[kDepths], codes_empty[kDepths];  // the codes of a stage have come; the workers have read them
+    uint64_t dy_full[kDepths];                           // dy's part of a stage has come
+    uint64_t ready[kDepths];                             // (leader) both CTAs' operands of a stage are in place
+    uint64_t used[kDepths];                              // the products of a stage are done
+    uint64_t sum_full[2], sum_empty[2];                  // a chunk's sums are in TMEM; (leader) both CTAs have taken them
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ uint32_t rank_of_cta() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrives on the leader's barrier.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+// mbar_wait for barriers that the other CTA arrives on
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+    const uint32_t addr = smem_u32(bar);
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (done) return true;
     }
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t i = i0 + ti + a, j = j0 + tj + b;
-            if (i >= w.x.cols || j >= w.n) continue;
-            float v = acc[a][b];
-            if (w.add) v += widen(static_cast<const O*>(w.add)[i * w.ld_add + j]);
-            static_cast<O*>(w.dw)[i * w.ld_dw + j] = narrow<O>(v);
+    return false;
+}
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The descriptor of an MN-major operand with 128-byte swizzle: boxes of 64 columns kBoxBytes apart, groups of 8 tokens 1 KB.
+__device__ __forceinline__ uint64_t operand(uint32_t at) {
+    return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(kBoxBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// float32 sums of bfloat16 (or binary16) products, both operands MN-major, 256 x 256
+template <typename T>
+__host__ __device__ constexpr uint32_t instruction() {
+    constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | 1u << 15 | 1u << 16 | (kTile / 8) << 17 | (kTile / 16) << 24;
+}
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t how, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(how), "r"((uint32_t)add)
+        : "memory");
+}
+// The barrier (in both CTAs) completes when every product so far is done.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of the thread's row of TMEM
+__device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Two codes as 16-bit floats times the step: bytes `pick` (a byte permutation's selector) of w.
+//   bfloat16: 128 + (q & 127) and 128 + (q & 128) have the bits 0x4300 | those, and their difference is q
+//   binary16: 1024 + (q + 128) has the bits 0x6400 | (q ^ 128)
+template <typename T>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t low, uint32_t sign, uint32_t pick, uint32_t step) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const uint32_t a = __byte_perm(low, 0x43434343u, pick), c = __byte_perm(sign, 0x43434343u, pick);
+        asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(a), "r"(c), "r"(step));
+    } else {
+        const uint32_t a = __byte_perm(low, 0x64646464u, pick);
+        asm("{\n\t.reg .b32 d;\n\tsub.rn.f16x2 d, %1, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
+            : "=r"(r)
+            : "r"(a), "r"(0x64806480u), "r"(step));  // 1152
+    }
+    return r;
+}
+
+// Sixteen codes of a token, all of one block, into the operand's stage: 8 features to 16 bytes, which lie in the row of 128
+// bytes where the swizzle puts them. Half the lanes store their second 8 first, so that the 8 lanes of a row use all banks.
+template <typename T>
+__device__ __forceinline__ void decode(unsigned char* stage, int token, int part, uint4 codes, uint32_t step8) {
+    const float s = step_value(step8);
+    const T one = narrow<T>(s);
+    const uint32_t h = *reinterpret_cast<const unsigned short*>(&one), step = h | h << 16;
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint4 out[2];
+    uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t low = bf16 ? w[i] & 0x7F7F7F7Fu : w[i] ^ 0x80808080u, sign = w[i] & 0x80808080u;
+        o[2 * i] = decode_pair<T>(low, sign, 0x4140u, step);
+        o[2 * i + 1] = decode_pair<T>(low, sign, 0x4342u, step);
+    }
+    unsigned char* row = stage + (part / 4) * kBoxBytes + token * 128;
+    const int first = part / 4, at0 = (((part % 4) * 2 + first) ^ (token % 8)) * 16;
+    const int at1 = (((part % 4) * 2 + 1 - first) ^ (token % 8)) * 16;
+    *reinterpret_cast<uint4*>(row + at0) = first ? out[1] : out[0];
+    *reinterpret_cast<uint4*>(row + at1) = first ? out[0] : out[1];
+}
+
+template <typename O>
+__device__ __forceinline__ void write_dw(const Wgrad& w, int64_t i, int64_t j, float v) {
+    if (i >= w.x.cols || j >= w.n) return;
+    if (w.add) v += widen(static_cast<const O*>(w.add)[i * w.ld_add + j]);
+    static_cast<O*>(w.dw)[i * w.ld_dw + j] = narrow<O>(v);
+}
+
+template <typename T, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap dy_map, Wgrad w, Deal deal,
+                 float* partial) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Barriers bar;
+    unsigned char* base = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    unsigned char* dy_stage = base;
+    unsigned char* x_stage = base + kDepths * kOperandBytes;
+    unsigned char* code_stage = base + 2 * kDepths * kOperandBytes;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)rank_of_cta(), pair = blockIdx.x / 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kDepths; ++i) {
+            mbar_init(&bar.codes_full[i], 1);
+            mbar_init(&bar.codes_empty[i], kWorkerWarps);
+            mbar_init(&bar.dy_full[i], 1);
+            mbar_init(&bar.ready[i], 2 * kWorkerWarps);
+            mbar_init(&bar.used[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sum_full[i], 1);
+            mbar_init(&bar.sum_empty[i], 2 * kWorkerWarps);
+        }
+        mbar_fence_init();
+    }
+    if (warp == kWorkerWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bar.tmem);
+    wait_prerequisite();
+    allow_dependents();
+
+    const int all = pieces_of(deal);
+    bool ok = true;
+    if (warp == kWorkerWarps) {  // the producer
+        if (lane == 0) {
+            int64_t it = 0;
+            for (int i = pair; i < all && ok; i += deal.pairs) {
+                const Piece p = piece_at(deal, i);
+                const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf, i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
+                for (int k = p.from; k < p.to; ++k, ++it) {
+                    const int s = (int)(it % kDepths);
+                    const uint32_t last = (uint32_t)(it / kDepths - 1) & 1;
+                    if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], last) && wait_cluster(&bar.used[s], last))) break;
+                    mbar_arrive_expect_tx(&bar.codes_full[s], kCodeBytes);
+                    load_box(code_stage + s * kCodeBytes, &codes_map, i0, k * kDepth, &bar.codes_full[s]);
+                    mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
+                    load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
+                    load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
+                }
+            }
+            // no copy is left in flight when the CTA ends
+            for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) {
+                mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+                mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+            }
+        }
+    } else if (warp == kWorkerWarps + 1) {  // the products, issued by one thread of the leader
+        if (lane == 0 && rank == 0) {
+            int64_t it = 0, chunk = 0;
+            for (int i = pair; i < all && ok; i += deal.pairs) {
+                const Piece p = piece_at(deal, i);
+                for (int k = p.from; k < p.to && ok; ++k, ++it) {
+                    const int s = (int)(it % kDepths), b = (int)(chunk & 1), within = (k - p.from) % kChunkStages;
+                    if (within == 0 && chunk >= 2 && !(ok = wait_cluster(&bar.sum_empty[b], (uint32_t)(chunk / 2 - 1) & 1))) break;
+                    if (!(ok = wait_cluster(&bar.ready[s], (uint32_t)(it / kDepths) & 1))) break;
+                    fence_after();
+                    const uint64_t a = operand(smem_u32(dy_stage + s * kOperandBytes));
+                    const uint64_t x = operand(smem_u32(x_stage + s * kOperandBytes));
+#pragma unroll
+                    for (int d = 0; d < kDepth / 16; ++d)  // 16 tokens are 2 KB further on
+                        multiply(tmem + b * kTile, a + d * (2048 >> 4), x + d * (2048 >> 4), instruction<T>(), within + d > 0);
+                    commit(&bar.used[s]);
+                    if (within == kChunkStages - 1 || k == p.to - 1) {
+                        commit(&bar.sum_full[b]);
+                        ++chunk;
+                    }
+                }
+            }
+        }
+    } else {  // the workers
+        const int quarter = warp % 4, group = warp / 4;  // of the accumulator's rows; of its columns
+        const uint32_t own = tmem + ((uint32_t)quarter << 21) + group * kHalf;
+        const int token = threadIdx.x / 8, part = threadIdx.x % 8;
+        const uint8_t* steps = reinterpret_cast<const uint8_t*>(w.x.steps);
+        const int64_t blocks = (w.x.cols + kBlock - 1) / kBlock;
+        int64_t it = 0, chunk = 0;
+        for (int i = pair; i < all && ok; i += deal.pairs) {
+            const Piece p = piece_at(deal, i);
+            const int64_t j0 = (int64_t)(p.tile / deal.feature_tiles) * kTile + rank * kHalf, i_tile = (int64_t)(p.tile % deal.feature_tiles) * kTile;
+            const int64_t block = (i_tile + rank * kHalf + part * 16) / kBlock;
+            auto step_at = [&](int k, int u) -> uint32_t {
+                const int64_t t = (int64_t)k * kDepth + token + u * 32;
+                return k < p.to && t < w.x.rows && block < blocks ? __ldg(steps + t * w.x.ld_s + block) : 0u;
+            };
+            float sum[kHalf];
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
+            auto take = [&]() {  // the oldest chunk's sums that have not been taken
+                const int b = (int)(chunk & 1);
+                if (!wait_cluster(&bar.sum_full[b], (uint32_t)(chunk / 2) & 1)) return false;
+                ++chunk;
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32) {
+                    uint32_t v[32];
+                    load_sums(own + b * kTile + c, v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[c + e] += __uint_as_float(v[e]);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&bar.sum_empty[b]);
+                return true;
+            };
+            // the steps come from memory: two stages ahead
+            uint32_t now[2], next[2], later[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) now[u] = step_at(p.from, u), next[u] = step_at(p.from + 1, u);
+            int waiting = 0;  // chunks whose operands are in place and whose sums have not been taken
+            for (int k = p.from; k < p.to; ++k, ++it) {
+                const int s = (int)(it % kDepths);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) later[u] = step_at(k + 2, u);
+                if (!(ok = mbar_wait(&bar.codes_full[s], (uint32_t)(it / kDepths) & 1))) break;
+                uint4 codes[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    codes[u] = *reinterpret_cast<const uint4*>(code_stage + s * kCodeBytes + (token + u * 32) * kHalf + part * 16);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
+                if (it >= kDepths && !(ok = wait_cluster(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) decode<T>(x_stage + s * kOperandBytes, token + u * 32, part, codes[u], now[u]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (warp == 0 && !(ok = mbar_wait(&bar.dy_full[s], (uint32_t)(it / kDepths) & 1))) break;
+                __syncwarp();
+                if (lane == 0) arrive_leader(&bar.ready[s]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) now[u] = next[u], next[u] = later[u];
+                if ((k - p.from) % kChunkStages == kChunkStages - 1 || k == p.to - 1) {
+                    if (waiting && !(ok = take())) break;
+                    waiting = 1;
+                }
+            }
+            if (ok && waiting) ok = take();
+            if (!ok) break;
+            // lanes hold neighbouring outputs, so a feature's stores are contiguous
+            const int64_t j = j0 + quarter * 32 + lane;
+            if (p.piece < 0) {
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c) write_dw<O>(w, i_tile + group * kHalf + c, j, sum[c]);
+            } else {
+                float* out = partial + ((int64_t)p.piece * 2 + rank) * kHalf * kTile + threadIdx.x;
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c) out[c * kWorkers] = sum[c];
+            }
+        }
+    }
+    if (!ok) atomicOr(&g_wgrad_status, kStatusWgrad);
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // the other CTA's products have read this CTA's shared memory, its arrivals have landed
+    fence_after();
+    if (warp == kWorkerWarps + 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Joins the parts of split tiles (none where there are no tokens): a CTA takes 8 of a worker's columns.
+template <typename O>
+__global__ void __launch_bounds__(kWorkers) wgrad_join_kernel(Wgrad w, Deal deal, const float* partial) {
+    wait_prerequisite();
+    allow_dependents();
+    constexpr int kColumns = 8, kCtas = kHalf / kColumns;
+    const int c0 = blockIdx.x % kCtas * kColumns, rank = blockIdx.x / kCtas % 2, k = blockIdx.x / (2 * kCtas);
+    const int tile = deal.whole + k, quarter = threadIdx.x / 32 % 4, group = threadIdx.x / kHalf, lane = threadIdx.x % 32;
+    const int64_t j = (int64_t)(tile / deal.feature_tiles) * kTile + rank * kHalf + quarter * 32 + lane;
+    const int64_t i0 = (int64_t)(tile % deal.feature_tiles) * kTile + group * kHalf;
+    float sum[kColumns] = {};
+    for (int part = 0; part < deal.parts; ++part) {
+        const float* in = partial + (((int64_t)k * deal.parts + part) * 2 + rank) * kHalf * kTile + threadIdx.x;
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c) sum[c] += __ldcg(in + (c0 + c) * kWorkers);
+    }
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) write_dw<O>(w, i0 + c0 + c, j, sum[c]);
+}
+
+// dy with its rows at 16-byte boundaries, for TMA: 8 elements to a thread.
+__global__ void __launch_bounds__(256) align_rows_kernel(const unsigned short* dy, int64_t ld, int64_t rows, int64_t n,
+                                                         unsigned short* out, int64_t ld_out) {
+    wait_prerequisite();
+    allow_dependents();
+    const int64_t per = ld_out / 8;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < rows * per; q += (int64_t)gridDim.x * 256) {
+        const int64_t row = q / per, col = q % per * 8;
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = col + 2 * i;
+            const uint32_t lo = c < n ? dy[row * ld + c] : 0u, hi = c + 1 < n ? dy[row * ld + c + 1] : 0u;
+            v[i] = lo | hi << 16;
+        }
+        *reinterpret_cast<uint4*>(out + row * ld_out + col) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+Deal deal_of(int64_t tokens, int64_t features, int64_t n, int sms) {
+    Deal d{};
+    d.pairs = sms / 2 < 1 ? 1 : sms / 2;
+    d.feature_tiles = (int)((features + kTile - 1) / kTile);
+    d.tiles = (int)((n + kTile - 1) / kTile) * d.feature_tiles;
+    d.stages = (int)((tokens + kDepth - 1) / kDepth);
+    d.whole = d.tiles / d.pairs * d.pairs;
+    const int rest = d.tiles - d.whole;
+    d.parts = 1;
+    if (rest) {
+        d.parts = d.pairs / rest;
+        if (d.parts > d.stages / kChunkStages) d.parts = d.stages / kChunkStages;  // a chunk at least
+        if (d.parts < 1) d.parts = 1;
+    }
+    if (d.stages == 0) d.whole = 0, d.parts = 0;  // nothing to add up: the join alone writes every tile
+    return d;
+}
+
+bool rows_aligned(const void* dy, int64_t ld) { return reinterpret_cast<uintptr_t>(dy) % 16 == 0 && ld % 8 == 0 && ld > 0; }
+
+int64_t partial_bytes(const Deal& d) {
+    return d.parts > 1 ? (int64_t)(d.tiles - d.whole) * d.parts * kTile * kTile * sizeof(float) : 0;
+}
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encode_fn() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (Encode) nullptr;
+        }
+        return reinterpret_cast<Encode>(p);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t cols, int64_t rows, int64_t stride_bytes,
+            uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+    const Encode fn = encode_fn();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride_bytes};
+    const cuuint32_t box[2] = {box_cols, (cuuint32_t)kDepth}, one[2] = {1, 1};
+    return fn && fn(map, type, 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, int64_t ctas, int threads, size_t shared, void* stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, typename O>
+cudaError_t launch_typed(const Wgrad& w, const Deal& d, float* partial, void* stream) {
+    if (d.stages) {
+        CUtensorMap codes, dy;
+        const auto type = std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if (!encode(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.x.codes, (w.x.cols + kBlock - 1) / kBlock * kBlock, w.x.rows, w.x.ld,
+                    kHalf, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode(&dy, type, w.dy, w.n, w.x.rows, w.ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+        const auto kernel = wgrad_kernel<T, O>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
+        const int all = pieces_of(d);
+        if (e == cudaSuccess)
+            e = launch_after(kernel, 2 * (int64_t)(all < d.pairs ? all : d.pairs), kThreads2, kSharedBytes, stream, codes, dy, w, d,
+                             partial);
+        if (e != cudaSuccess) return e;
+    }
+    if (d.parts == 1) return cudaSuccess;
+    return launch_after(wgrad_join_kernel<O>, (int64_t)(d.tiles - d.whole) * 2 * (kHalf / 8), kWorkers, 0, stream, w, d,
+                        (const float*)partial);
 }
 
 template <typename T>
-void launch_simple(const Wgrad& w, cudaStream_t st) {
-    const dim3 grid((unsigned)((w.n + kTile - 1) / kTile), (unsigned)((w.x.cols + kTile - 1) / kTile));
-    if (w.dw_dtype == MICA_F32) wgrad_simple_kernel<T, float><<<grid, kSimpleThreads, 0, st>>>(w);
-    else if (w.dw_dtype == MICA_F16) wgrad_simple_kernel<T, __half><<<grid, kSimpleThreads, 0, st>>>(w);
-    else wgrad_simple_kernel<T, __nv_bfloat16><<<grid, kSimpleThreads, 0, st>>>(w);
+cudaError_t launch_into(const Wgrad& w, const Deal& d, float* partial, void* stream) {
+    return w.dw_dtype == MICA_F32   ? launch_typed<T, float>(w, d, partial, stream)
+           : w.dw_dtype == MICA_F16 ? launch_typed<T, __half>(w, d, partial, stream)
+                                    : launch_typed<T, __nv_bfloat16>(w, d, partial, stream);
 }
 
 }  // namespace
 
-int64_t wgrad_workspace(int64_t, int64_t, int64_t, int) { return 0; }
+int64_t wgrad_workspace(int64_t tokens, int64_t features, int64_t n, const void* dy, int64_t ld_dy, int sms) {
+    if (features == 0 || n == 0) return 0;
+    return partial_bytes(deal_of(tokens, features, n, sms)) + (rows_aligned(dy, ld_dy) ? 0 : tokens * ((n + 7) / 8 * 8) * 2);
+}
 
-int launch_wgrad(const Wgrad& w, void*, int, void* stream) {
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (w.dy_dtype == MICA_F16) launch_simple<__half>(w, st);
-    else launch_simple<__nv_bfloat16>(w, st);
-    count_launches(1);
-    return (int)cudaGetLastError();
+int launch_wgrad(const Wgrad& in, void* workspace, int sms, void* stream) {
+    Wgrad w = in;
+    const Deal d = deal_of(w.x.rows, w.x.cols, w.n, sms);
+    float* partial = static_cast<float*>(workspace);
+    if (d.stages && !rows_aligned(w.dy, w.ld_dy)) {
+        unsigned short* copy = reinterpret_cast<unsigned short*>(static_cast<char*>(workspace) + partial_bytes(d));
+        const int64_t ld = (w.n + 7) / 8 * 8, threads = w.x.rows * (ld / 8), ctas = (threads + 255) / 256;
+        const cudaError_t e = launch_after(align_rows_kernel, ctas < (1 << 16) ? ctas : (1 << 16), 256, 0, stream,
+                                           static_cast<const unsigned short*>(w.dy), w.ld_dy, w.x.rows, w.n, copy, ld);
+        if (e != cudaSuccess) return (int)e;
+        w.dy = copy;
+        w.ld_dy = ld;
+    }
+    return (int)(w.dy_dtype == MICA_F16 ? launch_into<__half>(w, d, partial, stream)
+                                        : launch_into<__nv_bfloat16>(w, d, partial, stream));
+}
+
+int read_wgrad_status(unsigned int* status) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_wgrad_status, sizeof v);
+    if (e != cudaSuccess) return (int)e;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_wgrad_status, &zero, sizeof zero);
+    }
+    *status = v;
+    return (int)e;
 }
 
 }  // namespace mica

@@ -64,7 +64,7 @@ def _train() -> ctypes.CDLL:
             getattr(L, name).restype = ctypes.c_int
         L.mica_preference_workspace.argtypes = [_I64, _I32]
         L.mica_preference_workspace.restype = _I64
-        L.mica_packed_wgrad_workspace.argtypes = [_I64, _I64, _I64]
+        L.mica_packed_wgrad_workspace.argtypes = [_KP, _P, _I64, _I64]
         L.mica_packed_wgrad_workspace.restype = _I64
         _lib = L
     return _lib
@@ -344,7 +344,7 @@ def mica_packed_wgrad(packed: PackedActivation, dy: torch.Tensor, *, add: torch.
     L = _train()
     with _On(stream, dy.device) as s:
         dw = _output(out, (features, n), out_dtype, "out", dy)
-        size = L.mica_packed_wgrad_workspace(tokens, features, n)
+        size = L.mica_packed_wgrad_workspace(packed._c, dy.data_ptr(), ld, n)
         work = torch.empty(size, dtype=torch.uint8, device=dy.device) if size else None
         _check(L.mica_packed_wgrad(packed._c, dy.data_ptr(), ld, code, n, None if add is None else add.data_ptr(),
                                    0 if add is None else _matrix(add, "add"), dw.data_ptr(), _matrix(dw, "out"),

@@ -199,13 +199,14 @@ MICA_API mica_status mica_act_grad(const mica_packed* p, int32_t act, int32_t ga
  * source). dw: features x n, row stride ld_dw, MICA_F32, MICA_F16 or MICA_BF16; add: the same type with row stride
  * ld_add, NULL for zeros, or dw itself (accumulation in place). The products are exact and summed in float32, add is
  * added in float32, and the result is rounded once. No tokens: dw = add. workspace: mica_packed_wgrad_workspace bytes
- * for the same extents, 16-byte aligned (it may be 0 bytes, and NULL then).
+ * for the same arguments, 16-byte aligned (it may be 0 bytes, and NULL then): sums of parts, at most 20 MB, and a copy of a
+ * dy whose rows are not 16-byte aligned.
  * Errors: NULL / COUNT / DTYPE / ADDRESS / OVERLAP / DEVICE / CUDA.
  */
 MICA_API mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, int64_t ld_dy, int32_t dy_dtype, int64_t n,
                                        const void* add, int64_t ld_add, void* dw, int64_t ld_dw, int32_t dw_dtype,
                                        void* workspace, int64_t workspace_bytes, void* stream);
-MICA_API int64_t mica_packed_wgrad_workspace(int64_t tokens, int64_t features, int64_t n);
+MICA_API int64_t mica_packed_wgrad_workspace(const mica_packed* x, const void* dy, int64_t ld_dy, int64_t n);
 
 #ifdef __cplusplus
 }
