@@ -32,7 +32,7 @@ namespace {
 constexpr int kHalf = 128, kTile = 2 * kHalf;  // outputs, and features: of a CTA, of a pair
 constexpr int kDepth = 64;                     // tokens of a stage
 constexpr int kDepths = 5;                     // stages
-constexpr int kChunkStages = 4;                // stages between two visits to the accumulator
+constexpr int kChunkStages = 8;                // stages between two visits to the accumulator
 constexpr int kWorkers = 256, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 64;
 constexpr int kOperandBytes = kDepth * kHalf * 2, kCodeBytes = kDepth * kHalf, kBoxBytes = kDepth * 128;
 constexpr int kSharedBytes = 1024 + kDepths * (2 * kOperandBytes + kCodeBytes);
@@ -67,6 +67,7 @@ struct Barriers {
     uint64_t used[kDepths];                              // the products of a stage are done
     uint64_t sum_full[2], sum_empty[2];                  // a chunk's sums are in TMEM; (leader) both CTAs have taken them
     uint32_t tmem;
+    alignas(16) uint32_t steps[kDepths][kDepth];  // a token's four blocks of 32 features
 };
 
 __device__ __forceinline__ uint32_t rank_of_cta() {
@@ -82,24 +83,15 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 at;\n\t"
         "mapa.shared::cluster.u32 at, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
+        "mbarrier.arrive.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
-// mbar_wait for barriers that the other CTA arrives on
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-    const uint32_t addr = smem_u32(bar);
-    for (uint32_t i = 0; i < kMaxPolls; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (done) return true;
-    }
-    return false;
+// Four bytes, or zeros, to shared memory without waiting for them; a thread's arrival on `bar` once all of its have landed.
+__device__ __forceinline__ void copy4(uint32_t* dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
@@ -138,15 +130,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of the thread's row of TMEM
-__device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&v)[32]) {
+// 16 columns of the thread's row of TMEM
+__device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -214,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     const int rank = (int)rank_of_cta(), pair = blockIdx.x / 2;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kDepths; ++i) {
-            mbar_init(&bar.codes_full[i], 1);
+            mbar_init(&bar.codes_full[i], 1 + 32);
             mbar_init(&bar.codes_empty[i], kWorkerWarps);
             mbar_init(&bar.dy_full[i], 1);
             mbar_init(&bar.ready[i], 2 * kWorkerWarps);
@@ -241,27 +230,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     const int all = pieces_of(deal);
     bool ok = true;
     if (warp == kWorkerWarps) {  // the producer
-        if (lane == 0) {
-            int64_t it = 0;
-            for (int i = pair; i < all && ok; i += deal.pairs) {
-                const Piece p = piece_at(deal, i);
-                const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf, i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
-                for (int k = p.from; k < p.to; ++k, ++it) {
-                    const int s = (int)(it % kDepths);
-                    const uint32_t last = (uint32_t)(it / kDepths - 1) & 1;
-                    if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], last) && wait_cluster(&bar.used[s], last))) break;
+        const uint8_t* steps = reinterpret_cast<const uint8_t*>(w.x.steps);
+        int64_t it = 0;
+        for (int i = pair; i < all && ok; i += deal.pairs) {
+            const Piece p = piece_at(deal, i);
+            const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf, i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
+            for (int k = p.from; k < p.to; ++k, ++it) {
+                const int s = (int)(it % kDepths);
+                const uint32_t last = (uint32_t)(it / kDepths - 1) & 1;
+                if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], last) && mbar_wait(&bar.used[s], last))) break;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.codes_full[s], kCodeBytes);
                     load_box(code_stage + s * kCodeBytes, &codes_map, i0, k * kDepth, &bar.codes_full[s]);
                     mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
                     load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
                     load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
                 }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int64_t t = (int64_t)k * kDepth + lane + u * 32;
+                    const bool there = t < w.x.rows && i0 < w.x.cols;
+                    copy4(&bar.steps[s][lane + u * 32], there ? steps + t * w.x.ld_s + i0 / kBlock : steps, there);
+                }
+                arrive_copied(&bar.codes_full[s]);
+                __syncwarp();
             }
-            // no copy is left in flight when the CTA ends
-            for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) {
-                mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
-                mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
-            }
+        }
+        // no copy is left in flight when the CTA ends
+        for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) {
+            mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+            mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
         }
     } else if (warp == kWorkerWarps + 1) {  // the products, issued by one thread of the leader
         if (lane == 0 && rank == 0) {
@@ -270,8 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 const Piece p = piece_at(deal, i);
                 for (int k = p.from; k < p.to && ok; ++k, ++it) {
                     const int s = (int)(it % kDepths), b = (int)(chunk & 1), within = (k - p.from) % kChunkStages;
-                    if (within == 0 && chunk >= 2 && !(ok = wait_cluster(&bar.sum_empty[b], (uint32_t)(chunk / 2 - 1) & 1))) break;
-                    if (!(ok = wait_cluster(&bar.ready[s], (uint32_t)(it / kDepths) & 1))) break;
+                    if (within == 0 && chunk >= 2 && !(ok = mbar_wait(&bar.sum_empty[b], (uint32_t)(chunk / 2 - 1) & 1))) break;
+                    if (!(ok = mbar_wait(&bar.ready[s], (uint32_t)(it / kDepths) & 1))) break;
                     fence_after();
                     const uint64_t a = operand(smem_u32(dy_stage + s * kOperandBytes));
                     const uint64_t x = operand(smem_u32(x_stage + s * kOperandBytes));
@@ -290,62 +288,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         const int quarter = warp % 4, group = warp / 4;  // of the accumulator's rows; of its columns
         const uint32_t own = tmem + ((uint32_t)quarter << 21) + group * kHalf;
         const int token = threadIdx.x / 8, part = threadIdx.x % 8;
-        const uint8_t* steps = reinterpret_cast<const uint8_t*>(w.x.steps);
-        const int64_t blocks = (w.x.cols + kBlock - 1) / kBlock;
         int64_t it = 0, chunk = 0;
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
             const int64_t j0 = (int64_t)(p.tile / deal.feature_tiles) * kTile + rank * kHalf, i_tile = (int64_t)(p.tile % deal.feature_tiles) * kTile;
-            const int64_t block = (i_tile + rank * kHalf + part * 16) / kBlock;
-            auto step_at = [&](int k, int u) -> uint32_t {
-                const int64_t t = (int64_t)k * kDepth + token + u * 32;
-                return k < p.to && t < w.x.rows && block < blocks ? __ldg(steps + t * w.x.ld_s + block) : 0u;
-            };
             float sum[kHalf];
 #pragma unroll
             for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
             auto take = [&]() {  // the oldest chunk's sums that have not been taken
                 const int b = (int)(chunk & 1);
-                if (!wait_cluster(&bar.sum_full[b], (uint32_t)(chunk / 2) & 1)) return false;
+                if (!mbar_wait(&bar.sum_full[b], (uint32_t)(chunk / 2) & 1)) return false;
                 ++chunk;
                 fence_after();
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
-                    uint32_t v[32];
+                for (int c = 0; c < kHalf; c += 16) {
+                    uint32_t v[16];
                     load_sums(own + b * kTile + c, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sum[c + e] += __uint_as_float(v[e]);
+                    for (int e = 0; e < 16; ++e) sum[c + e] += __uint_as_float(v[e]);
                 }
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_leader(&bar.sum_empty[b]);
                 return true;
             };
-            // the steps come from memory: two stages ahead
-            uint32_t now[2], next[2], later[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) now[u] = step_at(p.from, u), next[u] = step_at(p.from + 1, u);
             int waiting = 0;  // chunks whose operands are in place and whose sums have not been taken
             for (int k = p.from; k < p.to; ++k, ++it) {
                 const int s = (int)(it % kDepths);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) later[u] = step_at(k + 2, u);
                 if (!(ok = mbar_wait(&bar.codes_full[s], (uint32_t)(it / kDepths) & 1))) break;
                 uint4 codes[2];
+                uint32_t step[2];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
                     codes[u] = *reinterpret_cast<const uint4*>(code_stage + s * kCodeBytes + (token + u * 32) * kHalf + part * 16);
+                    step[u] = reinterpret_cast<const uint8_t*>(&bar.steps[s][token + u * 32])[part / 2];
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
-                if (it >= kDepths && !(ok = wait_cluster(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+                if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) decode<T>(x_stage + s * kOperandBytes, token + u * 32, part, codes[u], now[u]);
+                for (int u = 0; u < 2; ++u) decode<T>(x_stage + s * kOperandBytes, token + u * 32, part, codes[u], step[u]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 if (warp == 0 && !(ok = mbar_wait(&bar.dy_full[s], (uint32_t)(it / kDepths) & 1))) break;
                 __syncwarp();
                 if (lane == 0) arrive_leader(&bar.ready[s]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) now[u] = next[u], next[u] = later[u];
                 if ((k - p.from) % kChunkStages == kChunkStages - 1 || k == p.to - 1) {
                     if (waiting && !(ok = take())) break;
                     waiting = 1;
