@@ -33,7 +33,10 @@ constexpr int kHalf = 128, kTile = 2 * kHalf;  // outputs, and features: of a CT
 constexpr int kDepth = 64;                     // tokens of a stage
 constexpr int kDepths = 5;                     // stages
 constexpr int kChunkStages = 8;                // stages between two visits to the accumulator
-constexpr int kWorkers = 256, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 64;
+constexpr int kWorkers = 512, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 96;
+constexpr int kGroups = 2, kGroupWarps = kWorkerWarps / kGroups;  // of workers: they decode stages in turn
+constexpr int kColumns = kTile * kHalf / kWorkers;  // of the accumulator, that a worker sums up
+enum Role { kCodes = kWorkerWarps, kDy, kProducts };              // the other warps
 constexpr int kOperandBytes = kDepth * kHalf * 2, kCodeBytes = kDepth * kHalf, kBoxBytes = kDepth * 128;
 constexpr int kSharedBytes = 1024 + kDepths * (2 * kOperandBytes + kCodeBytes);
 
@@ -140,7 +143,19 @@ __device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Two codes as 16-bit floats times the step: bytes `pick` (a byte permutation's selector) of w.
+// A block's step in both halves of a register, from a token's four stored exponents (byte `b` of them). 255 gives an
+// infinity, whose product with the block's codes, all 0, is a NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t step_pair(uint32_t four, int b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        return __byte_perm(four, 0, 0x4040u | b | b << 8) << 7;
+    } else {
+        const __half2 s = __float2half2_rn(__uint_as_float(__byte_perm(four, 0, 0x4440u | b) << 23));
+        return *reinterpret_cast<const uint32_t*>(&s);
+    }
+}
+
+// Two codes (bytes `pick`, a byte permutation's selector) as 16-bit floats times the step:
 //   bfloat16: 128 + (q & 127) and 128 + (q & 128) have the bits 0x4300 | those, and their difference is q
 //   binary16: 1024 + (q + 128) has the bits 0x6400 | (q ^ 128)
 template <typename T>
@@ -158,16 +173,11 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t low, uint32_t sign, uin
     return r;
 }
 
-// Sixteen codes of a token, all of one block, into the operand's stage: 8 features to 16 bytes, which lie in the row of 128
-// bytes where the swizzle puts them. Half the lanes store their second 8 first, so that the 8 lanes of a row use all banks.
+// Sixteen codes of a token, all of one block, to the two 16-byte pieces of its row that the swizzle puts them in.
 template <typename T>
-__device__ __forceinline__ void decode(unsigned char* stage, int token, int part, uint4 codes, uint32_t step8) {
-    const float s = step_value(step8);
-    const T one = narrow<T>(s);
-    const uint32_t h = *reinterpret_cast<const unsigned short*>(&one), step = h | h << 16;
+__device__ __forceinline__ void decode(unsigned char* at, unsigned char* at2, uint4 codes, uint32_t step) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint4 out[2];
-    uint32_t* o = reinterpret_cast<uint32_t*>(out);
+    uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -175,18 +185,26 @@ __device__ __forceinline__ void decode(unsigned char* stage, int token, int part
         o[2 * i] = decode_pair<T>(low, sign, 0x4140u, step);
         o[2 * i + 1] = decode_pair<T>(low, sign, 0x4342u, step);
     }
-    unsigned char* row = stage + (part / 4) * kBoxBytes + token * 128;
-    const int first = part / 4, at0 = (((part % 4) * 2 + first) ^ (token % 8)) * 16;
-    const int at1 = (((part % 4) * 2 + 1 - first) ^ (token % 8)) * 16;
-    *reinterpret_cast<uint4*>(row + at0) = first ? out[1] : out[0];
-    *reinterpret_cast<uint4*>(row + at1) = first ? out[0] : out[1];
+    *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(at2) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-template <typename O>
-__device__ __forceinline__ void write_dw(const Wgrad& w, int64_t i, int64_t j, float v) {
-    if (i >= w.x.cols || j >= w.n) return;
-    if (w.add) v += widen(static_cast<const O*>(w.add)[i * w.ld_add + j]);
-    static_cast<O*>(w.dw)[i * w.ld_dw + j] = narrow<O>(v);
+// dw[i + c][j] = add + sum[c], eight features' loads at a time
+template <typename O, int kCount>
+__device__ __forceinline__ void write_dw(const Wgrad& w, int64_t i, int64_t j, const float (&sum)[kCount]) {
+    if (j >= w.n) return;
+    const int there = (int)(w.x.cols - i < kCount ? w.x.cols - i : kCount);
+    const O* add = static_cast<const O*>(w.add) + i * w.ld_add + j;
+    O* dw = static_cast<O*>(w.dw) + i * w.ld_dw + j;
+#pragma unroll
+    for (int c0 = 0; c0 < kCount; c0 += 8) {
+        float a[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) a[c] = w.add && c0 + c < there ? widen(add[(c0 + c) * w.ld_add]) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c0 + c < there) dw[(c0 + c) * w.ld_dw] = narrow<O>(sum[c0 + c] + a[c]);
+    }
 }
 
 template <typename T, typename O>
@@ -204,9 +222,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kDepths; ++i) {
             mbar_init(&bar.codes_full[i], 1 + 32);
-            mbar_init(&bar.codes_empty[i], kWorkerWarps);
+            mbar_init(&bar.codes_empty[i], kGroupWarps);
             mbar_init(&bar.dy_full[i], 1);
-            mbar_init(&bar.ready[i], 2 * kWorkerWarps);
+            mbar_init(&bar.ready[i], 2 * kGroupWarps);
             mbar_init(&bar.used[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -215,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         }
         mbar_fence_init();
     }
-    if (warp == kWorkerWarps + 1) {
+    if (warp == kProducts) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
@@ -229,22 +247,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
 
     const int all = pieces_of(deal);
     bool ok = true;
-    if (warp == kWorkerWarps) {  // the producer
+    if (warp == kCodes) {  // loads codes and steps
         const uint8_t* steps = reinterpret_cast<const uint8_t*>(w.x.steps);
         int64_t it = 0;
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
-            const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf, i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
+            const int i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
             for (int k = p.from; k < p.to; ++k, ++it) {
                 const int s = (int)(it % kDepths);
-                const uint32_t last = (uint32_t)(it / kDepths - 1) & 1;
-                if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], last) && mbar_wait(&bar.used[s], last))) break;
+                if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], (uint32_t)(it / kDepths - 1) & 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.codes_full[s], kCodeBytes);
                     load_box(code_stage + s * kCodeBytes, &codes_map, i0, k * kDepth, &bar.codes_full[s]);
-                    mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
-                    load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
-                    load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -257,11 +271,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             }
         }
         // no copy is left in flight when the CTA ends
-        for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) {
-            mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
-            mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+        for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+    } else if (warp == kDy) {  // loads dy
+        if (lane == 0) {
+            int64_t it = 0;
+            for (int i = pair; i < all && ok; i += deal.pairs) {
+                const Piece p = piece_at(deal, i);
+                const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf;
+                for (int k = p.from; k < p.to; ++k, ++it) {
+                    const int s = (int)(it % kDepths);
+                    if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+                    mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
+                    load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
+                    load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
+                }
+            }
+            for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
         }
-    } else if (warp == kWorkerWarps + 1) {  // the products, issued by one thread of the leader
+    } else if (warp == kProducts) {  // issued by one thread of the leader
         if (lane == 0 && rank == 0) {
             int64_t it = 0, chunk = 0;
             for (int i = pair; i < all && ok; i += deal.pairs) {
@@ -285,23 +312,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             }
         }
     } else {  // the workers
-        const int quarter = warp % 4, group = warp / 4;  // of the accumulator's rows; of its columns
-        const uint32_t own = tmem + ((uint32_t)quarter << 21) + group * kHalf;
-        const int token = threadIdx.x / 8, part = threadIdx.x % 8;
+        // A thread decodes 2 x 16 codes of a token, in the order of the halves that puts a store's 8 lanes (two tokens) on
+        // different banks; and sums up one row and kColumns columns of the accumulator.
+        const int quarter = warp % 4, first_column = warp / 4 * kColumns, group = warp / kGroupWarps;
+        const uint32_t own = tmem + ((uint32_t)quarter << 21) + first_column;
+        const int in_group = threadIdx.x % (kWorkers / kGroups), token = in_group / 4, part = in_group % 4, odd = token % 2;
+        const unsigned char* from = code_stage + token * kHalf + part * 16;
+        unsigned char* to = x_stage + token * 128 + ((part * 2) ^ (token % 8)) * 16;
         int64_t it = 0, chunk = 0;
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
             const int64_t j0 = (int64_t)(p.tile / deal.feature_tiles) * kTile + rank * kHalf, i_tile = (int64_t)(p.tile % deal.feature_tiles) * kTile;
-            float sum[kHalf];
+            float sum[kColumns];
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
+            for (int c = 0; c < kColumns; ++c) sum[c] = 0.0f;
             auto take = [&]() {  // the oldest chunk's sums that have not been taken
                 const int b = (int)(chunk & 1);
                 if (!mbar_wait(&bar.sum_full[b], (uint32_t)(chunk / 2) & 1)) return false;
                 ++chunk;
                 fence_after();
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 16) {
+                for (int c = 0; c < kColumns; c += 16) {
                     uint32_t v[16];
                     load_sums(own + b * kTile + c, v);
 #pragma unroll
@@ -314,24 +345,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             };
             int waiting = 0;  // chunks whose operands are in place and whose sums have not been taken
             for (int k = p.from; k < p.to; ++k, ++it) {
-                const int s = (int)(it % kDepths);
-                if (!(ok = mbar_wait(&bar.codes_full[s], (uint32_t)(it / kDepths) & 1))) break;
-                uint4 codes[2];
-                uint32_t step[2];
+                if ((it & 1) == group) {
+                    const int s = (int)(it % kDepths);
+                    if (!(ok = mbar_wait(&bar.codes_full[s], (uint32_t)(it / kDepths) & 1))) break;
+                    uint4 codes[2];
+                    const uint32_t steps = bar.steps[s][token];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    codes[u] = *reinterpret_cast<const uint4*>(code_stage + s * kCodeBytes + (token + u * 32) * kHalf + part * 16);
-                    step[u] = reinterpret_cast<const uint8_t*>(&bar.steps[s][token + u * 32])[part / 2];
+                    for (int h = 0; h < 2; ++h)
+                        codes[h] = *reinterpret_cast<const uint4*>(from + s * kCodeBytes + (h ^ odd) * 64);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
+                    if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        unsigned char* at = to + s * kOperandBytes + (h ^ odd) * kBoxBytes;
+                        decode<T>(at, reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(at) ^ 16), codes[h],
+                                  step_pair<T>(steps, (h ^ odd) * 2 + part / 2));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (warp % kGroupWarps == 0 && !(ok = mbar_wait(&bar.dy_full[s], (uint32_t)(it / kDepths) & 1))) break;
+                    __syncwarp();
+                    if (lane == 0) arrive_leader(&bar.ready[s]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
-                if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) decode<T>(x_stage + s * kOperandBytes, token + u * 32, part, codes[u], step[u]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                if (warp == 0 && !(ok = mbar_wait(&bar.dy_full[s], (uint32_t)(it / kDepths) & 1))) break;
-                __syncwarp();
-                if (lane == 0) arrive_leader(&bar.ready[s]);
                 if ((k - p.from) % kChunkStages == kChunkStages - 1 || k == p.to - 1) {
                     if (waiting && !(ok = take())) break;
                     waiting = 1;
@@ -342,12 +377,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             // lanes hold neighbouring outputs, so a feature's stores are contiguous
             const int64_t j = j0 + quarter * 32 + lane;
             if (p.piece < 0) {
-#pragma unroll
-                for (int c = 0; c < kHalf; ++c) write_dw<O>(w, i_tile + group * kHalf + c, j, sum[c]);
+                write_dw<O>(w, i_tile + first_column, j, sum);
             } else {
                 float* out = partial + ((int64_t)p.piece * 2 + rank) * kHalf * kTile + threadIdx.x;
 #pragma unroll
-                for (int c = 0; c < kHalf; ++c) out[c * kWorkers] = sum[c];
+                for (int c = 0; c < kColumns; ++c) out[c * kWorkers] = sum[c];
             }
         }
     }
@@ -357,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     __syncthreads();
     cluster_sync();  // the other CTA's products have read this CTA's shared memory, its arrivals have landed
     fence_after();
-    if (warp == kWorkerWarps + 1)
+    if (warp == kProducts)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -366,19 +400,17 @@ template <typename O>
 __global__ void __launch_bounds__(kWorkers) wgrad_join_kernel(Wgrad w, Deal deal, const float* partial) {
     wait_prerequisite();
     allow_dependents();
-    constexpr int kColumns = 8, kCtas = kHalf / kColumns;
-    const int c0 = blockIdx.x % kCtas * kColumns, rank = blockIdx.x / kCtas % 2, k = blockIdx.x / (2 * kCtas);
-    const int tile = deal.whole + k, quarter = threadIdx.x / 32 % 4, group = threadIdx.x / kHalf, lane = threadIdx.x % 32;
-    const int64_t j = (int64_t)(tile / deal.feature_tiles) * kTile + rank * kHalf + quarter * 32 + lane;
-    const int64_t i0 = (int64_t)(tile % deal.feature_tiles) * kTile + group * kHalf;
-    float sum[kColumns] = {};
+    constexpr int kSome = 8, kCtas = kColumns / kSome;
+    const int c0 = blockIdx.x % kCtas * kSome, rank = blockIdx.x / kCtas % 2, k = blockIdx.x / (2 * kCtas);
+    const int tile = deal.whole + k, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float sum[kSome] = {};
     for (int part = 0; part < deal.parts; ++part) {
         const float* in = partial + (((int64_t)k * deal.parts + part) * 2 + rank) * kHalf * kTile + threadIdx.x;
 #pragma unroll
-        for (int c = 0; c < kColumns; ++c) sum[c] += __ldcg(in + (c0 + c) * kWorkers);
+        for (int c = 0; c < kSome; ++c) sum[c] += __ldcg(in + (c0 + c) * kWorkers);
     }
-#pragma unroll
-    for (int c = 0; c < kColumns; ++c) write_dw<O>(w, i0 + c0 + c, j, sum[c]);
+    write_dw<O>(w, (int64_t)(tile % deal.feature_tiles) * kTile + warp / 4 * kColumns + c0,
+                (int64_t)(tile / deal.feature_tiles) * kTile + rank * kHalf + warp % 4 * 32 + lane, sum);
 }
 
 // dy with its rows at 16-byte boundaries, for TMA: 8 elements to a thread.
@@ -485,7 +517,7 @@ cudaError_t launch_typed(const Wgrad& w, const Deal& d, float* partial, void* st
         if (e != cudaSuccess) return e;
     }
     if (d.parts == 1) return cudaSuccess;
-    return launch_after(wgrad_join_kernel<O>, (int64_t)(d.tiles - d.whole) * 2 * (kHalf / 8), kWorkers, 0, stream, w, d,
+    return launch_after(wgrad_join_kernel<O>, (int64_t)(d.tiles - d.whole) * 2 * (kColumns / 8), kWorkers, 0, stream, w, d,
                         (const float*)partial);
 }
 
