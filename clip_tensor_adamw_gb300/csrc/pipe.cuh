@@ -55,5 +55,19 @@ __device__ __forceinline__ void bulk_copy_g2s_hint(void* smem_dst, const void* g
         : "memory");
 }
 
+// A place in a ring of kCount stages: the stage and how often the ring has been around, mod 2. A stage's `full` barrier is
+// waited on with parity `round`, its `empty` barrier with `round ^ 1` (which is through at once the first time around).
+template <int kCount>
+struct Turn {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == kCount) {
+            at = 0;
+            round ^= 1;
+        }
+    }
+};
+
 }  // namespace
 }  // namespace mica

@@ -89,6 +89,13 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         "mbarrier.arrive.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
+// Waits for the last copies queued, up to a ring's.
+__device__ __forceinline__ void drain(uint64_t* full, const Turn<kDepths>& turn, int queued) {
+    for (int q = 0; q < kDepths; ++q) {  // stages before `at` were filled in this round, the others in the last
+        if (q < turn.at) mbar_wait(&full[q], turn.round);
+        else if (queued == kDepths) mbar_wait(&full[q], turn.round ^ 1);
+    }
+}
 // Four bytes, or zeros, to shared memory without waiting for them; a thread's arrival on `bar` once all of its have landed.
 __device__ __forceinline__ void copy4(uint32_t* dst, const void* src, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
@@ -249,13 +256,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     bool ok = true;
     if (warp == kCodes) {  // loads codes and steps
         const uint8_t* steps = reinterpret_cast<const uint8_t*>(w.x.steps);
-        int64_t it = 0;
+        Turn<kDepths> turn;
+        int queued = 0;
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
             const int i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
-            for (int k = p.from; k < p.to; ++k, ++it) {
-                const int s = (int)(it % kDepths);
-                if (it >= kDepths && !(ok = mbar_wait(&bar.codes_empty[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+            for (int k = p.from; k < p.to; ++k, turn.next()) {
+                const int s = turn.at;
+                if (!(ok = mbar_wait(&bar.codes_empty[s], turn.round ^ 1))) break;
+                if (queued < kDepths) ++queued;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.codes_full[s], kCodeBytes);
                     load_box(code_stage + s * kCodeBytes, &codes_map, i0, k * kDepth, &bar.codes_full[s]);
@@ -271,32 +280,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             }
         }
         // no copy is left in flight when the CTA ends
-        for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) mbar_wait(&bar.codes_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+        drain(bar.codes_full, turn, queued);
     } else if (warp == kDy) {  // loads dy
         if (lane == 0) {
-            int64_t it = 0;
+            Turn<kDepths> turn;
+            int queued = 0;
             for (int i = pair; i < all && ok; i += deal.pairs) {
                 const Piece p = piece_at(deal, i);
                 const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf;
-                for (int k = p.from; k < p.to; ++k, ++it) {
-                    const int s = (int)(it % kDepths);
-                    if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+                for (int k = p.from; k < p.to; ++k, turn.next()) {
+                    const int s = turn.at;
+                    if (!(ok = mbar_wait(&bar.used[s], turn.round ^ 1))) break;
+                    if (queued < kDepths) ++queued;
                     mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
                     load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
                     load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
                 }
             }
-            for (int64_t q = it < kDepths ? 0 : it - kDepths; q < it; ++q) mbar_wait(&bar.dy_full[q % kDepths], (uint32_t)(q / kDepths) & 1);
+            drain(bar.dy_full, turn, queued);
         }
     } else if (warp == kProducts) {  // issued by one thread of the leader
         if (lane == 0 && rank == 0) {
-            int64_t it = 0, chunk = 0;
+            Turn<kDepths> turn;
+            Turn<2> sums;
             for (int i = pair; i < all && ok; i += deal.pairs) {
                 const Piece p = piece_at(deal, i);
-                for (int k = p.from; k < p.to && ok; ++k, ++it) {
-                    const int s = (int)(it % kDepths), b = (int)(chunk & 1), within = (k - p.from) % kChunkStages;
-                    if (within == 0 && chunk >= 2 && !(ok = mbar_wait(&bar.sum_empty[b], (uint32_t)(chunk / 2 - 1) & 1))) break;
-                    if (!(ok = mbar_wait(&bar.ready[s], (uint32_t)(it / kDepths) & 1))) break;
+                int within = 0;  // the chunk
+                for (int k = p.from; k < p.to; ++k, turn.next()) {
+                    const int s = turn.at, b = sums.at;
+                    if (within == 0 && !(ok = mbar_wait(&bar.sum_empty[b], sums.round ^ 1))) break;
+                    if (!(ok = mbar_wait(&bar.ready[s], turn.round))) break;
                     fence_after();
                     const uint64_t a = operand(smem_u32(dy_stage + s * kOperandBytes));
                     const uint64_t x = operand(smem_u32(x_stage + s * kOperandBytes));
@@ -304,9 +317,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                     for (int d = 0; d < kDepth / 16; ++d)  // 16 tokens are 2 KB further on
                         multiply(tmem + b * kTile, a + d * (2048 >> 4), x + d * (2048 >> 4), instruction<T>(), within + d > 0);
                     commit(&bar.used[s]);
-                    if (within == kChunkStages - 1 || k == p.to - 1) {
+                    if (++within == kChunkStages || k == p.to - 1) {
                         commit(&bar.sum_full[b]);
-                        ++chunk;
+                        sums.next();
+                        within = 0;
                     }
                 }
             }
@@ -319,7 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         const int in_group = threadIdx.x % (kWorkers / kGroups), token = in_group / 4, part = in_group % 4, odd = token % 2;
         const unsigned char* from = code_stage + token * kHalf + part * 16;
         unsigned char* to = x_stage + token * 128 + ((part * 2) ^ (token % 8)) * 16;
-        int64_t it = 0, chunk = 0;
+        Turn<kDepths> turn;
+        Turn<2> sums;
+        int whose = 0;  // group's turn it is
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
             const int64_t j0 = (int64_t)(p.tile / deal.feature_tiles) * kTile + rank * kHalf, i_tile = (int64_t)(p.tile % deal.feature_tiles) * kTile;
@@ -327,9 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
 #pragma unroll
             for (int c = 0; c < kColumns; ++c) sum[c] = 0.0f;
             auto take = [&]() {  // the oldest chunk's sums that have not been taken
-                const int b = (int)(chunk & 1);
-                if (!mbar_wait(&bar.sum_full[b], (uint32_t)(chunk / 2) & 1)) return false;
-                ++chunk;
+                const int b = sums.at;
+                if (!mbar_wait(&bar.sum_full[b], sums.round)) return false;
+                sums.next();
                 fence_after();
 #pragma unroll
                 for (int c = 0; c < kColumns; c += 16) {
@@ -343,11 +359,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 if (lane == 0) arrive_leader(&bar.sum_empty[b]);
                 return true;
             };
-            int waiting = 0;  // chunks whose operands are in place and whose sums have not been taken
-            for (int k = p.from; k < p.to; ++k, ++it) {
-                if ((it & 1) == group) {
-                    const int s = (int)(it % kDepths);
-                    if (!(ok = mbar_wait(&bar.codes_full[s], (uint32_t)(it / kDepths) & 1))) break;
+            bool waiting = false;  // a chunk whose operands are in place and whose sums have not been taken
+            int within = 0;        // the chunk
+            for (int k = p.from; k < p.to; ++k, turn.next(), whose ^= 1) {
+                if (whose == group) {
+                    const int s = turn.at;
+                    if (!(ok = mbar_wait(&bar.codes_full[s], turn.round))) break;
                     uint4 codes[2];
                     const uint32_t steps = bar.steps[s][token];
 #pragma unroll
@@ -355,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                         codes[h] = *reinterpret_cast<const uint4*>(from + s * kCodeBytes + (h ^ odd) * 64);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
-                    if (it >= kDepths && !(ok = mbar_wait(&bar.used[s], (uint32_t)(it / kDepths - 1) & 1))) break;
+                    if (!(ok = mbar_wait(&bar.used[s], turn.round ^ 1))) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         unsigned char* at = to + s * kOperandBytes + (h ^ odd) * kBoxBytes;
@@ -363,13 +380,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                                   step_pair<T>(steps, (h ^ odd) * 2 + part / 2));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if (warp % kGroupWarps == 0 && !(ok = mbar_wait(&bar.dy_full[s], (uint32_t)(it / kDepths) & 1))) break;
+                    if (warp % kGroupWarps == 0 && !(ok = mbar_wait(&bar.dy_full[s], turn.round))) break;
                     __syncwarp();
                     if (lane == 0) arrive_leader(&bar.ready[s]);
                 }
-                if ((k - p.from) % kChunkStages == kChunkStages - 1 || k == p.to - 1) {
+                if (++within == kChunkStages || k == p.to - 1) {
                     if (waiting && !(ok = take())) break;
-                    waiting = 1;
+                    waiting = true;
+                    within = 0;
                 }
             }
             if (ok && waiting) ok = take();
