@@ -32,9 +32,9 @@ namespace {
 constexpr int kHalf = 128, kTile = 2 * kHalf;  // outputs, and features: of a CTA, of a pair
 constexpr int kDepth = 64;                     // tokens of a stage
 constexpr int kDepths = 5;                     // stages
-constexpr int kChunkStages = 8;                // stages between two visits to the accumulator
+constexpr int kChunkStages = 16;               // stages between two visits to the accumulator
 constexpr int kWorkers = 512, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 96;
-constexpr int kGroups = 2, kGroupWarps = kWorkerWarps / kGroups;  // of workers: they decode stages in turn
+constexpr int kGroups = 4, kGroupWarps = kWorkerWarps / kGroups;  // of workers: they decode stages in turn
 constexpr int kColumns = kTile * kHalf / kWorkers;  // of the accumulator, that a worker sums up
 enum Role { kCodes = kWorkerWarps, kDy, kProducts };              // the other warps
 constexpr int kOperandBytes = kDepth * kHalf * 2, kCodeBytes = kDepth * kHalf, kBoxBytes = kDepth * 128;
@@ -65,8 +65,8 @@ __device__ __forceinline__ Piece piece_at(const Deal& d, int i) {
 
 struct Barriers {
     uint64_t codes_full[kDepths], codes_empty[kDepths];  // the codes of a stage have come; the workers have read them
-    uint64_t dy_full[kDepths];                           // dy's part of a stage has come
-    uint64_t ready[kDepths];                             // (leader) both CTAs' operands of a stage are in place
+    uint64_t dy_full[kDepths];                           // (leader) both CTAs' parts of dy of a stage have come
+    uint64_t ready[kDepths];                             // (leader) both CTAs' codes of a stage are decoded
     uint64_t used[kDepths];                              // the products of a stage are done
     uint64_t sum_full[2], sum_empty[2];                  // a chunk's sums are in TMEM; (leader) both CTAs have taken them
     uint32_t tmem;
@@ -92,8 +92,8 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
 // Waits for the last copies queued, up to a ring's.
 __device__ __forceinline__ void drain(uint64_t* full, const Turn<kDepths>& turn, int queued) {
     for (int q = 0; q < kDepths; ++q) {  // stages before `at` were filled in this round, the others in the last
-        if (q < turn.at) mbar_wait(&full[q], turn.round);
-        else if (queued == kDepths) mbar_wait(&full[q], turn.round ^ 1);
+        if (q < turn.at) mbar_wait_idle(&full[q], turn.round);
+        else if (queued == kDepths) mbar_wait_idle(&full[q], turn.round ^ 1);
     }
 }
 // Four bytes, or zeros, to shared memory without waiting for them; a thread's arrival on `bar` once all of its have landed.
@@ -107,6 +107,17 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int 
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
             smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The same, completing on the leader's barrier.
+__device__ __forceinline__ void load_box_for_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %4, 0;\n\t"
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[at];\n\t}" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
@@ -162,17 +173,17 @@ __device__ __forceinline__ uint32_t step_pair(uint32_t four, int b) {
     }
 }
 
-// Two codes (bytes `pick`, a byte permutation's selector) as 16-bit floats times the step:
+// The codes in bytes 0 and 2 of w as 16-bit floats times the step:
 //   bfloat16: 128 + (q & 127) and 128 + (q & 128) have the bits 0x4300 | those, and their difference is q
 //   binary16: 1024 + (q + 128) has the bits 0x6400 | (q ^ 128)
 template <typename T>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t low, uint32_t sign, uint32_t pick, uint32_t step) {
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t step) {
     uint32_t r;
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const uint32_t a = __byte_perm(low, 0x43434343u, pick), c = __byte_perm(sign, 0x43434343u, pick);
+        const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, c = (w & 0x00800080u) | 0x43004300u;
         asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(a), "r"(c), "r"(step));
     } else {
-        const uint32_t a = __byte_perm(low, 0x64646464u, pick);
+        const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u;
         asm("{\n\t.reg .b32 d;\n\tsub.rn.f16x2 d, %1, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
             : "=r"(r)
             : "r"(a), "r"(0x64806480u), "r"(step));  // 1152
@@ -180,23 +191,24 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t low, uint32_t sign, uin
     return r;
 }
 
-// Sixteen codes of a token, all of one block, to the two 16-byte pieces of its row that the swizzle puts them in.
+// Sixteen codes of a token, all of one block, to the two 16-byte pieces of its row that the swizzle puts them in. Of each
+// four features the middle ones change places, which write_dw undoes: so a pair takes a mask and not a permutation.
 template <typename T>
 __device__ __forceinline__ void decode(unsigned char* at, unsigned char* at2, uint4 codes, uint32_t step) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-        const uint32_t low = bf16 ? w[i] & 0x7F7F7F7Fu : w[i] ^ 0x80808080u, sign = w[i] & 0x80808080u;
-        o[2 * i] = decode_pair<T>(low, sign, 0x4140u, step);
-        o[2 * i + 1] = decode_pair<T>(low, sign, 0x4342u, step);
+        o[2 * i] = decode_pair<T>(w[i], step);
+        o[2 * i + 1] = decode_pair<T>(w[i] >> 8, step);
     }
     *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(at2) = make_uint4(o[4], o[5], o[6], o[7]);
 }
+// The feature of an operand's column.
+__host__ __device__ constexpr int feature_of(int column) { return column % 4 == 1 ? column + 1 : column % 4 == 2 ? column - 1 : column; }
 
-// dw[i + c][j] = add + sum[c], eight features' loads at a time
+// dw[i + c][j] = add + the sum of feature c, eight features' loads at a time
 template <typename O, int kCount>
 __device__ __forceinline__ void write_dw(const Wgrad& w, int64_t i, int64_t j, const float (&sum)[kCount]) {
     if (j >= w.n) return;
@@ -210,7 +222,7 @@ __device__ __forceinline__ void write_dw(const Wgrad& w, int64_t i, int64_t j, c
         for (int c = 0; c < 8; ++c) a[c] = w.add && c0 + c < there ? widen(add[(c0 + c) * w.ld_add]) : 0.0f;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            if (c0 + c < there) dw[(c0 + c) * w.ld_dw] = narrow<O>(sum[c0 + c] + a[c]);
+            if (c0 + c < there) dw[(c0 + c) * w.ld_dw] = narrow<O>(sum[feature_of(c0 + c)] + a[c]);
     }
 }
 
@@ -263,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             const int i0 = p.tile % deal.feature_tiles * kTile + rank * kHalf;
             for (int k = p.from; k < p.to; ++k, turn.next()) {
                 const int s = turn.at;
-                if (!(ok = mbar_wait(&bar.codes_empty[s], turn.round ^ 1))) break;
+                if (!(ok = mbar_wait_idle(&bar.codes_empty[s], turn.round ^ 1))) break;
                 if (queued < kDepths) ++queued;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.codes_full[s], kCodeBytes);
@@ -290,14 +302,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf;
                 for (int k = p.from; k < p.to; ++k, turn.next()) {
                     const int s = turn.at;
-                    if (!(ok = mbar_wait(&bar.used[s], turn.round ^ 1))) break;
+                    if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
                     if (queued < kDepths) ++queued;
-                    mbar_arrive_expect_tx(&bar.dy_full[s], kOperandBytes);
-                    load_box(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
-                    load_box(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.dy_full[s], 2 * kOperandBytes);
+                    load_box_for_pair(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
+                    load_box_for_pair(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
                 }
             }
-            drain(bar.dy_full, turn, queued);
+            if (rank == 0) drain(bar.dy_full, turn, queued);  // (for both: the other CTA stays until the last cluster_sync)
         }
     } else if (warp == kProducts) {  // issued by one thread of the leader
         if (lane == 0 && rank == 0) {
@@ -308,8 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 int within = 0;  // the chunk
                 for (int k = p.from; k < p.to; ++k, turn.next()) {
                     const int s = turn.at, b = sums.at;
-                    if (within == 0 && !(ok = mbar_wait(&bar.sum_empty[b], sums.round ^ 1))) break;
-                    if (!(ok = mbar_wait(&bar.ready[s], turn.round))) break;
+                    if (within == 0 && !(ok = mbar_wait_idle(&bar.sum_empty[b], sums.round ^ 1))) break;
+                    if (!(ok = mbar_wait_idle(&bar.dy_full[s], turn.round) && mbar_wait_idle(&bar.ready[s], turn.round))) break;
                     fence_after();
                     const uint64_t a = operand(smem_u32(dy_stage + s * kOperandBytes));
                     const uint64_t x = operand(smem_u32(x_stage + s * kOperandBytes));
@@ -326,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             }
         }
     } else {  // the workers
-        // A thread decodes 2 x 16 codes of a token, in the order of the halves that puts a store's 8 lanes (two tokens) on
+        // A thread decodes 2 x 16 codes of two tokens, in the order of the halves that puts a store's 8 lanes (two tokens) on
         // different banks; and sums up one row and kColumns columns of the accumulator.
         const int quarter = warp % 4, first_column = warp / 4 * kColumns, group = warp / kGroupWarps;
         const uint32_t own = tmem + ((uint32_t)quarter << 21) + first_column;
@@ -344,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             for (int c = 0; c < kColumns; ++c) sum[c] = 0.0f;
             auto take = [&]() {  // the oldest chunk's sums that have not been taken
                 const int b = sums.at;
-                if (!mbar_wait(&bar.sum_full[b], sums.round)) return false;
+                if (!mbar_wait_idle(&bar.sum_full[b], sums.round)) return false;
                 sums.next();
                 fence_after();
 #pragma unroll
@@ -361,26 +373,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             };
             bool waiting = false;  // a chunk whose operands are in place and whose sums have not been taken
             int within = 0;        // the chunk
-            for (int k = p.from; k < p.to; ++k, turn.next(), whose ^= 1) {
+            for (int k = p.from; k < p.to; ++k, turn.next(), whose = (whose + 1) % kGroups) {
                 if (whose == group) {
                     const int s = turn.at;
-                    if (!(ok = mbar_wait(&bar.codes_full[s], turn.round))) break;
-                    uint4 codes[2];
-                    const uint32_t steps = bar.steps[s][token];
+                    if (!(ok = mbar_wait_idle(&bar.codes_full[s], turn.round))) break;
+                    constexpr int kApart = kWorkers / kGroups / 4, kTokens = kDepth / kApart;  // of a thread
+                    uint4 codes[kTokens][2];
+                    uint32_t steps[kTokens];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        codes[h] = *reinterpret_cast<const uint4*>(from + s * kCodeBytes + (h ^ odd) * 64);
+                    for (int u = 0; u < kTokens; ++u) {
+                        steps[u] = bar.steps[s][token + u * kApart];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            codes[u][h] = *reinterpret_cast<const uint4*>(from + s * kCodeBytes + u * kApart * kHalf + (h ^ odd) * 64);
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
-                    if (!(ok = mbar_wait(&bar.used[s], turn.round ^ 1))) break;
+                    if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        unsigned char* at = to + s * kOperandBytes + (h ^ odd) * kBoxBytes;
-                        decode<T>(at, reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(at) ^ 16), codes[h],
-                                  step_pair<T>(steps, (h ^ odd) * 2 + part / 2));
-                    }
+                    for (int u = 0; u < kTokens; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            unsigned char* at = to + s * kOperandBytes + u * kApart * 128 + (h ^ odd) * kBoxBytes;
+                            decode<T>(at, reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(at) ^ 16), codes[u][h],
+                                      step_pair<T>(steps[u], (h ^ odd) * 2 + part / 2));
+                        }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if (warp % kGroupWarps == 0 && !(ok = mbar_wait(&bar.dy_full[s], turn.round))) break;
                     __syncwarp();
                     if (lane == 0) arrive_leader(&bar.ready[s]);
                 }
