@@ -617,13 +617,16 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
         uint64_t keep, drop;
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
-        int64_t row = blockIdx.x, y, slot = 0;
+        int64_t row = blockIdx.x, y;
+        Turn<kStages> turn;
+        Turn<kEntries> entries;
+        int queued = 0;
         float c;
         head(row, &y, &c);
         ask_next_row(ring);
         bool ok = true;
-        for (int r = 0; ok; ++r) {
-            if (!mbar_wait(&ring.asked, r & 1)) {
+        for (uint32_t asked = 0; ok; asked ^= 1) {
+            if (!mbar_wait(&ring.asked, asked)) {
                 ok = false;
                 break;
             }
@@ -634,19 +637,20 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                 ask_next_row(ring);
                 head(next, &next_y, &next_c);  // (arrives while this row's copies are queued)
             }
-            const int e = r % kEntries;
-            if (r >= kEntries && !(ok = mbar_wait(&ring.entry_empty[e], (r / kEntries - 1) & 1))) break;
+            if (!(ok = mbar_wait(&ring.entry_empty[entries.at], entries.round ^ 1))) break;
             const float zy = !kStream && y >= 0 && y < L.vocab ? widen(logits[row * L.ld + y]) : -INFINITY;
-            ring.entry[e] = RowEntry{row, y, c, zy};
-            mbar_arrive(&ring.entry_full[e]);
+            ring.entry[entries.at] = RowEntry{row, y, c, zy};
+            mbar_arrive(&ring.entry_full[entries.at]);
+            entries.next();
             if (y >= 0 && c != 0.0f) {
                 const T* z = logits + row * L.ld;
                 const int lead = (int)(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
                 const int lo = lead > 0, hi = (lead + L.vocab) / n;
                 for (int pass = 0; pass < kPasses && ok; ++pass)
-                    for (int k = lo; k < hi; k += kStageVectors, ++slot) {
-                        const int s = (int)(slot % kStages);
-                        if (slot >= kStages && !(ok = mbar_wait(&ring.empty[s], (uint32_t)(slot / kStages - 1) & 1))) break;
+                    for (int k = lo; k < hi; k += kStageVectors, turn.next()) {
+                        const int s = turn.at;
+                        if (!(ok = mbar_wait(&ring.empty[s], turn.round ^ 1))) break;
+                        if (queued < kStages) ++queued;
                         const uint32_t bytes = (uint32_t)min(kStageVectors, hi - k) * 16;
                         mbar_arrive_expect_tx(&ring.full[s], bytes);
                         if (kPasses == 1) bulk_copy_g2s(stages + s * kStageBytes, z + (k * n - lead), bytes, &ring.full[s]);
@@ -655,29 +659,27 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             }
             row = next, y = next_y, c = next_c;
             if (row < 0 && ok) {  // the end: an entry of its own
-                ++r;
-                const int last = r % kEntries;
-                if (r >= kEntries && !(ok = mbar_wait(&ring.entry_empty[last], (r / kEntries - 1) & 1))) break;
-                ring.entry[last] = RowEntry{-1, -1, 0.0f, 0.0f};
-                mbar_arrive(&ring.entry_full[last]);
+                if (!(ok = mbar_wait(&ring.entry_empty[entries.at], entries.round ^ 1))) break;
+                ring.entry[entries.at] = RowEntry{-1, -1, 0.0f, 0.0f};
+                mbar_arrive(&ring.entry_full[entries.at]);
                 break;
             }
         }
         if (!ok) atomicOr(&g_logits_status, kStatusRowProducer);
         // no copy is left in flight when the CTA ends
-        for (int64_t j = slot < kStages ? 0 : slot - kStages; j < slot; ++j) mbar_wait(&ring.full[j % kStages], (j / kStages) & 1);
+        drain(ring.full, turn, queued);
         return;
     }
 
-    int64_t slot = 0;
-    int joins = 0;
+    Turn<kStages> turn;
+    Turn<kEntries> entries;
+    uint32_t joins = 0;  // mod 2
     auto give_up = [&] { atomicOr(&g_logits_status, kStatusRowConsumer); };
-    for (int r = 0;; ++r) {
-        const int e = r % kEntries;
-        if (!mbar_wait(&ring.entry_full[e], (r / kEntries) & 1)) return give_up();
-        const RowEntry at = ring.entry[e];
+    for (;; entries.next()) {
+        if (!mbar_wait(&ring.entry_full[entries.at], entries.round)) return give_up();
+        const RowEntry at = ring.entry[entries.at];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ring.entry_empty[e]);
+        if (lane == 0) mbar_arrive(&ring.entry_empty[entries.at]);
         const int64_t row = at.row, y = at.y;
         if (row < 0) return;
         const T* z = logits + row * L.ld;
@@ -693,9 +695,9 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
         const float zy = at.zy;
         Running q{zy, 0.0f, 0.0f};
         if constexpr (!kStream) {
-            for (int k = g.lo; k < g.hi; k += kStageVectors, ++slot) {
-                const int s = (int)(slot % kStages), left = g.hi - k;
-                if (!mbar_wait(&ring.full[s], (uint32_t)(slot / kStages) & 1)) return give_up();
+            for (int k = g.lo; k < g.hi; k += kStageVectors, turn.next()) {
+                const int s = turn.at, left = g.hi - k;
+                if (!mbar_wait(&ring.full[s], turn.round)) return give_up();
                 const unsigned char* stage = stages + s * kStageBytes;
                 if (left >= kStageVectors) {
                     Vec<T> v[kPerThread];
@@ -722,13 +724,13 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                 add_vectors<T, kMoment>(L, v, q);
             }
             q = join_warp<kMoment>(L, q);
-            Running* part = ring.part[joins & 1];
+            Running* part = ring.part[joins];
             if (lane == 0) {
                 part[warp] = q;
                 mbar_arrive(&ring.joined);
             }
-            if (!mbar_wait(&ring.joined, joins & 1)) return give_up();
-            ++joins;
+            if (!mbar_wait(&ring.joined, joins)) return give_up();
+            joins ^= 1;
             q = join_warp<kMoment>(L, lane < kConsumers / 32 ? part[lane] : Running{-INFINITY, 0.0f, 0.0f});
             c = finish_row<kKind>(L, P, out, row, y, zy, q, c, threadIdx.x == 0);
         } else {
@@ -744,9 +746,9 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                 grad_values(L, load_edge(z, j0, L.vocab), grad, j0, d);
                 store_some(dz, j0, L.vocab, d);
             }
-            for (int k = g.lo; k < g.hi; k += kStageVectors, ++slot) {
-                const int s = (int)(slot % kStages), left = g.hi - k, j0 = (k + (int)threadIdx.x) * n - g.lead;
-                if (!mbar_wait(&ring.full[s], (uint32_t)(slot / kStages) & 1)) return give_up();
+            for (int k = g.lo; k < g.hi; k += kStageVectors, turn.next()) {
+                const int s = turn.at, left = g.hi - k, j0 = (k + (int)threadIdx.x) * n - g.lead;
+                if (!mbar_wait(&ring.full[s], turn.round)) return give_up();
                 const unsigned char* stage = stages + s * kStageBytes;
                 if (left >= kStageVectors) {
                     Vec<T> v[kPerThread];

@@ -86,5 +86,14 @@ struct Turn {
     }
 };
 
+// Waits for the last copies queued, up to a ring's.
+template <int kCount>
+__device__ __forceinline__ void drain(uint64_t* full, const Turn<kCount>& turn, int queued) {
+    for (int q = 0; q < kCount; ++q) {  // stages before `at` were filled in this round, the others in the last
+        if (q < turn.at) mbar_wait(&full[q], turn.round);
+        else if (queued == kCount) mbar_wait(&full[q], turn.round ^ 1);
+    }
+}
+
 }  // namespace
 }  // namespace mica

@@ -89,13 +89,6 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         "mbarrier.arrive.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
-// Waits for the last copies queued, up to a ring's.
-__device__ __forceinline__ void drain(uint64_t* full, const Turn<kDepths>& turn, int queued) {
-    for (int q = 0; q < kDepths; ++q) {  // stages before `at` were filled in this round, the others in the last
-        if (q < turn.at) mbar_wait_idle(&full[q], turn.round);
-        else if (queued == kDepths) mbar_wait_idle(&full[q], turn.round ^ 1);
-    }
-}
 // Four bytes, or zeros, to shared memory without waiting for them; a thread's arrival on `bar` once all of its have landed.
 __device__ __forceinline__ void copy4(uint32_t* dst, const void* src, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
