@@ -65,8 +65,7 @@ __device__ __forceinline__ Piece piece_at(const Deal& d, int i) {
 
 struct Barriers {
     uint64_t codes_full[kDepths], codes_empty[kDepths];  // the codes of a stage have come; the workers have read them
-    uint64_t dy_full[kDepths];                           // (leader) both CTAs' parts of dy of a stage have come
-    uint64_t ready[kDepths];                             // (leader) both CTAs' codes of a stage are decoded
+    uint64_t ready[kDepths];                             // (leader) a stage's operands: dy has come, the codes are decoded, in both CTAs
     uint64_t used[kDepths];                              // the products of a stage are done
     uint64_t sum_full[2], sum_empty[2];                  // a chunk's sums are in TMEM; (leader) both CTAs have taken them
     uint32_t tmem;
@@ -88,6 +87,12 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         "mapa.shared::cluster.u32 at, %0, 0;\n\t"
         "mbarrier.arrive.shared::cluster.b64 _, [at];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
+}
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 // Four bytes, or zeros, to shared memory without waiting for them; a thread's arrival on `bar` once all of its have landed.
 __device__ __forceinline__ void copy4(uint32_t* dst, const void* src, bool there) {
@@ -235,8 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         for (int i = 0; i < kDepths; ++i) {
             mbar_init(&bar.codes_full[i], 1 + 32);
             mbar_init(&bar.codes_empty[i], kGroupWarps);
-            mbar_init(&bar.dy_full[i], 1);
-            mbar_init(&bar.ready[i], 2 * kGroupWarps);
+            mbar_init(&bar.ready[i], 2 * kGroupWarps + 1);
             mbar_init(&bar.used[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -289,23 +293,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
     } else if (warp == kDy) {  // loads dy
         if (lane == 0) {
             Turn<kDepths> turn;
-            int queued = 0;
             for (int i = pair; i < all && ok; i += deal.pairs) {
                 const Piece p = piece_at(deal, i);
                 const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf;
                 for (int k = p.from; k < p.to; ++k, turn.next()) {
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
-                    if (queued < kDepths) ++queued;
-                    if (rank == 0) mbar_arrive_expect_tx(&bar.dy_full[s], 2 * kOperandBytes);
-                    load_box_for_pair(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.dy_full[s]);
-                    load_box_for_pair(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.dy_full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.ready[s], 2 * kOperandBytes);
+                    load_box_for_pair(dy_stage + s * kOperandBytes, &dy_map, j0, k * kDepth, &bar.ready[s]);
+                    load_box_for_pair(dy_stage + s * kOperandBytes + kBoxBytes, &dy_map, j0 + 64, k * kDepth, &bar.ready[s]);
                 }
             }
-            if (rank == 0) drain(bar.dy_full, turn, queued);  // (for both: the other CTA stays until the last cluster_sync)
+            // Every copy has landed when the last products are done. Where a wait gave up they are given 2 ms.
+            for (int i = 0; !ok && i < 200; ++i) __nanosleep(10000);
         }
-    } else if (warp == kProducts) {  // issued by one thread of the leader
-        if (lane == 0 && rank == 0) {
+    } else if (warp == kProducts) {  // issued by one thread of the leader, in code that the whole warp runs alike
+        if (rank == 0) {
+            const bool one = elect_one();
+            const uint64_t dy0 = operand(smem_u32(dy_stage)), x0 = operand(smem_u32(x_stage));
             Turn<kDepths> turn;
             Turn<2> sums;
             for (int i = pair; i < all && ok; i += deal.pairs) {
@@ -314,16 +319,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 for (int k = p.from; k < p.to; ++k, turn.next()) {
                     const int s = turn.at, b = sums.at;
                     if (within == 0 && !(ok = mbar_wait_idle(&bar.sum_empty[b], sums.round ^ 1))) break;
-                    if (!(ok = mbar_wait_idle(&bar.dy_full[s], turn.round) && mbar_wait_idle(&bar.ready[s], turn.round))) break;
+                    if (!(ok = mbar_wait_idle(&bar.ready[s], turn.round))) break;
                     fence_after();
-                    const uint64_t a = operand(smem_u32(dy_stage + s * kOperandBytes));
-                    const uint64_t x = operand(smem_u32(x_stage + s * kOperandBytes));
+                    const uint32_t at = (uint32_t)s * (kOperandBytes >> 4);
+                    const bool last = ++within == kChunkStages || k == p.to - 1;
+                    if (one) {
 #pragma unroll
-                    for (int d = 0; d < kDepth / 16; ++d)  // 16 tokens are 2 KB further on
-                        multiply(tmem + b * kTile, a + d * (2048 >> 4), x + d * (2048 >> 4), instruction<T>(), within + d > 0);
-                    commit(&bar.used[s]);
-                    if (++within == kChunkStages || k == p.to - 1) {
-                        commit(&bar.sum_full[b]);
+                        for (int d = 0; d < kDepth / 16; ++d)  // 16 tokens are 2 KB further on
+                            multiply(tmem + b * kTile, dy0 + (at + d * (2048 >> 4)), x0 + (at + d * (2048 >> 4)), instruction<T>(),
+                                     within > 1 || d > 0);
+                        commit(&bar.used[s]);
+                        if (last) commit(&bar.sum_full[b]);
+                    }
+                    if (last) {
                         sums.next();
                         within = 0;
                     }
