@@ -191,8 +191,17 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t step) {
 
 // Sixteen codes of a token, all of one block, to the two 16-byte pieces of its row that the swizzle puts them in. Of each
 // four features the middle ones change places, which write_dw undoes: so a pair takes a mask and not a permutation.
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
+    return r;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 template <typename T>
-__device__ __forceinline__ void decode(unsigned char* at, unsigned char* at2, uint4 codes, uint32_t step) {
+__device__ __forceinline__ void decode(uint32_t at, uint4 codes, uint32_t step) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t o[8];
 #pragma unroll
@@ -200,8 +209,8 @@ __device__ __forceinline__ void decode(unsigned char* at, unsigned char* at2, ui
         o[2 * i] = decode_pair<T>(w[i], step);
         o[2 * i + 1] = decode_pair<T>(w[i] >> 8, step);
     }
-    *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(at2) = make_uint4(o[4], o[5], o[6], o[7]);
+    store_shared(at, o[0], o[1], o[2], o[3]);
+    store_shared(at ^ 16, o[4], o[5], o[6], o[7]);
 }
 // The feature of an operand's column.
 __host__ __device__ constexpr int feature_of(int column) { return column % 4 == 1 ? column + 1 : column % 4 == 2 ? column - 1 : column; }
@@ -344,18 +353,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         const int quarter = warp % 4, first_column = warp / 4 * kColumns, group = warp / kGroupWarps;
         const uint32_t own = tmem + ((uint32_t)quarter << 21) + first_column;
         const int in_group = threadIdx.x % (kWorkers / kGroups), token = in_group / 4, part = in_group % 4, odd = token % 2;
-        const unsigned char* from = code_stage + token * kHalf + part * 16;
-        unsigned char* to = x_stage + token * 128 + ((part * 2) ^ (token % 8)) * 16;
+        const uint32_t from = smem_u32(code_stage) + token * kHalf + part * 16;
+        const uint32_t to = smem_u32(x_stage) + token * 128 + ((part * 2) ^ (token % 8)) * 16;
         Turn<kDepths> turn;
         Turn<2> sums;
         int whose = 0;  // group's turn it is
         for (int i = pair; i < all && ok; i += deal.pairs) {
             const Piece p = piece_at(deal, i);
-            const int64_t j0 = (int64_t)(p.tile / deal.feature_tiles) * kTile + rank * kHalf, i_tile = (int64_t)(p.tile % deal.feature_tiles) * kTile;
+            const int j0 = p.tile / deal.feature_tiles * kTile + rank * kHalf, i_tile = p.tile % deal.feature_tiles * kTile;
             float sum[kColumns];
 #pragma unroll
             for (int c = 0; c < kColumns; ++c) sum[c] = 0.0f;
-            auto take = [&]() {  // the oldest chunk's sums that have not been taken
+            auto take = [&]() {  // the oldest such chunk's sums
                 const int b = sums.at;
                 if (!mbar_wait_idle(&bar.sum_full[b], sums.round)) return false;
                 sums.next();
@@ -372,47 +381,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
                 if (lane == 0) arrive_leader(&bar.sum_empty[b]);
                 return true;
             };
-            bool waiting = false;  // a chunk whose operands are in place and whose sums have not been taken
+            int waiting = 0;  // chunks whose operands are in place and whose sums have not been taken
             int within = 0;        // the chunk
             for (int k = p.from; k < p.to; ++k, turn.next(), whose = (whose + 1) % kGroups) {
                 if (whose == group) {
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.codes_full[s], turn.round))) break;
                     constexpr int kApart = kWorkers / kGroups / 4, kTokens = kDepth / kApart;  // of a thread
-                    uint4 codes[kTokens][2];
-                    uint32_t steps[kTokens];
-#pragma unroll
-                    for (int u = 0; u < kTokens; ++u) {
-                        steps[u] = bar.steps[s][token + u * kApart];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            codes[u][h] = *reinterpret_cast<const uint4*>(from + s * kCodeBytes + u * kApart * kHalf + (h ^ odd) * 64);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.codes_empty[s]);
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
 #pragma unroll
-                    for (int u = 0; u < kTokens; ++u)
+                    for (int u = 0; u < kTokens; ++u) {
+                        const uint32_t steps = bar.steps[s][token + u * kApart];
+                        uint4 codes[2];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            unsigned char* at = to + s * kOperandBytes + u * kApart * 128 + (h ^ odd) * kBoxBytes;
-                            decode<T>(at, reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(at) ^ 16), codes[u][h],
-                                      step_pair<T>(steps[u], (h ^ odd) * 2 + part / 2));
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            codes[h] = load_shared(from + s * kCodeBytes + u * kApart * kHalf + (h ^ odd) * 64);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            decode<T>(to + s * kOperandBytes + u * kApart * 128 + (h ^ odd) * kBoxBytes, codes[h],
+                                      step_pair<T>(steps, (h ^ odd) * 2 + part / 2));
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) arrive_leader(&bar.ready[s]);
+                    if (lane == 0) {
+                        mbar_arrive(&bar.codes_empty[s]);
+                        arrive_leader(&bar.ready[s]);
+                    }
                 }
-                if (++within == kChunkStages || k == p.to - 1) {
+                // the groups empty TMEM at different times, so that the others go on decoding
+                if (++within == kChunkStages) {
                     if (waiting && !(ok = take())) break;
-                    waiting = true;
+                    waiting = 1;
                     within = 0;
                 }
             }
-            if (ok && waiting) ok = take();
+            if (within) ++waiting;
+            while (ok && waiting-- > 0) ok = take();
             if (!ok) break;
             // lanes hold neighbouring outputs, so a feature's stores are contiguous
-            const int64_t j = j0 + quarter * 32 + lane;
+            const int j = j0 + quarter * 32 + lane;
             if (p.piece < 0) {
                 write_dw<O>(w, i_tile + first_column, j, sum);
             } else {
@@ -480,7 +487,8 @@ Deal deal_of(int64_t tokens, int64_t features, int64_t n, int sms) {
     d.parts = 1;
     if (rest) {
         d.parts = d.pairs / rest;
-        if (d.parts > d.stages / kChunkStages) d.parts = d.stages / kChunkStages;  // a chunk at least
+        // a chunk at least: 509 tokens of 27 tiles take 16 us whole and 23 us with the second kernel that two parts cost
+        if (d.parts > d.stages / kChunkStages) d.parts = d.stages / kChunkStages;
         if (d.parts < 1) d.parts = 1;
     }
     if (d.stages == 0) d.whole = 0, d.parts = 0;  // nothing to add up: the join alone writes every tile

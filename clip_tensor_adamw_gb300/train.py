@@ -102,19 +102,21 @@ def _type(t: torch.Tensor, what: str) -> int:
 
 def _matrix(t: torch.Tensor, what: str) -> int:
     """A matrix whose rows are contiguous; its row stride."""
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions, not {t.dim()}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.ndim != 2:
+        raise ValueError(f"{what} must have two dimensions, not {t.ndim}")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _vector(t: torch.Tensor | None, n: int, what: str, dtype=torch.float32) -> int | None:
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.ndim != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n} elements, not {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -130,11 +132,11 @@ def _output(t: torch.Tensor | None, shape: tuple, dtype, what: str, like: torch.
 
 def _logits(logits: torch.Tensor, targets: torch.Tensor, temperature: float) -> _Logits:
     code, ld = _type(logits, "logits"), _matrix(logits, "logits")
-    rows = logits.shape[0]
+    rows, vocab = logits.shape
     if targets.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"targets must be int32 or int64, not {targets.dtype}")
     y = _vector(targets, rows, "targets", targets.dtype)
-    return _Logits(logits.data_ptr(), y, rows, logits.shape[1], ld, float(temperature), code, targets.element_size())
+    return _Logits(logits.data_ptr(), y, rows, vocab, ld, float(temperature), code, targets.element_size())
 
 
 def _dlogits(out: torch.Tensor | None, logits: torch.Tensor, ld: int) -> torch.Tensor:

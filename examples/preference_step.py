@@ -52,7 +52,7 @@ class Block:
         mica.mica_act_grad(h, dh, "gelu_tanh", out=dh)
         mica.mica_packed_wgrad(x, dh, out=self.g[0])
 
-    def step(self, lr: float = 1e-3, max_norm: float = 1.0) -> torch.Tensor:
+    def step(self, lr: float, max_norm: float = 1.0) -> torch.Tensor:
         self.steps += 1
         norm, _ = mica.mica_clip_adamw_step(self.W, self.G, self.M, self.V, max_norm=max_norm, lr=lr, beta1=0.9,
                                             beta2=0.95, eps=1e-8, weight_decay=0.0, step=self.steps)
@@ -76,7 +76,8 @@ def make_batch(pairs: int, length: int, width: int, vocab: int, seed: int = 1):
     return x, targets, ends
 
 
-def run(steps: int = 20, pairs: int = 8, length: int = 96, width: int = 384, vocab: int = 5003) -> list[float]:
+def run(steps: int = 20, pairs: int = 8, length: int = 96, width: int = 384, vocab: int = 5003,
+        lr: float = 2e-5) -> list[float]:
     model = Block(width, vocab)
     x, targets, ends = make_batch(pairs, length, width, vocab)
     reference = mica.mica_token_logps(model.forward(x), targets)  # the frozen policy's scores: the model's own, before
@@ -85,7 +86,7 @@ def run(steps: int = 20, pairs: int = 8, length: int = 96, width: int = 384, voc
         logits = model.forward(x, keep=True)
         r = mica.mica_preference_loss(logits, targets, ends, reference, beta=0.1, out=logits)
         model.backward(r.dlogits)
-        model.step()
+        model.step(lr)
         losses.append(r.loss)
     mica.mica_sync()
     return [v.item() for v in losses]

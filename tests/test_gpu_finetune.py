@@ -15,7 +15,7 @@ import preference_step  # noqa: E402
 
 
 def test_example_learns():
-    losses = preference_step.run(steps=12, pairs=4, length=40, width=128, vocab=1009)
+    losses = preference_step.run(steps=12, pairs=4, length=40, width=128, vocab=1009, lr=1e-3)
     # the first step's policy is the reference but for the activations' rounding: log 2
     assert abs(losses[0] - math.log(2.0)) < 0.02
     assert losses[-1] < 0.2 * losses[0] and all(math.isfinite(v) for v in losses)
