@@ -56,37 +56,6 @@ __device__ __forceinline__ float exponent(const LogitRows& L, float z, float ori
     return fmaf(d, L.a_hi, d * L.a_lo);
 }
 
-// Two float32 in one register pair: additions and products of both in one instruction, each rounded as it would be alone.
-// What bounds these kernels next to memory is the instructions that they issue.
-struct Two {
-    uint64_t v;
-};
-__device__ __forceinline__ Two two(float lo, float hi) {
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 each(Two a) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a.v));
-    return f;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // A part that has seen nothing but -inf counts from 0, so that no difference of two infinities makes its zero weight a NaN.
 __device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.0f : m; }
 

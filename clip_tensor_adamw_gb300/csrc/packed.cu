@@ -49,6 +49,7 @@ struct Eight {
             return __half2float(__ushort_as_half((unsigned short)(p >> (16 * (i % 2)))));
         }
     }
+    __device__ __forceinline__ Two pair(int i) const { return two(get(2 * i), get(2 * i + 1)); }
     // the bits of the largest magnitude, as a float32's
     __device__ __forceinline__ uint32_t most() const {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(w);
@@ -59,7 +60,7 @@ struct Eight {
             return m;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, p[i] & 0x7FFF7FFFu);
+            for (int i = 0; i < 4; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(p[i] & 0x7FFF7FFFu));
             m = max(m & 0xFFFFu, m >> 16);
             if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
             else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
@@ -114,7 +115,7 @@ __device__ __forceinline__ void store8(T* p, int64_t there, bool aligned, const 
 // Packs a thread's eight columns (its three neighbours hold the block's others) and writes codes and, one of the four, the
 // step. Every lane of the warp calls it.
 template <typename T>
-__device__ __forceinline__ void pack8(const Eight<T>& x, bool there, const mica_packed& p, int64_t row, int64_t col) {
+__device__ __forceinline__ void pack8(const Eight<T>& x, bool there, int8_t* codes, uint8_t* steps, bool writes_step) {
     constexpr bool kHalf = std::is_same<T, __half>::value;
     uint32_t most = x.most();
     most = max(most, __shfl_xor_sync(~0u, most, 1));
@@ -128,23 +129,21 @@ __device__ __forceinline__ void pack8(const Eight<T>& x, bool there, const mica_
         float c[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(x.get(i), -top), top);
-        if (step != 255u) q = make_uint2(codes_of(c[0], c[1], c[2], c[3], inv), codes_of(c[4], c[5], c[6], c[7], inv));
+        if (step != 255u)
+            q = make_uint2(codes_of(two(c[0], c[1]), two(c[2], c[3]), inv), codes_of(two(c[4], c[5]), two(c[6], c[7]), inv));
     } else {
-        q = make_uint2(codes_of(x.get(0), x.get(1), x.get(2), x.get(3), inv), codes_of(x.get(4), x.get(5), x.get(6), x.get(7), inv));
+        q = make_uint2(codes_of(x.pair(0), x.pair(1), inv), codes_of(x.pair(2), x.pair(3), inv));
     }
-    *reinterpret_cast<uint2*>(reinterpret_cast<int8_t*>(p.codes) + row * p.ld + col) = q;
-    if (col % kBlock == 0) reinterpret_cast<uint8_t*>(p.steps)[row * p.ld_s + col / kBlock] = (uint8_t)step;
+    *reinterpret_cast<uint2*>(codes) = q;
+    if (writes_step) *steps = (uint8_t)step;
 }
 
 struct RawCodes {
     uint2 q;
     uint32_t step;
 };
-__device__ __forceinline__ RawCodes load_codes(const mica_packed& p, int64_t row, int64_t col) {
-    RawCodes r;
-    r.q = __ldcs(reinterpret_cast<const uint2*>(reinterpret_cast<const int8_t*>(p.codes) + row * p.ld + col));
-    r.step = __ldg(reinterpret_cast<const uint8_t*>(p.steps) + row * p.ld_s + col / kBlock);
-    return r;
+__device__ __forceinline__ RawCodes load_codes(const int8_t* codes, const uint8_t* steps) {
+    return RawCodes{__ldcs(reinterpret_cast<const uint2*>(codes)), __ldg(steps)};
 }
 __device__ __forceinline__ void decode8(const RawCodes& r, float (&x)[8]) {
     const float s = step_value(r.step);
@@ -171,6 +170,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(Shape shape, const T
     const int64_t padded = (F + kBlock - 1) / kBlock * kBlock;  // codes past the columns are written too, as 0
     const bool in = aligned16(x, ld_x), out = kAct != MICA_ACT_NONE && aligned16(y, ld_y);
     const T* from = x + at.row * ld_x + at.col;
+    T* to = kAct != MICA_ACT_NONE ? y + at.row * ld_y + at.col : nullptr;
+    int8_t* codes = reinterpret_cast<int8_t*>(p.codes) + at.row * p.ld + at.col;
+    uint8_t* steps = reinterpret_cast<uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
+    const bool first = at.col % kBlock == 0;
     Eight<T> v[kItems], up[kGated ? kItems : 1];
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
@@ -181,19 +184,20 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(Shape shape, const T
     }
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-        const int64_t row = at.row + u * at.apart;
-        const bool there = row < p.rows && at.col < padded;
-        pack8(v[u], there, p, row, at.col);
-        if (kGated) pack8(up[u], there, p, row, at.col + F);
+        const bool there = at.row + u * at.apart < p.rows && at.col < padded;
+        pack8(v[u], there, codes + u * at.apart * p.ld, steps + u * at.apart * p.ld_s, first);
+        if (kGated) pack8(up[u], there, codes + u * at.apart * p.ld + F, steps + u * at.apart * p.ld_s + F / kBlock, first);
         if (kAct != MICA_ACT_NONE && there) {
             float a[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float slope;
-                act_of<kAct>(v[u].get(i), a[i], slope);
-                if (kGated) a[i] *= up[u].get(i);
+            for (int i = 0; i < 4; ++i) {
+                Two r = act_pair<kAct>(v[u].pair(i));
+                if (kGated) r = r * up[u].pair(i);
+                const float2 f = each(r);
+                a[2 * i] = f.x;
+                a[2 * i + 1] = f.y;
             }
-            store8(y + row * ld_y + at.col, F - at.col, out, a);
+            store8(to + u * at.apart * ld_y, F - at.col, out, a);
         }
     }
 }
@@ -205,19 +209,20 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(Shape shape, mica_
     const Places at(shape, kItems, p.rows);
     const bool out = aligned16(x, ld_x);
     if (at.col >= p.cols) return;
+    const int8_t* codes = reinterpret_cast<const int8_t*>(p.codes) + at.row * p.ld + at.col;
+    const uint8_t* steps = reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
+    T* to = x + at.row * ld_x + at.col;
     RawCodes raw[kItems];
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-        const int64_t row = at.row + u * at.apart;
-        if (row < p.rows) raw[u] = load_codes(p, row, at.col);
+        if (at.row + u * at.apart < p.rows) raw[u] = load_codes(codes + u * at.apart * p.ld, steps + u * at.apart * p.ld_s);
     }
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-        const int64_t row = at.row + u * at.apart;
-        if (row >= p.rows) return;
+        if (at.row + u * at.apart >= p.rows) return;
         float v[8];
         decode8(raw[u], v);
-        store8(x + row * ld_x + at.col, p.cols - at.col, out, v);
+        store8(to + u * at.apart * ld_x, p.cols - at.col, out, v);
     }
 }
 
@@ -229,7 +234,9 @@ __global__ void __launch_bounds__(kPackThreads) act_grad_kernel(Shape shape, mic
     const int64_t F = kGated ? p.cols / 2 : p.cols;
     const Places at(shape, 1, p.rows);
     if (at.col >= F || at.row >= p.rows) return;
-    const RawCodes gate = load_codes(p, at.row, at.col), up = load_codes(p, at.row, kGated ? at.col + F : at.col);
+    const int8_t* codes = reinterpret_cast<const int8_t*>(p.codes) + at.row * p.ld + at.col;
+    const uint8_t* steps = reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
+    const RawCodes gate = load_codes(codes, steps), up = load_codes(codes + (kGated ? F : 0), steps + (kGated ? F / kBlock : 0));
     const Eight<T> g = load8(dy + at.row * ld_dy + at.col, F - at.col, aligned16(dy, ld_dy));
     float v[8], a[8], b[8];
     decode8(gate, v);

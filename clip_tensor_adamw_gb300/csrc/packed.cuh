@@ -37,23 +37,33 @@ __device__ __forceinline__ float largest_code(uint32_t step, bool half_source) {
 }
 // Four codes x / 2^e, to nearest, ties to even: x * inv is exact (unless it underflows to well below 1/2), and adding
 // 1.5 * 2^23 rounds it to an integer, whose two's complement is then in the low byte.
-__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d, float inv) {
-    const uint32_t p = __float_as_uint(fmaf(a, inv, 12582912.0f)), q = __float_as_uint(fmaf(b, inv, 12582912.0f));
-    const uint32_t r = __float_as_uint(fmaf(c, inv, 12582912.0f)), t = __float_as_uint(fmaf(d, inv, 12582912.0f));
-    return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(r, t, 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t codes_of(Two a, Two b, float inv) {
+    const Two k = two(inv, inv), magic = two(12582912.0f, 12582912.0f);
+    const float2 p = each(fma2(a, k, magic)), q = each(fma2(b, k, magic));
+    return __byte_perm(__byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x0040),
+                       __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040), 0x5410);
 }
 // Byte i of w, a code, as a float: 2^23 + (q + 128) has the bits 0x4B000000 | (q ^ 128).
 __device__ __forceinline__ float code_value(uint32_t flipped, int i) {
     return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440u | i)) - 8388736.0f;
 }
 
-// 1 / (1 + exp(-w)), from the hardware's power of two and reciprocal (some 2^-22 of its value, and |w| 2^-24 in the tail)
-__device__ __forceinline__ float logistic(float w) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(w * -1.44269504088896341f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// 1 / (1 + 2^t), from the hardware's power of two and reciprocal (some 2^-22 of its value, and |t| 2^-24 in the tail): the
+// logistic function of w for t = -log2(e) w
+__device__ __forceinline__ float fast_exp2(float t) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+__device__ __forceinline__ float fast_reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float logistic_of(float t) { return fast_reciprocal(1.0f + fast_exp2(t)); }
+
+constexpr float kLog2E = 1.44269504088896341f;
+constexpr float kGelu1 = 2.0f * 0.797884560802865356f, kGelu3 = kGelu1 * 0.044715f;  // 2 u = kGelu1 x + kGelu3 x^3
 
 // The activation functions and their slopes, in float32. GELU's tanh form is x * logistic(2 u), u = c (x + b x^3), since
 // (1 + tanh u) / 2 = logistic(2 u); its slope is h + x h (1 - h) 2 u'. Past |x| = 20, where h is 0 or 1, x^2 is held, so
@@ -61,16 +71,15 @@ __device__ __forceinline__ float logistic(float w) {
 template <int kAct>
 __device__ __forceinline__ void act_of(float x, float& y, float& slope) {
     if constexpr (kAct == MICA_ACT_GELU_TANH) {
-        constexpr float c2 = 2.0f * 0.797884560802865356f, b = 0.044715f;
-        const float x2 = fminf(x * x, 400.0f), h = logistic(c2 * x * fmaf(b, x2, 1.0f));
+        const float x2 = fminf(x * x, 400.0f), h = logistic_of(x * fmaf(-kLog2E * kGelu3, x2, -kLog2E * kGelu1));
         y = x * h;
-        slope = fmaf(y * (1.0f - h), fmaf(3.0f * b * c2, x2, c2), h);
+        slope = fmaf(y * (1.0f - h), fmaf(3.0f * kGelu3, x2, kGelu1), h);
     } else if constexpr (kAct == MICA_ACT_GELU) {
         const float p = normcdff(x);
         y = x * p;
         slope = fmaf(x * 0.398942280401432678f, expf(-0.5f * x * x), p);
     } else if constexpr (kAct == MICA_ACT_SILU) {
-        const float h = logistic(x);
+        const float h = logistic_of(-kLog2E * x);
         y = x * h;
         slope = fmaf(y, 1.0f - h, h);
     } else if constexpr (kAct == MICA_ACT_RELU) {
@@ -79,6 +88,25 @@ __device__ __forceinline__ void act_of(float x, float& y, float& slope) {
     } else {
         y = x;
         slope = 1.0f;
+    }
+}
+
+// Two of the functions' values at a time.
+template <int kAct>
+__device__ __forceinline__ Two act_pair(Two x) {
+    if constexpr (kAct == MICA_ACT_GELU_TANH || kAct == MICA_ACT_SILU) {
+        Two t = two(-kLog2E, -kLog2E);
+        if constexpr (kAct == MICA_ACT_GELU_TANH)
+            t = fma2(two(-kLog2E * kGelu3, -kLog2E * kGelu3), x * x, two(-kLog2E * kGelu1, -kLog2E * kGelu1));
+        const float2 e = each(x * t);
+        const float2 d = each(two(fast_exp2(e.x), fast_exp2(e.y)) + two(1.0f, 1.0f));
+        return x * two(fast_reciprocal(d.x), fast_reciprocal(d.y));
+    } else {
+        const float2 v = each(x);
+        float a, b, slope;
+        act_of<kAct>(v.x, a, slope);
+        act_of<kAct>(v.y, b, slope);
+        return two(a, b);
     }
 }
 
