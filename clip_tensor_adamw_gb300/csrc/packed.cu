@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(Shape shape, const T
     const T* from = x + at.row * ld_x + at.col;
     T* to = kAct != MICA_ACT_NONE ? y + at.row * ld_y + at.col : nullptr;
     int8_t* codes = reinterpret_cast<int8_t*>(p.codes) + at.row * p.ld + at.col;
-    uint8_t* steps = reinterpret_cast<uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
+    uint8_t* steps = reinterpret_cast<uint8_t*>(p.steps) + at.row * p.ld_s + (at.col >> 5);
     const bool first = at.col % kBlock == 0;
     Eight<T> v[kItems], up[kGated ? kItems : 1];
 #pragma unroll
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(Shape shape, mica_
     const bool out = aligned16(x, ld_x);
     if (at.col >= p.cols) return;
     const int8_t* codes = reinterpret_cast<const int8_t*>(p.codes) + at.row * p.ld + at.col;
-    const uint8_t* steps = reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
+    const uint8_t* steps = reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + (at.col >> 5);
     T* to = x + at.row * ld_x + at.col;
     RawCodes raw[kItems];
 #pragma unroll
@@ -234,9 +234,11 @@ __global__ void __launch_bounds__(kPackThreads) act_grad_kernel(Shape shape, mic
     const int64_t F = kGated ? p.cols / 2 : p.cols;
     const Places at(shape, 1, p.rows);
     if (at.col >= F || at.row >= p.rows) return;
-    const int8_t* codes = reinterpret_cast<const int8_t*>(p.codes) + at.row * p.ld + at.col;
-    const uint8_t* steps = reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + at.col / kBlock;
-    const RawCodes gate = load_codes(codes, steps), up = load_codes(codes + (kGated ? F : 0), steps + (kGated ? F / kBlock : 0));
+    auto codes_at = [&](int64_t col) {
+        return load_codes(reinterpret_cast<const int8_t*>(p.codes) + at.row * p.ld + col,
+                          reinterpret_cast<const uint8_t*>(p.steps) + at.row * p.ld_s + (col >> 5));
+    };
+    const RawCodes gate = codes_at(at.col), up = codes_at(kGated ? at.col + F : at.col);
     const Eight<T> g = load8(dy + at.row * ld_dy + at.col, F - at.col, aligned16(dy, ld_dy));
     float v[8], a[8], b[8];
     decode8(gate, v);
