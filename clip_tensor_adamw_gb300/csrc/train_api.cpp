@@ -149,7 +149,8 @@ mica_status check_packed(const mica_packed* p, const char* what) {
 mica_status add_packed(const mica_packed* p, bool written, Buffers* b) {
     const int64_t blocks = (p->cols + 31) / 32;
     MICA_TRY(b->matrix(p->codes, p->rows, blocks * 32, p->ld, 1, 16, written, "codes"));
-    return b->matrix(p->steps, p->rows, blocks, p->ld_s, 1, 4, written, "steps");
+    // (four steps are read at a time; only a row's blocks are written)
+    return b->matrix(p->steps, p->rows, written ? blocks : (blocks + 3) / 4 * 4, p->ld_s, 1, 4, written, "steps");
 }
 
 mica_status check_act(const mica_packed* p, int32_t act, int32_t gated, int32_t least) {

@@ -152,7 +152,7 @@ MICA_API mica_status mica_policy_loss(const mica_logits* z, const float* old_log
  *   codes   int8 [rows][ld], 16-byte aligned, ld a multiple of 32 and >= cols; the last block's codes past cols
  *           are 0
  *   steps   uint8 [rows][ld_s], 4-byte aligned, ld_s a multiple of 4 and >= ceil(cols / 32): e + 127; 255 for NaNs. The
- *           entries past the last block are not written and not used.
+ *           entries past the last block are not written and not used (but read: the last row has all of a multiple of 4).
  *   dtype   the source's type, MICA_F32, MICA_F16 or MICA_BF16
  */
 typedef struct {

@@ -494,3 +494,28 @@ def test_many_long_rows(rows, vocab, ld, offset, dtype):
         again = mica.mica_preference_loss(z, y, cu, ref, beta=0.1, out=z)
         assert torch.equal(again.dlogits, r.dlogits)
     mica.mica_sync()
+
+
+def test_many_long_rows_in_a_graph_and_on_two_streams():
+    """Rows handed out by the hardware: replayed from a graph on new logits, and by two launches at once."""
+    rows, vocab = 900, 18001
+    z, y = make(rows, vocab, torch.bfloat16, seed=4)
+    c = torch.randn(rows, generator=gen(2), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    mica.mica_token_logps_grad(z, y, c)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        held = [mica.mica_token_logps(z, y), mica.mica_token_logps_grad(z, y, c)]
+    for seed in (5, 6):
+        z.copy_(make(rows, vocab, torch.bfloat16, seed=seed)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held[0], mica.mica_token_logps(z, y))
+        assert torch.equal(held[1], mica.mica_token_logps_grad(z, y, c))
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = [mica.mica_token_logps_grad(z, y, c, stream=s) for s in (one, two, one, two)]
+    torch.cuda.synchronize()
+    for d in a:
+        assert torch.equal(d, held[1])
+    mica.mica_sync()
