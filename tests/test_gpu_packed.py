@@ -3,8 +3,8 @@ backward passes, and the weight gradient, over types, odd sizes, strides and ext
 
 Tolerances. The format is exact: codes, steps and values are compared for equality. The activation functions are computed in
 float32 (some 2^-22 of their terms' sizes) and rounded once. The weight gradient sums exact products in float32: with a
-chunk of at most 1,024 tokens summed by the tensor cores, 16 at a time (which may truncate each addition: 2^-23 of the
-running size), and the chunks (here at most 5) added to nearest, |error| <= 2^-23 * (64 + 32) * sum |x dy| for any order,
+chunk of at most 512 tokens summed by the tensor cores, 16 at a time (which may truncate each addition: 2^-23 of the
+running size), and the chunks (here at most 9) added to nearest, |error| <= 2^-23 * (32 + 64) * sum |x dy| for any order,
 then one rounding.
 """
 import math
