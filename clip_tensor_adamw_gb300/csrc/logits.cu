@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(
 // ----------------------------------------------------------------------------------------------------------------------
 //
 // Where there are more rows than CTAs, what a CTA per row loses is its start and its joins: the loads stop there. Here a
-// CTA takes row after row. One producer thread keeps a ring of kStages stages filled with bulk copies, the row's vectors
+// CTA takes row after row. One producer thread keeps a ring of stages filled with bulk copies, the row's vectors
 // once for the statistics and, for a gradient, once more for it (from L2), and goes on to the next row while the consumers
-// join this one's parts: the loads depend on nothing that they compute. Eight consumer warps take a stage each together.
+// join this one's parts: the loads depend on nothing that they compute. The consumer warps take each stage together.
 // Rows are handed out by the hardware: the grid has a CTA for each row, and a CTA that is at work cancels one that has not
 // begun and takes its row, so that rows that do not count leave no CTA idle. Every wait is bounded.
 // A CTA's consumer threads, its ring, and the CTAs of an SM.
@@ -479,17 +479,19 @@ struct RingShape {
     static constexpr int threads = kThreads + 32, stage_bytes = kVectors * 16, bytes = kCount * stage_bytes;
     static constexpr int per_thread = kVectors / kThreads;
 };
-// Reading only: three CTAs, so that others compute while one joins a row (8,192 rows of 50,257 bfloat16 logits, of which
-// 6,144 count: 106 us, 5.8 TB/s; with two 123 us, with one of 512 threads 178 us).
-using ReadRing = RingShape<256, 2048, 2, 3>;
+// Each the best of a dozen shapes. Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
+// bfloat16 logits, of which 6,144 count: 100 us, 6.2 TB/s; three of 256 threads 104 us, two of 384 120 us, one of 512 178 us).
+using ReadRing = RingShape<192, 1536, 2, 4>;
 // A gradient reads its row again, which has to be in L2 still: of long rows one at a time on an SM (6,144 rows of 131,072:
-// 502 us, 6.0 TB/s, against 535 us with two CTAs and 625 us with three), of others two (6,144 rows of 50,257: 217 us
-// against 261 us with one).
-using GradRing = RingShape<256, 2048, 3, 2>;
+// 486 us, 6.2 TB/s, against 535 us with two CTAs and 625 us with three), of others two (6,144 rows of 50,257: 196 us,
+// with 256 threads 214 us; 260 us with one CTA).
+using GradRing = RingShape<384, 2304, 3, 2>;
 using LongGradRing = RingShape<512, 2048, 6, 1>;
+// One pass that reads and writes.
+using StreamRing = RingShape<512, 2048, 3, 2>;
 constexpr int64_t kLongRowBytes = 160 << 10;
 constexpr int kEntries = 2;
-constexpr int64_t kRingRows = 608;
+constexpr int64_t kRingRows = 300;
 
 // Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_logits_status).
 __device__ unsigned int g_logits_status;
@@ -917,12 +919,12 @@ __global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTer
     }
 }
 
-// Many long rows go through the ring. Measured both ways, in us, the ring first: log-probabilities of 8,192 rows of 8,192
-// bfloat16 logits 42 and 36, 16,384: 51 and 52, 32,768: 73 and 95; policy gradients of 6,144 rows of 16,384: 95 and 79,
-// 50,257: 217 and 267; of 600 rows of 131,072: 59 and 74, of 300: 38 and 39.
+// Many long rows go through the ring. Measured both ways, in us, the ring first, bfloat16: log-probabilities of 8,192 rows of
+// 8,192 logits 34 and 36, 32,768: 69 and 91; of 300 rows of 50,257: 17 and 18, of 1,200: 24 and 30; policy gradients of 6,144
+// rows of 16,384: 91 and 79, 32,768: 135 and 154, 50,257: 196 and 267; of 300 rows of 131,072: 33 and 43.
 bool takes_ring(const LogitRows& L, bool grad) {
     const int64_t bytes = L.vocab * (L.dtype == MICA_F32 ? 4 : 2);
-    return L.rows >= kRingRows && bytes >= (grad ? 64 << 10 : 32 << 10);
+    return L.rows >= kRingRows && bytes >= (grad ? 64 << 10 : 16 << 10);
 }
 
 // How a row is cut otherwise: C CTAs of `threads` threads.
@@ -966,7 +968,7 @@ cudaError_t launch_ring(const LogitRows& L, const PolicyTerms& P, const RowOut& 
         return e != cudaSuccess ? e : launch_clusters(kernel, L.rows, 1, S::threads, S::bytes, stream, L, P, out);
     };
     if constexpr (kKind == kLogps || kKind == kEntropy) return go(ReadRing{});
-    else if constexpr (kStream) return go(GradRing{});
+    else if constexpr (kStream) return go(StreamRing{});
     else return L.vocab * (int64_t)sizeof(T) > kLongRowBytes ? go(LongGradRing{}) : go(GradRing{});
 }
 

@@ -16,7 +16,7 @@
 // sixteen warps, four groups of four that take stages in turn, decode them into the operand. The same warps empty TMEM, a
 // chunk behind. Three more warps load codes, load dy, and issue the products.
 //
-// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 293 us, 1,150 TFLOP/s, the tensor pipe 56% active; without the
+// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 293 us, 1,150 TFLOP/s, the tensor pipe 54% active; without the
 // decoding it would take some 240 us. A stage moves 96 KB through an SM's shared memory (the products read 48, dy and codes
 // are written with 24, codes read with 8, operands written with 16), 750 clocks' worth against the products' 512. Two
 // groups of eight decoding warps took 11% longer.
