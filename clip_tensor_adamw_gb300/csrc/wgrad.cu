@@ -73,7 +73,7 @@ __device__ __forceinline__ Piece piece_at(const Deal& d, int i) {
 
 struct Barriers {
     uint64_t codes_full[kDepths], codes_empty[kDepths];  // the codes of a stage have come; the workers have read them
-    uint64_t ready[kDepths];                             // (leader) a stage's operands: dy has come, the codes are decoded, in both CTAs
+    uint64_t ready[kDepths];                             // (leader) dy has come and the codes are decoded, in both CTAs
     uint64_t used[kDepths];                              // the products of a stage are done
     uint64_t sum_full[2], sum_empty[2];                  // a chunk's sums are in TMEM; (leader) both CTAs have taken them
     uint32_t tmem;
@@ -187,7 +187,9 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t step) {
     uint32_t r;
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
         const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, c = (w & 0x00800080u) | 0x43004300u;
-        asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(a), "r"(c), "r"(step));
+        asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}"
+            : "=r"(r)
+            : "r"(a), "r"(c), "r"(step));
     } else {
         const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u;
         asm("{\n\t.reg .b32 d;\n\tsub.rn.f16x2 d, %1, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
@@ -221,7 +223,9 @@ __device__ __forceinline__ void decode(uint32_t at, uint4 codes, uint32_t step) 
     store_shared(at ^ 16, o[4], o[5], o[6], o[7]);
 }
 // The feature of an operand's column.
-__host__ __device__ constexpr int feature_of(int column) { return column % 4 == 1 ? column + 1 : column % 4 == 2 ? column - 1 : column; }
+__host__ __device__ constexpr int feature_of(int column) {
+    return column % 4 == 1 ? column + 1 : column % 4 == 2 ? column - 1 : column;
+}
 
 // dw[i + c][j] = add + the sum of feature c, eight features' loads at a time
 template <typename O, int kCount>
@@ -267,7 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
         mbar_fence_init();
     }
     if (warp == kProducts) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar.tmem)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar.tmem))
+                     : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     fence_before();
@@ -556,17 +561,18 @@ template <typename T, typename O>
 cudaError_t launch_typed(const Wgrad& w, const Deal& d, float* partial, void* stream) {
     if (d.stages) {
         CUtensorMap codes, dy;
-        const auto type = std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        if (!encode(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.x.codes, (w.x.cols + kBlock - 1) / kBlock * kBlock, w.x.rows, w.x.ld,
-                    kHalf, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        const auto type = std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const int64_t padded = (w.x.cols + kBlock - 1) / kBlock * kBlock;
+        if (!encode(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.x.codes, padded, w.x.rows, w.x.ld, kHalf,
+                    CU_TENSOR_MAP_SWIZZLE_NONE) ||
             !encode(&dy, type, w.dy, w.n, w.x.rows, w.ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
         const auto kernel = wgrad_kernel<T, O>;
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
-        const int all = pieces_of(d);
+        const int all = pieces_of(d), pairs = all < d.pairs ? all : d.pairs;
         if (e == cudaSuccess)
-            e = launch_after(kernel, 2 * (int64_t)(all < d.pairs ? all : d.pairs), kThreads2, kSharedBytes, stream, codes, dy, w, d,
-                             partial);
+            e = launch_after(kernel, 2 * (int64_t)pairs, kThreads2, kSharedBytes, stream, codes, dy, w, d, partial);
         if (e != cudaSuccess) return e;
     }
     if (d.parts == 1) return cudaSuccess;
