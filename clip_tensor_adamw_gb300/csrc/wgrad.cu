@@ -43,6 +43,7 @@ constexpr int kDepths = 5;                     // stages
 constexpr int kChunkStages = 8;                // stages between two visits to the accumulator
 constexpr int kWorkers = 512, kWorkerWarps = kWorkers / 32, kThreads2 = kWorkers + 96;
 constexpr int kGroups = 4, kGroupWarps = kWorkerWarps / kGroups;  // of workers: they decode stages in turn
+static_assert(kGroups <= kDepths, "a group would miss two phases of a stage's barriers");
 constexpr int kColumns = kTile * kHalf / kWorkers;  // of the accumulator, that a worker sums up
 enum Role { kCodes = kWorkerWarps, kDy, kProducts };              // the other warps
 constexpr int kOperandBytes = kDepth * kHalf * 2, kCodeBytes = kDepth * kHalf, kBoxBytes = kDepth * 128;
@@ -399,9 +400,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads2, 1)
             for (int k = p.from; k < p.to; ++k, turn.next(), whose = (whose + 1) % kGroups) {
                 if (whose == group) {
                     const int s = turn.at;
-                    if (!(ok = mbar_wait_idle(&bar.codes_full[s], turn.round))) break;
                     constexpr int kApart = kWorkers / kGroups / 4, kTokens = kDepth / kApart;  // of a thread
+                    // The order matters: a group takes every kGroups-th stage of a ring of kDepths, so it has not seen
+                    // whether the stage's last codes (another group's) have come, and a wait by parity passes on the phase
+                    // before the last too. When the products of those codes are done, the codes had come, and the second
+                    // wait can only mean this stage's. The first is safe by itself: products end in order, and the group's
+                    // own last stage waited for later ones than this barrier's phase before.
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
+                    if (!(ok = mbar_wait_idle(&bar.codes_full[s], turn.round))) break;
 #pragma unroll
                     for (int u = 0; u < kTokens; ++u) {
                         const uint32_t steps = bar.steps[s][token + u * kApart];

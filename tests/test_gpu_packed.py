@@ -243,6 +243,24 @@ def test_wgrad(tokens, features, n, xt, gt):
     assert torch.equal(dw, mica.mica_packed_wgrad(p, dy))
 
 
+@pytest.mark.parametrize("tokens,features,n", [(200, 2300, 2600), (1100, 2300, 4700), (1030, 5000, 2100)])
+def test_wgrad_many_tiles(tokens, features, n):
+    """More tiles than pairs of SMs: a pair takes tile after tile, whole ones and, of 1,024 tokens and more, parts of split
+    ones, its rings going on from one to the next. The same bits each time, and added to a gradient in place."""
+    x = make(tokens, features, torch.bfloat16, seed=tokens, spread=2.0)
+    dy = make(tokens, n, torch.bfloat16, seed=n, spread=2.0)
+    p = mica.mica_act_pack(x)
+    dw = mica.mica_packed_wgrad(p, dy)
+    wgrad_check(p, dy, dw)
+    for _ in range(5):
+        assert torch.equal(dw, mica.mica_packed_wgrad(p, dy))
+    add = make(features, n, torch.float32, seed=5, spread=2.0)
+    got = mica.mica_packed_wgrad(p, dy, add=add)
+    wgrad_check(p, dy, got, add)
+    assert torch.equal(got, mica.mica_packed_wgrad(p, dy, add=add, out=add))
+    mica.mica_sync()
+
+
 @pytest.mark.parametrize("n,ld,offset,ld_dw,off_dw", [(64, 64, 1, 64, 0), (64, 65, 0, 67, 1), (100, 104, 4, 100, 2),
                                                       (257, 257, 0, 260, 0), (256, 256, 8, 256, 4), (40, 0, 0, 41, 3)])
 @pytest.mark.parametrize("ot", DTYPES, ids=str)
