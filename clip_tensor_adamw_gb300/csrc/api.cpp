@@ -132,7 +132,7 @@ mica_status check_device_span(const void* p, size_t bytes, size_t align, int dev
         size_t size = 0;
         if (fn(&base, &size, (unsigned long long)reinterpret_cast<uintptr_t>(p)) == 0) {
             const unsigned long long end = base + size, q = (unsigned long long)reinterpret_cast<uintptr_t>(p);
-            if (q + bytes > end)
+            if (bytes > end - q)  // (q + bytes could wrap round)
                 return fail(MICA_ERR_ADDRESS, "%s[%lld] = %p: %zu bytes run past the end of its allocation", what,
                             (long long)index, p, bytes);
         }

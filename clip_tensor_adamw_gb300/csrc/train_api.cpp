@@ -96,10 +96,15 @@ mica_status check_extent(int64_t rows, int64_t cols, int64_t least_cols, const c
     return MICA_OK;
 }
 
-mica_status check_stride(int64_t ld, int64_t least, const char* what) {
+// A row stride, and with it the span of `rows` x `cols` elements (both checked), which no larger than 2^44 (16 TB of bytes)
+// can be multiplied by an element's size, and added to an address, without wrapping round.
+mica_status check_stride(int64_t ld, int64_t least, int64_t rows, int64_t cols, const char* what) {
     if (ld < least || ld > ((int64_t)1 << 40))
         return fail(MICA_ERR_COUNT, "%s: the row stride %lld is outside [%lld, 2^40]", what, (long long)ld,
                     (long long)least);
+    if (rows > 1 && ld > (((int64_t)1 << 44) - cols) / (rows - 1))
+        return fail(MICA_ERR_COUNT, "%s: %lld rows with the stride %lld span more than 2^44 elements", what,
+                    (long long)rows, (long long)ld);
     return MICA_OK;
 }
 
@@ -115,7 +120,7 @@ mica_status check_logits(const mica_logits* z, LogitRows* L) {
     float a_hi = (float)a;  // the largest float32 below a, so that the rest is positive
     if (a_hi >= a) a_hi = std::nextafter(a_hi, 0.0f);
     MICA_TRY(check_extent(z->rows, z->vocab, 1, "logits"));
-    MICA_TRY(check_stride(z->ld, 0, "logits"));
+    MICA_TRY(check_stride(z->ld, 0, z->rows, z->vocab, "logits"));
     *L = LogitRows{z->logits, z->targets, z->rows, z->ld, (int32_t)z->vocab, z->dtype, z->target_bytes == 8,
                    (float)(1.0 / z->temperature), 1.0 / z->temperature, (float)a, a_hi, (float)(a - a_hi)};
     return MICA_OK;
@@ -139,8 +144,8 @@ mica_status check_packed(const mica_packed* p, const char* what) {
     if (!p) return fail(MICA_ERR_NULL, "%s is NULL", what);
     if (!is_type(p->dtype)) return fail(MICA_ERR_DTYPE, "%s: the source's type must be float32, float16 or bfloat16", what);
     MICA_TRY(check_extent(p->rows, p->cols, 0, what));
-    MICA_TRY(check_stride(p->ld, p->cols, "codes"));
-    MICA_TRY(check_stride(p->ld_s, (p->cols + 31) / 32, "steps"));
+    MICA_TRY(check_stride(p->ld, p->cols, p->rows, p->cols, "codes"));
+    MICA_TRY(check_stride(p->ld_s, (p->cols + 31) / 32, p->rows, p->cols, "steps"));
     if (p->ld % 32) return fail(MICA_ERR_COUNT, "codes: the row stride %lld is not a multiple of 32", (long long)p->ld);
     if (p->ld_s % 4) return fail(MICA_ERR_COUNT, "steps: the row stride %lld is not a multiple of 4", (long long)p->ld_s);
     return MICA_OK;
@@ -184,7 +189,7 @@ extern "C" mica_status mica_token_logps_grad(const mica_logits* z, const float* 
                                              void* stream) {
     LogitRows L;
     MICA_TRY(check_logits(z, &L));
-    MICA_TRY(check_stride(ld_d, z->vocab, "dlogits"));
+    MICA_TRY(check_stride(ld_d, z->vocab, z->rows, z->vocab, "dlogits"));
     if (z->rows == 0) return ok();
     int dev = 0;
     MICA_TRY(current_device(&dev));
@@ -220,7 +225,7 @@ extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t*
         return fail(MICA_ERR_HYPER, "label_smoothing goes with the sigmoid loss only");
     if (!std::isfinite(hp->grad_scale)) return fail(MICA_ERR_HYPER, "grad_scale %g is not finite", hp->grad_scale);
     if (hp->flags & ~MICA_PREF_LENGTH_NORM) return fail(MICA_ERR_HYPER, "unknown flags 0x%x", hp->flags);
-    if (dlogits) MICA_TRY(check_stride(ld_d, z->vocab, "dlogits"));
+    if (dlogits) MICA_TRY(check_stride(ld_d, z->vocab, z->rows, z->vocab, "dlogits"));
     const int64_t need = mica_preference_workspace(z->rows, pairs);
     if (need && !workspace) return fail(MICA_ERR_NULL, "workspace is NULL");
     if (workspace_bytes < need)
@@ -267,7 +272,7 @@ extern "C" mica_status mica_policy_loss(const mica_logits* z, const float* old_l
         return fail(MICA_ERR_HYPER, "kl_coef %g is not finite and >= 0", hp->kl_coef);
     if (!std::isfinite(hp->denom) || !(hp->denom > 0.0)) return fail(MICA_ERR_HYPER, "denom %g is not finite and > 0", hp->denom);
     if (!std::isfinite(hp->grad_scale)) return fail(MICA_ERR_HYPER, "grad_scale %g is not finite", hp->grad_scale);
-    if (dlogits) MICA_TRY(check_stride(ld_d, z->vocab, "dlogits"));
+    if (dlogits) MICA_TRY(check_stride(ld_d, z->vocab, z->rows, z->vocab, "dlogits"));
     int dev = 0;
     MICA_TRY(current_device(&dev));
     Buffers b(dev);
@@ -297,8 +302,8 @@ extern "C" mica_status mica_act_pack(const void* x, int64_t ld_x, const mica_pac
     MICA_TRY(check_act(p, act, gated, MICA_ACT_NONE));
     const int64_t out = gated ? p->cols / 2 : p->cols;
     const size_t es = bytes_of(p->dtype);
-    MICA_TRY(check_stride(ld_x, 0, "x"));
-    if (act != MICA_ACT_NONE) MICA_TRY(check_stride(ld_y, out, "y"));
+    MICA_TRY(check_stride(ld_x, 0, p->rows, p->cols, "x"));
+    if (act != MICA_ACT_NONE) MICA_TRY(check_stride(ld_y, out, p->rows, out, "y"));
     else if (y) return fail(MICA_ERR_HYPER, "y is given without an activation function");
     if (p->rows == 0 || p->cols == 0) return ok();
     int dev = 0;
@@ -313,7 +318,7 @@ extern "C" mica_status mica_act_pack(const void* x, int64_t ld_x, const mica_pac
 
 extern "C" mica_status mica_act_unpack(const mica_packed* p, void* x, int64_t ld_x, void* stream) {
     MICA_TRY(check_packed(p, "the checkpoint"));
-    MICA_TRY(check_stride(ld_x, p->cols, "x"));
+    MICA_TRY(check_stride(ld_x, p->cols, p->rows, p->cols, "x"));
     if (p->rows == 0 || p->cols == 0) return ok();
     int dev = 0;
     MICA_TRY(current_device(&dev));
@@ -330,8 +335,8 @@ extern "C" mica_status mica_act_grad(const mica_packed* p, int32_t act, int32_t 
     MICA_TRY(check_act(p, act, gated, MICA_ACT_GELU_TANH));
     if (!is_type(dtype)) return fail(MICA_ERR_DTYPE, "dy must be float32, float16 or bfloat16");
     const int64_t in = gated ? p->cols / 2 : p->cols;
-    MICA_TRY(check_stride(ld_dy, 0, "dy"));
-    MICA_TRY(check_stride(ld_dx, p->cols, "dx"));
+    MICA_TRY(check_stride(ld_dy, 0, p->rows, in, "dy"));
+    MICA_TRY(check_stride(ld_dx, p->cols, p->rows, p->cols, "dx"));
     if (p->rows == 0 || p->cols == 0) return ok();
     int dev = 0;
     MICA_TRY(current_device(&dev));
@@ -347,7 +352,9 @@ extern "C" mica_status mica_act_grad(const mica_packed* p, int32_t act, int32_t 
 
 extern "C" int64_t mica_packed_wgrad_workspace(const mica_packed* x, const void* dy, int64_t ld_dy, int64_t n) {
     int dev = 0;
-    if (check_packed(x, "the checkpoint") != MICA_OK || n < 0 || n > MICA_MAX_COLS || current_device(&dev) != MICA_OK) return 0;
+    if (check_packed(x, "the checkpoint") != MICA_OK || n < 0 || n > MICA_MAX_COLS ||
+        check_stride(n, n, x->cols, n, "dw") != MICA_OK || current_device(&dev) != MICA_OK)
+        return 0;
     return wgrad_workspace(x->rows, x->cols, n, dy, ld_dy, sm_count(dev));
 }
 
@@ -360,9 +367,9 @@ extern "C" mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, i
         return fail(MICA_ERR_DTYPE, "a float16 dy needs the checkpoint of a float16 activation");
     if (!is_type(dw_dtype)) return fail(MICA_ERR_DTYPE, "dw must be float32, float16 or bfloat16");
     MICA_TRY(check_extent(x->rows, n, 0, "dy"));
-    MICA_TRY(check_stride(ld_dy, 0, "dy"));
-    MICA_TRY(check_stride(ld_dw, n, "dw"));
-    if (add) MICA_TRY(check_stride(ld_add, 0, "add"));
+    MICA_TRY(check_stride(ld_dy, 0, x->rows, n, "dy"));
+    MICA_TRY(check_stride(ld_dw, n, x->cols, n, "dw"));
+    if (add) MICA_TRY(check_stride(ld_add, 0, x->cols, n, "add"));
     if (x->cols == 0 || n == 0) return ok();
     int dev = 0;
     MICA_TRY(current_device(&dev));

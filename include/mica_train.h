@@ -17,7 +17,7 @@
  * details, MICA_SYNC_DEBUG and mica_sync are the same):
  *   - Matrices are device pointers with a row stride in elements (`ld`); the elements of a row are contiguous. Every
  *     alignment to the element is taken. Only rows * ld spans are checked: [p, p + ((rows-1)*ld + cols)) has to lie in
- *     p's allocation.
+ *     p's allocation (MICA_ERR_ADDRESS); one of more than 2^44 elements is MICA_ERR_COUNT whatever p is.
  *   - Nothing is allocated and no table is cached. What a call needs besides its outputs is the caller's workspace,
  *     whose size a call of its own gives; its contents need not be set and are not read by a later call.
  *   - Results do not depend on the order in which CTAs run: no floating-point atomics.

@@ -156,3 +156,40 @@ def test_python_checks_need_no_device():
     assert p.codes.shape == (4, 64) and p.steps.shape == (4, 4) and p.shape == (4, 33)
     with pytest.raises(ValueError):
         mica.mica_act_grad(p, torch.zeros(4, 32), "silu")
+
+
+def test_spans_that_would_wrap_are_refused():
+    """(rows - 1) * ld + columns elements in bytes may pass 64 bits with each factor in its range; such a matrix is refused
+    before anything else looks at it, on a machine without a GPU too."""
+    L = train._train()
+    for rows, ld in (((1 << 24) + 1, 1 << 40), (1 << 30, 1 << 40), ((1 << 22) + 1, 1 << 40), (1 << 24, 1 << 40)):
+        z = logits(rows=rows, ld=ld)
+        assert L.mica_token_logps(z, 0x3000, None, None) == COUNT
+        assert L.mica_token_logps_grad(z, 0x3000, 0x4000, 100, None) == COUNT
+        assert L.mica_preference_loss(z, 0x3000, 1, None, pref(), 0x4000, None, 0x5000, None, 0, 0x6000, 1 << 40, None) == COUNT
+        assert L.mica_policy_loss(z, 0x3000, 0x4000, None, None, policy(), 0x5000, 0x6000, None, 0, None) == COUNT
+        z = logits(rows=rows)
+        assert L.mica_token_logps_grad(z, 0x3000, 0x4000, ld, None) == COUNT
+        assert L.mica_preference_loss(z, 0x3000, 1, None, pref(), 0x4000, None, 0x5000, 0x7000, ld, 0x6000, 1 << 40,
+                                      None) == COUNT
+        assert L.mica_policy_loss(z, 0x3000, 0x4000, None, None, policy(), 0x5000, 0x6000, 0x7000, ld, None) == COUNT
+        for wide in (dict(ld=ld), dict(ld_s=ld)):
+            p = packed(rows=rows, **wide)
+            assert L.mica_act_pack(0x3000, 100, p, 0, 0, None, 0, None) == COUNT
+            assert L.mica_act_unpack(p, 0x3000, 100, None) == COUNT
+            assert L.mica_act_grad(p, 1, 0, 0x3000, 100, F32, 0x4000, 100, None) == COUNT
+            assert L.mica_packed_wgrad(p, 0x3000, 8, BF16, 8, None, 0, 0x4000, 8, F32, None, 0, None) == COUNT
+        p = packed(rows=rows)
+        assert L.mica_act_pack(0x3000, ld, p, 0, 0, None, 0, None) == COUNT
+        assert L.mica_act_pack(0x3000, 100, p, 3, 0, 0x4000, ld, None) == COUNT
+        assert L.mica_act_unpack(p, 0x3000, ld, None) == COUNT
+        assert L.mica_act_grad(p, 1, 0, 0x3000, ld, F32, 0x4000, 100, None) == COUNT
+        assert L.mica_act_grad(p, 1, 0, 0x3000, 100, F32, 0x4000, ld, None) == COUNT
+        assert L.mica_packed_wgrad(p, 0x3000, ld, BF16, 8, None, 0, 0x4000, 8, F32, None, 0, None) == COUNT
+    p = packed(cols=1 << 24, ld=1 << 24, ld_s=1 << 20)
+    for add, ld_add, ld_dw in ((None, 0, 1 << 40), (0x5000, 1 << 40, 8)):
+        assert L.mica_packed_wgrad(p, 0x3000, 8, BF16, 8, add, ld_add, 0x4000, ld_dw, F32, None, 0, None) == COUNT
+    assert L.mica_packed_wgrad(p, 0x3000, 1 << 24, BF16, 1 << 24, None, 0, 0x4000, 1 << 24, F32, None, 0, None) == COUNT
+    assert L.mica_packed_wgrad_workspace(p, 0x3000, 1 << 24, 1 << 24) == 0
+    # one row may have any stride: it spans its columns
+    assert L.mica_act_unpack(packed(rows=1, ld=1 << 40), None, 1 << 40, None) not in (OK, COUNT)
