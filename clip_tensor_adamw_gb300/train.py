@@ -140,11 +140,13 @@ def _logits(logits: torch.Tensor, targets: torch.Tensor, temperature: float) -> 
 
 
 def _dlogits(out: torch.Tensor | None, logits: torch.Tensor, ld: int) -> torch.Tensor:
-    """A given buffer, or a new one laid out as the logits are (rows as far apart, so that they are equally aligned)."""
+    """A given buffer, or a new one whose rows lie as the logits' do within lines of 128 bytes (so that both are equally
+    aligned), and no further apart than that takes: the logits may be every so many rows of a larger tensor."""
     if out is None:
         rows, vocab = logits.shape
         if ld <= vocab:
             return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        ld = vocab + (ld - vocab) % (128 // logits.element_size())
         return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
     if out.shape != logits.shape or out.dtype != logits.dtype:
         raise ValueError("dlogits must have the logits' shape and dtype")

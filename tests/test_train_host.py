@@ -193,3 +193,18 @@ def test_spans_that_would_wrap_are_refused():
     assert L.mica_packed_wgrad_workspace(p, 0x3000, 1 << 24, 1 << 24) == 0
     # one row may have any stride: it spans its columns
     assert L.mica_act_unpack(packed(rows=1, ld=1 << 40), None, 1 << 40, None) not in (OK, COUNT)
+
+
+def test_a_gradient_takes_no_more_memory_than_its_rows():
+    """The logits of the last tokens of a batch are far apart; their gradient is not, and lies as they do within 128 bytes."""
+    import torch
+    batch = torch.zeros(3, 7, 1009, dtype=torch.bfloat16)
+    for z in (batch[:, -1], batch[:, 3, :1000], torch.zeros(5, 1024)[:, :1009], torch.zeros(5, 1009),
+              torch.zeros(4, 1, 130)[:, 0], torch.zeros(1, 64).expand(6, 64)):
+        ld = train._matrix(z, "logits")
+        d = train._dlogits(None, z, ld)
+        assert d.shape == z.shape and d.dtype == z.dtype
+        line = 128 // z.element_size()
+        assert d.untyped_storage().nbytes() <= z.shape[0] * (z.shape[1] + line - 1) * z.element_size()
+        if ld > z.shape[1]:
+            assert (train._matrix(d, "dlogits") - ld) % line == 0
