@@ -107,13 +107,19 @@ struct Vec {
         else return __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i % 2)))));
     }
     __device__ __forceinline__ Two pair(int i) const { return two(get(2 * i), get(2 * i + 1)); }
-    __device__ __forceinline__ float max() const {
+    template <int kCount>
+    __device__ __forceinline__ static float max(const Vec (&v)[kCount]) {
         if constexpr (sizeof(T) == 4) {
-            return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+            float m = v[0].get(0);
+#pragma unroll
+            for (int i = 1; i < kCount * n; ++i) m = fmaxf(m, v[i / n].get(i % n));
+            return m;
         } else {
             using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
-            const T2* p = reinterpret_cast<const T2*>(&raw);
-            const T2 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+            const T2* p = reinterpret_cast<const T2*>(v);
+            T2 m = p[0];
+#pragma unroll
+            for (int i = 1; i < kCount * 4; ++i) m = __hmax2(m, p[i]);
             return fmaxf(widen(m.x), widen(m.y));
         }
     }
@@ -312,17 +318,27 @@ __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
     r.m = m;
 }
 
+// Counts a part from the largest of some vectors that it is about to take, where that is larger. Log-probabilities with
+// entropies are counted so throughout: an entropy is log s, which is then not negative, plus the mean of -x, which is not
+// either. Counted from a target far below the maximum it would be the difference of two numbers as large as that distance, in
+// float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons take some 4% of the time
+// (8,192 rows of 50,257 bfloat16 logits, of which 6,144 count, with entropies: 104 us, counted from the target 100). Without
+// entropies they are made too, so that the log-probabilities are the same bits; there they take nothing.
+template <bool kMoment, typename T, int kCount>
+__device__ __forceinline__ void count_from_highest(const LogitRows& L, const Vec<T> (&v)[kCount], Running& r) {
+    const float m = Vec<T>::max(v);
+    if (m > r.m) raise<kMoment>(L, r, m);
+}
+
 // Adds some vectors to a thread's part. Weights are counted from an origin that need not be the maximum: any will do as long
-// as one weight of the row is at least 1 and none comes near 2^128. So the target's logit serves, until a sum passes 2^60;
-// the elements are compared only then (and where the target is banned, or an infinity or a NaN is among them).
+// as one weight of the row is at least 1 and none comes near 2^128. So for a gradient the target's logit serves, until a sum
+// passes 2^60; the elements are compared only then (and where the target is banned, or an infinity or a NaN is among them).
 template <typename T, bool kMoment, int kCount>
 __device__ __forceinline__ void add_vectors(const LogitRows& L, const Vec<T> (&v)[kCount], Running& r) {
     float s, u;
     sum_weights<T, kMoment, false>(L, v, r.m, s, u);
     if (!(s < 0x1p60f) || (kMoment && !(fabsf(u) < 0x1p100f))) {
-        float m = v[0].max();
-#pragma unroll
-        for (int j = 1; j < kCount; ++j) m = fmaxf(m, v[j].max());
+        const float m = Vec<T>::max(v);
         if (!(s < 0x1p60f) && m > r.m) raise<kMoment>(L, r, m);
         sum_weights<T, kMoment, true>(L, v, origin(r.m), s, u);
     }
@@ -419,7 +435,7 @@ __device__ __forceinline__ float finish_row(const LogitRows& L, const PolicyTerm
 template <typename T, int kThreads, RowKind kKind>
 __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(LogitRows L, PolicyTerms P, RowOut out) {
     constexpr int n = Vec<T>::n;
-    constexpr bool kGrad = kKind == kGiven || kKind == kPolicy, kMoment = kKind == kEntropy;
+    constexpr bool kGrad = kKind == kGiven || kKind == kPolicy, kMoment = kKind == kEntropy, kHighest = !kGrad;
     __shared__ Parts parts;
     wait_prerequisite();
     allow_dependents();
@@ -444,14 +460,17 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             v[u] = Vec<T>{kGrad ? ld16_again(at + u * kThreads * n) : ld16_stream(at + u * kThreads * n)};
+        if (kHighest) count_from_highest<kMoment>(L, v, r);
         add_vectors<T, kMoment>(L, v, r);
     }
     for (; k < g.hi; k += kThreads) {
         const Vec<T> v[1] = {{kGrad ? ld16_again(z + (k * n - g.lead)) : ld16_stream(z + (k * n - g.lead))}};
+        if (kHighest) count_from_highest<kMoment>(L, v, r);
         add_vectors<T, kMoment>(L, v, r);
     }
     if (g.edge >= 0) {
         const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
+        if (kHighest) count_from_highest<kMoment>(L, v, r);
         add_vectors<T, kMoment>(L, v, r);
     }
     r = join_parts<kMoment>(L, parts, r);
@@ -481,7 +500,7 @@ struct RingShape {
     static constexpr int threads = kThreads + 32, stage_bytes = kVectors * 16, bytes = kCount * stage_bytes;
     static constexpr int per_thread = kVectors / kThreads;
 };
-// Each the best of a dozen shapes. Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
+// Each the best of a dozen shapes (the first with weights counted from the target). Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
 // bfloat16 logits, of which 6,144 count: 100 us, 6.2 TB/s; three of 256 threads 104 us, two of 384 120 us, one of 512 178 us).
 using ReadRing = RingShape<192, 1536, 2, 4>;
 // A gradient reads its row again, which has to be in L2 still: of long rows one at a time on an SM (6,144 rows of 131,072:
@@ -554,7 +573,7 @@ __device__ __forceinline__ Vec<T> stage_vector(const unsigned char* stage, int i
 template <typename T, RowKind kKind, bool kStream, typename S>
 __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, PolicyTerms P, RowOut out) {
     constexpr int n = Vec<T>::n;
-    constexpr bool kGrad = kKind == kGiven || kKind == kPolicy, kMoment = kKind == kEntropy;
+    constexpr bool kGrad = kKind == kGiven || kKind == kPolicy, kMoment = kKind == kEntropy, kHighest = !kGrad;
     constexpr int kPasses = kGrad && !kStream ? 2 : 1;
     extern __shared__ __align__(128) unsigned char stages[];
     constexpr int kStages = S::stages, kStageVectors = S::vectors, kStageBytes = S::stage_bytes;
@@ -679,6 +698,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                     for (int u = 0; u < kPerThread; ++u) v[u] = stage_vector<T>(stage, (int)threadIdx.x + u * kConsumers);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring.empty[s]);
+                    if (kHighest) count_from_highest<kMoment>(L, v, q);
 #pragma unroll
                     for (int u = 0; u < kPerThread; u += 2) {
                         const Vec<T> two_of[2] = {v[u], v[u + 1]};
@@ -687,6 +707,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                 } else {
                     for (int i = (int)threadIdx.x; i < left; i += kConsumers) {
                         const Vec<T> v[1] = {stage_vector<T>(stage, i)};
+                        if (kHighest) count_from_highest<kMoment>(L, v, q);
                         add_vectors<T, kMoment>(L, v, q);
                     }
                     __syncwarp();
@@ -695,6 +716,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             }
             if (g.edge >= 0) {
                 const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
+                if (kHighest) count_from_highest<kMoment>(L, v, q);
                 add_vectors<T, kMoment>(L, v, q);
             }
             q = join_warp<kMoment>(L, q);

@@ -519,3 +519,45 @@ def test_many_long_rows_in_a_graph_and_on_two_streams():
     for d in a:
         assert torch.equal(d, held[1])
     mica.mica_sync()
+
+
+def peaked(rows, vocab, gap, dtype, seed=0):
+    """Rows with one likely token, a target `gap` below it, and the others so far below that they add nothing: (logits,
+    targets, entropies in float64)."""
+    g = gen(seed)
+    z = -150.0 - torch.rand((rows, vocab), generator=g, device="cuda")
+    likely = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    y = (likely + torch.randint(1, vocab, (rows,), generator=g, device="cuda")) % vocab
+    at = torch.arange(rows, device="cuda")
+    z[at, likely] = 20.0
+    z[at, y] = 20.0 - gap
+    z = z.to(dtype)
+    return z, y, reference(z, y)[1]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,vocab", [(12, 1009), (9, 50257), (320, 16411)])  # the row kernel, clusters of it, the ring
+def test_entropy_of_confident_rows(rows, vocab, dtype):
+    """An unlikely target leaves the entropy its digits, and above 0. The row's sum is 1 + w, w = e^-gap (the other tokens'
+    weights are under e^-150): one rounding, u, and log of it another. The moment is w gap: the exponent of w is off by
+    gap / ln 2 of some u, the power of two by 4 u, the products and joins by 12 u more."""
+    for gap in (1.0, 8.0, 15.0, 20.5, 25.0, 30.0, 41.0, 60.0):
+        z, y, want = peaked(rows, vocab, gap, dtype, seed=int(gap))
+        lp, h = mica.mica_token_logps(z, y, entropy=True)
+        assert (h >= 0).all(), (gap, float(h.min()))
+        close(h, want, 2 * U + (2 * gap + 16) * U * want)
+        close(lp, reference(z, y)[0], (2 * gap + 16) * U * (1 + gap))
+        other = (y + 1) % vocab  # (an even less likely target)
+        close(mica.mica_token_logps(z, other, entropy=True)[1], want, 2 * U + (2 * gap + 16) * U * want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,vocab", [(40, 1000), (11, 50257), (330, 20011)])
+def test_entropy_does_not_depend_on_the_target(rows, vocab, dtype):
+    """The same rows with likely and unlikely targets. An entropy is log(sum) plus the mean of -x: the sum is off by
+    rel(vocab), and both sides of the mean by as much again and by some 8 u, so by rel(vocab) * (1 + 2 h) + 8 u h."""
+    z, y = make(rows, vocab, dtype, seed=vocab, skip=0.0)
+    want = reference(z, y)[1]
+    for target in (y, z.float().argmin(1), z.float().argmax(1)):
+        h = mica.mica_token_logps(z, target, entropy=True)[1]
+        close(h, want, rel(vocab) * (1 + 2 * want) + 8 * U * want)
