@@ -805,6 +805,11 @@ struct Sum {
         add(o.hi);
         lo += o.lo;
     }
+    // the sum over n, to as many bits: what hi / n rounds away is exactly a float32 times 1 / n
+    __device__ __forceinline__ Sum over(float n) const {
+        const float q = hi / n;
+        return Sum{q, (fmaf(-q, n, hi) + lo) / n};
+    }
     __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
 };
 
@@ -859,8 +864,9 @@ __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log
 __device__ __forceinline__ int64_t clamp_row(int64_t x, int64_t rows) { return x < 0 ? 0 : x > rows ? rows : x; }
 
 // One CTA. Teams of warps sum the sequences (as many teams as sequences, at most one a warp); then the threads take the
-// pairs' losses and slopes; then the teams write their sequences' coefficients. sums[s]: a sequence's sum, then its rows'
-// coefficient.
+// pairs' losses and slopes; then the teams write their sequences' coefficients. sums[s] and sums[2 n + s], n sequences: a
+// sequence's sum (a pair's difference may be far smaller than its sums, and is rounded once), and sums[n + s], 1 over what
+// that was divided by; then sums[s]: its rows' coefficient.
 __global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTerms P, const float* logps,
                                                             const float* rest, float* sums, float* loss, float* rewards,
                                                             float* coef) {
@@ -904,16 +910,20 @@ __global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTer
                 d.add(part[warp + w]);
                 scored += count[warp + w];
             }
-            const float share = P.length_norm ? 1.0f / (float)(scored > 0 ? scored : 1) : 1.0f;
-            sums[s] = P.length_norm ? d.value() / (float)(scored > 0 ? scored : 1) : d.value();
-            sums[n + s] = share;
-            if (rewards) rewards[s] = P.beta * sums[s];
+            const float by = P.length_norm && scored > 0 ? (float)scored : 1.0f;
+            if (P.length_norm) d = d.over(by);
+            sums[s] = d.hi;
+            sums[n + s] = 1.0f / by;
+            sums[2 * n + s] = d.lo;
+            if (rewards) rewards[s] = P.beta * d.value();
         }
     }
     __syncthreads();
     Sum mine{};
     for (int p = threadIdx.x; p < P.pairs; p += kSumThreads) {
-        const float d = sums[2 * p] - sums[2 * p + 1], h = P.beta * d;
+        Sum apart{sums[2 * p], sums[2 * n + 2 * p]};
+        apart.add(Sum{-sums[2 * p + 1], -sums[2 * n + 2 * p + 1]});
+        const float d = apart.value(), h = P.beta * d;
         float l, slope;  // the pair's loss and its derivative by d
         if (P.kind == MICA_PREF_SIGMOID) {
             l = (1.0f - P.smoothing) * softplus(-h) + (P.smoothing > 0.0f ? P.smoothing * softplus(h) : 0.0f);

@@ -57,7 +57,7 @@ struct PairTerms {
     float beta, smoothing;
     float grad_factor;  // grad_scale / (pairs * temperature)
 };
-// loss, rewards (or null) and, where coef is not null, each row's coefficient, from the logps and their rests; sums: 4 * pairs
+// loss, rewards (or null) and, where coef is not null, each row's coefficient, from the logps and their rests; sums: 6 * pairs
 // floats of workspace
 int launch_pairs(const LogitRows& L, const PairTerms& P, const float* logps, const float* rest, float* sums, float* loss,
                  float* rewards, float* coef, void* stream);

@@ -202,10 +202,10 @@ extern "C" mica_status mica_token_logps_grad(const mica_logits* z, const float* 
                         "log-probabilities' gradient launch");
 }
 
-// workspace: two floats per sequence | a RowStat, the rest of a log-probability and a coefficient per row
+// workspace: three floats per sequence | a RowStat, the rest of a log-probability and a coefficient per row
 extern "C" int64_t mica_preference_workspace(int64_t rows, int32_t pairs) {
     if (rows < 0 || rows > MICA_MAX_ROWS || pairs < 0 || pairs > (1 << 24)) return 0;
-    return (int64_t)((size_t)pairs * 4 * sizeof(float) + round16((size_t)rows * (sizeof(RowStat) + 2 * sizeof(float))));
+    return (int64_t)((size_t)pairs * 6 * sizeof(float) + round16((size_t)rows * (sizeof(RowStat) + 2 * sizeof(float))));
 }
 
 extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t* cu_seqlens, int32_t pairs,
@@ -244,7 +244,7 @@ extern "C" mica_status mica_preference_loss(const mica_logits* z, const int32_t*
     MICA_TRY(b.disjoint());
 
     float* sums = static_cast<float*>(workspace);
-    RowStat* stat = reinterpret_cast<RowStat*>(sums + 4 * (size_t)pairs);
+    RowStat* stat = reinterpret_cast<RowStat*>(sums + 6 * (size_t)pairs);
     float* rest = reinterpret_cast<float*>(stat + z->rows);
     float* coef = rest + z->rows;
     const PairTerms P{cu_seqlens, ref_logps, pairs, hp->kind, (hp->flags & MICA_PREF_LENGTH_NORM) != 0,

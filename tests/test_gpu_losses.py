@@ -561,3 +561,29 @@ def test_entropy_does_not_depend_on_the_target(rows, vocab, dtype):
     for target in (y, z.float().argmin(1), z.float().argmax(1)):
         h = mica.mica_token_logps(z, target, entropy=True)[1]
         close(h, want, rel(vocab) * (1 + 2 * want) + 8 * U * want)
+
+
+@pytest.mark.parametrize("length_norm", [False, True])
+def test_long_sequences_that_nearly_cancel(length_norm):
+    """Two long sequences alike but for one row, and no reference policy: the sums are some -3e4, of which float32 has 2e-3,
+    and their difference that of one row. The rows alike cancel exactly, so what may be off is the one row's two
+    log-probabilities, and 2^-40 of the sums."""
+    n, vocab, beta = 1500, 64, 0.5
+    g = gen(11)
+    z = torch.randn((n, vocab), generator=g, device="cuda")
+    y = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    z[torch.arange(n, device="cuda"), y] -= 15.0
+    z, y = torch.cat([z, z]), torch.cat([y, y])
+    z[n + 700, y[700]] += 0.37
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    r = mica.mica_preference_loss(z, y, cu, beta=beta, kind="ipo", length_norm=length_norm)
+    lp, _, p = reference(z, y)
+    share = 1.0 / n if length_norm else 1.0
+    gap = ((lp[700] - lp[n + 700]) * share - 0.5 / beta).item()
+    lp_tol = 2 * (rel(vocab) + 6 * U * 25 + 64 * U) * share + 2.0 ** -40 * 3e4 * share
+    assert abs(lp[:n].sum().item()) > 2e4
+    close(r.loss, torch.tensor([gap * gap], dtype=torch.float64, device="cuda"), 2 * abs(gap) * lp_tol + 4 * U * gap * gap)
+    k = torch.cat([torch.full((n,), 2 * gap * share), torch.full((n,), -2 * gap * share)]).double().cuda()
+    close_grad(r.dlogits, grad_of(p, y, k), p, k, vocab, torch.full_like(k, 2 * lp_tol * share) + 8 * U * k.abs())
+    # the difference of the gradient's two coefficients of a row alike in both is exactly twice the one
+    assert torch.equal(r.dlogits[:700], -r.dlogits[n:n + 700])
