@@ -777,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_grad_ke
     const bool same = (reinterpret_cast<uintptr_t>(dz) - reinterpret_cast<uintptr_t>(z)) % 16 == 0;
     const int64_t y = target_of(L, row);
     const RowVectors g = row_vectors(z, L.vocab);
-    const float c = y < 0 ? 0.0f : y < L.vocab ? coef[row] : NAN;
-    if (c == 0.0f) {
+    const float given = y < 0 ? 0.0f : coef[row], c = y < L.vocab ? given : NAN;
+    if (given == 0.0f) {  // (a row in no sequence, whatever its target)
         zero_row<T, kThreads>(g, L.vocab, dz, same);
         return;
     }

@@ -46,7 +46,8 @@ extern "C" {
  * x = z / temperature and the target y = targets[t]:  logp = x[y] - log sum_j exp(x[j]).
  *   - target < 0: the row does not count. It is not read; its log-probability and entropy are 0, and its gradient
  *     row is zeros, whatever it holds.
- *   - target >= vocab: the log-probability and the row's gradient are NaN (nothing out of range is read).
+ *   - target >= vocab: the log-probability is NaN (nothing out of range is read), and so is the row's gradient unless
+ *     its coefficient is 0.
  *   - a logit of -inf is a banned token (probability 0); a row with nothing else gives NaN, as 0/0 does.
  *   - ld may be anything >= 0 (0: every row the same) as long as the matrix is only read.
  */
@@ -98,7 +99,7 @@ typedef struct {
  * of logp - ref_logps over its scored rows (target >= 0); one without such rows has the sum 0. ref_logps: [rows], the
  * reference policy's log-probabilities (mica_token_logps), or NULL for zeros; those of rows that do not count are not
  * read. cu_seqlens: 2 * pairs + 1 device int32, non-decreasing; bounds outside [0, rows] are clamped to it and a
- * sequence that ends before it starts is empty. Rows in no sequence get zero gradients.
+ * sequence that ends before it starts is empty. Rows in no sequence get zero gradients, whatever their targets.
  *   *loss     = the mean over pairs (0 when there are none)
  *   rewards   [2 * pairs]: beta times the sequences' sums, or NULL
  *   logps     [rows]: the policy's log-probabilities

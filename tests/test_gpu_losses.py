@@ -587,3 +587,18 @@ def test_long_sequences_that_nearly_cancel(length_norm):
     close_grad(r.dlogits, grad_of(p, y, k), p, k, vocab, torch.full_like(k, 2 * lp_tol * share) + 8 * U * k.abs())
     # the difference of the gradient's two coefficients of a row alike in both is exactly twice the one
     assert torch.equal(r.dlogits[:700], -r.dlogits[n:n + 700])
+
+
+@pytest.mark.parametrize("rows,vocab", [(9, 50), (9, 50257), (310, 33001)])  # few short rows, few long ones, many
+def test_targets_past_the_vocabulary_in_no_sequence(rows, vocab):
+    """A row in no sequence gets zeros, whatever its target; one in a sequence makes its pair's loss and gradient NaN."""
+    z, y = make(rows, vocab, torch.bfloat16, seed=vocab, skip=0.0)
+    y[rows - 1] = vocab
+    cu = torch.tensor([1, 3, 4, 6, 8], dtype=torch.int32, device="cuda")
+    r = mica.mica_preference_loss(z, y, cu)
+    assert r.logps[rows - 1].isnan() and r.loss.isfinite().all()
+    assert not r.dlogits[0].any() and not r.dlogits[8:].any() and r.dlogits[1:8].any(1).all()
+    y[2] = vocab + 7
+    r = mica.mica_preference_loss(z, y, cu)
+    assert r.loss.isnan().all() and r.dlogits[1:4].isnan().any(1).all() and r.dlogits[2].isnan().all()
+    assert r.dlogits[4:8].isfinite().all() and not r.dlogits[0].any() and not r.dlogits[8:].any()
