@@ -231,16 +231,26 @@ struct RowGrad {
     int at;  // the target, or -16
 };
 
+// The weights' exponents of two elements, counted from -away, as the statistics were taken with. (One float for log2(e) /
+// temperature would put the weight of a row's likeliest token, and so 1 - p, off by up to 2^-24 of its exponent against the
+// sum that has it; the rounding to 16 bits hides that, so there one product less is taken.)
+template <typename T>
+__device__ __forceinline__ Two exponents(const LogitRows& L, Two z, Two away) {
+    const Two d = z + away;
+    if constexpr (sizeof(T) == 4) return fma2(d, two(L.a_hi, L.a_hi), d * two(L.a_lo, L.a_lo));
+    else return d * two(L.a, L.a);
+}
+
 // One vector of the gradient c * ((j == y) - p), from the element j0 on.
 template <typename T>
 __device__ __forceinline__ void grad_values(const LogitRows& L, const Vec<T>& v, const RowGrad& q, int j0,
                                             float (&d)[Vec<T>::n]) {
     constexpr int n = Vec<T>::n;
     const float k = -q.c * q.inv;
-    const Two o = two(-q.o, -q.o), a = two(L.a, L.a), kk = two(k, k);
+    const Two away = two(-q.o, -q.o), kk = two(k, k);
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
-        const float2 x = each((v.pair(i) + o) * a);
+        const float2 x = each(exponents<T>(L, v.pair(i), away));
         const float2 e = each(two(exp2_fast(x.x), exp2_fast(x.y)) * kk);
         d[2 * i] = e.x;
         d[2 * i + 1] = e.y;
@@ -248,7 +258,7 @@ __device__ __forceinline__ void grad_values(const LogitRows& L, const Vec<T>& v,
     if ((unsigned)(q.at - j0) < (unsigned)n) {
 #pragma unroll
         for (int i = 0; i < n; ++i)
-            if (j0 + i == q.at) d[i] = q.c * (1.0f - q.inv * exp2_fast((v.get(i) - q.o) * L.a));
+            if (j0 + i == q.at) d[i] = q.c * (1.0f - q.inv * exp2_fast(each(exponents<T>(L, two(v.get(i), 0.0f), away)).x));
     }
 }
 

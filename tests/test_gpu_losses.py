@@ -602,3 +602,25 @@ def test_targets_past_the_vocabulary_in_no_sequence(rows, vocab):
     r = mica.mica_preference_loss(z, y, cu)
     assert r.loss.isnan().all() and r.dlogits[1:4].isnan().any(1).all() and r.dlogits[2].isnan().all()
     assert r.dlogits[4:8].isfinite().all() and not r.dlogits[0].any() and not r.dlogits[8:].any()
+
+
+@pytest.mark.parametrize("rows,vocab", [(12, 1009), (9, 50257), (320, 16411), (310, 41003)])
+def test_float32_gradient_of_confident_rows(rows, vocab):
+    """The softmax of a row's likeliest token is its weight's share of the sum that has that weight in it, so it is off by a
+    few u however far the target is: the sum's rounding, the reciprocal's and three products'. (The row kernel, clusters of
+    it, and both rings.)"""
+    for t in (1.0, 0.7):
+        for gap in (3.0, 11.0, 20.0, 26.5):
+            z, y, _ = peaked(rows, vocab, gap, torch.float32, seed=int(gap))
+            p = reference(z, y, t)[2]
+            c = torch.ones(rows, device="cuda")
+            d = mica.mica_token_logps_grad(z, y, c, temperature=t)
+            close(d, grad_of(p, y, c.double() / t), (8 * U * p + 8 * U) / t + 1e-30)
+            likely = z.argmax(1, keepdim=True)
+            top = d.gather(1, likely).double() * t
+            close(top, -p.gather(1, likely), 8 * U * torch.ones_like(top))
+            n = rows // 2
+            cu = torch.tensor([0, n, rows], dtype=torch.int32, device="cuda")
+            r = mica.mica_preference_loss(z, y, cu, beta=0.1, kind="ipo", temperature=t)
+            k = r.dlogits.double().gather(1, y[:, None]) / (1.0 - p.gather(1, y[:, None]))  # the rows' coefficients
+            close(r.dlogits.gather(1, likely).double() / k, -p.gather(1, likely), 16 * U * torch.ones_like(top))
