@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "host.h"
 #include "mica_train.h"
@@ -119,10 +120,11 @@ mica_status check_logits(const mica_logits* z, LogitRows* L) {
     const double a = 1.4426950408889634074 / z->temperature;
     float a_hi = (float)a;  // the largest float32 below a, so that the rest is positive
     if (a_hi >= a) a_hi = std::nextafter(a_hi, 0.0f);
+    const float a_lo = std::fmax((float)(a - a_hi), std::numeric_limits<float>::denorm_min());
     MICA_TRY(check_extent(z->rows, z->vocab, 1, "logits"));
     MICA_TRY(check_stride(z->ld, 0, z->rows, z->vocab, "logits"));
     *L = LogitRows{z->logits, z->targets, z->rows, z->ld, (int32_t)z->vocab, z->dtype, z->target_bytes == 8,
-                   (float)(1.0 / z->temperature), 1.0 / z->temperature, (float)a, a_hi, (float)(a - a_hi)};
+                   (float)(1.0 / z->temperature), 1.0 / z->temperature, (float)a, a_hi, a_lo};
     return MICA_OK;
 }
 

@@ -624,3 +624,32 @@ def test_float32_gradient_of_confident_rows(rows, vocab):
             r = mica.mica_preference_loss(z, y, cu, beta=0.1, kind="ipo", temperature=t)
             k = r.dlogits.double().gather(1, y[:, None]) / (1.0 - p.gather(1, y[:, None]))  # the rows' coefficients
             close(r.dlogits.gather(1, likely).double() / k, -p.gather(1, likely), 16 * U * torch.ones_like(top))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_banned_tokens_at_extreme_temperatures(dtype):
+    """log2(e) / temperature in two floats, the second of which may be below float32's least: a banned token's weight is 0
+    at any temperature."""
+    near = []
+    a = torch.tensor(1.5e-30, dtype=torch.float32)
+    while len(near) < 3:  # temperatures whose quotient is a little above a float32
+        a = torch.nextafter(a, torch.tensor(1.0))
+        t = 1.4426950408889634074 / a.item()
+        for _ in range(4):
+            rest = 1.4426950408889634074 / t - a.item()
+            if 0 < rest < 2.0 ** -150 and t <= 1e30:
+                near.append(t)
+                break
+            t = math.nextafter(t, 0.0)
+    vocab = 101
+    for t in near + [1e30, 1e-30, 1e20, 1e-20]:
+        z, y = make(7, vocab, dtype, seed=3, skip=0.0)
+        z[:, 60:] = -math.inf
+        y %= 60
+        z[torch.arange(7), y] = 40.0  # (the likeliest by far where the temperature is low)
+        lp, h = mica.mica_token_logps(z, y, temperature=t, entropy=True)
+        want, want_h, p = reference(z, y, t)
+        close(lp, want, rel(vocab) + 6 * U * want.abs() + 64 * U)
+        close(h, want_h, 30 * rel(vocab))
+        d = mica.mica_token_logps_grad(z, y, torch.full((7,), min(t, 1.0), device="cuda"), temperature=t)
+        assert not d.isnan().any() and not d[:, 60:].any()
