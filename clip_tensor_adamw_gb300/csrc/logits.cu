@@ -1,6 +1,7 @@
 // The losses over logits: log-probabilities, preference and policy losses, and the gradient of the logits.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -526,6 +527,7 @@ constexpr int64_t kRingRows = 300;
 
 // Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_logits_status).
 __device__ unsigned int g_logits_status;
+std::atomic<bool> g_ring_launched{false};  // in this process; until then nothing can have set it
 enum : unsigned int { kStatusRowProducer = 0x20u, kStatusRowConsumer = 0x40u };
 
 // A row handed to the consumers; row < 0: no more.
@@ -1010,6 +1012,7 @@ cudaError_t launch_ring(const LogitRows& L, const PolicyTerms& P, const RowOut& 
     auto go = [&](auto shape) {
         using S = decltype(shape);
         const auto kernel = ring_kernel<T, kKind, kStream, S>;
+        g_ring_launched = true;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
         return e != cudaSuccess ? e : launch_clusters(kernel, L.rows, 1, S::threads, S::bytes, stream, L, P, out);
     };
@@ -1079,6 +1082,8 @@ int launch_pairs(const LogitRows& L, const PairTerms& P, const float* logps, con
 }
 
 int read_logits_status(unsigned int* status) {
+    *status = 0;
+    if (!g_ring_launched) return (int)cudaSuccess;
     unsigned int v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_logits_status, sizeof v);
     if (e != cudaSuccess) return (int)e;

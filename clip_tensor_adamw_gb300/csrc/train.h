@@ -80,7 +80,8 @@ struct Wgrad {
     void* dw;
     int64_t ld_dw;
 };
-// The status words of these kernels' bounded waits, as read_device_status (plan.h).
+// The status words of these kernels' bounded waits, as read_device_status (plan.h); 0, and nothing is copied, in a process
+// that has launched none of them.
 int read_logits_status(unsigned int* status);
 int read_wgrad_status(unsigned int* status);
 

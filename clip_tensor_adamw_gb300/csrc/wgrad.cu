@@ -26,6 +26,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "packed.cuh"
@@ -51,6 +52,7 @@ constexpr int kSharedBytes = 1024 + kDepths * (2 * kOperandBytes + kCodeBytes);
 
 // Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_wgrad_status).
 __device__ unsigned int g_wgrad_status;
+std::atomic<bool> g_wgrad_launched{false};  // in this process; until then nothing can have set it
 enum : unsigned int { kStatusWgrad = 0x80u };
 
 // How the work is dealt: `whole` tiles one after another, then `split` tiles in `parts` along the tokens.
@@ -575,6 +577,7 @@ cudaError_t launch_typed(const Wgrad& w, const Deal& d, float* partial, void* st
             !encode(&dy, type, w.dy, w.n, w.x.rows, w.ld_dy * 2, 64, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
         const auto kernel = wgrad_kernel<T, O>;
+        g_wgrad_launched = true;
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
         const int all = pieces_of(d), pairs = all < d.pairs ? all : d.pairs;
         if (e == cudaSuccess)
@@ -618,6 +621,8 @@ int launch_wgrad(const Wgrad& in, void* workspace, int sms, void* stream) {
 }
 
 int read_wgrad_status(unsigned int* status) {
+    *status = 0;
+    if (!g_wgrad_launched) return (int)cudaSuccess;
     unsigned int v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_wgrad_status, sizeof v);
     if (e != cudaSuccess) return (int)e;

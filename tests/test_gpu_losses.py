@@ -653,3 +653,38 @@ def test_banned_tokens_at_extreme_temperatures(dtype):
         close(h, want_h, 30 * rel(vocab))
         d = mica.mica_token_logps_grad(z, y, torch.full((7,), min(t, 1.0), device="cuda"), temperature=t)
         assert not d.isnan().any() and not d[:, 60:].any()
+
+
+def test_sync_reads_no_status_of_kernels_that_never_ran():
+    """mica_sync copies back the status words of kernels with bounded waits: those of the operators before the step only
+    in a process that has launched them."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from torch.profiler import ProfilerActivity, profile
+import clip_tensor_adamw_gb300 as mica
+g = mica.TensorList([torch.ones(5000, device="cuda")])
+z = torch.randn(400, 20000, device="cuda")
+y = torch.zeros(400, dtype=torch.int64, device="cuda")
+mica.mica_clip_grad_norms(g, 1.0)
+mica.mica_sync()
+def copies():
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as p:
+        mica.mica_sync()
+        torch.cuda.synchronize()
+    return sum("memcpy" in e.name.lower() and "dtoh" in e.name.lower().replace(" ", "") for e in p.events())
+copies()
+before = copies()
+mica.mica_token_logps(z, y)
+print("copies", before, copies())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0, out.stderr
+    before, after = map(int, out.stdout.split("copies")[1].split())
+    if after == 0:
+        pytest.skip("no record of copies on this machine")
+    assert (before, after) == (2, 3)
