@@ -627,16 +627,16 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
         float c;
         head(row, &y, &c);
         ask_next_row(ring);
-        bool ok = true;
-        for (uint32_t asked = 0; ok; asked ^= 1) {
-            if (!mbar_wait(&ring.asked, asked)) {
-                ok = false;
-                break;
-            }
+        bool ok = true, asking = true;  // asking: an answer is on its way
+        uint32_t asked = 0;             // its phase
+        while (ok) {
+            if (!(ok = mbar_wait(&ring.asked, asked))) break;
+            asked ^= 1;
             const int64_t next = row_of(next_row(ring));
             int64_t next_y = -1;
             float next_c = 0.0f;
-            if (next >= 0) {
+            asking = next >= 0;
+            if (asking) {
                 ask_next_row(ring);
                 head(next, &next_y, &next_c);  // (arrives while this row's copies are queued)
             }
@@ -671,8 +671,9 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             }
         }
         if (!ok) atomicOr(&g_logits_status, kStatusRowProducer);
-        // no copy is left in flight when the CTA ends
+        // no copy is left in flight when the CTA ends, and no answer (after a wait that gave up)
         drain(ring.full, turn, queued);
+        if (asking) mbar_wait(&ring.asked, asked);
         return;
     }
 
