@@ -688,3 +688,48 @@ print("copies", before, copies())
     if after == 0:
         pytest.skip("no record of copies on this machine")
     assert (before, after) == (2, 3)
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,ld,offset", [
+    (torch.bfloat16, 320, 50257, 50257, 0), (torch.float16, 310, 50257, 50260, 3),      # unaligned 16-bit rows over 64 KB
+    (torch.bfloat16, 305, 90001, 90001, 1), (torch.float16, 304, 98304, 98304, 0),      # rows over 160 KB
+    (torch.float32, 303, 41003, 41003, 0), (torch.float32, 304, 45056, 45060, 2)], ids=str)
+def test_gradients_of_many_longer_rows(dtype, rows, vocab, ld, offset):
+    """What test_many_long_rows has no rows long enough for: the gradient's ring over long rows and over unaligned ones."""
+    z, y = make(rows, vocab, dtype, seed=vocab, ld=ld, offset=offset)
+    y[50:90] = -1
+    z[7, 10:] = -math.inf
+    y[7] = 4
+    c = torch.randn(rows, generator=gen(5), device="cuda")
+    c[::5] = 0.0
+    k = torch.where(y >= 0, c.double() / 0.9, 0.0)
+    p = reference(z, y, 0.9)[2]
+    d = mica.mica_token_logps_grad(z, y, c, temperature=0.9)
+    close_grad(d, grad_of(p, y, k), p, k, vocab)
+    apart = torch.full((rows * (vocab + 1) + 8,), 7.0, dtype=dtype, device="cuda")
+    out = apart[1:].as_strided((rows, vocab), (vocab + 1, 1))
+    mica.mica_token_logps_grad(z, y, c, temperature=0.9, out=out)
+    assert torch.equal(out, d)
+    out.fill_(7.0)
+    assert (apart == 7.0).all()
+    del apart, out
+    lp64, _, p = reference(z, y)
+    lp_tol = float((rel(vocab) + 6 * U * lp64.abs() + 64 * U).max())
+    old = (lp64 + 0.05 * c).float()
+    adv = torch.randn(rows, generator=gen(9), device="cuda")
+    q = mica.mica_policy_loss(z, y, old, adv, denom=100.0, clip_low=1.0, clip_high=math.inf)
+    k = torch.where(y >= 0, -torch.exp(lp64 - old.double()) * adv / 100, 0.0)
+    c_tol = k.abs() * (2 * lp_tol + 16 * U * (1 + old.abs()))
+    close_grad(q.dlogits, grad_of(p, y, k), p, k, vocab, c_tol)
+    cu = torch.arange(0, rows + 1, 60, dtype=torch.int32, device="cuda")[:5].clone()
+    r = mica.mica_preference_loss(z, y, cu, old, beta=0.1)
+    loss, rewards, dlp = preference_reference(lp64, y >= 0, cu.tolist(), old.double(), 0.1, "sigmoid", 0.0, False)
+    close(r.rewards, rewards, 0.1 * 60 * lp_tol + 2 * U * rewards.abs())
+    c_tol = torch.where(y >= 0, 120 * lp_tol * 0.0025 / 2 + 8 * U * dlp.abs(), 0.0)
+    close_grad(r.dlogits, grad_of(p, y, dlp), p, dlp, vocab, c_tol)
+    again = z.clone(memory_format=torch.preserve_format) if ld == vocab else None
+    assert torch.equal(mica.mica_policy_loss(z, y, old, adv, denom=100.0, clip_low=1.0, clip_high=math.inf,
+                                             out=z).dlogits, q.dlogits)
+    if again is not None and offset == 0:
+        assert torch.equal(mica.mica_preference_loss(again, y, cu, old, beta=0.1, out=again).dlogits, r.dlogits)
+    mica.mica_sync()
