@@ -10,10 +10,6 @@
 namespace mica {
 namespace {
 
-using F32 = float;
-using F16 = __half;
-using BF16 = __nv_bfloat16;
-
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -27,9 +23,15 @@ __device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// 2^x by the hardware's approximation, off by some 2^-22 of its value.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Two float32 in one register pair: additions and products of both in one instruction, each rounded as it would be alone.
-// What bounds a streaming kernel of
-// 16-bit elements next to memory is the instructions that it issues.
+// What bounds a streaming kernel of 16-bit elements next to memory is the instructions that it issues.
 struct Two {
     uint64_t v;
 };

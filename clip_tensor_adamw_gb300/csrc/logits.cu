@@ -24,12 +24,6 @@ constexpr int64_t kFewCtas = 608;  // (100 rows of 50,257 logits: 16.3 us a call
 constexpr double kLn2 = 0.693147180559945309;
 constexpr float kFarBelow = -1000.0f;  // an exponent of 2 whose power is 0, and finite (0 * it is 0)
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // ----------------------------------------------------------------------------------------------------------------------
 // rows
 // ----------------------------------------------------------------------------------------------------------------------

@@ -50,17 +50,12 @@ __device__ __forceinline__ float code_value(uint32_t flipped, int i) {
 
 // 1 / (1 + 2^t), from the hardware's power of two and reciprocal (some 2^-22 of its value, and |t| 2^-24 in the tail): the
 // logistic function of w for t = -log2(e) w
-__device__ __forceinline__ float fast_exp2(float t) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    return e;
-}
 __device__ __forceinline__ float fast_reciprocal(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float logistic_of(float t) { return fast_reciprocal(1.0f + fast_exp2(t)); }
+__device__ __forceinline__ float logistic_of(float t) { return fast_reciprocal(1.0f + exp2_fast(t)); }
 
 constexpr float kLog2E = 1.44269504088896341f;
 constexpr float kGelu1 = 2.0f * 0.797884560802865356f, kGelu3 = kGelu1 * 0.044715f;  // 2 u = kGelu1 x + kGelu3 x^3
@@ -99,7 +94,7 @@ __device__ __forceinline__ Two act_pair(Two x) {
         if constexpr (kAct == MICA_ACT_GELU_TANH)
             t = fma2(two(-kLog2E * kGelu3, -kLog2E * kGelu3), x * x, two(-kLog2E * kGelu1, -kLog2E * kGelu1));
         const float2 e = each(x * t);
-        const float2 d = each(two(fast_exp2(e.x), fast_exp2(e.y)) + two(1.0f, 1.0f));
+        const float2 d = each(two(exp2_fast(e.x), exp2_fast(e.y)) + two(1.0f, 1.0f));
         return x * two(fast_reciprocal(d.x), fast_reciprocal(d.y));
     } else {
         const float2 v = each(x);

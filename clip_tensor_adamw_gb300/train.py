@@ -281,7 +281,7 @@ class PackedActivation:
         return (self.codes.shape[0], self.cols)
 
 
-def _act(act: str, gated: bool, cols: int) -> int:
+def _act(act: str) -> int:
     if act not in _ACTS:
         raise ValueError(f"act {act!r} is none of {sorted(_ACTS)}")
     return _ACTS[act]
@@ -294,7 +294,7 @@ def mica_act_pack(x: torch.Tensor, act: str = "none", *, gated: bool = False, pa
     the columns through the function and multiplies it by the second. ``packed`` and ``out`` are filled when given."""
     code, ld = _type(x, "x"), _matrix(x, "x")
     rows, cols = x.shape
-    kind = _act(act, gated, cols)
+    kind = _act(act)
     with _On(stream, x.device) as s:
         p = PackedActivation.empty(rows, cols, x.dtype, x.device) if packed is None else packed
         if p.shape != (rows, cols) or p.dtype != x.dtype:
@@ -320,7 +320,7 @@ def mica_act_grad(packed: PackedActivation, dy: torch.Tensor, act: str, *, gated
     may be ``dy`` itself when not gated."""
     code, ld = _type(dy, "dy"), _matrix(dy, "dy")
     rows, cols = packed.shape
-    kind = _act(act, gated, cols)
+    kind = _act(act)
     if tuple(dy.shape) != (rows, cols // 2 if gated else cols):
         raise ValueError(f"dy must have the shape of the function's output, not {tuple(dy.shape)}")
     with _On(stream, dy.device) as s:
