@@ -23,6 +23,9 @@ constexpr int kBatch = 4;        // vectors of a thread in flight
 constexpr int64_t kFewCtas = 608;  // (100 rows of 50,257 logits: 16.3 us a call with 608, 19.2 with 304, 17.1 with 1,216)
 constexpr double kLn2 = 0.693147180559945309;
 constexpr float kFarBelow = -1000.0f;  // an exponent of 2 whose power is 0, and finite (0 * it is 0)
+// How much the hardware's 2^x is low on average, of its value, for x < -1 (-2e-8 from there to 0, +3e-8 above 1, exact for
+// whole x): every log-probability of a sequence would be as much too high, and a sequence's sum has hundreds.
+constexpr double kLow = 5.0e-8;
 
 // ----------------------------------------------------------------------------------------------------------------------
 // rows
@@ -42,7 +45,7 @@ constexpr float kFarBelow = -1000.0f;  // an exponent of 2 whose power is 0, and
 // Vectors start at 16-byte addresses, whatever the row's alignment (an odd vocabulary puts each row elsewhere): the first
 // and the last may reach outside the row, and are then read and written element by element, the rest as -inf.
 
-// z[j] - max in units of log2, 2^that being the weight: a = log2(e) / temperature split in two floats, since the relative
+// z[j] - origin in units of log2, 2^that being the weight: a = log2(e) / temperature split in two floats, since the relative
 // error of one alone (up to 2^-24) would shift every log-probability of a sequence the same way. a_lo > 0 (the host sees
 // to it), so that a banned token's -inf stays -inf.
 __device__ __forceinline__ float exponent(const LogitRows& L, float z, float origin) {
@@ -314,10 +317,17 @@ __device__ __forceinline__ void sum_weights(const LogitRows& L, const Vec<T> (&v
     u = w.x + w.y;
 }
 
+// 2^x for the factor of a part that is counted anew, x <= 0: from the nearest integer, whose power the hardware has exactly,
+// and what remains of x, where its error is 1e-8 on average (see kLow) and not the same way for every part.
+__device__ __forceinline__ float exp2_factor(float x) {
+    const float i = rintf(x);
+    return exp2_fast(i) * exp2_fast(x - i);
+}
+
 // Counts a part from `m` instead, a larger origin.
 template <bool kMoment>
 __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
-    const float x = fmaxf(exponent(L, r.m, m), kFarBelow), f = exp2_fast(x);
+    const float x = fmaxf(exponent(L, r.m, m), kFarBelow), f = exp2_factor(x);
     if (kMoment) r.u = f * fmaf(r.s, x, r.u);
     r.s *= f;
     r.m = m;
@@ -325,10 +335,11 @@ __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
 
 // Counts a part from the largest of some vectors that it is about to take, where that is larger. Log-probabilities with
 // entropies are counted so throughout: an entropy is log s, which is then not negative, plus the mean of -x, which is not
-// either. Counted from a target far below the maximum it would be the difference of two numbers as large as that distance, in
-// float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons take some 4% of the time
-// (8,192 rows of 50,257 bfloat16 logits, of which 6,144 count, with entropies: 104 us, counted from the target 100). Without
-// entropies they are made too, so that the log-probabilities are the same bits; there they take nothing.
+// either. Counted from a target far below the maximum it would be the difference of two numbers as large as that distance,
+// in float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons take some 4% of the time
+// (8,192 rows of 50,257 bfloat16 logits, of which 6,144 count, with entropies: 104 us, counted from the target 100; 117 with
+// the weights counted from the target and the moment from the maximum). Without entropies they are made too, so that the
+// log-probabilities are the same bits; there they take nothing.
 template <bool kMoment, typename T, int kCount>
 __device__ __forceinline__ void count_from_highest(const LogitRows& L, const Vec<T> (&v)[kCount], Running& r) {
     const float m = Vec<T>::max(v);
@@ -361,7 +372,7 @@ template <bool kMoment>
 __device__ __forceinline__ Running join_warp(const LogitRows& L, const Running& p) {
     Running r;
     r.m = warp_max(p.m);
-    const float x = fmaxf(exponent(L, p.m, origin(r.m)), kFarBelow), f = exp2_fast(x);
+    const float x = fmaxf(exponent(L, p.m, origin(r.m)), kFarBelow), f = exp2_factor(x);
     r.s = warp_add(p.s * f);
     r.u = kMoment ? warp_add(f * fmaf(p.s, x, p.u)) : 0.0f;
     return r;
@@ -421,7 +432,7 @@ __device__ __forceinline__ float finish_row(const LogitRows& L, const PolicyTerm
     const float o = origin(r.m);
     if constexpr (kKind == kLogps || kKind == kEntropy) {
         if (head) {
-            const double log_sum = wide_log(r.s);
+            const double log_sum = wide_log(r.s) + kLow * (1.0f - 1.0f / r.s);  // (the largest weight is exactly 1)
             const double lp = y < L.vocab ? ((double)zy - o) * L.wide_inv_t - log_sum : NAN;
             out.logps[row] = (float)lp;
             if (kKind == kLogps && out.rest_logps) out.rest_logps[row] = isfinite(lp) ? (float)(lp - (float)lp) : 0.0f;
@@ -505,8 +516,9 @@ struct RingShape {
     static constexpr int threads = kThreads + 32, stage_bytes = kVectors * 16, bytes = kCount * stage_bytes;
     static constexpr int per_thread = kVectors / kThreads;
 };
-// Each the best of a dozen shapes (the first with weights counted from the target). Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
-// bfloat16 logits, of which 6,144 count: 100 us, 6.2 TB/s; three of 256 threads 104 us, two of 384 120 us, one of 512 178 us).
+// Each the best of a dozen shapes. Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
+// bfloat16 logits, of which 6,144 count, with entropies: 104 us, 5.9 TB/s; while weights were counted from the target, 100 us,
+// three CTAs of 256 threads 104 us, two of 384 120 us, one of 512 178 us).
 using ReadRing = RingShape<192, 1536, 2, 4>;
 // A gradient reads its row again, which has to be in L2 still: of long rows one at a time on an SM (6,144 rows of 131,072:
 // 486 us, 6.2 TB/s, against 535 us with two CTAs and 625 us with three), of others two (6,144 rows of 50,257: 196 us,

@@ -733,3 +733,21 @@ def test_gradients_of_many_longer_rows(dtype, rows, vocab, ld, offset):
     if again is not None and offset == 0:
         assert torch.equal(mica.mica_preference_loss(again, y, cu, old, beta=0.1, out=again).dlogits, r.dlogits)
     mica.mica_sync()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("vocab", [1000, 16411])  # the row kernel, the ring
+def test_log_probabilities_err_to_both_sides(vocab, dtype):
+    """A preference loss adds up a sequence's log-probabilities, so what counts is their error's mean. Rounding one, under 16 in
+    size, is off by 0.29 * 2^-20 on average either way, the mean of 4,000 by 4.4e-9: 5 of those, and 2e-8 for the rest."""
+    rows = 4000
+    z, y = make(rows, vocab, dtype, seed=vocab, skip=0.0)
+    z.mul_(torch.linspace(0.2, 1.0, rows, device="cuda").to(dtype)[:, None])
+    near = z.float().topk(30, 1).indices[torch.arange(rows, device="cuda"), torch.randint(0, 30, (rows,), generator=gen(1),
+                                                                                         device="cuda")]
+    for target in (near, y):
+        want = reference(z, target)[0]
+        fine = want > -16
+        assert fine.sum() > 3000
+        e = (mica.mica_token_logps(z, target).double() - want)[fine]
+        assert abs(e.mean().item()) < 4.2e-8 * math.sqrt(4000 / len(e)), e.mean().item()
