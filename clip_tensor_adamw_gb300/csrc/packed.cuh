@@ -48,14 +48,18 @@ __device__ __forceinline__ float code_value(uint32_t flipped, int i) {
     return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440u | i)) - 8388736.0f;
 }
 
-// 1 / (1 + 2^t), from the hardware's power of two and reciprocal (some 2^-22 of its value, and |t| 2^-24 in the tail): the
-// logistic function of w for t = -log2(e) w
 __device__ __forceinline__ float fast_reciprocal(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float logistic_of(float t) { return fast_reciprocal(1.0f + exp2_fast(t)); }
+// h = 1 / (1 + 2^t), from the hardware's power of two and reciprocal (some 2^-22 of its value, and |t| 2^-24 in the tail): the
+// logistic function of w for t = -log2(e) w; and rest = 1 - h, as 2^t h, since an h near 1 has no digits left of it.
+__device__ __forceinline__ void logistic_of(float t, float& h, float& rest) {
+    const float e = exp2_fast(t);
+    h = fast_reciprocal(1.0f + e);
+    rest = fminf(e, 0x1p100f) * h;  // (an infinite e makes h 0; beyond 2^100 what rest is for is multiplied by h too)
+}
 
 constexpr float kLog2E = 1.44269504088896341f;
 constexpr float kGelu1 = 2.0f * 0.797884560802865356f, kGelu3 = kGelu1 * 0.044715f;  // 2 u = kGelu1 x + kGelu3 x^3
@@ -66,17 +70,20 @@ constexpr float kGelu1 = 2.0f * 0.797884560802865356f, kGelu3 = kGelu1 * 0.04471
 template <int kAct>
 __device__ __forceinline__ void act_of(float x, float& y, float& slope) {
     if constexpr (kAct == MICA_ACT_GELU_TANH) {
-        const float x2 = fminf(x * x, 400.0f), h = logistic_of(x * fmaf(-kLog2E * kGelu3, x2, -kLog2E * kGelu1));
+        const float x2 = fminf(x * x, 400.0f);
+        float h, rest;
+        logistic_of(x * fmaf(-kLog2E * kGelu3, x2, -kLog2E * kGelu1), h, rest);
         y = x * h;
-        slope = fmaf(y * (1.0f - h), fmaf(3.0f * kGelu3, x2, kGelu1), h);
+        slope = fmaf(y * rest, fmaf(3.0f * kGelu3, x2, kGelu1), h);
     } else if constexpr (kAct == MICA_ACT_GELU) {
         const float p = normcdff(x);
         y = x * p;
         slope = fmaf(x * 0.398942280401432678f, expf(-0.5f * x * x), p);
     } else if constexpr (kAct == MICA_ACT_SILU) {
-        const float h = logistic_of(-kLog2E * x);
+        float h, rest;
+        logistic_of(-kLog2E * x, h, rest);
         y = x * h;
-        slope = fmaf(y, 1.0f - h, h);
+        slope = fmaf(y, rest, h);
     } else if constexpr (kAct == MICA_ACT_RELU) {
         y = x > 0.0f ? x : (x <= 0.0f ? 0.0f : x);  // (a NaN stays one)
         slope = x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x);

@@ -167,6 +167,17 @@ def test_grad_by_differences():
         close(got, num, 1e-6 * (1 + v.abs()))
 
 
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_float32_slopes_of_large_inputs(act):
+    """From x = 3 on the slope is h, off by a rounding of 1 + e, two of the reciprocal and one of the sum, plus a term that
+    has 1 - h in it: 0.013 for GELU and 0.15 for SiLU at x = 3, less beyond, off by at most 20 u of itself."""
+    x = torch.linspace(3.0, 12.0, 32 * 40, device="cuda").reshape(40, 32)
+    p = mica.mica_act_pack(x)
+    v = mica.mica_act_unpack(p).double().requires_grad_()
+    want, = torch.autograd.grad(act64(v, act).sum(), v)
+    close(mica.mica_act_grad(p, torch.ones_like(x), act), want, 5 * U + {"gelu_tanh": 0.013, "silu": 0.15}[act] * 20 * U)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("cols,ld,offset", [(100, 100, 1), (100, 128, 0), (96, 97, 3), (1601, 1608, 8), (64, 0, 0)])
 def test_strides(cols, ld, offset, dtype):
