@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             c = finish_row<kKind>(L, P, out, row, y, zy, q, c, threadIdx.x == 0);
         } else {
             const RowStat st = out.stat[row];
-            q = Running{st.zmax, 1.0f / st.inv_sum, 0.0f};
+            q = Running{st.origin, 1.0f / st.inv_sum, 0.0f};
             if (y >= L.vocab) c = NAN;
         }
         if constexpr (kGrad) {
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_grad_ke
         return;
     }
     const RowStat st = stat[row];
-    grad_row<T, kThreads>(L, z, g, RowGrad{origin(st.zmax), c, st.inv_sum, y < L.vocab ? (int)y : -16}, dz, same);
+    grad_row<T, kThreads>(L, z, g, RowGrad{origin(st.origin), c, st.inv_sum, y < L.vocab ? (int)y : -16}, dz, same);
 }
 
 // ----------------------------------------------------------------------------------------------------------------------

@@ -18,13 +18,15 @@ struct LogitRows {
     int32_t wide_targets;  // int64 targets
     float inv_t;           // 1 / temperature
     double wide_inv_t;
-    // log2(e) / temperature, rounded, and as a_hi + a_lo with a_lo > 0: exp(x - max) = 2^((z - zmax) * (a_hi + a_lo))
+    // log2(e) / temperature, rounded, and as a_hi + a_lo with a_lo > 0: exp((z - origin) / temperature) =
+    // 2^((z - origin) * (a_hi + a_lo))
     float a, a_hi, a_lo;
 };
 
-// A row's softmax statistics: the largest logit and 1 / sum exp.
+// A row's softmax statistics: the logit that its weights are counted from (the largest; -inf: nothing but that in the row),
+// and 1 over their sum.
 struct RowStat {
-    float zmax;
+    float origin;
     float inv_sum;
 };
 

@@ -16,10 +16,11 @@
 // sixteen warps, four groups of four that take stages in turn, decode them into the operand. The same warps empty TMEM, a
 // chunk behind. Three more warps load codes, load dy, and issue the products.
 //
-// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 293 us, 1,150 TFLOP/s, the tensor pipe 54% active; without the
+// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 293 to 302 us, 1,130 TFLOP/s, the tensor pipe 54% active; without the
 // decoding it would take some 240 us. A stage moves 96 KB through an SM's shared memory (the products read 48, dy and codes
-// are written with 24, codes read with 8, operands written with 16), 750 clocks' worth against the products' 512. Two
-// groups of eight decoding warps took 11% longer.
+// are written with 24, codes read with 8, operands written with 16), 750 clocks' worth against the products' 512. Beside
+// that, tiles of 256 cover 1,792 features where there are 1,600 (12% more products), and nineteen warps leave a thread 96
+// registers, of which its sums take 64: 92 to 120 bytes are spilled. Two groups of eight decoding warps took 11% longer.
 //
 // Whole tiles are dealt to the pairs in turn; what remains for the last round is split along the tokens so that every pair
 // has a share, whose sums a second kernel joins in a fixed order.

@@ -98,7 +98,7 @@ typedef struct {
  * cu_seqlens[s] .. cu_seqlens[s+1] - 1, pair p is sequences 2p (chosen) and 2p + 1 (rejected). A sequence's sum is that
  * of logp - ref_logps over its scored rows (target >= 0); one without such rows has the sum 0. ref_logps: [rows], the
  * reference policy's log-probabilities (mica_token_logps), or NULL for zeros; those of rows that do not count are not
- * read. cu_seqlens: 2 * pairs + 1 device int32, non-decreasing; bounds outside [0, rows] are clamped to it and a
+ * used. cu_seqlens: 2 * pairs + 1 device int32, non-decreasing; bounds outside [0, rows] are clamped to it and a
  * sequence that ends before it starts is empty. Rows in no sequence get zero gradients, whatever their targets.
  *   *loss     = the mean over pairs (0 when there are none)
  *   rewards   [2 * pairs]: beta times the sequences' sums, or NULL
@@ -133,7 +133,7 @@ typedef struct {
  *           clipped when the clamped product is the smaller
  *   logps   [rows]
  *   dlogits the gradient of grad_scale * loss, as in mica_token_logps_grad; NULL for the loss alone
- * old_logps, advantages, ref_logps and weights are [rows] float32; those of rows that do not count are not read. The
+ * old_logps, advantages, ref_logps and weights are [rows] float32; those of rows that do not count are not used. The
  * sums are taken in pairs of float32 (some 45 bits). No workspace.
  * Errors: as mica_preference_loss.
  */
@@ -200,8 +200,8 @@ MICA_API mica_status mica_act_grad(const mica_packed* p, int32_t act, int32_t ga
  * source). dw: features x n, row stride ld_dw, MICA_F32, MICA_F16 or MICA_BF16; add: the same type with row stride
  * ld_add, NULL for zeros, or dw itself (accumulation in place). The products are exact and summed in float32, add is
  * added in float32, and the result is rounded once. No tokens: dw = add. workspace: mica_packed_wgrad_workspace bytes
- * for the same arguments, 16-byte aligned (it may be 0 bytes, and NULL then): sums of parts, at most 20 MB, and a copy of a
- * dy whose rows are not 16-byte aligned.
+ * for the same arguments, 16-byte aligned (it may be 0 bytes, and NULL then): sums of parts, at most 20 MB, and a
+ * copy of a dy whose rows are not 16-byte aligned (as large as dy: tokens x n elements, n rounded up to a multiple of 8).
  * Errors: NULL / COUNT / DTYPE / ADDRESS / OVERLAP / DEVICE / CUDA.
  */
 MICA_API mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, int64_t ld_dy, int32_t dy_dtype, int64_t n,
