@@ -320,7 +320,7 @@ __device__ __forceinline__ void sum_weights(const LogitRows& L, const Vec<T> (&v
 // 2^x for the factor of a part that is counted anew, x <= 0: from the nearest integer, whose power the hardware has exactly,
 // and what remains of x, where its error is 1e-8 on average (see kLow) and not the same way for every part.
 __device__ __forceinline__ float exp2_factor(float x) {
-    const float i = rintf(x);
+    const float i = (x + 12582912.0f) - 12582912.0f;  // 1.5 * 2^23
     return exp2_fast(i) * exp2_fast(x - i);
 }
 
@@ -333,17 +333,17 @@ __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
     r.m = m;
 }
 
-// Counts a part from the largest of some vectors that it is about to take, where that is larger. Log-probabilities with
+// Counts a part from m, the largest of some vectors that it is about to take, where that is larger. Log-probabilities with
 // entropies are counted so throughout: an entropy is log s, which is then not negative, plus the mean of -x, which is not
 // either. Counted from a target far below the maximum it would be the difference of two numbers as large as that distance,
-// in float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons take some 4% of the time
-// (8,192 rows of 50,257 bfloat16 logits, of which 6,144 count, with entropies: 104 us, counted from the target 100; 117 with
-// the weights counted from the target and the moment from the maximum). Without entropies they are made too, so that the
-// log-probabilities are the same bits; there they take nothing.
-template <bool kMoment, typename T, int kCount>
-__device__ __forceinline__ void count_from_highest(const LogitRows& L, const Vec<T> (&v)[kCount], Running& r) {
-    const float m = Vec<T>::max(v);
-    if (m > r.m) raise<kMoment>(L, r, m);
+// in float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons cost up to 7% (8,192 rows of
+// 50,257 bfloat16 logits, of which 6,144 count, with entropies: 105 us, counted from the target 100; 117 with the weights
+// counted from the target and the moment from the maximum). Without entropies they are made too, so that the
+// log-probabilities are the same bits.
+template <bool kMoment>
+__device__ __forceinline__ void count_from_highest(const LogitRows& L, float m, Running& r) {
+    if (r.s == 0.0f) r.m = fmaxf(r.m, m);  // nothing to scale (a NaN target is in the sum by itself)
+    else if (m > r.m) raise<kMoment>(L, r, m);
 }
 
 // Adds some vectors to a thread's part. Weights are counted from an origin that need not be the maximum: any will do as long
@@ -421,7 +421,9 @@ __device__ __forceinline__ void skip_outputs(const RowOut& out, int64_t row) {
 __device__ __forceinline__ double wide_log(float s) {
     const uint32_t bits = __float_as_uint(s);
     if (!(s >= 0x1p-126f && s < INFINITY)) return logf(s);
-    return ((int)(bits >> 23) - 127) * kLn2 + logf(__uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u));
+    // (kLow is of the share that is not the largest weight's, which is exactly 1: to within 3e-8)
+    return fma((double)((int)(bits >> 23) - 127), kLn2, s < 1.5f ? 0.0 : kLow) +
+           logf(__uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u));
 }
 
 // Writes a row's results (one thread, `head`) and returns the gradient's coefficient, c itself where it was given, in every
@@ -432,7 +434,7 @@ __device__ __forceinline__ float finish_row(const LogitRows& L, const PolicyTerm
     const float o = origin(r.m);
     if constexpr (kKind == kLogps || kKind == kEntropy) {
         if (head) {
-            const double log_sum = wide_log(r.s) + kLow * (1.0f - 1.0f / r.s);  // (the largest weight is exactly 1)
+            const double log_sum = wide_log(r.s);
             const double lp = y < L.vocab ? ((double)zy - o) * L.wide_inv_t - log_sum : NAN;
             out.logps[row] = (float)lp;
             if (kKind == kLogps && out.rest_logps) out.rest_logps[row] = isfinite(lp) ? (float)(lp - (float)lp) : 0.0f;
@@ -476,17 +478,31 @@ __global__ void __launch_bounds__(kThreads, kRowResident / kThreads) row_kernel(
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             v[u] = Vec<T>{kGrad ? ld16_again(at + u * kThreads * n) : ld16_stream(at + u * kThreads * n)};
-        if (kHighest) count_from_highest<kMoment>(L, v, r);
+        if (kHighest) count_from_highest<kMoment>(L, Vec<T>::max(v), r);
         add_vectors<T, kMoment>(L, v, r);
     }
-    for (; k < g.hi; k += kThreads) {
-        const Vec<T> v[1] = {{kGrad ? ld16_again(z + (k * n - g.lead)) : ld16_stream(z + (k * n - g.lead))}};
-        if (kHighest) count_from_highest<kMoment>(L, v, r);
-        add_vectors<T, kMoment>(L, v, r);
+    if constexpr (kHighest) {  // fewer than a batch are left
+        Vec<T> v[kBatch - 1];
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kBatch - 1; ++u)
+            if (k + u * kThreads < g.hi) v[u] = Vec<T>{ld16_stream(z + ((k + u * kThreads) * n - g.lead))};
+#pragma unroll
+        for (int u = 0; u < kBatch - 1; ++u)
+            if (k + u * kThreads < g.hi) m = fmaxf(m, Vec<T>::max({v[u]}));
+        count_from_highest<kMoment>(L, m, r);
+#pragma unroll
+        for (int u = 0; u < kBatch - 1; ++u)
+            if (k + u * kThreads < g.hi) add_vectors<T, kMoment>(L, {v[u]}, r);
+    } else {
+        for (; k < g.hi; k += kThreads) {
+            const Vec<T> v[1] = {{ld16_again(z + (k * n - g.lead))}};
+            add_vectors<T, kMoment>(L, v, r);
+        }
     }
     if (g.edge >= 0) {
         const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
-        if (kHighest) count_from_highest<kMoment>(L, v, r);
+        if (kHighest) count_from_highest<kMoment>(L, Vec<T>::max(v), r);
         add_vectors<T, kMoment>(L, v, r);
     }
     r = join_parts<kMoment>(L, parts, r);
@@ -516,9 +532,11 @@ struct RingShape {
     static constexpr int threads = kThreads + 32, stage_bytes = kVectors * 16, bytes = kCount * stage_bytes;
     static constexpr int per_thread = kVectors / kThreads;
 };
-// Each the best of a dozen shapes. Reading only: four CTAs, so that others compute while one joins a row (8,192 rows of 50,257
-// bfloat16 logits, of which 6,144 count, with entropies: 104 us, 5.9 TB/s; while weights were counted from the target, 100 us,
-// three CTAs of 256 threads 104 us, two of 384 120 us, one of 512 178 us).
+// Each the best of a dozen shapes. Reading only: many CTAs, so that others compute while one joins a row, and smaller ones the
+// shorter the rows. Log-probabilities without and with entropies in us, four CTAs of 192 threads and then six of 128, bfloat16:
+// 8,192 rows of 8,192 logits 39 and 43, 31 and 37; of 16,384 52 and 58, 46 and 54; of 32,768 80 and 91, 85 and 89; 6,144 of
+// 50,257 92 and 100, 99 and 105. Three CTAs of 256 threads take 95 and 107 for the last, two of 384 112 and 126.
+using ShortReadRing = RingShape<128, 1024, 2, 6>;
 using ReadRing = RingShape<192, 1536, 2, 4>;
 // A gradient reads its row again, which has to be in L2 still: of long rows one at a time on an SM (6,144 rows of 131,072:
 // 486 us, 6.2 TB/s, against 535 us with two CTAs and 625 us with three), of others two (6,144 rows of 50,257: 196 us,
@@ -527,9 +545,9 @@ using GradRing = RingShape<384, 2304, 3, 2>;
 using LongGradRing = RingShape<512, 2048, 6, 1>;
 // One pass that reads and writes.
 using StreamRing = RingShape<512, 2048, 3, 2>;
-constexpr int64_t kLongRowBytes = 160 << 10;
+constexpr int64_t kLongReadBytes = 48 << 10, kLongRowBytes = 160 << 10;
 constexpr int kEntries = 2;
-constexpr int64_t kRingRows = 300;
+constexpr int64_t kRingRows = 300, kShortRingRows = 4096;
 
 // Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_logits_status).
 __device__ unsigned int g_logits_status;
@@ -717,16 +735,21 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
                     for (int u = 0; u < kPerThread; ++u) v[u] = stage_vector<T>(stage, (int)threadIdx.x + u * kConsumers);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring.empty[s]);
-                    if (kHighest) count_from_highest<kMoment>(L, v, q);
+                    if (kHighest) count_from_highest<kMoment>(L, Vec<T>::max(v), q);
 #pragma unroll
                     for (int u = 0; u < kPerThread; u += 2) {
                         const Vec<T> two_of[2] = {v[u], v[u + 1]};
                         add_vectors<T, kMoment>(L, two_of, q);
                     }
                 } else {
+                    if (kHighest) {
+                        float m = q.m;
+                        for (int i = (int)threadIdx.x; i < left; i += kConsumers)
+                            m = fmaxf(m, Vec<T>::max({stage_vector<T>(stage, i)}));
+                        count_from_highest<kMoment>(L, m, q);
+                    }
                     for (int i = (int)threadIdx.x; i < left; i += kConsumers) {
                         const Vec<T> v[1] = {stage_vector<T>(stage, i)};
-                        if (kHighest) count_from_highest<kMoment>(L, v, q);
                         add_vectors<T, kMoment>(L, v, q);
                     }
                     __syncwarp();
@@ -735,7 +758,7 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             }
             if (g.edge >= 0) {
                 const Vec<T> v[1] = {load_edge(z, g.edge * n - g.lead, L.vocab)};
-                if (kHighest) count_from_highest<kMoment>(L, v, q);
+                if (kHighest) count_from_highest<kMoment>(L, Vec<T>::max(v), q);
                 add_vectors<T, kMoment>(L, v, q);
             }
             q = join_warp<kMoment>(L, q);
@@ -746,8 +769,10 @@ __global__ void __launch_bounds__(S::threads, S::ctas) ring_kernel(LogitRows L, 
             }
             if (!mbar_wait(&ring.joined, joins)) return give_up();
             joins ^= 1;
-            q = join_warp<kMoment>(L, lane < kConsumers / 32 ? part[lane] : Running{-INFINITY, 0.0f, 0.0f});
-            c = finish_row<kKind>(L, P, out, row, y, zy, q, c, threadIdx.x == 0);
+            if (kGrad || warp == 0) {
+                q = join_warp<kMoment>(L, lane < kConsumers / 32 ? part[lane] : Running{-INFINITY, 0.0f, 0.0f});
+                c = finish_row<kKind>(L, P, out, row, y, zy, q, c, threadIdx.x == 0);
+            }
         } else {
             const RowStat st = out.stat[row];
             q = Running{st.origin, 1.0f / st.inv_sum, 0.0f};
@@ -974,12 +999,14 @@ __global__ void __launch_bounds__(kSumThreads) pairs_kernel(LogitRows L, PairTer
     }
 }
 
-// Many long rows go through the ring. Measured both ways, in us, the ring first, bfloat16: log-probabilities of 8,192 rows of
-// 8,192 logits 34 and 36, 32,768: 69 and 91; of 300 rows of 50,257: 17 and 18, of 1,200: 24 and 30; policy gradients of 6,144
-// rows of 16,384: 91 and 79, 32,768: 135 and 154, 50,257: 196 and 267; of 300 rows of 131,072: 33 and 43.
+// Many rows go through the ring, the shorter the more there have to be. Measured both ways, in us, the ring first, bfloat16:
+// log-probabilities of 8,192 rows of 1,024 logits 21 and 19, 1,536: 23 and 27, 4,096: 27 and 40, 32,768: 80 and 90; of 1,200
+// rows of 50,257 26 and 26, of 300 of 16,384 10 and 12; policy gradients of 6,144 rows of 16,384: 91 and 79, 32,768: 135 and
+// 154, 50,257: 196 and 267; of 300 rows of 131,072: 33 and 43.
 bool takes_ring(const LogitRows& L, bool grad) {
     const int64_t bytes = L.vocab * (L.dtype == MICA_F32 ? 4 : 2);
-    return L.rows >= kRingRows && bytes >= (grad ? 64 << 10 : 16 << 10);
+    if (grad) return L.rows >= kRingRows && bytes >= 64 << 10;
+    return (L.rows >= kRingRows && bytes >= 16 << 10) || (L.rows >= kShortRingRows && bytes >= 3 << 10);
 }
 
 // How a row is cut otherwise: C CTAs of `threads` threads.
@@ -1023,7 +1050,8 @@ cudaError_t launch_ring(const LogitRows& L, const PolicyTerms& P, const RowOut& 
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
         return e != cudaSuccess ? e : launch_clusters(kernel, L.rows, 1, S::threads, S::bytes, stream, L, P, out);
     };
-    if constexpr (kKind == kLogps || kKind == kEntropy) return go(ReadRing{});
+    if constexpr (kKind == kLogps || kKind == kEntropy)
+        return L.vocab * (int64_t)sizeof(T) > kLongReadBytes ? go(ReadRing{}) : go(ShortReadRing{});
     else if constexpr (kStream) return go(StreamRing{});
     else return L.vocab * (int64_t)sizeof(T) > kLongRowBytes ? go(LongGradRing{}) : go(GradRing{});
 }

@@ -751,3 +751,31 @@ def test_log_probabilities_err_to_both_sides(vocab, dtype):
         assert fine.sum() > 3000
         e = (mica.mica_token_logps(z, target).double() - want)[fine]
         assert abs(e.mean().item()) < 4.2e-8 * math.sqrt(4000 / len(e)), e.mean().item()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,vocab,ld,offset", [(4100, 1537, 1537, 1), (4500, 2048, 2048, 0), (4096, 4099, 4104, 3),
+                                                  (4097, 12301, 12301, 0)])
+def test_very_many_short_rows(rows, vocab, ld, offset, dtype):
+    """Log-probabilities and entropies of short rows in such number that they take the ring: part of a stage, or one and a
+    part; runs of rows that do not count, masked values."""
+    z, y = make(rows, vocab, dtype, seed=rows, ld=ld, offset=offset)
+    y[1000:2500] = -1
+    y[5] = vocab + 3
+    z[7, 10:] = -math.inf
+    y[7] = 4
+    z[8] = torch.finfo(dtype).min
+    z[9] = -math.inf
+    z[10, vocab // 2] = math.nan
+    z[11, vocab - 1] = math.inf
+    z[12, y[12]] = -math.inf
+    y[[8, 9, 10, 11]] = 1
+    want, want_h, _ = reference(z, y.clamp(max=vocab - 1), 0.9)
+    want[5] = math.nan
+    lp, h = mica.mica_token_logps(z, y, temperature=0.9, entropy=True)
+    close(lp, want, rel(vocab) + 6 * U * want.abs().nan_to_num(0, 0, 0) + 64 * U)
+    close(h, want_h, rel(vocab) * (1 + 2 * want_h.nan_to_num(0)) + 8 * U * want_h.nan_to_num(0))
+    assert lp[[5, 9, 10, 11]].isnan().all() and lp[12] in (0, -math.inf) and not lp[y < 0].any() and not h[y < 0].any()
+    alone = mica.mica_token_logps(z, y, temperature=0.9)
+    assert torch.equal(lp.view(torch.int32), alone.view(torch.int32))
+    mica.mica_sync()
