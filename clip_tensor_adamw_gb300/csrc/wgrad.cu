@@ -9,14 +9,14 @@
 // no rounding and the products are exact. The tensor cores' additions are truncated: their sums leave TMEM every 512 tokens
 // (kChunkStages stages) and are added in registers. A float32 gradient's error, of its norm, at 16,384 tokens: 1.8e-7 with
 // bfloat16 and 4.3e-7 with binary16 operands (8.6e-7 with 1,024 tokens a visit, 1.1e-5 with none; 7.6e-7 for a product in
-// float32). 1,024 tokens a visit would take 283 us where 512 take 293.
+// float32). 1,024 tokens a visit would take 3% less.
 //
 // Both operands are MN-major: a stage is [64 tokens][64 columns] boxes with 128-byte swizzle, as dy lies in memory and as
 // the codes do, so nothing is transposed. dy comes by TMA; the codes come by TMA into a stage of their own, from which
 // sixteen warps, four groups of four that take stages in turn, decode them into the operand. The same warps empty TMEM, a
 // chunk behind. Three more warps load codes, load dy, and issue the products.
 //
-// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 293 to 302 us, 1,130 TFLOP/s, the tensor pipe 54% active; without the
+// What bounds it: 16,384 x 1,600 x 6,400 bfloat16 takes 299 to 308 us, 1,110 TFLOP/s, the tensor pipe 54% active; without the
 // decoding it would take some 240 us. A stage moves 96 KB through an SM's shared memory (the products read 48, dy and codes
 // are written with 24, codes read with 8, operands written with 16), 750 clocks' worth against the products' 512. Beside
 // that, tiles of 256 cover 1,792 features where there are 1,600 (12% more products), and nineteen warps leave a thread 96
