@@ -336,9 +336,9 @@ __device__ __forceinline__ void raise(const LogitRows& L, Running& r, float m) {
 // Counts a part from m, the largest of some vectors that it is about to take, where that is larger. Log-probabilities with
 // entropies are counted so throughout: an entropy is log s, which is then not negative, plus the mean of -x, which is not
 // either. Counted from a target far below the maximum it would be the difference of two numbers as large as that distance,
-// in float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons cost up to 7% (8,192 rows of
-// 50,257 bfloat16 logits, of which 6,144 count, with entropies: 105 us, counted from the target 100; 117 with the weights
-// counted from the target and the moment from the maximum). Without entropies they are made too, so that the
+// in float32, and of a confident row little is left (20 nats: 1e-6 off, and below 0). The comparisons cost up to 7% (8,192
+// rows of 50,257 bfloat16 logits, of which 6,144 count, with entropies: 104 us, counted from the target 100; 117 with the
+// weights counted from the target and the moment from the maximum). Without entropies they are made too, so that the
 // log-probabilities are the same bits.
 template <bool kMoment>
 __device__ __forceinline__ void count_from_highest(const LogitRows& L, float m, Running& r) {
