@@ -84,7 +84,7 @@ def draw(rng):
         if rng.random() < 0.7:
             features = (features + 7) // 8 * 8
         # the largest listed case's products, scored rows only
-        most = {"linear_logps": 6144 * 1600 * 50257, "linear_grad": 3072 * 768 * 50257,
+        most = {"linear_logps": 6144 * 1600 * 50257, "linear_grad": 4096 * 3 // 4 * 768 * 50257,
                 "linear_ce": 3584 * 1600 * 131072}[op]
         tokens = _log_int(rng, 1, max(1, min(8192, most // (features * vocab))))
         return dict(op=op, tokens=tokens, features=features, vocab=vocab, dtype=dtype,
