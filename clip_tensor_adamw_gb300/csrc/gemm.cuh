@@ -1,0 +1,393 @@
+// A matrix product on the tensor cores whose operands, tiles and epilogue a policy gives: what the losses from hidden states
+// (linear.cu) and the orthogonalisation (muon.cu) are made of.
+//
+// A pair of CTAs takes a tile of 256 x 256 sums, 64 steps of the summed dimension at a time: each CTA holds 128 rows of the
+// tile and loads half of both operands, and tcgen05.mma of the pair multiplies both halves with one another. The grid is one
+// pair for two SMs; pairs take pieces of work in turn. One warp loads stages by TMA, one issues products, and eight empty the
+// accumulators, of which TMEM holds two, so that a tile's epilogue runs under the next tile's products.
+//
+// An operand is K-major (the summed dimension contiguous) or MN-major; either way a stage is boxes of 64 x 64 elements with
+// 128-byte swizzle, so that one tensor map serves a matrix in both roles and nothing is transposed: only the step from one
+// product of 16 to the next differs, 32 bytes or 2 KB. Elements outside the matrix are read as zeros.
+//
+// A policy P is the kernel's parameter, with
+//   Deal deal(int pairs) const                      how the work is dealt; computed once a thread
+//   bool piece(const Deal&, int i, Piece*) const    the i-th piece of work; false when there are no more
+//   struct Epilogue                                 what becomes of a piece's sums, made for each piece by each of its threads:
+//     Epilogue(const P&, const Deal&, const Piece&, const Place&)
+//     void chunk(int c, float (&v)[32])             columns [32 c, 32 c + 32) of the thread's row of its half, in order
+//     void done()
+#pragma once
+
+#include <atomic>
+
+#include "elem.cuh"
+#include "mma.cuh"
+#include "stream.cuh"
+
+namespace mica {
+namespace {
+
+constexpr int kHalf = 128, kTile = 2 * kHalf;  // rows and columns: of a CTA, of a pair
+constexpr int kDepth = 64;                     // the summed dimension of a stage
+constexpr int kStages = 6;
+constexpr int kTakers = 8;                     // warps that empty the accumulators
+constexpr int kGemmThreads = (kTakers + 2) * 32;
+enum GemmRole { kLoader = kTakers, kMultiplier };
+constexpr int kOperandBytes = kHalf * kDepth * 2, kBoxBytes = 64 * kDepth * 2;
+constexpr int kStagingBytes = 32 * 32 * 4;     // of a warp
+constexpr int kGemmShared = 1024 + kStages * 2 * kOperandBytes + kTakers * kStagingBytes;
+constexpr int kChunks = kHalf / 32;            // of 32 columns, that a taker has of a tile
+
+// Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_gemm_status).
+__device__ unsigned int g_gemm_status;
+std::atomic<bool> g_gemm_launched{false};  // in this process; until then nothing can have set it
+
+// An operand: its map, the coordinate of its third dimension, and whether its rows run along the summed dimension.
+struct Operand {
+    const CUtensorMap* map;
+    int z;
+    bool k_major;
+};
+
+// Stages [from, to) of the tile whose first row and column are m0 and n0.
+struct Piece {
+    Operand a, b;
+    int m0, n0;
+    int from, to;
+    int tile;  // for the epilogue, as the policy likes
+    int part;  // >= 0: part of a split tile
+};
+
+// Where a taker stands: its row of the tile, its half's first column, the warp's staging buffer.
+struct Place {
+    int row, first_column, lane;
+    unsigned char* staging;
+};
+
+struct GemmBarriers {
+    uint64_t full[kStages];              // (leader) a stage's operands have come, in both CTAs
+    uint64_t used[kStages];              // the products of a stage are done
+    uint64_t sum_full[2], sum_empty[2];  // a tile's sums are in TMEM; (leader) both CTAs have taken them
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ void load_box3_for_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %5, 0;\n\t"
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [at];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A CTA's half of a stage's operand: 128 rows (or columns) from `at` on, by 64 of the summed dimension from k on.
+__device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& o, int at, int k, uint64_t* bar) {
+    load_box3_for_pair(dst, o.map, o.k_major ? k : at, o.k_major ? at : k, o.z, bar);
+    load_box3_for_pair(dst + kBoxBytes, o.map, o.k_major ? k : at + 64, o.k_major ? at + 64 : k, o.z, bar);
+}
+
+// The descriptor of either kind of operand: 128-byte swizzle, groups of 8 lines of 128 bytes 1 KB apart; boxes of 64 columns
+// kBoxBytes apart, which counts for MN-major operands only.
+__device__ __forceinline__ uint64_t operand_descriptor(uint32_t at) {
+    return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(kBoxBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// float32 sums of bfloat16 (or binary16) products, 256 x 256
+template <typename T>
+__device__ __forceinline__ uint32_t instruction(bool a_k_major, bool b_k_major) {
+    constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | (a_k_major ? 0u : 1u << 15) | (b_k_major ? 0u : 1u << 16) | (kTile / 8) << 17 |
+           (kTile / 16) << 24;
+}
+
+// 32 columns of the thread's row of TMEM
+__device__ __forceinline__ void load_sums32(uint32_t at, float (&f)[32]) {
+    uint32_t v[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+          "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+template <typename T, typename P>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ P p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ GemmBarriers bar;
+    unsigned char* a_stage = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    unsigned char* b_stage = a_stage + kStages * kOperandBytes;
+    unsigned char* staging = b_stage + kStages * kOperandBytes;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)rank_of_cta(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.used[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sum_full[i], 1);
+            mbar_init(&bar.sum_empty[i], 2 * kTakers);
+        }
+        mbar_fence_init();
+    }
+    if (warp == kMultiplier) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bar.tmem);
+    wait_prerequisite();
+    allow_dependents();
+
+    const typename P::Deal deal = p.deal(pairs);
+    bool ok = true;
+    Piece q;
+    if (warp == kLoader) {
+        if (lane == 0) {
+            Turn<kStages> turn;
+            for (int i = pair; ok && p.piece(deal, i, &q); i += pairs)
+                for (int k = q.from; k < q.to; ++k, turn.next()) {
+                    const int s = turn.at;
+                    if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 4 * kOperandBytes);
+                    load_operand(a_stage + s * kOperandBytes, q.a, q.m0 + rank * kHalf, k * kDepth, &bar.full[s]);
+                    load_operand(b_stage + s * kOperandBytes, q.b, q.n0 + rank * kHalf, k * kDepth, &bar.full[s]);
+                }
+            // Every copy has landed when the last products are done. Where a wait gave up they are given 2 ms.
+            for (int i = 0; !ok && i < 200; ++i) __nanosleep(10000);
+        }
+    } else if (warp == kMultiplier) {  // issued by one thread of the leader, in code that the whole warp runs alike
+        if (rank == 0) {
+            const bool one = elect_one();
+            const uint64_t a0 = operand_descriptor(smem_u32(a_stage)), b0 = operand_descriptor(smem_u32(b_stage));
+            Turn<kStages> turn;
+            Turn<2> sums;
+            for (int i = pair; ok && p.piece(deal, i, &q); i += pairs) {
+                const int b = sums.at;
+                const uint32_t how = instruction<T>(q.a.k_major, q.b.k_major);
+                const uint32_t a_step = (q.a.k_major ? 32 : 2048) >> 4, b_step = (q.b.k_major ? 32 : 2048) >> 4;
+                if (!(ok = mbar_wait_idle(&bar.sum_empty[b], sums.round ^ 1))) break;
+                fence_after();
+                for (int k = q.from; k < q.to; ++k, turn.next()) {
+                    const int s = turn.at;
+                    if (!(ok = mbar_wait_idle(&bar.full[s], turn.round))) break;
+                    fence_after();
+                    if (one) {
+                        const uint32_t at = (uint32_t)s * (kOperandBytes >> 4);
+#pragma unroll
+                        for (int d = 0; d < kDepth / 16; ++d)
+                            multiply(tmem + b * kTile, a0 + (at + d * a_step), b0 + (at + d * b_step), how, k > q.from || d > 0);
+                        commit(&bar.used[s]);
+                        if (k == q.to - 1) commit(&bar.sum_full[b]);
+                    }
+                }
+                sums.next();
+            }
+        }
+    } else {
+        const int quarter = warp % 4, half = warp / 4;
+        const Place place{rank * kHalf + quarter * 32 + lane, half * kHalf, lane, staging + warp * kStagingBytes};
+        const uint32_t own = tmem + ((uint32_t)quarter << 21) + half * kHalf;
+        Turn<2> sums;
+        for (int i = pair; p.piece(deal, i, &q); i += pairs) {
+            const int b = sums.at;
+            typename P::Epilogue epilogue(p, deal, q, place);
+            if (!(ok = mbar_wait_idle(&bar.sum_full[b], sums.round))) break;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+                float v[32];
+                load_sums32(own + b * kTile + c * 32, v);
+                if (c == kChunks - 1) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader(&bar.sum_empty[b]);
+                }
+                epilogue.chunk(c, v);
+            }
+            epilogue.done();
+            sums.next();
+        }
+    }
+    if (!ok) atomicOr(&g_gemm_status, p.kStatus);
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    cluster_sync();  // the other CTA's products have read this CTA's shared memory, its arrivals have landed
+    fence_after();
+    if (warp == kMultiplier) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------------------------------------------------------------------------------------------
+// splitting a long sum
+// ------------------------------------------------------------------------------------------------------------------------
+
+// `whole` tiles one after another, then the rest (fewer than there are pairs) in `parts` along the summed dimension.
+struct SplitDeal {
+    int tiles, stages, whole, parts, pieces;
+};
+
+// least: stages that a part should have to be worth the launch that joins the parts
+__host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs, int least) {
+    SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles};
+    const int rest = tiles - d.whole;
+    if (stages == 0) {  // nothing to add up: what joins the parts writes every tile
+        d.whole = d.parts = d.pieces = 0;
+        return d;
+    }
+    if (rest) {
+        d.parts = pairs / rest < stages / least ? pairs / rest : stages / least;
+        if (d.parts < 1) d.parts = 1;
+        d.pieces = d.whole + rest * d.parts;
+    }
+    return d;
+}
+
+// The i-th piece's tile, stages and part; false when there are no more.
+__device__ __forceinline__ bool split_piece(const SplitDeal& d, int i, Piece* q) {
+    if (i >= d.pieces) return false;
+    if (i < d.whole || d.parts == 1) {
+        *q = Piece{{}, {}, 0, 0, 0, d.stages, i, -1};
+        return true;
+    }
+    const int k = i - d.whole, part = k % d.parts;
+    *q = Piece{{}, {}, 0, 0, (int)((int64_t)d.stages * part / d.parts), (int)((int64_t)d.stages * (part + 1) / d.parts),
+               d.whole + k / d.parts, k};
+    return true;
+}
+constexpr int64_t kPartFloats = (int64_t)kTile * kTile;  // of a part's sums, row by row
+
+// ------------------------------------------------------------------------------------------------------------------------
+// from a row to a thread, to coalesced accesses
+// ------------------------------------------------------------------------------------------------------------------------
+
+// 32 rows x 32 float32 of a warp, a row to a lane, handed on as four columns of a row at a time, eight lanes to a row:
+// put(row, column, values). Through shared memory, whose 16-byte units change places so that no two lanes of a phase meet.
+template <typename Put>
+__device__ __forceinline__ void by_columns(unsigned char* staging, int lane, const float (&v)[32], Put put) {
+    float4* s = reinterpret_cast<float4*>(staging);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+        const int row = it * 4 + lane / 8, j = lane % 8;
+        put(row, j * 4, s[row * 8 + (j ^ (row & 7))]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// 32 rows x 32 elements of 16 bits of a warp, a row to a lane, handed on as eight columns of a row at a time, four lanes to a
+// row: put(row, column, 16 bytes).
+template <typename Put>
+__device__ __forceinline__ void by_columns16(unsigned char* staging, int lane, const uint32_t (&v)[16], Put put) {
+    uint4* s = reinterpret_cast<uint4*>(staging);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        s[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int row = it * 8 + lane / 4, j = lane % 4;
+        put(row, j * 8, s[row * 4 + (j ^ ((row >> 1) & 3))]);
+    }
+}
+
+// Four values to a row of O, the first at `at`, of which `there` are in the matrix; wide: rows are aligned for one store.
+template <typename O>
+__device__ __forceinline__ void store4(O* at, float4 v, int there, bool wide) {
+    if (wide && there >= 4) {
+        if constexpr (sizeof(O) == 4)
+            *reinterpret_cast<float4*>(at) = v;
+        else
+            *reinterpret_cast<uint2*>(at) = make_uint2(pack2<O>(v.x, v.y), pack2<O>(v.z, v.w));
+        return;
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < there) at[i] = narrow<O>(f[i]);
+}
+template <typename O>
+__device__ __forceinline__ float4 load4(const O* at, int there, bool wide) {
+    if (wide && there >= 4) {
+        if constexpr (sizeof(O) == 4) {
+            return *reinterpret_cast<const float4*>(at);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(at);
+            const O* e = reinterpret_cast<const O*>(&u);
+            return make_float4(widen(e[0]), widen(e[1]), widen(e[2]), widen(e[3]));
+        }
+    }
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < there ? widen(at[i]) : 0.0f;
+    return make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// ------------------------------------------------------------------------------------------------------------------------
+// the host side
+// ------------------------------------------------------------------------------------------------------------------------
+
+// A map of `count` matrices of rows x cols elements of 16 bits, one after another; false where the driver refuses it.
+bool matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t cols, int64_t rows, int64_t ld,
+                int64_t count) {
+    const Encode fn = encode_fn();
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(count > 1 ? ld * rows : ld) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kDepth, 1}, one[3] = {1, 1, 1};
+    return fn && fn(map, type, 3, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// pieces: how many there can be at most
+template <typename T, typename P>
+cudaError_t launch_gemm(const P& p, int64_t pieces, int sms, void* stream) {
+    const auto kernel = gemm_kernel<T, P>;
+    g_gemm_launched = true;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmShared);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
+    return launch_after(kernel, 2 * (pieces < pairs ? pieces : pairs), kGemmThreads, kGemmShared, stream, p);
+}
+
+cudaError_t read_gemm_status(unsigned int* status) {
+    *status = 0;
+    if (!g_gemm_launched) return cudaSuccess;
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_gemm_status, sizeof v);
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_gemm_status, &zero, sizeof zero);
+    }
+    *status = v;
+    return e;
+}
+
+}  // namespace
+}  // namespace mica

@@ -1,5 +1,6 @@
 """Python binding of the operators of include/mica_train.h, taking torch tensors: losses over logits with the gradient
-of the logits, and activation checkpoints in 8 bits with the backward passes that read them.
+of the logits, losses from hidden states with the gradients of these and of the output embedding, and activation
+checkpoints in 8 bits with the backward passes that read them.
 
 As in mica.py, this module only marshals arguments: every element is read and written by the library's kernels, and there
 is no fallback. What a call returns is allocated on the stream that it runs on (``stream``, by default the current one),
@@ -42,7 +43,22 @@ class _Packed(ctypes.Structure):
                 ("dtype", _I32), ("reserved", _I32)]
 
 
+class _Linear(ctypes.Structure):
+    _fields_ = [("h", _P), ("w", _P), ("targets", _P), ("rows", _I64), ("features", _I64), ("vocab", _I64),
+                ("ld_h", _I64), ("ld_w", _I64), ("temperature", _F64), ("dtype", _I32), ("target_bytes", _I32)]
+
+
+class _LinearGrads(ctypes.Structure):
+    _fields_ = [("dh", _P), ("dw", _P), ("add", _P), ("ld_dh", _I64), ("ld_dw", _I64), ("ld_add", _I64),
+                ("dw_dtype", _I32), ("reserved", _I32)]
+
+
+class _CrossEntropyHP(ctypes.Structure):
+    _fields_ = [("denom", _F64), ("grad_scale", _F64)]
+
+
 _LP, _QP, _OP, _KP = (ctypes.POINTER(t) for t in (_Logits, _PreferenceHP, _PolicyHP, _Packed))
+_HP, _GP, _CP = (ctypes.POINTER(t) for t in (_Linear, _LinearGrads, _CrossEntropyHP))
 _lib = None
 
 
@@ -59,6 +75,9 @@ def _train() -> ctypes.CDLL:
             "mica_act_unpack": [_KP, _P, _I64, _P],
             "mica_act_grad": [_KP, _I32, _I32, _P, _I64, _I32, _P, _I64, _P],
             "mica_packed_wgrad": [_KP, _P, _I64, _I32, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P],
+            "mica_linear_logps": [_HP, _P, _P, _P, _I64, _P],
+            "mica_linear_logps_grad": [_HP, _P, _P, _GP, _P, _I64, _P],
+            "mica_linear_cross_entropy": [_HP, _CP, _P, _P, _GP, _P, _I64, _P],
         }.items():
             getattr(L, name).argtypes = args
             getattr(L, name).restype = ctypes.c_int
@@ -66,6 +85,13 @@ def _train() -> ctypes.CDLL:
         L.mica_preference_workspace.restype = _I64
         L.mica_packed_wgrad_workspace.argtypes = [_KP, _P, _I64, _I64]
         L.mica_packed_wgrad_workspace.restype = _I64
+        for name, args in {
+            "mica_linear_logps_workspace": [_HP],
+            "mica_linear_grad_workspace": [_HP, _GP],
+            "mica_linear_cross_entropy_workspace": [_HP, _GP],
+        }.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = _I64
         _lib = L
     return _lib
 
@@ -354,3 +380,108 @@ def mica_packed_wgrad(packed: PackedActivation, dy: torch.Tensor, *, add: torch.
                                    0 if add is None else _matrix(add, "add"), dw.data_ptr(), _matrix(dw, "out"),
                                    _type(dw, "out"), None if work is None else work.data_ptr(), size, s))
     return dw
+
+
+class LinearCrossEntropy(NamedTuple):
+    loss: torch.Tensor          # [1]
+    logps: torch.Tensor         # [rows]
+    dh: torch.Tensor | None     # the gradients of grad_scale * loss
+    dw: torch.Tensor | None
+
+
+def _linear(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, temperature: float) -> _Linear:
+    if h.dtype not in (torch.float16, torch.bfloat16) or w.dtype != h.dtype:
+        raise TypeError(f"h and w must both be float16 or bfloat16, not {h.dtype} and {w.dtype}")
+    ld_h, ld_w = _matrix(h, "h"), _matrix(w, "w")
+    (rows, features), (vocab, other) = h.shape, w.shape
+    if other != features:
+        raise ValueError(f"h has {features} features and w {other}")
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"targets must be int32 or int64, not {targets.dtype}")
+    y = _vector(targets, rows, "targets", targets.dtype)
+    return _Linear(h.data_ptr(), w.data_ptr(), y, rows, features, vocab, ld_h, ld_w, float(temperature), _TYPES[h.dtype],
+                   targets.element_size())
+
+
+def _linear_grads(h: torch.Tensor, w: torch.Tensor, want_dh: bool, want_dw: bool, dh: torch.Tensor | None,
+                  dw: torch.Tensor | None, add: torch.Tensor | None, dw_dtype: torch.dtype | None):
+    """(dh, dw, the call's argument, or None where no gradient is wanted)"""
+    if not (want_dh or want_dw):
+        return None, None, None
+    dh = _output(dh, tuple(h.shape), h.dtype, "dh", h) if want_dh else None
+    if want_dw:
+        if dw_dtype is None:
+            dw_dtype = dw.dtype if dw is not None else add.dtype if add is not None else w.dtype
+        if add is not None and (add.shape != w.shape or add.dtype != dw_dtype):
+            raise ValueError(f"add must be {dw_dtype} of shape {tuple(w.shape)}, not {add.dtype} of {tuple(add.shape)}")
+        dw = _output(dw, tuple(w.shape), dw_dtype, "dw", w)
+    elif add is not None:
+        raise ValueError("add is given without dw")
+    else:
+        dw = None
+    g = _LinearGrads(None if dh is None else dh.data_ptr(), None if dw is None else dw.data_ptr(),
+                     None if add is None else add.data_ptr(), 0 if dh is None else _matrix(dh, "dh"),
+                     0 if dw is None else _matrix(dw, "dw"), 0 if add is None else _matrix(add, "add"),
+                     0 if dw is None else _type(dw, "dw"), 0)
+    return dh, dw, g
+
+
+def mica_linear_logps(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, *, temperature: float = 1.0,
+                      lse: bool = False, stream=None):
+    """Log-probabilities of ``targets`` (int32 or int64, [rows]; negative: not scored, 0) under the softmax of
+    ``h @ w.T / temperature``, float32 [rows], without keeping the logits. ``h``: hidden states [rows, features], ``w``:
+    the output embedding [vocabulary, features], both float16 or bfloat16, any row stride. With ``lse`` also the
+    logarithms of the sums of exp of the logits, which mica_linear_logps_grad takes: ``(logps, lse)``."""
+    l = _linear(h, w, targets, temperature)
+    L = _train()
+    with _On(stream, h.device) as s:
+        logps = torch.empty(l.rows, dtype=torch.float32, device=h.device)
+        z = torch.empty_like(logps) if lse else None
+        size = L.mica_linear_logps_workspace(l)
+        work = torch.empty(size, dtype=torch.uint8, device=h.device)
+        _check(L.mica_linear_logps(l, logps.data_ptr(), None if z is None else z.data_ptr(), work.data_ptr(), size, s))
+    return (logps, z) if lse else logps
+
+
+def mica_linear_logps_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                           dlogps: torch.Tensor, *, temperature: float = 1.0, want_dh: bool = True,
+                           want_dw: bool = True, dh: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                           add: torch.Tensor | None = None, dw_dtype: torch.dtype | None = None, stream=None):
+    """The gradients ``(dh, dw)`` of hidden states and embedding given that of mica_linear_logps's result, for any loss
+    over log-probabilities. ``dh`` has h's dtype, ``dw`` ``dw_dtype`` (by default that of ``dw``, then of ``add``, then
+    of w); ``dw`` is ``add`` plus the gradient, and ``add`` may be ``dw`` itself. ``want_dh`` and ``want_dw`` leave one
+    out (None)."""
+    l = _linear(h, w, targets, temperature)
+    z, d = _vector(lse, l.rows, "lse"), _vector(dlogps, l.rows, "dlogps")
+    L = _train()
+    with _On(stream, h.device) as s:
+        dh, dw, g = _linear_grads(h, w, want_dh, want_dw, dh, dw, add, dw_dtype)
+        if g is None:
+            return None, None
+        size = L.mica_linear_grad_workspace(l, g)
+        work = torch.empty(size, dtype=torch.uint8, device=h.device)
+        _check(L.mica_linear_logps_grad(l, z, d, g, work.data_ptr(), size, s))
+    return dh, dw
+
+
+def mica_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, *, denom: float | None = None,
+                              temperature: float = 1.0, grad_scale: float = 1.0, grad: bool = True,
+                              want_dh: bool = True, want_dw: bool = True, dh: torch.Tensor | None = None,
+                              dw: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                              dw_dtype: torch.dtype | None = None, stream=None) -> LinearCrossEntropy:
+    """Softmax cross entropy of ``targets`` under ``h @ w.T / temperature``, summed over the scored rows and divided by
+    ``denom`` (None: their number), and the gradients of ``grad_scale`` times it, without keeping the logits. Arguments
+    as mica_linear_logps and mica_linear_logps_grad; ``grad=False`` leaves both gradients out."""
+    l = _linear(h, w, targets, temperature)
+    if denom is not None and not denom > 0.0:
+        raise ValueError(f"denom must be > 0, not {denom}")
+    hp = _CrossEntropyHP(0.0 if denom is None else float(denom), float(grad_scale))
+    L = _train()
+    with _On(stream, h.device) as s:
+        loss = torch.empty(1, dtype=torch.float32, device=h.device)
+        logps = torch.empty(l.rows, dtype=torch.float32, device=h.device)
+        dh, dw, g = _linear_grads(h, w, grad and want_dh, grad and want_dw, dh, dw, add, dw_dtype)
+        size = L.mica_linear_cross_entropy_workspace(l, g)
+        work = torch.empty(size, dtype=torch.uint8, device=h.device)
+        _check(L.mica_linear_cross_entropy(l, hp, loss.data_ptr(), logps.data_ptr(), g, work.data_ptr(), size, s))
+    return LinearCrossEntropy(loss, logps, dh, dw)

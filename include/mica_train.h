@@ -12,6 +12,9 @@
  *   mica_act_unpack         the values a checkpoint stands for
  *   mica_act_grad           an activation function's backward pass from a checkpoint
  *   mica_packed_wgrad       a linear layer's weight gradient from its input's checkpoint
+ *   mica_linear_logps       log-probabilities of given tokens from hidden states and an output embedding, no logits kept
+ *   mica_linear_logps_grad  the gradients of both, given that of the log-probabilities (any loss over them)
+ *   mica_linear_cross_entropy  softmax cross entropy from hidden states, with both gradients
  *
  * Conventions, where they differ from mica_optim.h's (ownership, streams, validation before anything is queued, error
  * details, MICA_SYNC_DEBUG and mica_sync are the same):
@@ -208,6 +211,86 @@ MICA_API mica_status mica_packed_wgrad(const mica_packed* x, const void* dy, int
                                        const void* add, int64_t ld_add, void* dw, int64_t ld_dw, int32_t dw_dtype,
                                        void* workspace, int64_t workspace_bytes, void* stream);
 MICA_API int64_t mica_packed_wgrad_workspace(const mica_packed* x, const void* dy, int64_t ld_dy, int64_t n);
+
+/*
+ * Hidden states, an output embedding and the token scored in each row: row t's logits are
+ * z[j] = sum_k h[t*ld_h + k] * w[j*ld_w + k] / temperature, j < vocab. They are not kept: no buffer grows with
+ * rows * vocab, only with rows and with vocab.
+ *   - the products are exact and summed in float32; maxima and sums over the vocabulary are float32
+ *   - target < 0: the row does not count. It is not read; its log-probability is 0 and its gradient zeros, whatever it
+ *     holds. Rows that do not count cost next to nothing
+ *   - target >= vocab: the log-probability is NaN (nothing out of range is read), and so are the gradients that the row
+ *     takes part in, unless its coefficient is 0
+ *   - h and w have the same type, MICA_F16 or MICA_BF16, any alignment and row stride (rows that are not 16-byte aligned
+ *     are copied into the workspace first)
+ */
+typedef struct {
+    const void* h;        /* rows x features */
+    const void* w;        /* vocab x features, as an embedding's table or a linear layer's [out][in] */
+    const void* targets;  /* [rows], int32 or int64 */
+    int64_t rows;         /* [0, MICA_MAX_ROWS] */
+    int64_t features;     /* [1, MICA_MAX_FEATURES] */
+    int64_t vocab;        /* [1, MICA_MAX_COLS] */
+    int64_t ld_h, ld_w;
+    double temperature;   /* [2^-20, 2^20] */
+    int32_t dtype;        /* MICA_F16 or MICA_BF16 */
+    int32_t target_bytes; /* 4 or 8 */
+} mica_linear;
+#define MICA_MAX_FEATURES ((int64_t)1 << 16)
+
+/*
+ * Log-probabilities of the rows' targets, logps[rows] float32, and, when lse is not NULL, lse[rows] float32: the logarithm of
+ * the sum of exp of the row's logits (0 where the row does not count). workspace: mica_linear_logps_workspace bytes for the
+ * same argument, 16-byte aligned.
+ * Errors: NULL / COUNT (also a workspace too small) / DTYPE / HYPER (temperature) / ADDRESS / OVERLAP / DEVICE / CUDA.
+ */
+MICA_API mica_status mica_linear_logps(const mica_linear* l, float* logps, float* lse, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+MICA_API int64_t mica_linear_logps_workspace(const mica_linear* l);
+
+/*
+ * Where the gradients go: dh (rows x features, of h's type) and dw (vocab x features, MICA_F32, MICA_F16 or MICA_BF16), each
+ * or neither NULL; dw = add + the gradient, where add is of dw's type, NULL for zeros, or dw itself (accumulation in place).
+ * The gradient of the logits is rounded to h's type (scaled, in binary16, so that its largest row uses the whole range), as
+ * the tensor cores take it: so dh and dw are off by some 2^-9 (bfloat16) or 2^-12 (binary16) of their norm, whatever dw's
+ * type; sums are float32 and rounded once.
+ */
+typedef struct {
+    void* dh;
+    void* dw;
+    const void* add;
+    int64_t ld_dh, ld_dw, ld_add;
+    int32_t dw_dtype;
+    int32_t reserved; /* 0 */
+} mica_linear_grads;
+
+/*
+ * The gradients given that of the log-probabilities, dlogps[rows] float32, and lse[rows] as mica_linear_logps gives it: with
+ * d[t][j] = dlogps[t] / temperature * ((j == target) - exp(z[t][j] - lse[t])), dh = d w and dw = add + d^T h. A row whose
+ * target is negative or whose dlogps is 0 does not count: its dh is zeros. workspace: mica_linear_grad_workspace bytes for
+ * the same arguments, 16-byte aligned: about 512 MB for large batches, 2 bytes x rows x vocab for smaller ones, and where
+ * the rows are taken in more than one piece and dw is of 16 bits, 4 bytes x vocab x features.
+ * Errors: as mica_linear_logps.
+ */
+MICA_API mica_status mica_linear_logps_grad(const mica_linear* l, const float* lse, const float* dlogps,
+                                            const mica_linear_grads* g, void* workspace, int64_t workspace_bytes,
+                                            void* stream);
+MICA_API int64_t mica_linear_grad_workspace(const mica_linear* l, const mica_linear_grads* g);
+
+typedef struct {
+    double denom;      /* >= 0, finite: what the sum over rows is divided by; 0: the number of rows that count */
+    double grad_scale; /* finite */
+} mica_cross_entropy_hp;
+
+/*
+ * Softmax cross entropy: *loss = -(sum of logps over the rows that count) / denom (0 when none count), logps[rows], and the
+ * gradients of grad_scale * loss where g is not NULL. workspace: mica_linear_cross_entropy_workspace bytes.
+ * Errors: as mica_linear_logps.
+ */
+MICA_API mica_status mica_linear_cross_entropy(const mica_linear* l, const mica_cross_entropy_hp* hp, float* loss,
+                                               float* logps, const mica_linear_grads* g, void* workspace,
+                                               int64_t workspace_bytes, void* stream);
+MICA_API int64_t mica_linear_cross_entropy_workspace(const mica_linear* l, const mica_linear_grads* g);
 
 #ifdef __cplusplus
 }
