@@ -12,6 +12,7 @@ from .mica import (GroupIndex, MicaError, TensorList, lib, mica_accumulate_clip_
                    mica_launch_count, mica_release_cache,
                    mica_scale_tensors, mica_selftest_grid_wait_timeout, mica_selftest_wait_timeout, mica_sgd_steps,
                    mica_sync, mica_work_items)
+from .muon import mica_muon_steps, mica_orthogonalize
 from .train import (LinearCrossEntropy, PackedActivation, PolicyLoss, PreferenceLoss, mica_act_grad, mica_act_pack,
                     mica_act_unpack, mica_linear_cross_entropy, mica_linear_logps, mica_linear_logps_grad,
                     mica_packed_wgrad, mica_policy_loss, mica_preference_loss, mica_token_logps, mica_token_logps_grad)
@@ -24,5 +25,5 @@ __all__ = ["GroupIndex", "MicaError", "TensorList", "lib", "mica_accumulate_clip
            "mica_scale_tensors", "mica_selftest_grid_wait_timeout", "mica_selftest_wait_timeout", "mica_sgd_steps",
            "mica_sync", "mica_work_items",
            "PackedActivation", "PolicyLoss", "PreferenceLoss", "mica_act_grad", "mica_act_pack", "mica_act_unpack",
-           "LinearCrossEntropy", "mica_linear_cross_entropy", "mica_linear_logps", "mica_linear_logps_grad",
+           "mica_muon_steps", "mica_orthogonalize", "LinearCrossEntropy", "mica_linear_cross_entropy", "mica_linear_logps", "mica_linear_logps_grad",
            "mica_packed_wgrad", "mica_policy_loss", "mica_preference_loss", "mica_token_logps", "mica_token_logps_grad"]

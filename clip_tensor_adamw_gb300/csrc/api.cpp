@@ -17,6 +17,7 @@
 
 #include "host.h"
 #include "linear.h"
+#include "muon.h"
 #include "mica_optim.h"
 #include "plan.h"
 #include "train.h"
@@ -66,11 +67,12 @@ static mica_status check_device_status(const char* what) {
     unsigned int st = 0, fst = 0;
     int e = read_device_status(&st);
     if (e == (int)cudaSuccess) e = read_fused_status(&fst);
-    unsigned int rows = 0, wgrad = 0, linear = 0;
+    unsigned int rows = 0, wgrad = 0, linear = 0, muon = 0;
     if (e == (int)cudaSuccess) e = read_logits_status(&rows);
     if (e == (int)cudaSuccess) e = read_wgrad_status(&wgrad);
     if (e == (int)cudaSuccess) e = read_linear_status(&linear);
-    st |= rows | wgrad | linear;
+    if (e == (int)cudaSuccess) e = read_muon_status(&muon);
+    st |= rows | wgrad | linear | muon;
     if (e != (int)cudaSuccess) return cuda_fail((cudaError_t)e, what);
     if (fst) return fail(MICA_ERR_CUDA, "%s: a fused kernel's grid-wide wait gave up (status 0x%x); its results are "
                          "not valid, and the list's table must be released (mica_release_cache)", what, fst);
