@@ -55,8 +55,10 @@ struct Piece {
     Operand a, b;
     int m0, n0;
     int from, to;
-    int tile;  // for the epilogue, as the policy likes
-    int part;  // >= 0: part of a split tile
+    int tile;   // for the epilogue, as the policy likes
+    int part;   // >= 0: part of a split tile
+    int low;    // > 0: both operands are sums of two matrices, the second (the rounding's rest) `low` further on in z: the
+    int depth;  // products of stages [0, depth) of high and high, high and low, low and high follow one another
 };
 
 // Where a taker stands: its row of the tile, its half's first column, the warp's staging buffer.
@@ -83,9 +85,9 @@ __device__ __forceinline__ void load_box3_for_pair(void* dst, const CUtensorMap*
 }
 
 // A CTA's half of a stage's operand: 128 rows (or columns) from `at` on, by 64 of the summed dimension from k on.
-__device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& o, int at, int k, uint64_t* bar) {
-    load_box3_for_pair(dst, o.map, o.k_major ? k : at, o.k_major ? at : k, o.z, bar);
-    load_box3_for_pair(dst + kBoxBytes, o.map, o.k_major ? k : at + 64, o.k_major ? at + 64 : k, o.z, bar);
+__device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& o, int at, int k, int z, uint64_t* bar) {
+    load_box3_for_pair(dst, o.map, o.k_major ? k : at, o.k_major ? at : k, z, bar);
+    load_box3_for_pair(dst + kBoxBytes, o.map, o.k_major ? k : at + 64, o.k_major ? at + 64 : k, z, bar);
 }
 
 // The descriptor of either kind of operand: 128-byte swizzle, groups of 8 lines of 128 bytes 1 KB apart; boxes of 64 columns
@@ -162,8 +164,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
                     if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 4 * kOperandBytes);
-                    load_operand(a_stage + s * kOperandBytes, q.a, q.m0 + rank * kHalf, k * kDepth, &bar.full[s]);
-                    load_operand(b_stage + s * kOperandBytes, q.b, q.n0 + rank * kHalf, k * kDepth, &bar.full[s]);
+                    int az = q.a.z, bz = q.b.z, at = k;
+                    if (q.low && k >= q.depth) {
+                        if (k < 2 * q.depth) bz += q.low, at -= q.depth;
+                        else az += q.low, at -= 2 * q.depth;
+                    }
+                    load_operand(a_stage + s * kOperandBytes, q.a, q.m0 + rank * kHalf, at * kDepth, az, &bar.full[s]);
+                    load_operand(b_stage + s * kOperandBytes, q.b, q.n0 + rank * kHalf, at * kDepth, bz, &bar.full[s]);
                 }
             // Every copy has landed when the last products are done. Where a wait gave up they are given 2 ms.
             for (int i = 0; !ok && i < 200; ++i) __nanosleep(10000);
@@ -259,12 +266,12 @@ __host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs
 __device__ __forceinline__ bool split_piece(const SplitDeal& d, int i, Piece* q) {
     if (i >= d.pieces) return false;
     if (i < d.whole || d.parts == 1) {
-        *q = Piece{{}, {}, 0, 0, 0, d.stages, i, -1};
+        *q = Piece{{}, {}, 0, 0, 0, d.stages, i, -1, 0, 0};
         return true;
     }
     const int k = i - d.whole, part = k % d.parts;
     *q = Piece{{}, {}, 0, 0, (int)((int64_t)d.stages * part / d.parts), (int)((int64_t)d.stages * (part + 1) / d.parts),
-               d.whole + k / d.parts, k};
+               d.whole + k / d.parts, k, 0, 0};
     return true;
 }
 constexpr int64_t kPartFloats = (int64_t)kTile * kTile;  // of a part's sums, row by row

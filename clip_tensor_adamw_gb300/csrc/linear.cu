@@ -235,7 +235,7 @@ struct Logits {
     // rows first: h stays in L2 while W passes once
     __device__ __forceinline__ bool piece_at(const Deal& d, int i, Piece* q) const {
         if (i >= d.pieces) return false;
-        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, 0, stages, i, -1};
+        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, 0, stages, i, -1, 0, 0};
         return true;
     }
 };

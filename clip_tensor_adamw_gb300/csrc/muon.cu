@@ -12,6 +12,9 @@
 // singular values stay of order 1. They are scaled by 2^10, so that elements down to 2^-24 are normal. With a x folded into
 // B's diagonal the last product needs no other input. A result is off by 1.0e-3 to 1.6e-3 of its norm for gradients with
 // most of their energy in a few directions (bfloat16: 0.8e-2 to 1.5e-2).
+//
+// Where that is not enough (kPreciseSide, and on request) x, A and B are pairs of binary16, the second what the first's
+// rounding left out, and each product is three: high x high, high x low, low x high. A result is then off by some 1e-6.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,6 +33,10 @@ constexpr int64_t kBatchElements = (int64_t)128 << 20;
 constexpr int kItem = 8192;          // elements that a CTA of the streaming kernels has in registers
 constexpr int kMostItems = 2048;     // parts of a matrix's square sum
 constexpr float kScale = 1024.0f;
+// Matrices whose smaller side is at most this are held in pairs: a small matrix's elements are large beside a weight's, so the
+// error would show in a float32 weight (a step of rate r changes the weights' norm by r / 0.02 sqrt(side) of it or so), and
+// its products, a tile or a few for each matrix, are short.
+constexpr int kPreciseSide = 256;
 
 struct Class {
     CUtensorMap x[2], a, b;
@@ -37,6 +44,7 @@ struct Class {
     __half* pa;
     __half* pb;
     int rows, cols, count, first;    // first: of its matrices, in the batch
+    int low;                         // 0, or `count`: the low halves' first place in z
     int side, ld_x, ld_a;            // side: A's
     int gram_tiles, out_tiles;       // of a matrix
     int gram_before, out_before;     // tiles of the classes before
@@ -161,6 +169,9 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ B
     if (threadIdx.x == 0) squares[blockIdx.x] = sum;
 }
 
+// What rounding to binary16 leaves out.
+__device__ __forceinline__ float rest_of(float x) { return x - __half2float(__float2half_rn(x)); }
+
 // x = 2^10 u / (|u| + eps) in binary16, rows ld_x apart.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
@@ -194,6 +205,7 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
         __syncthreads();
     }
     __half* x = c.px[0] + (int64_t)it.z * c.rows * c.ld_x;
+    const int64_t low = (int64_t)c.low * c.rows * c.ld_x;
     for (int64_t at = it.from + threadIdx.x * 4; at < it.to; at += 1024) {
         const int there = it.to - at < 4 ? (int)(it.to - at) : 4;
         if (!skip) {
@@ -207,15 +219,22 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
             }
             const int64_t row = at / c.cols;
             const int col = (int)(at - row * c.cols);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] *= scale;
             if (even) {
-                store4(x + row * c.ld_x + col, make_float4(e[0] * scale, e[1] * scale, e[2] * scale, e[3] * scale), there, true);
+                __half* to = x + row * c.ld_x + col;
+                store4(to, make_float4(e[0], e[1], e[2], e[3]), there, true);
+                if (low) store4(to + low, make_float4(rest_of(e[0]), rest_of(e[1]), rest_of(e[2]), rest_of(e[3])), there, true);
             } else {
                 __half* to = x + row * c.ld_x;
                 int j = col;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (j == c.cols) j = 0, to += c.ld_x;
-                    if (i < there) to[j] = __float2half_rn(e[i] * scale);
+                    if (i < there) {
+                        to[j] = __float2half_rn(e[i]);
+                        if (low) to[j + low] = __float2half_rn(rest_of(e[i]));
+                    }
                     ++j;
                 }
             }
@@ -235,6 +254,12 @@ struct Where {
 __device__ __forceinline__ Where unpack(int tile) { return Where{tile & 7, tile >> 3}; }
 static_assert(kMostClasses <= 8, "a piece's class has three bits");
 
+// Tile (m, n) of a product over `depth`.
+__device__ __forceinline__ Piece piece_of(const Class& c, const Operand& a, const Operand& b, int m, int n, int depth, int tile) {
+    const int stages = (depth + kDepth - 1) / kDepth;
+    return Piece{a, b, m * kTile, n * kTile, 0, c.low ? 3 * stages : stages, tile, -1, c.low, stages};
+}
+
 // Tiles on and above the diagonal of a symmetric matrix, row by row.
 __device__ __forceinline__ void triangle(int t, int tiles, int* i, int* j) {
     int row = 0;
@@ -246,22 +271,36 @@ __device__ __forceinline__ void triangle(int t, int tiles, int* i, int* j) {
     *j = row + t;
 }
 
-// A symmetric matrix's tile, and its mirror image: v into rows [row0, ..) x columns [col0, ..) of the warp's 32 x 32.
-__device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, int row0, int col0, int lane,
-                                                unsigned char* staging, const float (&v)[32], bool mirror) {
+// v, or what its rounding leaves out, of the warp's 32 x 32 at row0 and col0 of a matrix of rows x cols.
+__device__ __forceinline__ void store_half(__half* to, int ld, int rows, int cols, int row0, int col0, int lane,
+                                           unsigned char* staging, const float (&v)[32], int64_t low) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
-    by_columns16(staging, lane, w, [&](int r, int col, uint4 x) {
-        if (row0 + r < side && col0 + col < side)  // (ld is a multiple of 8: the 16 bytes are the row's)
+    auto put = [&](int r, int col, uint4 x) {
+        if (row0 + r < rows && col0 + col < cols)  // (ld is a multiple of 8: the 16 bytes are the row's)
             *reinterpret_cast<uint4*>(to + (int64_t)(row0 + r) * ld + col0 + col) = x;
-    });
-    if (!mirror) return;
-    const __half* h = reinterpret_cast<const __half*>(w);
-    if (row0 + lane < side)
+    };
+    by_columns16(staging, lane, w, put);
+    if (!low) return;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (col0 + i < side) to[(int64_t)(col0 + i) * ld + row0 + lane] = h[i];
+    for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(rest_of(v[2 * i]), rest_of(v[2 * i + 1]));
+    to += low;
+    by_columns16(staging, lane, w, put);
+}
+
+// A symmetric matrix's tile, and its mirror image.
+__device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, int row0, int col0, int lane,
+                                                unsigned char* staging, const float (&v)[32], bool mirror, int64_t low) {
+    store_half(to, ld, side, side, row0, col0, lane, staging, v, low);
+    if (!mirror || row0 + lane >= side) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (col0 + i < side) {
+            __half* at = to + (int64_t)(col0 + i) * ld + row0 + lane;
+            *at = __float2half_rn(v[i]);
+            if (low) at[low] = __float2half_rn(rest_of(v[i]));
+        }
 }
 
 // A = x x^T or x^T x
@@ -281,7 +320,7 @@ struct Gram {
         triangle((i - c.gram_before) % c.gram_tiles, (c.side + kTile - 1) / kTile, &m, &n);
         const Operand x{&c.x[from], z, c.wide()};
         const int depth = c.wide() ? c.cols : c.rows;
-        *q = Piece{x, x, m * kTile, n * kTile, 0, (depth + kDepth - 1) / kDepth, z << 3 | k, -1};
+        *q = piece_of(c, x, x, m, n, depth, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -302,7 +341,7 @@ struct Gram {
             if (row0 >= c.side || col >= c.side) return;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kScale;
-            store_symmetric(to, c.ld_a, c.side, row0, col, lane, staging, v, mirror);
+            store_symmetric(to, c.ld_a, c.side, row0, col, lane, staging, v, mirror, (int64_t)c.low * c.side * c.ld_a);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -324,7 +363,7 @@ struct Poly {
         int m, n;
         triangle((i - c.gram_before) % c.gram_tiles, (c.side + kTile - 1) / kTile, &m, &n);
         const Operand a{&c.a, z, true};
-        *q = Piece{a, a, m * kTile, n * kTile, 0, (c.side + kDepth - 1) / kDepth, z << 3 | k, -1};
+        *q = piece_of(c, a, a, m, n, c.side, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -344,10 +383,8 @@ struct Poly {
             col0 = q.n0 + at.first_column;
             mirror = q.m0 != q.n0;
         }
-        __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
-            const int col = col0 + 32 * k, row = row0 + lane;
-            if (row0 >= c.side || col >= c.side) return;
-            const __half* own = a + (int64_t)row * c.ld_a + col;
+        // v += b times 32 columns of A
+        __device__ __forceinline__ void add_row(const __half* own, int row, int col, float (&v)[32]) const {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint4 u{};
@@ -357,16 +394,25 @@ struct Poly {
                 for (int e = 0; e < 4; ++e) {
                     const float2 x = __half22float2(h[e]);
                     const int j = 8 * i + 2 * e;
-                    v[j] = fmaf(v[j], p.cc, p.cb * x.x);
-                    v[j + 1] = fmaf(v[j + 1], p.cc, p.cb * x.y);
+                    v[j] = fmaf(p.cb, x.x, v[j]);
+                    v[j + 1] = fmaf(p.cb, x.y, v[j + 1]);
                 }
             }
+        }
+        __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
+            const int col = col0 + 32 * k, row = row0 + lane;
+            if (row0 >= c.side || col >= c.side) return;
+            const __half* own = a + (int64_t)row * c.ld_a + col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= p.cc;
+            add_row(own, row, col, v);
+            if (c.low) add_row(own + (int64_t)c.low * c.side * c.ld_a, row, col, v);
             if ((unsigned)(row - col) < 32u) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (row == col + i) v[i] += p.ca;
             }
-            store_symmetric(to, c.ld_a, c.side, row0, col, lane, staging, v, mirror);
+            store_symmetric(to, c.ld_a, c.side, row0, col, lane, staging, v, mirror, (int64_t)c.low * c.side * c.ld_a);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -387,8 +433,7 @@ struct Apply {
         const int z = (i - c.out_before) / c.out_tiles, t = (i - c.out_before) % c.out_tiles;
         const int row_tiles = (c.rows + kTile - 1) / kTile;
         const Operand x{&c.x[from], z, !c.wide()}, poly{&c.b, z, true};
-        *q = Piece{c.wide() ? poly : x, c.wide() ? x : poly, t % row_tiles * kTile, t / row_tiles * kTile,
-                   0, (c.side + kDepth - 1) / kDepth, z << 3 | k, -1};
+        *q = piece_of(c, c.wide() ? poly : x, c.wide() ? x : poly, t % row_tiles, t / row_tiles, c.side, z << 3 | k);
         return true;
     }
 };
@@ -408,13 +453,9 @@ struct ApplyMiddle : Apply {
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col0 = this->col0 + 32 * k;
             if (row0 >= c.rows || col0 >= c.cols) return;
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(v[2 * i] * (1.0f / kScale), v[2 * i + 1] * (1.0f / kScale));
-            by_columns16(staging, lane, w, [&](int r, int col, uint4 x) {
-                if (row0 + r < c.rows && col0 + col < c.cols)
-                    *reinterpret_cast<uint4*>(to + (int64_t)(row0 + r) * c.ld_x + col0 + col) = x;
-            });
+            for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kScale;
+            store_half(to, c.ld_x, c.rows, c.cols, row0, col0, lane, staging, v, (int64_t)c.low * c.rows * c.ld_x);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -509,7 +550,7 @@ std::vector<std::vector<Shape>> batches_of(const int64_t* rows, const int64_t* c
 }
 
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
-int64_t place(const std::vector<Shape>& shapes, char* base, Batch* b, double** squares) {
+int64_t place(const std::vector<Shape>& shapes, bool precise, char* base, Batch* b, double** squares) {
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* p = base ? base + at : nullptr;
@@ -524,11 +565,12 @@ int64_t place(const std::vector<Shape>& shapes, char* base, Batch* b, double** s
         c.count = (int)s.which.size();
         c.first = b->matrices;
         c.side = (int)std::min(s.rows, s.cols);
+        c.low = precise || c.side <= kPreciseSide ? c.count : 0;
         c.ld_x = (int)round_up(s.cols, 8);
         c.ld_a = (int)round_up(c.side, 8);
-        for (int i = 0; i < 2; ++i) c.px[i] = reinterpret_cast<__half*>(take((int64_t)c.count * c.rows * c.ld_x * 2));
-        c.pa = reinterpret_cast<__half*>(take((int64_t)c.count * c.side * c.ld_a * 2));
-        c.pb = reinterpret_cast<__half*>(take((int64_t)c.count * c.side * c.ld_a * 2));
+        for (int i = 0; i < 2; ++i) c.px[i] = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.rows * c.ld_x * 2));
+        c.pa = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
+        c.pb = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
         const int tiles = (c.side + kTile - 1) / kTile;
         c.gram_tiles = tiles * (tiles + 1) / 2;
         c.out_tiles = ((c.rows + kTile - 1) / kTile) * ((c.cols + kTile - 1) / kTile);
@@ -552,9 +594,9 @@ bool maps(Batch* b) {
     for (int k = 0; k < b->classes; ++k) {
         Class& c = b->c[k];
         for (int i = 0; i < 2; ++i)
-            if (!matrix_map(&c.x[i], type, c.px[i], c.cols, c.rows, c.ld_x, c.count)) return false;
-        if (!matrix_map(&c.a, type, c.pa, c.side, c.side, c.ld_a, c.count) ||
-            !matrix_map(&c.b, type, c.pb, c.side, c.side, c.ld_a, c.count))
+            if (!matrix_map(&c.x[i], type, c.px[i], c.cols, c.rows, c.ld_x, c.count + c.low)) return false;
+        if (!matrix_map(&c.a, type, c.pa, c.side, c.side, c.ld_a, c.count + c.low) ||
+            !matrix_map(&c.b, type, c.pb, c.side, c.side, c.ld_a, c.count + c.low))
             return false;
     }
     return true;
@@ -589,7 +631,7 @@ cudaError_t last(const Muon& call, const Batch& b, const std::vector<Shape>& sha
 cudaError_t run(const Muon& call, const std::vector<Shape>& shapes, char* workspace, int sms, void* stream) {
     Batch b;
     double* squares;
-    place(shapes, workspace, &b, &squares);
+    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, workspace, &b, &squares);
     if (!maps(&b)) return cudaErrorInvalidValue;
     Streams s{};
     int k = 0;
@@ -643,12 +685,12 @@ cudaError_t run(const Muon& call, const std::vector<Shape>& shapes, char* worksp
 
 }  // namespace
 
-int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T) {
+int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint32_t flags) {
     int64_t most = 0;
     for (const auto& shapes : batches_of(rows, cols, T)) {
         Batch b;
         double* squares;
-        most = std::max(most, place(shapes, nullptr, &b, &squares));
+        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, nullptr, &b, &squares));
     }
     return most;
 }

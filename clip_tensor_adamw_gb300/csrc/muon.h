@@ -22,7 +22,7 @@ struct Muon {
     const float* d_factor;
 };
 
-int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T);
+int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint32_t flags);
 // returns a cudaError_t
 int launch_muon(const Muon& c, void* workspace, int sms, void* stream);
 int read_muon_status(unsigned int* status);

@@ -28,6 +28,7 @@ mica_status check_sizes(const int64_t* rows, const int64_t* cols, int32_t T) {
 // polynomial of it, 2^10 times) must stay within its range.
 mica_status check_iteration(const mica_newton_schulz* ns) {
     if (!ns) return fail(MICA_ERR_NULL, "the iteration is NULL");
+    if (ns->flags & ~MICA_NS_PRECISE) return fail(MICA_ERR_HYPER, "unknown flags 0x%x of the iteration", ns->flags);
     if (!(ns->eps >= 1e-30 && ns->eps <= 1.0)) return fail(MICA_ERR_HYPER, "eps %g is outside [1e-30, 1]", ns->eps);
     if (ns->steps < 1 || ns->steps > MICA_MAX_NS_STEPS)
         return fail(MICA_ERR_HYPER, "steps = %d is outside [1, %d]", ns->steps, MICA_MAX_NS_STEPS);
@@ -133,7 +134,7 @@ mica_status orthogonalize(const void* const* x, void* const* out, const int64_t*
     Lists lists(dev);
     MICA_TRY(lists.add(out, rows, cols, T, 2, true, "out"));
     MICA_TRY(lists.add(x, rows, cols, T, bytes_of(x_dtype), false, "x", x_dtype == out_dtype ? out : nullptr));
-    MICA_TRY(check_workspace(workspace, workspace_bytes, muon_workspace(rows, cols, T), &lists));
+    MICA_TRY(check_workspace(workspace, workspace_bytes, muon_workspace(rows, cols, T, ns->flags), &lists));
     MICA_TRY(lists.disjoint());
     const Muon c{rows, cols, T, x, x_dtype, nullptr, out, out_dtype, ns, mica_muon_hp{}, nullptr};
     return after_launch(launch_muon(c, workspace, sm_count(dev), stream), stream, "orthogonalisation launch");
@@ -162,7 +163,7 @@ mica_status muon_steps(float* const* w, void* const* g, float* const* m, const i
     MICA_TRY(lists.add(g, rows, cols, T, bytes_of(g_dtype), hp->zero_grad != 0, "g"));
     MICA_TRY(lists.add(reinterpret_cast<const void* const*>(m), rows, cols, T, 4, true, "m"));
     if (d_factor) MICA_TRY(lists.add(d_factor, 4, 4, false, "d_factor"));
-    MICA_TRY(check_workspace(workspace, workspace_bytes, muon_workspace(rows, cols, T), &lists));
+    MICA_TRY(check_workspace(workspace, workspace_bytes, muon_workspace(rows, cols, T, ns->flags), &lists));
     MICA_TRY(lists.disjoint());
     const Muon c{rows, cols, T, const_cast<const void* const*>(g), g_dtype, m, reinterpret_cast<void* const*>(w), MICA_F32,
                  ns, *hp, d_factor};
@@ -174,9 +175,9 @@ mica_status muon_steps(float* const* w, void* const* g, float* const* m, const i
 
 using namespace mica;
 
-extern "C" int64_t mica_newton_schulz_workspace(const int64_t* rows, const int64_t* cols, int32_t T) {
+extern "C" int64_t mica_newton_schulz_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint32_t flags) {
     try {
-        return check_sizes(rows, cols, T) == MICA_OK ? muon_workspace(rows, cols, T) : 0;
+        return check_sizes(rows, cols, T) == MICA_OK ? muon_workspace(rows, cols, T, flags) : 0;
     } catch (const std::bad_alloc&) {
         return 0;
     }

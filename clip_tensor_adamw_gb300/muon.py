@@ -20,7 +20,7 @@ _P, _I32, _I64, _F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c
 
 
 class _NewtonSchulz(ctypes.Structure):
-    _fields_ = [("coefficients", ctypes.POINTER(_F64)), ("eps", _F64), ("steps", _I32), ("reserved", _I32)]
+    _fields_ = [("coefficients", ctypes.POINTER(_F64)), ("eps", _F64), ("steps", _I32), ("flags", ctypes.c_uint32)]
 
 
 class _MuonHP(ctypes.Structure):
@@ -37,7 +37,7 @@ def _muon() -> ctypes.CDLL:
         L = lib()
         array, sizes, ns = ctypes.POINTER(_P), ctypes.POINTER(_I64), ctypes.POINTER(_NewtonSchulz)
         for name, args, result in (
-                ("mica_newton_schulz_workspace", [sizes, sizes, _I32], _I64),
+                ("mica_newton_schulz_workspace", [sizes, sizes, _I32, ctypes.c_uint32], _I64),
                 ("mica_orthogonalize", [array, array, sizes, sizes, _I32, _I32, _I32, ns, _P, _I64, _P], ctypes.c_int),
                 ("mica_muon_steps", [array, array, array, sizes, sizes, _I32, _I32, ctypes.POINTER(_MuonHP), ns, _P, _P,
                                      _I64, _P], ctypes.c_int)):
@@ -47,26 +47,26 @@ def _muon() -> ctypes.CDLL:
     return _lib
 
 
-def _sizes(L: TensorList, what: str):
+def _sizes(L: TensorList, what: str, precise: bool):
     """The rows and columns of a list's matrices, and the workspace that they take (kept with the list)."""
-    if getattr(L, "matrices", None) is None:
+    kept = L.__dict__.setdefault("matrices", {})
+    if precise not in kept:
         for i, t in enumerate(L.tensors):
             if t.ndim != 2:
                 raise ValueError(f"{what}[{i}] must have two dimensions, not {t.ndim}")
         rows, cols = ((ctypes.c_int64 * max(L.T, 1))(*(t.shape[d] for t in L.tensors)) for d in (0, 1))
-        size = _muon().mica_newton_schulz_workspace(rows, cols, L.T)
-        L.matrices = rows, cols, size
-    return L.matrices
+        kept[precise] = rows, cols, _muon().mica_newton_schulz_workspace(rows, cols, L.T, int(precise))
+    return kept[precise]
 
 
-def _iteration(steps: int, coefficients, eps: float) -> _NewtonSchulz:
+def _iteration(steps: int, coefficients, eps: float, precise: bool) -> _NewtonSchulz:
     rows = list(coefficients)
     if not hasattr(rows[0], "__len__"):
         rows = [rows] * steps
     if len(rows) != steps or any(len(r) != 3 for r in rows):
         raise ValueError("coefficients must be (a, b, c), or one such triple for each step")
     flat = [float(v) for r in rows for v in r]
-    return _NewtonSchulz((_F64 * max(len(flat), 1))(*flat), float(eps), int(steps), 0)
+    return _NewtonSchulz((_F64 * max(len(flat), 1))(*flat), float(eps), int(steps), int(precise))
 
 
 def _same(A: TensorList, B: TensorList, names: str) -> None:
@@ -75,15 +75,16 @@ def _same(A: TensorList, B: TensorList, names: str) -> None:
 
 
 def mica_orthogonalize(x, out=None, *, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7,
-                       out_dtype: torch.dtype | None = None, stream=None) -> TensorList:
+                       precise: bool = False, out_dtype: torch.dtype | None = None, stream=None) -> TensorList:
     """Each matrix of ``x`` (float32, float16 or bfloat16, contiguous) taken by ``steps`` Newton-Schulz products towards
     the nearest one with orthogonal rows or columns, in one go for the whole list: the direction of a Muon update.
     ``coefficients``: (a, b, c) of the polynomial a t + b t^3 + c t^5 that each singular value goes through in a step, or
-    one such triple for each step. ``out`` takes the results (float16 or bfloat16; it may be ``x`` itself); otherwise
+    one such triple for each step. ``precise`` holds what is stored between the products in pairs of float16 (three times
+    the work), as matrices whose smaller side is at most 256 always are. ``out`` takes the results (float16 or bfloat16; it may be ``x`` itself); otherwise
     they are new matrices of ``out_dtype`` (by default x's, or bfloat16 for float32). Returns the list of results."""
     X = _as_list(x)
-    rows, cols, size = _sizes(X, "x")
-    ns = _iteration(steps, coefficients, eps)
+    rows, cols, size = _sizes(X, "x", precise)
+    ns = _iteration(steps, coefficients, eps, precise)
     code = _TYPES.get(X.dtype, 0 if X.dtype is None else None)
     if code is None:
         raise TypeError(f"x: unsupported dtype {X.dtype}")
@@ -106,7 +107,7 @@ def mica_orthogonalize(x, out=None, *, steps: int = 5, coefficients=COEFFICIENTS
 def mica_muon_steps(w, g, m, *, lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True,
                     adjust: str = "original", factor: torch.Tensor | None = None, zero_grad: bool = False,
                     skip_nonfinite: bool = False, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7,
-                    stream=None) -> None:
+                    precise: bool = False, stream=None) -> None:
     """One Muon step over a list of weight matrices, in place: m += (1 - momentum) (factor g - m), u the Nesterov blend of
     both (or m), w = w (1 - lr weight_decay) - lr adjust(w) orthogonalised(u). ``w`` and ``m``: float32, ``g``: float32 or
     float16; ``factor``: the device scalar from mica_clip_grad_norms (None: 1). ``adjust``: what a matrix's rate is
@@ -120,13 +121,13 @@ def mica_muon_steps(w, g, m, *, lr: float, momentum: float = 0.95, weight_decay:
     _same(W, M, "w and m")
     if adjust not in _ADJUST:
         raise ValueError(f"adjust {adjust!r} is none of {sorted(_ADJUST)}")
-    rows, cols, size = _sizes(W, "w")
+    rows, cols, size = _sizes(W, "w", precise)
     gdt = _dtype_code(G, "g")
     if gdt not in (MICA_F32, MICA_F16):
         raise TypeError(f"g: unsupported dtype {G.dtype}")
     hp = _MuonHP(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)), _ADJUST[adjust], int(bool(zero_grad)),
                  MICA_STEP_SKIP_NONFINITE if skip_nonfinite else 0)
-    ns = _iteration(steps, coefficients, eps)
+    ns = _iteration(steps, coefficients, eps, precise)
     dev = W.tensors[0].device if W.T else torch.device("cuda", torch.cuda.current_device())
     with _On(stream, dev) as s:
         work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None

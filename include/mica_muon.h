@@ -34,19 +34,22 @@ extern "C" {
  * singular values that can occur (MICA_ERR_HYPER otherwise).
  * x, G and the polynomial of G are held in binary16 between the products (scaled by 2^10; products are exact and summed in
  * float32), which takes a result some 2^-9 to 2^-10 of its norm off; directions whose singular values in u are a thousand
- * times below the largest get correspondingly less accurate. A zero matrix gives zeros; a matrix with an infinity or a NaN
- * gives NaNs.
+ * times below the largest get correspondingly less accurate. With MICA_NS_PRECISE, and always for matrices whose smaller side
+ * is at most 256, they are held in pairs of binary16, at three times the operations, for results some 2^-19 off before they
+ * are rounded to out's type. A zero matrix gives zeros; a matrix with an infinity or a NaN gives NaNs.
  */
+#define MICA_NS_PRECISE 1u
 typedef struct {
     const double* coefficients; /* host, 3 * steps, finite */
     double eps;                 /* [1e-30, 1] */
     int32_t steps;              /* [1, MICA_MAX_NS_STEPS] */
-    int32_t reserved;           /* 0 */
+    uint32_t flags;             /* MICA_NS_PRECISE or 0 */
 } mica_newton_schulz;
 
-/* The workspace of both calls for a list of these sizes, in bytes (the pointer 16-byte aligned): some 4 bytes an element, of
- * at most some 128 M elements or the largest matrix at a time, and 4 bytes x the smaller side squared. */
-MICA_API int64_t mica_newton_schulz_workspace(const int64_t* rows, const int64_t* cols, int32_t T);
+/* The workspace of both calls for a list of these sizes and the iteration's flags, in bytes (the pointer 16-byte aligned):
+ * some 4 bytes an element, of at most 128 M elements or the largest matrix at a time, and 4 bytes x the smaller side
+ * squared; twice that for matrices held in pairs. */
+MICA_API int64_t mica_newton_schulz_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint32_t flags);
 
 /*
  * out[k] = the iterate of x[k]. x: MICA_F32, MICA_F16 or MICA_BF16; out: MICA_F16 or MICA_BF16; out[k] may be x[k] where

@@ -1,17 +1,14 @@
 """The orthogonalised step against its definition in float64, over shapes, types, options and the values that end in
 infinities and NaNs.
 
-Tolerances. x, G = x x^T and B = a I + b G + c G^2 are rounded to binary16 in each step: each is off by at most half a unit in
-the last place, relative 2^-11, element by element, and (as independent roundings) by e = 2^-11 / sqrt(3) of its Frobenius norm
-or less. Follow a step to first order, with s the largest singular value (at most 1.2), |B| at most 3.45 in the spectral norm
-and |G| at most 1.44, and X the relative Frobenius error of x before it:
-  dG = 2 s dx + e |G|,  dB = (|b| + 2 |c| |G|) dG + e |B|,  dx' = |B| dx + |dB| |x| + e |x'|
-which, fed with worst cases, grows without saying anything (a factor of some 30 a step); the actual error is that of the
-polynomial's condition. So the bound is measured in the model itself: the same iteration in float64 with every stored matrix
-rounded to binary16 (`stored`), whose distance from the definition is what these roundings do to this very input. The
-kernels round the same things; only sums differ, by 2^-20 or so, which flips some of those roundings. Two such runs are two
-draws of the same error, so a kernel's distance is held to twice the model's, plus the output's own rounding (2^-8 or 2^-11
-relative per element; 1 / sqrt(3) of it or less in the norm).
+Tolerances. x, G = x x^T and B = a I + b G + c G^2 are rounded to binary16 in each step, or (where the smaller side is at most
+256, and with `precise`) to a pair of binary16. What a rounding does to the end depends on the polynomial's condition at this
+very input, and worst-case bounds grow by some 30 a step without saying anything. So it is measured in a model: the same
+iteration in float64 with every stored matrix so rounded (`stored`), whose distance D from the definition is what these
+roundings do. The kernels round the same things; their float32 sums differ and flip some of those roundings, so theirs is
+another draw of the same error: twice the model's is allowed. In pairs the sums themselves count: over K terms they truncate at
+most (K / 16 + 4) 2^-23 of their size, where one binary16 rounds 2^-12, and errors this small act in proportion: D of single
+binary16 times (K / 16 + 4) 2^-11. Then the output's own rounding (2^-8 or 2^-11 relative per element, less in the norm).
 """
 import math
 
@@ -50,17 +47,25 @@ def half(x):
     return (x * 1024.0).half().double() / 1024.0
 
 
-def stored(u, **kw):
-    return iterate(u, keep=half, **kw)
+def pair(x):
+    return half(x) + half(x - half(x))
 
 
 def distance(a, b):
     return float((a.double() - b).norm())
 
 
-def check(got, u, **kw):
+def off(u, want, precise=False, **kw):
+    """How far a result may be from the definition's before its own rounding."""
+    single = distance(iterate(u, keep=half, **kw), want)
+    if not precise and min(u.shape) > 256:
+        return 2.0 * single
+    return 2.0 * distance(iterate(u, keep=pair, **kw), want) + single * (max(u.shape) / 16 + 4) * 2.0 ** -11
+
+
+def check(got, u, precise=False, **kw):
     want = iterate(u, **kw)
-    most = 2.0 * distance(stored(u, **kw), want) + HALF[got.dtype] * float(want.norm()) + 1e-6
+    most = off(u, want, precise, **kw) + HALF[got.dtype] * float(want.norm()) + 1e-6
     assert distance(got, want) <= most, (tuple(u.shape), distance(got, want), most)
 
 
@@ -76,6 +81,18 @@ def test_one_matrix(shape, dtype):
         r = mica.mica_orthogonalize([x], out_dtype=out)
         assert r.tensors[0].dtype == out
         check(r.tensors[0], x)
+
+
+@pytest.mark.parametrize("shape", [(300, 257), (257, 300), (1201, 777), (777, 1201), (600, 600)], ids=str)
+def test_precise(shape):
+    """Pairs of binary16 for larger matrices: what is left of a tiny singular value's direction shows the difference."""
+    g = gen(7)
+    x = torch.randn(shape, generator=g, device="cuda")
+    u, s, v = torch.linalg.svd(x, full_matrices=False)
+    x = (u * torch.logspace(0, -3, len(s), device="cuda")) @ v
+    r = mica.mica_orthogonalize([x], out_dtype=torch.float16, precise=True).tensors[0]
+    check(r, x, precise=True)
+    check(mica.mica_orthogonalize([x], out_dtype=torch.float16).tensors[0], x)
 
 
 def test_singular_values_end_near_one():
@@ -99,8 +116,8 @@ def test_a_list_is_its_matrices(dtype):
 
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("gdt", [torch.float32, torch.float16], ids=str)
-@pytest.mark.parametrize("adjust", ["none", "original", "match_rms_adamw"])
-def test_steps(adjust, gdt, nesterov):
+@pytest.mark.parametrize("adjust,precise", [("none", False), ("original", True), ("match_rms_adamw", False)])
+def test_steps(adjust, precise, gdt, nesterov):
     g = gen(3)
     shapes = [(100, 333), (333, 100), (64, 64), (1, 57), (257, 300)]
     scale = 1024.0 if gdt is torch.float16 else 1.0
@@ -113,7 +130,7 @@ def test_steps(adjust, gdt, nesterov):
         before_w, before_m, kept = [t.clone() for t in w], [t.clone() for t in m], [t.clone() for t in grads]
         zero = step == 1
         mica.mica_muon_steps(w, grads, m, lr=lr, momentum=mu, weight_decay=wd, nesterov=nesterov, adjust=adjust, factor=factor,
-                             zero_grad=zero)
+                             zero_grad=zero, precise=precise)
         for k, (r, c) in enumerate(shapes):
             gh = kept[k].double() * factor.double()
             want_m = before_m[k].double() + (1 - mu) * (gh - before_m[k].double())
@@ -123,6 +140,6 @@ def test_steps(adjust, gdt, nesterov):
                          0.2 * math.sqrt(max(r, c)) if adjust == "match_rms_adamw" else 1.0)
             o = iterate(u)
             want = before_w[k].double() * (1 - lr * wd) - rate * o
-            most = 2.0 * rate * distance(stored(u), o) + 8 * U * float(before_w[k].double().norm() + rate * o.norm()) + 1e-6 * rate
+            most = rate * off(u, o, precise) + 8 * U * float(before_w[k].double().norm() + rate * o.norm()) + 1e-6 * rate
             assert distance(w[k], want) <= most, (k, distance(w[k], want), most)
             assert not grads[k].any() if zero else torch.equal(grads[k], kept[k])
