@@ -246,19 +246,30 @@ struct SplitDeal {
     int tiles, stages, whole, parts, pieces;
 };
 
-// least: stages that a part should have to be worth the launch that joins the parts
-__host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs, int least) {
+// The number of parts is the one that makes the rest shortest by this count, in stages: rounds of parts, each with a part's
+// stages and kPartCost for filling and emptying it; and what joining takes, kJoinCost and a quarter of a stage for each part
+// (512 KB written and read). 48 tiles of 786 stages on 76 pairs: 1 part 221 us, 3 parts (2 rounds) 150 us.
+constexpr int kPartCost = 6, kJoinCost = 12, kLeastStages = 4, kMostRounds = 3;
+__host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs) {
     SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles};
     const int rest = tiles - d.whole;
     if (stages == 0) {  // nothing to add up: what joins the parts writes every tile
         d.whole = d.parts = d.pieces = 0;
         return d;
     }
-    if (rest) {
-        d.parts = pairs / rest < stages / least ? pairs / rest : stages / least;
-        if (d.parts < 1) d.parts = 1;
-        d.pieces = d.whole + rest * d.parts;
+    if (rest == 0) return d;
+    int best = stages + kPartCost;
+    for (int rounds = 1; rounds <= kMostRounds; ++rounds) {
+        int parts = rounds * pairs / rest;
+        if (parts > stages / kLeastStages) parts = stages / kLeastStages;
+        if (parts < 2) continue;
+        const int cost = rounds * ((stages + parts - 1) / parts + kPartCost) + kJoinCost + rest * parts / 4;
+        if (cost < best) {
+            best = cost;
+            d.parts = parts;
+        }
     }
+    d.pieces = d.whole + rest * d.parts;
     return d;
 }
 
@@ -280,19 +291,20 @@ constexpr int64_t kPartFloats = (int64_t)kTile * kTile;  // of a part's sums, ro
 // from a row to a thread, to coalesced accesses
 // ------------------------------------------------------------------------------------------------------------------------
 
-// 32 rows x 32 float32 of a warp, a row to a lane, handed on as four columns of a row at a time, eight lanes to a row:
-// put(row, column, values). Through shared memory, whose 16-byte units change places so that no two lanes of a phase meet.
-template <typename Put>
-__device__ __forceinline__ void by_columns(unsigned char* staging, int lane, const float (&v)[32], Put put) {
+// 32 rows x 32 float32 of a warp, a row to a lane, turned to four columns of a row at a time, eight lanes to a row: x[i] is
+// row 4 i + lane / 8, columns 4 (lane % 8) on. Through shared memory, whose 16-byte units change places so that no two lanes of
+// a phase meet.
+__device__ __forceinline__ void by_columns(unsigned char* staging, int lane, const float (&v)[32], float4 (&x)[8]) {
     float4* s = reinterpret_cast<float4*>(staging);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     __syncwarp();
+    const int j = lane % 8;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-        const int row = it * 4 + lane / 8, j = lane % 8;
-        put(row, j * 4, s[row * 8 + (j ^ (row & 7))]);
+    for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + lane / 8;
+        x[i] = s[row * 8 + (j ^ (row & 7))];
     }
 }
 
@@ -306,21 +318,50 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// 32 rows x 32 elements of 16 bits of a warp, a row to a lane, handed on as eight columns of a row at a time, four lanes to a
-// row: put(row, column, 16 bytes).
-template <typename Put>
-__device__ __forceinline__ void by_columns16(unsigned char* staging, int lane, const uint32_t (&v)[16], Put put) {
+// 32 rows x 32 elements of 16 bits of a warp, a row to a lane, turned to eight columns of a row at a time, four lanes to a row:
+// x[i] is row 8 i + lane / 4, columns 8 (lane % 4) on.
+__device__ __forceinline__ void by_columns16(unsigned char* staging, int lane, const uint32_t (&v)[16], uint4 (&x)[4]) {
     uint4* s = reinterpret_cast<uint4*>(staging);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         s[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     __syncwarp();
+    const int j = lane % 4;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int row = it * 8 + lane / 4, j = lane % 4;
-        put(row, j * 8, s[row * 4 + (j ^ ((row >> 1) & 3))]);
+    for (int i = 0; i < 4; ++i) {
+        const int row = i * 8 + lane / 4;
+        x[i] = s[row * 4 + (j ^ ((row >> 1) & 3))];
     }
+}
+
+// Eight elements of 16 bits to a row, of which `there` are in the matrix; wide: rows are aligned for one store.
+__device__ __forceinline__ void store8(unsigned short* at, uint4 x, int there, bool wide) {
+    if (wide && there >= 8) {
+        *reinterpret_cast<uint4*>(at) = x;
+        return;
+    }
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < there) at[i] = (unsigned short)(w[i / 2] >> (i % 2 * 16));
+}
+
+// The warp's 32 x 32 elements of 16 bits at (row0, col0) of a matrix whose first `rows` x `cols` are written.
+__device__ __forceinline__ void store_block(unsigned short* to, int64_t ld, int rows, int cols, int row0, int col0, int lane,
+                                            bool wide, unsigned char* staging, const uint32_t (&v)[16]) {
+    uint4 x[4];
+    by_columns16(staging, lane, v, x);
+    const int row = row0 + lane / 4, col = col0 + lane % 4 * 8;
+    unsigned short* at = to + row * ld + col;
+    if (wide && row0 + 32 <= rows && col0 + 32 <= cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + i * 8 * ld) = x[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (row + i * 8 < rows && col < cols) store8(at + i * 8 * ld, x[i], cols - col, wide);
 }
 
 // Four values to a row of O, the first at `at`, of which `there` are in the matrix; wide: rows are aligned for one store.

@@ -22,10 +22,9 @@ namespace mica {
 namespace {
 
 constexpr int kScanThreads = 1024, kScanItems = 8;
-constexpr int64_t kGradBytes = (int64_t)512 << 20;  // of d, that a piece of the rows takes
+constexpr int64_t kGradBytes = (int64_t)1 << 30;   // of d, that a piece of the rows takes
 constexpr int64_t kStatBytes = (int64_t)256 << 20;  // of the forward pass's maxima and sums
 constexpr int kMostRows = 16384;                    // of a piece in the forward pass
-constexpr int kLeastStages = 16;                    // of a part of a split tile
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What the scan of the targets leaves for the kernels after it.
@@ -241,7 +240,8 @@ struct Logits {
 };
 
 struct LogitSums : Logits {
-    RowSum* sums;  // [vocabulary / 128][most]
+    RowSum* sums;  // [most][vocabulary / 128]
+    int parts;
     float* at;     // [most] the targets' logits
 
     __device__ __forceinline__ bool piece(const Deal& d, int i, Piece* q) const { return piece_at(d, i, q); }
@@ -285,7 +285,7 @@ struct LogitSums : Logits {
             s.sum += (part[0] + part[1]) + (part[2] + part[3]);
         }
         __device__ __forceinline__ void done() {
-            if (live && column < p.vocab) p.sums[(int64_t)(column / kHalf) * p.most + row] = s;
+            if (live && column < p.vocab) p.sums[(int64_t)row * p.parts + column / kHalf] = s;
         }
     };
 };
@@ -307,22 +307,21 @@ __device__ __forceinline__ RowSum operator+(RowSum x, RowSum y) {
     return RowSum{o, x.sum * exp2_fast(x.origin - o) + y.sum * exp2_fast(y.origin - o)};
 }
 
-// 32 rows to a CTA, whose warps take parts of the vocabulary in turn; joined in a fixed order.
+// A warp to a row; joined in a fixed order.
 __global__ void __launch_bounds__(256) join_rows_kernel(Join j) {
-    __shared__ RowSum part[8][32];
     wait_prerequisite();
     allow_dependents();
     const Span span = span_of(j.meta->count, j.most, j.piece);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row = blockIdx.x * 32 + lane;
-    if (blockIdx.x * 32 >= span.rows) return;
+    const int lane = threadIdx.x % 32, row = blockIdx.x * 8 + threadIdx.x / 32;
+    if (row >= span.rows) return;
     RowSum s{-1e38f, 0.0f};
-    if (row < span.rows)
-#pragma unroll 8
-        for (int k = warp; k < j.parts; k += 8) s = s + j.sums[(int64_t)k * j.most + row];
-    part[warp][lane] = s;
-    __syncthreads();
-    if (warp || row >= span.rows) return;
-    for (int i = 1; i < 8; ++i) s = s + part[i][lane];
+    const RowSum* own = j.sums + (int64_t)row * j.parts;
+#pragma unroll 4
+    for (int k = lane; k < j.parts; k += 32) s = s + own[k];
+#pragma unroll
+    for (int d = 16; d; d /= 2)
+        s = s + RowSum{__shfl_xor_sync(~0u, s.origin, d), __shfl_xor_sync(~0u, s.sum, d)};
+    if (lane) return;
     const int64_t i = j.index[span.from + row];
     const float l = log2f(s.sum);
     j.logps[i] = j.target[row] < 0 ? NAN : (fmaf(j.at[row], j.a, -s.origin) - l) * kLn2;
@@ -381,7 +380,7 @@ struct LogitGrad : Logits {
         bool live;
         float c, origin;
         unsigned char* staging;
-        T* to;
+        unsigned short* to;
         __device__ __forceinline__ Epilogue(const LogitGrad& p, const Deal& d, const Piece& q, const Place& at)
             : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), lane(at.lane), staging(at.staging) {
             live = row < d.rows;
@@ -389,7 +388,7 @@ struct LogitGrad : Logits {
             c = live ? p.coef[row] : 0.0f;
             origin = live ? p.origin[row] : 0.0f;
             stored = (d.rows + 63) / 64 * 64 - (row - lane);  // rows of the warp's 32 that the weight gradient reads
-            to = p.d + (int64_t)(row - lane) * p.ld;
+            to = reinterpret_cast<unsigned short*>(p.d) + (int64_t)(row - lane) * p.ld;
         }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int first = column + 32 * k;
@@ -404,9 +403,7 @@ struct LogitGrad : Logits {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = live ? pack2<T>(v[2 * i], v[2 * i + 1]) : 0u;  // (whatever z was)
-            by_columns16(staging, lane, w, [&](int r, int col, uint4 x) {
-                if (r < stored && first + col < p.ld) *reinterpret_cast<uint4*>(to + (int64_t)r * p.ld + first + col) = x;
-            });
+            store_block(to, p.ld, stored, p.ld, 0, first, lane, true, staging, w);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -425,7 +422,7 @@ struct HiddenGrad {
     int most, piece_index, vocab, features;
     T* dh;
     int64_t ld;
-    int wide;
+    int wide, wide16;  // rows aligned for stores of four elements, of eight
     float* parts;
 
     struct Deal : SplitDeal {
@@ -439,7 +436,7 @@ struct HiddenGrad {
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
         static_cast<SplitDeal&>(r) = split_deal((span.rows + kTile - 1) / kTile * column_tiles, (vocab + kDepth - 1) / kDepth,
-                                                pairs, kLeastStages);
+                                                pairs);
         r.span = span;
         r.column_tiles = column_tiles;
         r.scale = m.inv_scale;
@@ -454,11 +451,29 @@ struct HiddenGrad {
         q->b = Operand{&w, 0, false};
         return true;
     }
-    // four sums of row `row` of the tile at (m0, n0)
+    __device__ __forceinline__ int rows_of(const Deal& r) const { return r.span.rows; }
+    // four sums of a row
     __device__ __forceinline__ void put(const Deal& r, int row, int col, float4 v) const {
         if (row >= r.span.rows || col >= features) return;
         const float s = r.scale;
-        store4<T>(dh + index[r.span.from + row] * ld + col, make_float4(v.x * s, v.y * s, v.z * s, v.w * s), features - col, wide);
+        store4<T>(dh + index[r.span.from + row] * ld + col, make_float4(v.x * s, v.y * s, v.z * s, v.w * s), features - col,
+                  wide);
+    }
+    // a warp's 32 x 32 of them
+    __device__ __forceinline__ void block(const Deal& r, int row0, int col0, const Place& at, float (&v)[32]) const {
+        if (row0 >= r.span.rows || col0 >= features) return;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * r.scale, v[2 * i + 1] * r.scale);
+        uint4 x[4];
+        by_columns16(at.staging, at.lane, w, x);
+        const int row = row0 + at.lane / 4, col = col0 + at.lane % 4 * 8;
+        if (col >= features) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row + 8 * i < r.span.rows)
+                store8(reinterpret_cast<unsigned short*>(dh + index[r.span.from + row + 8 * i] * ld + col), x[i], features - col,
+                       wide16);
     }
     __device__ __forceinline__ void tile_at(const Deal& r, int tile, int* m0, int* n0) const {
         *m0 = tile / r.column_tiles * kTile;
@@ -480,7 +495,7 @@ struct WeightGrad {
     int64_t ld_add;
     float* sums;   // null where there is one piece only
     int64_t ld_sums;
-    int wide, wide_add, wide_sums;
+    int wide, wide16, wide_add, wide_sums;
     float* parts;
 
     struct Deal : SplitDeal {
@@ -494,7 +509,7 @@ struct WeightGrad {
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
         static_cast<SplitDeal&>(r) = split_deal((vocab + kTile - 1) / kTile * column_tiles, (span.rows + kDepth - 1) / kDepth,
-                                                pairs, kLeastStages);
+                                                pairs);
         r.column_tiles = column_tiles;
         r.first = piece_index == 0;
         r.last = last_span(m.count, most, piece_index);
@@ -514,13 +529,52 @@ struct WeightGrad {
         if (row >= vocab || col >= features) return;
         const int there = features - col;
         const float s = r.scale;
-        v = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
         float4 a{};
         if (!r.first) a = load4(sums + row * ld_sums + col, there, wide_sums);
         else if (add) a = load4(add + row * ld_add + col, there, wide_add);
-        v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+        v = make_float4(fmaf(v.x, s, a.x), fmaf(v.y, s, a.y), fmaf(v.z, s, a.z), fmaf(v.w, s, a.w));  // (s: a power of two)
         if (r.last) store4<O>(dw + row * ld + col, v, there, wide);
         else store4<float>(sums + row * ld_sums + col, v, there, wide_sums);
+    }
+    __device__ __forceinline__ int rows_of(const Deal&) const { return vocab; }
+    __device__ __forceinline__ void block(const Deal& r, int row0, int col0, const Place& at, float (&v)[32]) const {
+        if (row0 >= vocab || col0 >= features) return;
+        if constexpr (sizeof(O) == 2) {
+            if (r.first && r.last && !add) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack2<O>(v[2 * i] * r.scale, v[2 * i + 1] * r.scale);
+                store_block(reinterpret_cast<unsigned short*>(dw), ld, vocab, features, row0, col0, at.lane, wide16, at.staging, w);
+                return;
+            }
+        }
+        float4 x[8];
+        by_columns(at.staging, at.lane, v, x);
+        const int row = row0 + at.lane / 8, col = col0 + at.lane % 8 * 4;
+        if (!(wide && wide_sums && wide_add && row0 + 32 <= vocab && col0 + 32 <= features)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) put(r, row + 4 * i, col, x[i]);
+            return;
+        }
+        float4 a[8] = {};
+        if (!r.first) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = load4(sums + (row + 4 * i) * ld_sums + col, 4, true);
+        } else if (add) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = load4(add + (row + 4 * i) * ld_add + col, 4, true);
+        }
+        const float s = r.scale;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = make_float4(fmaf(x[i].x, s, a[i].x), fmaf(x[i].y, s, a[i].y), fmaf(x[i].z, s, a[i].z), fmaf(x[i].w, s, a[i].w));
+        if (r.last) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store4<O>(dw + (row + 4 * i) * ld + col, x[i], 4, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store4<float>(sums + (row + 4 * i) * ld_sums + col, x[i], 4, true);
+        }
     }
     __device__ __forceinline__ void tile_at(const Deal& r, int tile, int* m0, int* n0) const {
         *m0 = tile / r.column_tiles * kTile;  // columns first: h stays in L2 while d passes once
@@ -540,19 +594,23 @@ struct Split : G {
             : p(p), deal(deal), q(q), at(at) {}
         __device__ __forceinline__ void chunk(int c, float (&v)[32]) {
             const int row0 = at.row - at.lane, col0 = at.first_column + 32 * c;
-            by_columns(at.staging, at.lane, v, [&](int row, int col, float4 x) {
-                if (q.part < 0)
-                    p.put(deal, q.m0 + row0 + row, q.n0 + col0 + col, x);
-                else
-                    *reinterpret_cast<float4*>(p.parts + q.part * kPartFloats + (row0 + row) * kTile + col0 + col) = x;
-            });
+            if (q.part < 0) {
+                p.block(deal, q.m0 + row0, q.n0 + col0, at, v);
+                return;
+            }
+            if (q.m0 + row0 >= p.rows_of(deal) || q.n0 + col0 >= p.features) return;
+            float4 x[8];
+            by_columns(at.staging, at.lane, v, x);
+            float* to = p.parts + q.part * kPartFloats + (row0 + at.lane / 8) * kTile + col0 + at.lane % 8 * 4;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(to + i * 4 * kTile) = x[i];
         }
         __device__ __forceinline__ void done() {}
     };
 };
 
-// Joins the parts of split tiles, 16 rows to a CTA at a time; where nothing is added up (no rows) every tile.
-constexpr int kJoinRows = 16;
+// Joins the parts of split tiles, 4 rows to a CTA at a time; where nothing is added up (no rows) every tile.
+constexpr int kJoinRows = 4;
 template <typename G>
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Split<G> p, int pairs) {
     wait_prerequisite();
@@ -560,21 +618,20 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
     const typename G::Deal deal = p.deal(pairs);
     if (deal.parts == 1 || p.empty(deal)) return;
     const int64_t all = (int64_t)(deal.tiles - deal.whole) * (kTile / kJoinRows);
+    const int col = threadIdx.x % 64 * 4;
     for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
-        const int k = (int)(u / (kTile / kJoinRows)), row0 = (int)(u % (kTile / kJoinRows)) * kJoinRows;
+        const int k = (int)(u / (kTile / kJoinRows)), row = (int)(u % (kTile / kJoinRows)) * kJoinRows + threadIdx.x / 64;
         int m0, n0;
         p.tile_at(deal, deal.whole + k, &m0, &n0);
-#pragma unroll
-        for (int i = 0; i < kJoinRows / 4; ++i) {
-            const int row = row0 + i * 4 + threadIdx.x / 64, col = threadIdx.x % 64 * 4;
-            float4 s{};
-            for (int part = 0; part < deal.parts; ++part) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    p.parts + ((int64_t)k * deal.parts + part) * kPartFloats + row * kTile + col));
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-            }
-            p.put(deal, m0 + row, n0 + col, s);
+        if (m0 + row >= p.rows_of(deal) || n0 + col >= p.features) continue;
+        const float* from = p.parts + (int64_t)k * deal.parts * kPartFloats + row * kTile + col;
+        float4 s{};
+#pragma unroll 8
+        for (int part = 0; part < deal.parts; ++part) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + part * kPartFloats));
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
         }
+        p.put(deal, m0 + row, n0 + col, s);
     }
 }
 
@@ -670,7 +727,7 @@ GradPlaces place_grad(const Linear& L, const LinearGrad& G, int sms, Places* p) 
     g.origin = p->take<float>(g.most);
     g.d = p->take<unsigned short>((int64_t)g.most * g.ld);
     const int pairs = sms / 2 < 1 ? 1 : sms / 2;
-    g.parts = p->take<float>(pairs * kPartFloats);
+    g.parts = p->take<float>(kMostRounds * pairs * kPartFloats);
     if (G.dw && L.rows > g.most && G.dw_dtype != MICA_F32) {
         g.ld_sums = round_up(L.features, 4);
         g.sums = p->take<float>(L.vocab * g.ld_sums);
@@ -748,10 +805,11 @@ cudaError_t forward(const Linear& L, const Common& c, const ForwardPlaces& f, fl
         LogitSums p{};
         if (!fill(&p, L, c, f.most, (int)piece)) return cudaErrorInvalidValue;
         p.sums = f.sums;
+        p.parts = f.parts;
         p.at = f.at;
         MICA_STEP((launch_gemm<T>(p, f.most / kTile * tiles_of(L.vocab), sms, stream)));
         const Join j{c.meta, c.index, c.target, f.sums, f.at, f.most, (int)piece, f.parts, p.a, logps, lse};
-        MICA_STEP(launch_after(join_rows_kernel, f.most / 32, 256, 0, stream, j));
+        MICA_STEP(launch_after(join_rows_kernel, f.most / 8, 256, 0, stream, j));
     }
     return cudaSuccess;
 }
@@ -781,6 +839,7 @@ cudaError_t weight_grad(const Linear& L, const Common& c, const GradPlaces& g, c
     p.ld_sums = sizeof(O) == 4 ? G.ld_dw : g.ld_sums;
     const size_t four = 4 * sizeof(O);
     p.wide = reinterpret_cast<uintptr_t>(G.dw) % four == 0 && G.ld_dw % 4 == 0;
+    p.wide16 = reinterpret_cast<uintptr_t>(G.dw) % 16 == 0 && G.ld_dw % 8 == 0;
     p.wide_add = reinterpret_cast<uintptr_t>(G.add) % four == 0 && G.ld_add % 4 == 0;
     p.wide_sums = sizeof(O) == 4 ? p.wide : 1;
     p.parts = g.parts;
@@ -815,6 +874,7 @@ cudaError_t backward(const Linear& L, const Common& c, const GradPlaces& g, cons
             q.dh = static_cast<T*>(G.dh);
             q.ld = G.ld_dh;
             q.wide = reinterpret_cast<uintptr_t>(G.dh) % 8 == 0 && G.ld_dh % 4 == 0;
+            q.wide16 = reinterpret_cast<uintptr_t>(G.dh) % 16 == 0 && G.ld_dh % 8 == 0;
             q.parts = g.parts;
             q.w = p.w;
             if (!matrix_map(&q.d, map_type(L.dtype), g.d, L.vocab, g.most, g.ld, 1)) return cudaErrorInvalidValue;

@@ -30,6 +30,8 @@ namespace {
 constexpr int kMostClasses = 8;      // of a batch
 constexpr int kMostMatrices = 256;
 constexpr int64_t kBatchElements = (int64_t)128 << 20;
+// Elements whose momentum and first x are taken one after the other, so that the second kernel finds g and m in L2.
+constexpr int64_t kGroupElements = (int64_t)8 << 20;
 constexpr int kItem = 8192;          // elements that a CTA of the streaming kernels has in registers
 constexpr int kMostItems = 2048;     // parts of a matrix's square sum
 constexpr float kScale = 1024.0f;
@@ -104,11 +106,11 @@ __device__ __forceinline__ float update_of(float g, float m, const Update& u) { 
 // vanishes, and is widened to float64 at its end.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
-                                                       Update u, double* squares) {
+                                                       Update u, int from, double* squares) {
     __shared__ float part[8];
     wait_prerequisite();
     allow_dependents();
-    const Item it = item_at(b, blockIdx.x);
+    const Item it = item_at(b, from + blockIdx.x);
     const int k = b.c[it.c].first + it.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const T* in = static_cast<const T*>(s.in[k]);
     float* m = kMuon ? s.m[k] : nullptr;
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ B
             sum += ldexp((double)q, 2 * e);
         }
     }
-    if (threadIdx.x == 0) squares[blockIdx.x] = sum;
+    if (threadIdx.x == 0) squares[from + blockIdx.x] = sum;
 }
 
 // What rounding to binary16 leaves out.
@@ -175,12 +177,12 @@ __device__ __forceinline__ float rest_of(float x) { return x - __half2float(__fl
 // x = 2^10 u / (|u| + eps) in binary16, rows ld_x apart.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
-                                                    Update u, const double* squares, double eps) {
+                                                    Update u, int from, const double* squares, double eps) {
     __shared__ double part[8];
     __shared__ float scale;
     wait_prerequisite();
     allow_dependents();
-    const Item it = item_at(b, blockIdx.x);
+    const Item it = item_at(b, from + blockIdx.x);
     const Class& c = b.c[it.c];
     const int k = c.first + it.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const T* in = static_cast<const T*>(s.in[k]);
@@ -271,22 +273,19 @@ __device__ __forceinline__ void triangle(int t, int tiles, int* i, int* j) {
     *j = row + t;
 }
 
-// v, or what its rounding leaves out, of the warp's 32 x 32 at row0 and col0 of a matrix of rows x cols.
+// v, and `low` elements further on what its rounding leaves out, to the warp's 32 x 32 at (row0, col0) of rows x cols. (ld is
+// a multiple of 8: what is stored past cols is the row's.)
 __device__ __forceinline__ void store_half(__half* to, int ld, int rows, int cols, int row0, int col0, int lane,
                                            unsigned char* staging, const float (&v)[32], int64_t low) {
     uint32_t w[16];
+    unsigned short* at = reinterpret_cast<unsigned short*>(to);
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
-    auto put = [&](int r, int col, uint4 x) {
-        if (row0 + r < rows && col0 + col < cols)  // (ld is a multiple of 8: the 16 bytes are the row's)
-            *reinterpret_cast<uint4*>(to + (int64_t)(row0 + r) * ld + col0 + col) = x;
-    };
-    by_columns16(staging, lane, w, put);
+    store_block(at, ld, rows, (cols + 7) & ~7, row0, col0, lane, true, staging, w);
     if (!low) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(rest_of(v[2 * i]), rest_of(v[2 * i + 1]));
-    to += low;
-    by_columns16(staging, lane, w, put);
+    store_block(at + low, ld, rows, (cols + 7) & ~7, row0, col0, lane, true, staging, w);
 }
 
 // A symmetric matrix's tile, and its mirror image.
@@ -294,13 +293,16 @@ __device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, in
                                                 unsigned char* staging, const float (&v)[32], bool mirror, int64_t low) {
     store_half(to, ld, side, side, row0, col0, lane, staging, v, low);
     if (!mirror || row0 + lane >= side) return;
+    __half* at = to + (int64_t)col0 * ld + row0 + lane;
+    const int there = side - col0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (col0 + i < side) {
-            __half* at = to + (int64_t)(col0 + i) * ld + row0 + lane;
-            *at = __float2half_rn(v[i]);
-            if (low) at[low] = __float2half_rn(rest_of(v[i]));
-        }
+    for (int i = 0; i < 32; ++i, at += ld)
+        if (i < there) *at = __float2half_rn(v[i]);
+    if (!low) return;
+    at = to + low + (int64_t)col0 * ld + row0 + lane;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, at += ld)
+        if (i < there) *at = __float2half_rn(rest_of(v[i]));
 }
 
 // A = x x^T or x^T x
@@ -487,21 +489,30 @@ struct ApplyLast : Apply {
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col0 = this->col0 + 32 * k;
             if (row0 >= c.rows || col0 >= c.cols) return;
-            by_columns(staging, lane, v, [&](int r, int col, float4 x) {
-                if (row0 + r >= c.rows || col0 + col >= c.cols) return;
-                O* at = to + (int64_t)(row0 + r) * c.cols + col0 + col;
-                const int there = c.cols - (col0 + col);
-                constexpr float kOne = 1.0f / (kScale * kScale);
-                if constexpr (kMuon) {
-                    const float4 w = load4(at, there, wide);
-                    const float rate = c.rate * kOne;
-                    x = make_float4(w.x * p.decay - x.x * rate, w.y * p.decay - x.y * rate, w.z * p.decay - x.z * rate,
-                                    w.w * p.decay - x.w * rate);
-                } else {
-                    x = make_float4(x.x * kOne, x.y * kOne, x.z * kOne, x.w * kOne);
-                }
-                store4(at, x, there, wide);
-            });
+            float4 x[8];
+            by_columns(staging, lane, v, x);
+            const int row = row0 + lane / 8, col = col0 + lane % 8 * 4, there = c.cols - col;
+            if (col >= c.cols) return;
+            O* at = to + (int64_t)row * c.cols + col;
+            const int64_t step = 4 * (int64_t)c.cols;
+            constexpr float kOne = 1.0f / (kScale * kScale);
+            if constexpr (kMuon) {
+                float4 w[8];
+                const float rate = c.rate * kOne;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (row + 4 * i < c.rows) w[i] = load4(at + i * step, there, wide);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = make_float4(w[i].x * p.decay - x[i].x * rate, w[i].y * p.decay - x[i].y * rate,
+                                       w[i].z * p.decay - x[i].z * rate, w[i].w * p.decay - x[i].w * rate);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = make_float4(x[i].x * kOne, x[i].y * kOne, x[i].z * kOne, x[i].w * kOne);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row + 4 * i < c.rows) store4(at + i * step, x[i], there, wide);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -610,8 +621,19 @@ bool maps(Batch* b) {
 
 template <typename T, bool kMuon>
 cudaError_t first(const Batch& b, const Streams& s, const Update& u, double* squares, double eps, void* stream) {
-    MICA_STEP(launch_after(momentum_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, squares));
-    return launch_after(first_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, (const double*)squares, eps);
+    int from = 0, to = 0;
+    int64_t elements = 0;
+    for (int k = 0; k < b.classes; ++k)
+        for (int z = 0; z < b.c[k].count; ++z) {
+            to += b.c[k].items;
+            elements += (int64_t)b.c[k].rows * b.c[k].cols;
+            if (elements < kGroupElements && to < b.items) continue;
+            MICA_STEP(launch_after(momentum_kernel<T, kMuon>, to - from, 256, 0, stream, b, s, u, from, squares));
+            MICA_STEP(launch_after(first_kernel<T, kMuon>, to - from, 256, 0, stream, b, s, u, from, (const double*)squares, eps));
+            from = to;
+            elements = 0;
+        }
+    return cudaSuccess;
 }
 
 template <typename O, bool kMuon>
