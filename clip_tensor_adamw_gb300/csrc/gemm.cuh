@@ -37,7 +37,6 @@ enum GemmRole { kLoader = kTakers, kMultiplier };
 constexpr int kOperandBytes = kHalf * kDepth * 2, kBoxBytes = 64 * kDepth * 2;
 constexpr int kStagingBytes = 32 * 32 * 4;     // of a warp
 constexpr int kGemmShared = 1024 + kStages * 2 * kOperandBytes + kTakers * kStagingBytes;
-constexpr int kChunks = kHalf / 32;            // of 32 columns, that a taker has of a tile
 
 // Set (OR-ed) by a kernel whose bounded wait gave up; read and cleared by the host (read_gemm_status).
 __device__ unsigned int g_gemm_status;
@@ -54,6 +53,7 @@ struct Operand {
 struct Piece {
     Operand a, b;
     int m0, n0;
+    int columns;  // of the tile, a multiple of 64 up to 256: the products take as long as there are
     int from, to;
     int tile;   // for the epilogue, as the policy likes
     int part;   // >= 0: part of a split tile
@@ -68,8 +68,8 @@ struct Place {
 };
 
 struct GemmBarriers {
-    uint64_t full[kStages];              // (leader) a stage's operands have come, in both CTAs
-    uint64_t used[kStages];              // the products of a stage are done
+    uint64_t full[kStages];          // (leader) a stage's operands have come, in both CTAs
+    uint64_t used[kStages];          // the products of a stage are done
     uint64_t sum_full[2], sum_empty[2];  // a tile's sums are in TMEM; (leader) both CTAs have taken them
     uint32_t tmem;
 };
@@ -84,11 +84,14 @@ __device__ __forceinline__ void load_box3_for_pair(void* dst, const CUtensorMap*
         : "memory");
 }
 
-// A CTA's half of a stage's operand: 128 rows (or columns) from `at` on, by 64 of the summed dimension from k on.
-__device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& o, int at, int k, int z, uint64_t* bar) {
+// A CTA's half of a stage's operand: 64 or 128 rows (or columns) from `at` on, by 64 of the summed dimension from k on.
+__device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& o, int at, int k, int z, bool both, uint64_t* bar) {
     load_box3_for_pair(dst, o.map, o.k_major ? k : at, o.k_major ? at : k, z, bar);
-    load_box3_for_pair(dst + kBoxBytes, o.map, o.k_major ? k : at + 64, o.k_major ? at + 64 : k, z, bar);
+    if (both) load_box3_for_pair(dst + kBoxBytes, o.map, o.k_major ? k : at + 64, o.k_major ? at + 64 : k, z, bar);
 }
+
+// A tile's columns where `left` are left of the matrix.
+__device__ __forceinline__ int columns_of(int left, int most) { return left < most ? (left + 63) & ~63 : most; }
 
 // The descriptor of either kind of operand: 128-byte swizzle, groups of 8 lines of 128 bytes 1 KB apart; boxes of 64 columns
 // kBoxBytes apart, which counts for MN-major operands only.
@@ -96,11 +99,12 @@ __device__ __forceinline__ uint64_t operand_descriptor(uint32_t at) {
     return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(kBoxBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// float32 sums of bfloat16 (or binary16) products, 256 x 256
+// float32 sums of bfloat16 (or binary16) products, 256 x columns
 template <typename T>
-__device__ __forceinline__ uint32_t instruction(bool a_k_major, bool b_k_major) {
+__device__ __forceinline__ uint32_t instruction(bool a_k_major, bool b_k_major, int columns) {
     constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-    return 1u << 4 | type << 7 | type << 10 | (a_k_major ? 0u : 1u << 15) | (b_k_major ? 0u : 1u << 16) | (kTile / 8) << 17 |
+    return 1u << 4 | type << 7 | type << 10 | (a_k_major ? 0u : 1u << 15) | (b_k_major ? 0u : 1u << 16) |
+           (uint32_t)(columns / 8) << 17 |
            (kTile / 16) << 24;
 }
 
@@ -163,14 +167,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 for (int k = q.from; k < q.to; ++k, turn.next()) {
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
-                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 4 * kOperandBytes);
+                    const bool both = q.columns > 128;
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * (kOperandBytes + (both ? 2 : 1) * kBoxBytes));
                     int az = q.a.z, bz = q.b.z, at = k;
                     if (q.low && k >= q.depth) {
                         if (k < 2 * q.depth) bz += q.low, at -= q.depth;
                         else az += q.low, at -= 2 * q.depth;
                     }
-                    load_operand(a_stage + s * kOperandBytes, q.a, q.m0 + rank * kHalf, at * kDepth, az, &bar.full[s]);
-                    load_operand(b_stage + s * kOperandBytes, q.b, q.n0 + rank * kHalf, at * kDepth, bz, &bar.full[s]);
+                    load_operand(a_stage + s * kOperandBytes, q.a, q.m0 + rank * kHalf, at * kDepth, az, true, &bar.full[s]);
+                    load_operand(b_stage + s * kOperandBytes, q.b, q.n0 + rank * (q.columns / 2), at * kDepth, bz, both,
+                                 &bar.full[s]);
                 }
             // Every copy has landed when the last products are done. Where a wait gave up they are given 2 ms.
             for (int i = 0; !ok && i < 200; ++i) __nanosleep(10000);
@@ -183,7 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             Turn<2> sums;
             for (int i = pair; ok && p.piece(deal, i, &q); i += pairs) {
                 const int b = sums.at;
-                const uint32_t how = instruction<T>(q.a.k_major, q.b.k_major);
+                const uint32_t how = instruction<T>(q.a.k_major, q.b.k_major, q.columns);
                 const uint32_t a_step = (q.a.k_major ? 32 : 2048) >> 4, b_step = (q.b.k_major ? 32 : 2048) >> 4;
                 if (!(ok = mbar_wait_idle(&bar.sum_empty[b], sums.round ^ 1))) break;
                 fence_after();
@@ -192,10 +198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     if (!(ok = mbar_wait_idle(&bar.full[s], turn.round))) break;
                     fence_after();
                     if (one) {
-                        const uint32_t at = (uint32_t)s * (kOperandBytes >> 4);
+                        const uint64_t a = a0 + (uint32_t)s * (kOperandBytes >> 4), b1 = b0 + (uint32_t)s * (kOperandBytes >> 4);
 #pragma unroll
                         for (int d = 0; d < kDepth / 16; ++d)
-                            multiply(tmem + b * kTile, a0 + (at + d * a_step), b0 + (at + d * b_step), how, k > q.from || d > 0);
+                            multiply(tmem + b * kTile, a + d * a_step, b1 + d * b_step, how, k > q.from || d > 0);
                         commit(&bar.used[s]);
                         if (k == q.to - 1) commit(&bar.sum_full[b]);
                     }
@@ -205,19 +211,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         }
     } else {
         const int quarter = warp % 4, half = warp / 4;
-        const Place place{rank * kHalf + quarter * 32 + lane, half * kHalf, lane, staging + warp * kStagingBytes};
-        const uint32_t own = tmem + ((uint32_t)quarter << 21) + half * kHalf;
+        Place place{rank * kHalf + quarter * 32 + lane, 0, lane, staging + warp * kStagingBytes};
         Turn<2> sums;
         for (int i = pair; p.piece(deal, i, &q); i += pairs) {
-            const int b = sums.at;
+            const int b = sums.at, chunks = q.columns / 64;
+            place.first_column = half * (q.columns / 2);
+            const uint32_t own = tmem + ((uint32_t)quarter << 21) + b * kTile + place.first_column;
             typename P::Epilogue epilogue(p, deal, q, place);
             if (!(ok = mbar_wait_idle(&bar.sum_full[b], sums.round))) break;
             fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
+            for (int c = 0; c < chunks; ++c) {
                 float v[32];
-                load_sums32(own + b * kTile + c * 32, v);
-                if (c == kChunks - 1) {
+                load_sums32(own + c * 32, v);
+                if (c == chunks - 1) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_leader(&bar.sum_empty[b]);
@@ -253,10 +260,6 @@ constexpr int kPartCost = 6, kJoinCost = 12, kLeastStages = 4, kMostRounds = 3;
 __host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs) {
     SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles};
     const int rest = tiles - d.whole;
-    if (stages == 0) {  // nothing to add up: what joins the parts writes every tile
-        d.whole = d.parts = d.pieces = 0;
-        return d;
-    }
     if (rest == 0) return d;
     int best = stages + kPartCost;
     for (int rounds = 1; rounds <= kMostRounds; ++rounds) {
@@ -277,11 +280,11 @@ __host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs
 __device__ __forceinline__ bool split_piece(const SplitDeal& d, int i, Piece* q) {
     if (i >= d.pieces) return false;
     if (i < d.whole || d.parts == 1) {
-        *q = Piece{{}, {}, 0, 0, 0, d.stages, i, -1, 0, 0};
+        *q = Piece{{}, {}, 0, 0, kTile, 0, d.stages, i, -1, 0, 0};
         return true;
     }
     const int k = i - d.whole, part = k % d.parts;
-    *q = Piece{{}, {}, 0, 0, (int)((int64_t)d.stages * part / d.parts), (int)((int64_t)d.stages * (part + 1) / d.parts),
+    *q = Piece{{}, {}, 0, 0, kTile, (int)((int64_t)d.stages * part / d.parts), (int)((int64_t)d.stages * (part + 1) / d.parts),
                d.whole + k / d.parts, k, 0, 0};
     return true;
 }
@@ -359,9 +362,17 @@ __device__ __forceinline__ void store_block(unsigned short* to, int64_t ld, int 
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + i * 8 * ld) = x[i];
         return;
     }
+    if (!wide) {  // a column to a lane, so that a row's stores are contiguous
+        const unsigned short* s = reinterpret_cast<const unsigned short*>(staging);
+        if (col0 + lane >= cols) return;
+        at = to + row0 * ld + col0 + lane;
+        for (int r = 0; r < 32 && row0 + r < rows; ++r)
+            at[r * ld] = s[r * 32 + ((lane / 8 ^ ((r >> 1) & 3)) * 8) + lane % 8];
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (row + i * 8 < rows && col < cols) store8(at + i * 8 * ld, x[i], cols - col, wide);
+        if (row + i * 8 < rows && col < cols) store8(at + i * 8 * ld, x[i], cols - col, true);
 }
 
 // Four values to a row of O, the first at `at`, of which `there` are in the matrix; wide: rows are aligned for one store.

@@ -234,7 +234,7 @@ struct Logits {
     // rows first: h stays in L2 while W passes once
     __device__ __forceinline__ bool piece_at(const Deal& d, int i, Piece* q) const {
         if (i >= d.pieces) return false;
-        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, 0, stages, i, -1, 0, 0};
+        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile, 0, stages, i, -1, 0, 0};
         return true;
     }
 };
@@ -442,11 +442,11 @@ struct HiddenGrad {
         r.scale = m.inv_scale;
         return r;
     }
-    __device__ __forceinline__ bool empty(const Deal& r) const { return r.span.rows == 0; }
     __device__ __forceinline__ bool piece(const Deal& r, int i, Piece* q) const {
         if (!split_piece(r, i, q)) return false;
         q->m0 = q->tile / r.column_tiles * kTile;
         q->n0 = q->tile % r.column_tiles * kTile;
+        q->columns = columns_of(features - q->n0, kTile);
         q->a = Operand{&d, 0, true};
         q->b = Operand{&w, 0, false};
         return true;
@@ -499,7 +499,7 @@ struct WeightGrad {
     float* parts;
 
     struct Deal : SplitDeal {
-        int column_tiles;
+        int column_tiles, first_stage;
         bool first, last, none;
         float scale;
     };
@@ -508,19 +508,22 @@ struct WeightGrad {
         const Span span = span_of(m.count, most, piece_index);
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
-        static_cast<SplitDeal&>(r) = split_deal((vocab + kTile - 1) / kTile * column_tiles, (span.rows + kDepth - 1) / kDepth,
-                                                pairs);
+        const int stages = (span.rows + kDepth - 1) / kDepth;
+        r.none = span.rows == 0 && piece_index > 0;
+        static_cast<SplitDeal&>(r) = split_deal(r.none ? 0 : (vocab + kTile - 1) / kTile * column_tiles, stages ? stages : 1, pairs);
+        r.first_stage = stages ? 0 : most / kDepth;  // without rows: past the matrices, where zeros are read
         r.column_tiles = column_tiles;
         r.first = piece_index == 0;
         r.last = last_span(m.count, most, piece_index);
-        r.none = span.rows == 0 && !r.first;
         r.scale = m.inv_scale;
         return r;
     }
-    __device__ __forceinline__ bool empty(const Deal& r) const { return r.none; }
     __device__ __forceinline__ bool piece(const Deal& r, int i, Piece* q) const {
         if (!split_piece(r, i, q)) return false;
         tile_at(r, q->tile, &q->m0, &q->n0);
+        q->columns = columns_of(features - q->n0, kTile);
+        q->from += r.first_stage;
+        q->to += r.first_stage;
         q->a = Operand{&d, 0, false};
         q->b = Operand{&h, 0, false};
         return true;
@@ -609,14 +612,14 @@ struct Split : G {
     };
 };
 
-// Joins the parts of split tiles, 4 rows to a CTA at a time; where nothing is added up (no rows) every tile.
+// Joins the parts of split tiles, 4 rows to a CTA at a time.
 constexpr int kJoinRows = 4;
 template <typename G>
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Split<G> p, int pairs) {
     wait_prerequisite();
     allow_dependents();
     const typename G::Deal deal = p.deal(pairs);
-    if (deal.parts == 1 || p.empty(deal)) return;
+    if (deal.parts == 1) return;
     const int64_t all = (int64_t)(deal.tiles - deal.whole) * (kTile / kJoinRows);
     const int col = threadIdx.x % 64 * 4;
     for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
@@ -814,10 +817,12 @@ cudaError_t forward(const Linear& L, const Common& c, const ForwardPlaces& f, fl
     return cudaSuccess;
 }
 
+// stages: how many there can be at most
 template <typename T, typename G>
-cudaError_t split_product(const Split<G>& p, int64_t tiles, int sms, void* stream) {
+cudaError_t split_product(const Split<G>& p, int64_t tiles, int64_t stages, int sms, void* stream) {
     const int pairs = sms / 2 < 1 ? 1 : sms / 2;
     MICA_STEP((launch_gemm<T>(p, pairs, sms, stream)));
+    if (stages < 2 * kLeastStages) return cudaSuccess;  // no tile is split
     const int64_t ctas = (tiles < pairs ? tiles : pairs) * (kTile / kJoinRows);
     return launch_after(join_parts_kernel<G>, ctas, 256, 0, stream, p, pairs);
 }
@@ -846,7 +851,7 @@ cudaError_t weight_grad(const Linear& L, const Common& c, const GradPlaces& g, c
     if (!matrix_map(&p.d, map_type(L.dtype), g.d, L.vocab, g.most, g.ld, 1) ||
         !matrix_map(&p.h, map_type(L.dtype), c.h, L.features, g.most, c.ld_h, 1))
         return cudaErrorInvalidValue;
-    return split_product<T>(p, tiles_of(L.vocab) * tiles_of(L.features), sms, stream);
+    return split_product<T>(p, tiles_of(L.vocab) * tiles_of(L.features), (L.rows + kDepth - 1) / kDepth, sms, stream);
 }
 
 // lse: as the forward pass leaves it; dlogps null: cross entropy
@@ -878,7 +883,7 @@ cudaError_t backward(const Linear& L, const Common& c, const GradPlaces& g, cons
             q.parts = g.parts;
             q.w = p.w;
             if (!matrix_map(&q.d, map_type(L.dtype), g.d, L.vocab, g.most, g.ld, 1)) return cudaErrorInvalidValue;
-            MICA_STEP((split_product<T>(q, g.most / kTile * tiles_of(L.features), sms, stream)));
+            MICA_STEP((split_product<T>(q, g.most / kTile * tiles_of(L.features), (L.vocab + kDepth - 1) / kDepth, sms, stream)));
         }
         if (G.dw)
             MICA_STEP((G.dw_dtype == MICA_F32   ? weight_grad<T, float>(L, c, g, G, (int)piece, sms, stream)

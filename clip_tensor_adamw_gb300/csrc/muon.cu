@@ -60,6 +60,7 @@ struct Class {
 struct Batch {
     Class c[kMostClasses];
     int classes, matrices, gram_pieces, out_pieces, items;
+    int width;  // a tile's columns
 };
 
 // The class that tile (or item) i belongs to.
@@ -208,40 +209,56 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
     }
     __half* x = c.px[0] + (int64_t)it.z * c.rows * c.ld_x;
     const int64_t low = (int64_t)c.low * c.rows * c.ld_x;
-    for (int64_t at = it.from + threadIdx.x * 4; at < it.to; at += 1024) {
-        const int there = it.to - at < 4 ? (int)(it.to - at) : 4;
-        if (!skip) {
-            const float4 g = load4(in + at, there, wide);
-            float e[4] = {g.x, g.y, g.z, g.w};
-            if (kMuon) {
-                const float4 now = load4(m + at, there, wide);
-                const float n[4] = {now.x, now.y, now.z, now.w};
+    // the row and column of the thread's elements, which go on by 1,024
+    int64_t at = it.from + threadIdx.x * 4;
+    int64_t row = at / c.cols;
+    int col = (int)(at - row * c.cols);
+    const int rows_on = 1024 / c.cols, cols_on = 1024 - rows_on * c.cols;
+    for (; at < it.to; at += 4 * 1024) {
+        float4 g[4], now[4];
+        int there[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = update_of(e[i] * f, n[i], u);
-            }
-            const int64_t row = at / c.cols;
-            const int col = (int)(at - row * c.cols);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t a = at + j * 1024;
+            there[j] = a >= it.to ? 0 : it.to - a < 4 ? (int)(it.to - a) : 4;
+            g[j] = load4(in + a, there[j], wide);
+            if (kMuon) now[j] = load4(m + a, there[j], wide);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= scale;
-            if (even) {
-                __half* to = x + row * c.ld_x + col;
-                store4(to, make_float4(e[0], e[1], e[2], e[3]), there, true);
-                if (low) store4(to + low, make_float4(rest_of(e[0]), rest_of(e[1]), rest_of(e[2]), rest_of(e[3])), there, true);
-            } else {
+        for (int j = 0; j < 4; ++j) {
+            if (!skip) {
+                float e[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+                if (kMuon) {
+                    const float n[4] = {now[j].x, now[j].y, now[j].z, now[j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[i] = update_of(e[i] * f, n[i], u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] *= scale;
                 __half* to = x + row * c.ld_x;
-                int j = col;
+                if (even) {
+                    store4(to + col, make_float4(e[0], e[1], e[2], e[3]), there[j], true);
+                    if (low)
+                        store4(to + col + low, make_float4(rest_of(e[0]), rest_of(e[1]), rest_of(e[2]), rest_of(e[3])), there[j],
+                               true);
+                } else {
+                    int k = col;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (j == c.cols) j = 0, to += c.ld_x;
-                    if (i < there) {
-                        to[j] = __float2half_rn(e[i]);
-                        if (low) to[j + low] = __float2half_rn(rest_of(e[i]));
+                    for (int i = 0; i < 4; ++i) {
+                        if (k == c.cols) k = 0, to += c.ld_x;
+                        if (i < there[j]) {
+                            to[k] = __float2half_rn(e[i]);
+                            if (low) to[k + low] = __float2half_rn(rest_of(e[i]));
+                        }
+                        ++k;
                     }
-                    ++j;
                 }
             }
+            if (kMuon && u.zero_grad) store4(const_cast<T*>(in) + at + j * 1024, float4{}, there[j], wide);
+            row += rows_on;
+            col += cols_on;
+            if (col >= c.cols) col -= c.cols, ++row;
         }
-        if (kMuon && u.zero_grad) store4(const_cast<T*>(in) + at, float4{}, there, wide);
     }
 }
 
@@ -256,21 +273,27 @@ struct Where {
 __device__ __forceinline__ Where unpack(int tile) { return Where{tile & 7, tile >> 3}; }
 static_assert(kMostClasses <= 8, "a piece's class has three bits");
 
-// Tile (m, n) of a product over `depth`.
-__device__ __forceinline__ Piece piece_of(const Class& c, const Operand& a, const Operand& b, int m, int n, int depth, int tile) {
+// Tile (m, n) of a product over `depth` with `cols` columns.
+__device__ __forceinline__ Piece piece_of(const Class& c, int width, const Operand& a, const Operand& b, int m, int n, int cols,
+                                          int depth, int tile) {
     const int stages = (depth + kDepth - 1) / kDepth;
-    return Piece{a, b, m * kTile, n * kTile, 0, c.low ? 3 * stages : stages, tile, -1, c.low, stages};
+    return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages, tile, -1, c.low, stages};
 }
 
-// Tiles on and above the diagonal of a symmetric matrix, row by row.
-__device__ __forceinline__ void triangle(int t, int tiles, int* i, int* j) {
+// Tiles on and above the diagonal of a symmetric matrix (of a row of tiles, those from the one on the diagonal on).
+__host__ __device__ inline int triangle_tiles(int side, int width) {
+    const int down = (side + kTile - 1) / kTile, across = (side + width - 1) / width;
+    return down * across - kTile / width * (down * (down - 1) / 2);
+}
+__device__ __forceinline__ void triangle(int t, int side, int width, int* i, int* j) {
+    const int across = (side + width - 1) / width, step = kTile / width;
     int row = 0;
-    while (t >= tiles - row) {
-        t -= tiles - row;
+    while (t >= across - step * row) {
+        t -= across - step * row;
         ++row;
     }
     *i = row;
-    *j = row + t;
+    *j = step * row + t;
 }
 
 // v, and `low` elements further on what its rounding leaves out, to the warp's 32 x 32 at (row0, col0) of rows x cols. (ld is
@@ -319,10 +342,10 @@ struct Gram {
         const Class& c = b.c[k];
         const int z = (i - c.gram_before) / c.gram_tiles;
         int m, n;
-        triangle((i - c.gram_before) % c.gram_tiles, (c.side + kTile - 1) / kTile, &m, &n);
+        triangle((i - c.gram_before) % c.gram_tiles, c.side, b.width, &m, &n);
         const Operand x{&c.x[from], z, c.wide()};
         const int depth = c.wide() ? c.cols : c.rows;
-        *q = piece_of(c, x, x, m, n, depth, z << 3 | k);
+        *q = piece_of(c, b.width, x, x, m, n, c.side, depth, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -336,7 +359,7 @@ struct Gram {
             to = c.pa + (int64_t)unpack(q.tile).z * c.side * c.ld_a;
             row0 = q.m0 + at.row - at.lane;
             col0 = q.n0 + at.first_column;
-            mirror = q.m0 != q.n0;
+            mirror = q.n0 >= q.m0 + kTile;
         }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col = col0 + 32 * k;
@@ -363,9 +386,9 @@ struct Poly {
         const Class& c = b.c[k];
         const int z = (i - c.gram_before) / c.gram_tiles;
         int m, n;
-        triangle((i - c.gram_before) % c.gram_tiles, (c.side + kTile - 1) / kTile, &m, &n);
+        triangle((i - c.gram_before) % c.gram_tiles, c.side, b.width, &m, &n);
         const Operand a{&c.a, z, true};
-        *q = piece_of(c, a, a, m, n, c.side, z << 3 | k);
+        *q = piece_of(c, b.width, a, a, m, n, c.side, c.side, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -383,7 +406,7 @@ struct Poly {
             to = c.pb + first;
             row0 = q.m0 + at.row - at.lane;
             col0 = q.n0 + at.first_column;
-            mirror = q.m0 != q.n0;
+            mirror = q.n0 >= q.m0 + kTile;
         }
         // v += b times 32 columns of A
         __device__ __forceinline__ void add_row(const __half* own, int row, int col, float (&v)[32]) const {
@@ -435,7 +458,7 @@ struct Apply {
         const int z = (i - c.out_before) / c.out_tiles, t = (i - c.out_before) % c.out_tiles;
         const int row_tiles = (c.rows + kTile - 1) / kTile;
         const Operand x{&c.x[from], z, !c.wide()}, poly{&c.b, z, true};
-        *q = piece_of(c, c.wide() ? poly : x, c.wide() ? x : poly, t % row_tiles, t / row_tiles, c.side, z << 3 | k);
+        *q = piece_of(c, b.width, c.wide() ? poly : x, c.wide() ? x : poly, t % row_tiles, t / row_tiles, c.cols, c.side, z << 3 | k);
         return true;
     }
 };
@@ -524,14 +547,14 @@ struct ApplyLast : Apply {
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// One class of a batch: matrices list[first], ..., by shape.
-struct Shape {
+// Matrices of one shape, by their places in the list.
+struct Group {
     int64_t rows, cols;
     std::vector<int32_t> which;
 };
 
 // The list cut into batches of classes. Classes with the longest sums come first, so that the last tiles are short ones.
-std::vector<std::vector<Shape>> batches_of(const int64_t* rows, const int64_t* cols, int32_t T) {
+std::vector<std::vector<Group>> batches_of(const int64_t* rows, const int64_t* cols, int32_t T) {
     std::vector<int32_t> order;
     for (int32_t k = 0; k < T; ++k)
         if (rows[k] > 0 && cols[k] > 0) order.push_back(k);
@@ -539,7 +562,7 @@ std::vector<std::vector<Shape>> batches_of(const int64_t* rows, const int64_t* c
         const int64_t a = std::max(rows[i], cols[i]), b = std::max(rows[j], cols[j]);
         return a != b ? a > b : rows[i] != rows[j] ? rows[i] > rows[j] : cols[i] > cols[j];
     });
-    std::vector<std::vector<Shape>> out;
+    std::vector<std::vector<Group>> out;
     int64_t elements = 0;
     int matrices = 0;
     for (int32_t k : order) {
@@ -552,7 +575,7 @@ std::vector<std::vector<Shape>> batches_of(const int64_t* rows, const int64_t* c
             matrices = 0;
             same = false;
         }
-        if (!same) out.back().push_back(Shape{rows[k], cols[k], {}});
+        if (!same) out.back().push_back(Group{rows[k], cols[k], {}});
         out.back().back().which.push_back(k);
         elements += n;
         ++matrices;
@@ -560,8 +583,17 @@ std::vector<std::vector<Shape>> batches_of(const int64_t* rows, const int64_t* c
     return out;
 }
 
+// A tile's columns: 256, or 128 where tiles of 256 would leave pairs without one. Products of 256 x 128 run at two thirds of
+// the rate of 256 x 256 (four layers of GPT-2 XL: 3.93 ms with 128 columns, 3.24 with 256), but a list too small for the GPU
+// is done sooner in twice as many (384 x 1536: 124 us with 128, 148 with 256).
+int width_of(const std::vector<Group>& shapes, int sms) {
+    int64_t gram = 0;
+    for (const Group& s : shapes) gram += triangle_tiles((int)std::min(s.rows, s.cols), kTile) * (int64_t)s.which.size();
+    return gram * 4 <= sms ? 128 : kTile;
+}
+
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
-int64_t place(const std::vector<Shape>& shapes, bool precise, char* base, Batch* b, double** squares) {
+int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* base, Batch* b, double** squares) {
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* p = base ? base + at : nullptr;
@@ -569,7 +601,8 @@ int64_t place(const std::vector<Shape>& shapes, bool precise, char* base, Batch*
         return p;
     };
     *b = Batch{};
-    for (const Shape& s : shapes) {
+    b->width = width_of(shapes, sms);
+    for (const Group& s : shapes) {
         Class& c = b->c[b->classes++];
         c.rows = (int)s.rows;
         c.cols = (int)s.cols;
@@ -582,9 +615,8 @@ int64_t place(const std::vector<Shape>& shapes, bool precise, char* base, Batch*
         for (int i = 0; i < 2; ++i) c.px[i] = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.rows * c.ld_x * 2));
         c.pa = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
         c.pb = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
-        const int tiles = (c.side + kTile - 1) / kTile;
-        c.gram_tiles = tiles * (tiles + 1) / 2;
-        c.out_tiles = ((c.rows + kTile - 1) / kTile) * ((c.cols + kTile - 1) / kTile);
+        c.gram_tiles = triangle_tiles(c.side, b->width);
+        c.out_tiles = ((c.rows + kTile - 1) / kTile) * ((c.cols + b->width - 1) / b->width);
         c.gram_before = b->gram_pieces;
         c.out_before = b->out_pieces;
         const int64_t n = s.rows * s.cols;
@@ -637,12 +669,12 @@ cudaError_t first(const Batch& b, const Streams& s, const Update& u, double* squ
 }
 
 template <typename O, bool kMuon>
-cudaError_t last(const Muon& call, const Batch& b, const std::vector<Shape>& shapes, int from, int sms, void* stream) {
+cudaError_t last(const Muon& call, const Batch& b, const std::vector<Group>& shapes, int from, int sms, void* stream) {
     ApplyLast<O, kMuon> p{};
     p.b = b;
     p.from = from;
     int k = 0;
-    for (const Shape& s : shapes)
+    for (const Group& s : shapes)
         for (int32_t i : s.which) p.out[k++] = static_cast<O*>(call.out[i]);
     p.decay = (float)(1.0 - call.hp.lr * call.hp.weight_decay);
     p.skip = (call.hp.flags & MICA_STEP_SKIP_NONFINITE) != 0;
@@ -650,14 +682,14 @@ cudaError_t last(const Muon& call, const Batch& b, const std::vector<Shape>& sha
     return launch_gemm<__half>(p, b.out_pieces, sms, stream);
 }
 
-cudaError_t run(const Muon& call, const std::vector<Shape>& shapes, char* workspace, int sms, void* stream) {
+cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* workspace, int sms, void* stream) {
     Batch b;
     double* squares;
-    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, workspace, &b, &squares);
+    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, sms, workspace, &b, &squares);
     if (!maps(&b)) return cudaErrorInvalidValue;
     Streams s{};
     int k = 0;
-    for (const Shape& shape : shapes)
+    for (const Group& shape : shapes)
         for (int32_t i : shape.which) {
             s.in[k] = call.in[i];
             s.m[k++] = call.m ? call.m[i] : nullptr;
@@ -712,7 +744,7 @@ int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint
     for (const auto& shapes : batches_of(rows, cols, T)) {
         Batch b;
         double* squares;
-        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, nullptr, &b, &squares));
+        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, 1, nullptr, &b, &squares));
     }
     return most;
 }
