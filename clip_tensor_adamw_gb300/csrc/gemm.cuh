@@ -11,8 +11,8 @@
 // product of 16 to the next differs, 32 bytes or 2 KB. Elements outside the matrix are read as zeros.
 //
 // A policy P is the kernel's parameter, with
-//   Deal deal(int pairs) const                      how the work is dealt; computed once a thread
-//   bool piece(const Deal&, int i, Piece*) const    the i-th piece of work; false when there are no more
+//   Deal deal(int pair, int pairs) const            how the work is dealt to one of the pairs; computed once a thread
+//   bool piece(Deal&, Piece*) const                 the pair's next piece of work; false when there are no more
 //   struct Epilogue                                 what becomes of a piece's sums, made for each piece by each of its threads:
 //     Epilogue(const P&, const Deal&, const Piece&, const Place&)
 //     void chunk(int c, float (&v)[32])             columns [32 c, 32 c + 32) of the thread's row of its half, in order
@@ -91,7 +91,7 @@ __device__ __forceinline__ void load_operand(unsigned char* dst, const Operand& 
 }
 
 // A tile's columns where `left` are left of the matrix.
-__device__ __forceinline__ int columns_of(int left, int most) { return left < most ? (left + 63) & ~63 : most; }
+__host__ __device__ inline int columns_of(int left, int most) { return left < most ? (left + 63) & ~63 : most; }
 
 // The descriptor of either kind of operand: 128-byte swizzle, groups of 8 lines of 128 bytes 1 KB apart; boxes of 64 columns
 // kBoxBytes apart, which counts for MN-major operands only.
@@ -157,13 +157,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     wait_prerequisite();
     allow_dependents();
 
-    const typename P::Deal deal = p.deal(pairs);
+    typename P::Deal deal = p.deal(pair, pairs);
     bool ok = true;
     Piece q;
     if (warp == kLoader) {
         if (lane == 0) {
             Turn<kStages> turn;
-            for (int i = pair; ok && p.piece(deal, i, &q); i += pairs)
+            while (ok && p.piece(deal, &q))
                 for (int k = q.from; k < q.to; ++k, turn.next()) {
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
@@ -187,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             const uint64_t a0 = operand_descriptor(smem_u32(a_stage)), b0 = operand_descriptor(smem_u32(b_stage));
             Turn<kStages> turn;
             Turn<2> sums;
-            for (int i = pair; ok && p.piece(deal, i, &q); i += pairs) {
+            while (ok && p.piece(deal, &q)) {
                 const int b = sums.at;
                 const uint32_t how = instruction<T>(q.a.k_major, q.b.k_major, q.columns);
                 const uint32_t a_step = (q.a.k_major ? 32 : 2048) >> 4, b_step = (q.b.k_major ? 32 : 2048) >> 4;
@@ -213,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int quarter = warp % 4, half = warp / 4;
         Place place{rank * kHalf + quarter * 32 + lane, 0, lane, staging + warp * kStagingBytes};
         Turn<2> sums;
-        for (int i = pair; p.piece(deal, i, &q); i += pairs) {
+        while (p.piece(deal, &q)) {
             const int b = sums.at, chunks = q.columns / 64;
             place.first_column = half * (q.columns / 2);
             const uint32_t own = tmem + ((uint32_t)quarter << 21) + b * kTile + place.first_column;
@@ -251,14 +251,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
 // `whole` tiles one after another, then the rest (fewer than there are pairs) in `parts` along the summed dimension.
 struct SplitDeal {
     int tiles, stages, whole, parts, pieces;
+    int next, pairs;  // the pair's next piece; and then every pairs-th
 };
 
 // The number of parts is the one that makes the rest shortest by this count, in stages: rounds of parts, each with a part's
 // stages and kPartCost for filling and emptying it; and what joining takes, kJoinCost and a quarter of a stage for each part
 // (512 KB written and read). 48 tiles of 786 stages on 76 pairs: 1 part 221 us, 3 parts (2 rounds) 150 us.
 constexpr int kPartCost = 6, kJoinCost = 12, kLeastStages = 4, kMostRounds = 3;
-__host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs) {
-    SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles};
+__host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pair, int pairs) {
+    SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles, pair, pairs};
     const int rest = tiles - d.whole;
     if (rest == 0) return d;
     int best = stages + kPartCost;
@@ -276,9 +277,11 @@ __host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pairs
     return d;
 }
 
-// The i-th piece's tile, stages and part; false when there are no more.
-__device__ __forceinline__ bool split_piece(const SplitDeal& d, int i, Piece* q) {
+// The next piece's tile, stages and part; false when there are no more.
+__device__ __forceinline__ bool split_piece(SplitDeal& d, Piece* q) {
+    const int i = d.next;
     if (i >= d.pieces) return false;
+    d.next += d.pairs;
     if (i < d.whole || d.parts == 1) {
         *q = Piece{{}, {}, 0, 0, kTile, 0, d.stages, i, -1, 0, 0};
         return true;

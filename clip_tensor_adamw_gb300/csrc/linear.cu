@@ -221,19 +221,21 @@ struct Logits {
     CUtensorMap h, w;
     const Meta* meta;
     const int* target;
-    int most, piece, vocab, stages;
+    int most, piece_index, vocab, stages;
     float a;  // log2(e) / T
 
     struct Deal {
-        int rows, row_tiles, pieces;
+        int rows, row_tiles, pieces, next, pairs;
     };
-    __device__ __forceinline__ Deal deal(int) const {
-        const int rows = span_of(meta->count, most, piece).rows, row_tiles = (rows + kTile - 1) / kTile;
-        return Deal{rows, row_tiles, row_tiles * ((vocab + kTile - 1) / kTile)};
+    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
+        const int rows = span_of(meta->count, most, piece_index).rows, row_tiles = (rows + kTile - 1) / kTile;
+        return Deal{rows, row_tiles, row_tiles * ((vocab + kTile - 1) / kTile), pair, pairs};
     }
     // rows first: h stays in L2 while W passes once
-    __device__ __forceinline__ bool piece_at(const Deal& d, int i, Piece* q) const {
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        const int i = d.next;
         if (i >= d.pieces) return false;
+        d.next += d.pairs;
         *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile, 0, stages, i, -1, 0, 0};
         return true;
     }
@@ -243,8 +245,6 @@ struct LogitSums : Logits {
     RowSum* sums;  // [most][vocabulary / 128]
     int parts;
     float* at;     // [most] the targets' logits
-
-    __device__ __forceinline__ bool piece(const Deal& d, int i, Piece* q) const { return piece_at(d, i, q); }
 
     struct Epilogue {
         const LogitSums& p;
@@ -372,8 +372,6 @@ struct LogitGrad : Logits {
     T* d;  // [most][ld]
     int ld;
 
-    __device__ __forceinline__ bool piece(const Deal& d, int i, Piece* q) const { return piece_at(d, i, q); }
-
     struct Epilogue {
         const LogitGrad& p;
         int row, column, target, lane, stored;
@@ -430,20 +428,20 @@ struct HiddenGrad {
         int column_tiles;
         float scale;
     };
-    __device__ __forceinline__ Deal deal(int pairs) const {
+    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
         const Meta m = *meta;
         const Span span = span_of(m.count, most, piece_index);
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
         static_cast<SplitDeal&>(r) = split_deal((span.rows + kTile - 1) / kTile * column_tiles, (vocab + kDepth - 1) / kDepth,
-                                                pairs);
+                                                pair, pairs);
         r.span = span;
         r.column_tiles = column_tiles;
         r.scale = m.inv_scale;
         return r;
     }
-    __device__ __forceinline__ bool piece(const Deal& r, int i, Piece* q) const {
-        if (!split_piece(r, i, q)) return false;
+    __device__ __forceinline__ bool piece(Deal& r, Piece* q) const {
+        if (!split_piece(r, q)) return false;
         q->m0 = q->tile / r.column_tiles * kTile;
         q->n0 = q->tile % r.column_tiles * kTile;
         q->columns = columns_of(features - q->n0, kTile);
@@ -503,14 +501,14 @@ struct WeightGrad {
         bool first, last, none;
         float scale;
     };
-    __device__ __forceinline__ Deal deal(int pairs) const {
+    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
         const Meta m = *meta;
         const Span span = span_of(m.count, most, piece_index);
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
         const int stages = (span.rows + kDepth - 1) / kDepth;
         r.none = span.rows == 0 && piece_index > 0;
-        static_cast<SplitDeal&>(r) = split_deal(r.none ? 0 : (vocab + kTile - 1) / kTile * column_tiles, stages ? stages : 1, pairs);
+        static_cast<SplitDeal&>(r) = split_deal(r.none ? 0 : (vocab + kTile - 1) / kTile * column_tiles, stages ? stages : 1, pair, pairs);
         r.first_stage = stages ? 0 : most / kDepth;  // without rows: past the matrices, where zeros are read
         r.column_tiles = column_tiles;
         r.first = piece_index == 0;
@@ -518,8 +516,8 @@ struct WeightGrad {
         r.scale = m.inv_scale;
         return r;
     }
-    __device__ __forceinline__ bool piece(const Deal& r, int i, Piece* q) const {
-        if (!split_piece(r, i, q)) return false;
+    __device__ __forceinline__ bool piece(Deal& r, Piece* q) const {
+        if (!split_piece(r, q)) return false;
         tile_at(r, q->tile, &q->m0, &q->n0);
         q->columns = columns_of(features - q->n0, kTile);
         q->from += r.first_stage;
@@ -618,7 +616,7 @@ template <typename G>
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Split<G> p, int pairs) {
     wait_prerequisite();
     allow_dependents();
-    const typename G::Deal deal = p.deal(pairs);
+    const typename G::Deal deal = p.deal(0, pairs);
     if (deal.parts == 1) return;
     const int64_t all = (int64_t)(deal.tiles - deal.whole) * (kTile / kJoinRows);
     const int col = threadIdx.x % 64 * 4;
@@ -793,7 +791,7 @@ bool fill(Logits* p, const Linear& L, const Common& c, int most, int piece) {
     p->meta = c.meta;
     p->target = c.target;
     p->most = most;
-    p->piece = piece;
+    p->piece_index = piece;
     p->vocab = L.vocab;
     p->stages = (L.features + kDepth - 1) / kDepth;
     p->a = (float)(1.4426950408889634074 / L.temperature);

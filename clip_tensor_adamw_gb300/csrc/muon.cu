@@ -30,10 +30,8 @@ namespace {
 constexpr int kMostClasses = 8;      // of a batch
 constexpr int kMostMatrices = 256;
 constexpr int64_t kBatchElements = (int64_t)128 << 20;
-// Elements whose momentum and first x are taken one after the other, so that the second kernel finds g and m in L2.
-constexpr int64_t kGroupElements = (int64_t)8 << 20;
 constexpr int kItem = 8192;          // elements that a CTA of the streaming kernels has in registers
-constexpr int kMostItems = 2048;     // parts of a matrix's square sum
+constexpr int kMostItems = 1024;     // parts of a matrix's square sum
 constexpr float kScale = 1024.0f;
 // Matrices whose smaller side is at most this are held in pairs: a small matrix's elements are large beside a weight's, so the
 // error would show in a float32 weight (a step of rate r changes the weights' norm by r / 0.02 sqrt(side) of it or so), and
@@ -48,8 +46,6 @@ struct Class {
     int rows, cols, count, first;    // first: of its matrices, in the batch
     int low;                         // 0, or `count`: the low halves' first place in z
     int side, ld_x, ld_a;            // side: A's
-    int gram_tiles, out_tiles;       // of a matrix
-    int gram_before, out_before;     // tiles of the classes before
     int items, items_before;         // of a matrix; of the classes before
     int64_t item;                    // elements
     float rate;                      // lr, adjusted
@@ -59,17 +55,9 @@ struct Class {
 
 struct Batch {
     Class c[kMostClasses];
-    int classes, matrices, gram_pieces, out_pieces, items;
+    int classes, matrices, items;
     int width;  // a tile's columns
 };
-
-// The class that tile (or item) i belongs to.
-template <int Class::*before>
-__device__ __forceinline__ int class_of(const Batch& b, int i) {
-    int k = 0;
-    while (k + 1 < b.classes && i >= b.c[k + 1].*before) ++k;
-    return k;
-}
 
 // ------------------------------------------------------------------------------------------------------------------------
 // momentum, norm, and the first x
@@ -92,7 +80,9 @@ struct Item {
     int64_t from, to;
 };
 __device__ __forceinline__ Item item_at(const Batch& b, int i) {
-    const int c = class_of<&Class::items_before>(b, i), k = i - b.c[c].items_before;
+    int c = 0;
+    while (c + 1 < b.classes && i >= b.c[c + 1].items_before) ++c;
+    const int k = i - b.c[c].items_before;
     const int z = k / b.c[c].items, part = k % b.c[c].items;
     const int64_t n = (int64_t)b.c[c].rows * b.c[c].cols, from = part * b.c[c].item;
     return Item{c, z, part, from, from + b.c[c].item < n ? from + b.c[c].item : n};
@@ -103,15 +93,15 @@ __device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_c
 __device__ __forceinline__ float momentum_of(float g, float m, const Update& u) { return m + u.keep * (g - m); }
 __device__ __forceinline__ float update_of(float g, float m, const Update& u) { return u.nesterov ? g + u.mu * (m - g) : m; }
 
-// m, and each item's square sum of u. A sum of squares counts from its item's largest element, so that none overflows or
-// vanishes, and is widened to float64 at its end.
+// m, and each item's square sum of u. A thread's squares count from its largest element, so that none overflows or vanishes,
+// and are widened to float64, of which this chip does next to nothing, once for every 16.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
-                                                       Update u, int from, double* squares) {
-    __shared__ float part[8];
+                                                       Update u, double* squares) {
+    __shared__ double part[8];
     wait_prerequisite();
     allow_dependents();
-    const Item it = item_at(b, from + blockIdx.x);
+    const Item it = item_at(b, blockIdx.x);
     const int k = b.c[it.c].first + it.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const T* in = static_cast<const T*>(s.in[k]);
     float* m = kMuon ? s.m[k] : nullptr;
@@ -119,18 +109,24 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ B
     if (kMuon && u.skip && !(f > 0.0f)) return;
     const bool wide = aligned16(in) && aligned16(m);
     double sum = 0.0;
-    for (int64_t base = it.from; base < it.to; base += kItem) {
-        float v[32];
+    constexpr int kLoads = 4;
+    for (int64_t base = it.from + threadIdx.x * 4; base < it.to; base += kLoads * 1024) {
+        float4 x[kLoads], old[kLoads];
+        int there[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int64_t at = base + j * 1024;
+            there[j] = at >= it.to ? 0 : it.to - at < 4 ? (int)(it.to - at) : 4;
+            x[j] = load4(in + at, there[j], wide);
+            if (kMuon) old[j] = load4(m + at, there[j], wide);
+        }
+        float v[4 * kLoads];
         float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t at = base + j * 1024 + threadIdx.x * 4;
-            const int there = at >= it.to ? 0 : it.to - at < 4 ? (int)(it.to - at) : 4;
-            const float4 x = load4(in + at, there, wide);
-            float e[4] = {x.x, x.y, x.z, x.w};
+        for (int j = 0; j < kLoads; ++j) {
+            float e[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
             if (kMuon) {
-                const float4 old = load4(m + at, there, wide);
-                const float o[4] = {old.x, old.y, old.z, old.w};
+                const float o[4] = {old[j].x, old[j].y, old[j].z, old[j].w};
                 float n[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -138,7 +134,7 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ B
                     n[i] = momentum_of(gh, o[i], u);
                     e[i] = update_of(gh, n[i], u);
                 }
-                store4(m + at, make_float4(n[0], n[1], n[2], n[3]), there, wide);
+                store4(m + base + j * 1024, make_float4(n[0], n[1], n[2], n[3]), there[j], wide);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -146,30 +142,22 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ B
                 top = fmaxf(top, fabsf(e[i]));
             }
         }
-#pragma unroll
-        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        __syncthreads();
-        if (lane == 0) part[warp] = top;
-        __syncthreads();
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, part[i]);
         int e = (int)(__float_as_uint(top) >> 23) - 127;  // top < 2^(e + 1)
         e = e < -100 ? -100 : e > 100 ? 100 : e;
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         float q = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) q = fmaf(v[i] * down, v[i] * down, q);
-#pragma unroll
-        for (int d = 16; d; d /= 2) q += __shfl_xor_sync(~0u, q, d);
-        __syncthreads();
-        if (lane == 0) part[warp] = q;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            q = 0.0f;
-            for (int i = 0; i < 8; ++i) q += part[i];
-            sum += ldexp((double)q, 2 * e);
-        }
+        for (int i = 0; i < 4 * kLoads; ++i) q = fmaf(v[i] * down, v[i] * down, q);
+        sum += (double)q * __hiloint2double((1023 + 2 * e) << 20, 0);
     }
-    if (threadIdx.x == 0) squares[from + blockIdx.x] = sum;
+#pragma unroll
+    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x) return;
+    sum = 0.0;
+    for (int i = 0; i < 8; ++i) sum += part[i];
+    squares[blockIdx.x] = sum;
 }
 
 // What rounding to binary16 leaves out.
@@ -178,12 +166,12 @@ __device__ __forceinline__ float rest_of(float x) { return x - __half2float(__fl
 // x = 2^10 u / (|u| + eps) in binary16, rows ld_x apart.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
-                                                    Update u, int from, const double* squares, double eps) {
+                                                    Update u, const double* squares, double eps) {
     __shared__ double part[8];
     __shared__ float scale;
     wait_prerequisite();
     allow_dependents();
-    const Item it = item_at(b, from + blockIdx.x);
+    const Item it = item_at(b, blockIdx.x);
     const Class& c = b.c[it.c];
     const int k = c.first + it.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const T* in = static_cast<const T*>(s.in[k]);
@@ -203,7 +191,9 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
         if (threadIdx.x == 0) {
             sum = 0.0;
             for (int i = 0; i < 8; ++i) sum += part[i];
-            scale = (float)((double)kScale / (sqrt(sum) + eps));
+            const float q = (float)sum;
+            const double norm = q > 1e-30f && q < 1e30f ? (double)sqrtf(q) : sqrt(sum);
+            scale = (float)((double)kScale / (norm + eps));
         }
         __syncthreads();
     }
@@ -266,12 +256,49 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
 // the products
 // ------------------------------------------------------------------------------------------------------------------------
 
-// Which tile of which matrix a piece is.
+// Which matrix a piece belongs to, in its `tile`.
 struct Where {
     int c, z;
 };
 __device__ __forceinline__ Where unpack(int tile) { return Where{tile & 7, tile >> 3}; }
 static_assert(kMostClasses <= 8, "a piece's class has three bits");
+
+// The pieces of a launch come in groups that take the same time: a class's whole tiles, and its narrow ones at the matrices'
+// right edge. The host deals them to the pairs, the long ones first and each to the pair that has least (so that a layer of
+// GPT-2 XL's tiles of 100, 75 and 25 stages end together), and writes that down as rounds: each of a round's pairs takes one
+// piece of its group, in the order of the pairs, so that neighbours share operands in L2.
+constexpr int kMostPairs = 96, kMostGroups = 2 * kMostClasses, kRounds = 64;
+struct Round {
+    uint32_t pairs[kMostPairs / 32];
+    int first;     // piece of the group
+    short repeat;  // rounds like this one, one after the other
+    short group;
+};
+struct Schedule {
+    Round rows[kRounds];
+    int rounds;
+    int tiles[kMostGroups];  // of a matrix; group 2 k: class k's whole tiles, 2 k + 1: its narrow ones
+};
+struct Turns {
+    int pair, at, repeat;
+};
+// The pair's next piece: its group and place there; false when there are no more.
+__device__ __forceinline__ bool next_piece(const Schedule& s, Turns& t, int* group, int* place) {
+    for (; t.at < s.rounds; ++t.at, t.repeat = 0) {
+        const Round& r = s.rows[t.at];
+        if (t.repeat == r.repeat || !(r.pairs[t.pair / 32] >> t.pair % 32 & 1)) continue;
+        int before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < kMostPairs / 32; ++i) {
+            all += __popc(r.pairs[i]);
+            before += i < t.pair / 32 ? __popc(r.pairs[i]) : i == t.pair / 32 ? __popc(r.pairs[i] & ((1u << t.pair % 32) - 1)) : 0;
+        }
+        *group = r.group;
+        *place = r.first + t.repeat++ * all + before;
+        return true;
+    }
+    return false;
+}
 
 // Tile (m, n) of a product over `depth` with `cols` columns.
 __device__ __forceinline__ Piece piece_of(const Class& c, int width, const Operand& a, const Operand& b, int m, int n, int cols,
@@ -280,13 +307,22 @@ __device__ __forceinline__ Piece piece_of(const Class& c, int width, const Opera
     return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages, tile, -1, c.low, stages};
 }
 
-// Tiles on and above the diagonal of a symmetric matrix (of a row of tiles, those from the one on the diagonal on).
+// Whole columns of tiles, and whether there is a narrow one.
+__host__ __device__ inline int whole_columns(int cols, int width) { return cols / width; }
+__host__ __device__ inline bool has_narrow(int cols, int width) { return cols % width != 0; }
+__host__ __device__ inline int row_tiles_of(int rows) { return (rows + kTile - 1) / kTile; }
+
+// Tiles on and above the diagonal of a symmetric matrix (of a row of tiles, those from the diagonal's on).
 __host__ __device__ inline int triangle_tiles(int side, int width) {
-    const int down = (side + kTile - 1) / kTile, across = (side + width - 1) / width;
-    return down * across - kTile / width * (down * (down - 1) / 2);
+    int tiles = 0;
+    for (int i = 0; i < row_tiles_of(side); ++i) {
+        const int n = whole_columns(side, width) - kTile / width * i;
+        tiles += n > 0 ? n : 0;
+    }
+    return tiles;
 }
 __device__ __forceinline__ void triangle(int t, int side, int width, int* i, int* j) {
-    const int across = (side + width - 1) / width, step = kTile / width;
+    const int across = whole_columns(side, width), step = kTile / width;
     int row = 0;
     while (t >= across - step * row) {
         t -= across - step * row;
@@ -295,6 +331,25 @@ __device__ __forceinline__ void triangle(int t, int side, int width, int* i, int
     *i = row;
     *j = step * row + t;
 }
+
+// What the two symmetric products share: the pieces of the tiles on and above the diagonal.
+struct Symmetric {
+    Batch b;
+    Schedule s;
+
+    using Deal = Turns;
+    __device__ __forceinline__ Deal deal(int pair, int) const { return Turns{pair, 0, 0}; }
+    __device__ __forceinline__ bool tile(Deal& d, int* k, int* z, int* m, int* n) const {
+        int group, place;
+        if (!next_piece(s, d, &group, &place)) return false;
+        *k = group / 2;
+        const int tiles = s.tiles[group], side = b.c[*k].side, t = place % tiles;
+        *z = place / tiles;
+        if (group & 1) *m = t, *n = whole_columns(side, b.width);
+        else triangle(t, side, b.width, m, n);
+        return true;
+    }
+};
 
 // v, and `low` elements further on what its rounding leaves out, to the warp's 32 x 32 at (row0, col0) of rows x cols. (ld is
 // a multiple of 8: what is stored past cols is the row's.)
@@ -311,41 +366,52 @@ __device__ __forceinline__ void store_half(__half* to, int ld, int rows, int col
     store_block(at + low, ld, rows, (cols + 7) & ~7, row0, col0, lane, true, staging, w);
 }
 
+// The mirror image of the warp's 32 x 32: a lane's elements become a column, which the staging buffer turns to rows.
+__device__ __forceinline__ void store_mirrored(__half* to, int ld, int side, int row0, int col0, int lane,
+                                               unsigned char* staging, const uint32_t (&w)[16]) {
+    unsigned short* t = reinterpret_cast<unsigned short*>(staging);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        t[(2 * i) * 32 + lane] = (unsigned short)w[i];
+        t[(2 * i + 1) * 32 + lane] = (unsigned short)(w[i] >> 16);
+    }
+    __syncwarp();
+    const int row = lane / 4, col = lane % 4 * 8, padded = (side + 7) & ~7;
+    unsigned short* at = reinterpret_cast<unsigned short*>(to) + (int64_t)(col0 + row) * ld + row0 + col;
+    if (row0 + col >= padded) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (col0 + row + 8 * i < side)
+            *reinterpret_cast<uint4*>(at + (int64_t)(8 * i) * ld) = reinterpret_cast<const uint4*>(staging)[(row + 8 * i) * 4 + lane % 4];
+}
+
 // A symmetric matrix's tile, and its mirror image.
 __device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, int row0, int col0, int lane,
                                                 unsigned char* staging, const float (&v)[32], bool mirror, int64_t low) {
     store_half(to, ld, side, side, row0, col0, lane, staging, v, low);
-    if (!mirror || row0 + lane >= side) return;
-    __half* at = to + (int64_t)col0 * ld + row0 + lane;
-    const int there = side - col0;
+    if (!mirror) return;
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i, at += ld)
-        if (i < there) *at = __float2half_rn(v[i]);
+    for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(v[2 * i], v[2 * i + 1]);
+    store_mirrored(to, ld, side, row0, col0, lane, staging, w);
     if (!low) return;
-    at = to + low + (int64_t)col0 * ld + row0 + lane;
 #pragma unroll
-    for (int i = 0; i < 32; ++i, at += ld)
-        if (i < there) *at = __float2half_rn(rest_of(v[i]));
+    for (int i = 0; i < 16; ++i) w[i] = pack2<__half>(rest_of(v[2 * i]), rest_of(v[2 * i + 1]));
+    store_mirrored(to + low, ld, side, row0, col0, lane, staging, w);
 }
 
 // A = x x^T or x^T x
-struct Gram {
+struct Gram : Symmetric {
     static constexpr unsigned int kStatus = 0x800u;
-    Batch b;
     int from;  // the buffer that x is in
 
-    struct Deal {};
-    __device__ __forceinline__ Deal deal(int) const { return Deal{}; }
-    __device__ __forceinline__ bool piece(const Deal&, int i, Piece* q) const {
-        if (i >= b.gram_pieces) return false;
-        const int k = class_of<&Class::gram_before>(b, i);
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        int k, z, m, n;
+        if (!tile(d, &k, &z, &m, &n)) return false;
         const Class& c = b.c[k];
-        const int z = (i - c.gram_before) / c.gram_tiles;
-        int m, n;
-        triangle((i - c.gram_before) % c.gram_tiles, c.side, b.width, &m, &n);
         const Operand x{&c.x[from], z, c.wide()};
-        const int depth = c.wide() ? c.cols : c.rows;
-        *q = piece_of(c, b.width, x, x, m, n, c.side, depth, z << 3 | k);
+        *q = piece_of(c, b.width, x, x, m, n, c.side, c.wide() ? c.cols : c.rows, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -373,20 +439,14 @@ struct Gram {
 };
 
 // B = a I + b A + c A^2
-struct Poly {
+struct Poly : Symmetric {
     static constexpr unsigned int kStatus = 0x1000u;
-    Batch b;
     float ca, cb, cc;
 
-    struct Deal {};
-    __device__ __forceinline__ Deal deal(int) const { return Deal{}; }
-    __device__ __forceinline__ bool piece(const Deal&, int i, Piece* q) const {
-        if (i >= b.gram_pieces) return false;
-        const int k = class_of<&Class::gram_before>(b, i);
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        int k, z, m, n;
+        if (!tile(d, &k, &z, &m, &n)) return false;
         const Class& c = b.c[k];
-        const int z = (i - c.gram_before) / c.gram_tiles;
-        int m, n;
-        triangle((i - c.gram_before) % c.gram_tiles, c.side, b.width, &m, &n);
         const Operand a{&c.a, z, true};
         *q = piece_of(c, b.width, a, a, m, n, c.side, c.side, z << 3 | k);
         return true;
@@ -408,30 +468,43 @@ struct Poly {
             col0 = q.n0 + at.first_column;
             mirror = q.n0 >= q.m0 + kTile;
         }
-        // v += b times 32 columns of A
-        __device__ __forceinline__ void add_row(const __half* own, int row, int col, float (&v)[32]) const {
+        // v += b times the warp's 32 x 32 of A (or of its low half, `low` elements further on): four lanes to a row, and through
+        // the staging buffer to a row to a lane
+        __device__ __forceinline__ void add_block(int64_t low, int col, float (&v)[32]) const {
+            uint4* s = reinterpret_cast<uint4*>(staging);
+            const __half* from = a + low + (int64_t)(row0 + lane / 4) * c.ld_a + col + lane % 4 * 8;
+            uint4 u[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (row0 + lane / 4 + 8 * i < c.side && col + lane % 4 * 8 < c.side)
+                    u[i] = __ldcg(reinterpret_cast<const uint4*>(from + (int64_t)(8 * i) * c.ld_a));
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint4 u{};
-                if (row < c.side && col + 8 * i < c.side) u = *reinterpret_cast<const uint4*>(own + 8 * i);
-                const __half2* h = reinterpret_cast<const __half2*>(&u);
+                const int row = i * 8 + lane / 4;
+                s[row * 4 + (lane % 4 ^ ((row >> 1) & 3))] = u[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = s[lane * 4 + (i ^ ((lane >> 1) & 3))];
+                const __half2* h = reinterpret_cast<const __half2*>(&x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 x = __half22float2(h[e]);
+                    const float2 f = __half22float2(h[e]);
                     const int j = 8 * i + 2 * e;
-                    v[j] = fmaf(p.cb, x.x, v[j]);
-                    v[j + 1] = fmaf(p.cb, x.y, v[j + 1]);
+                    v[j] = fmaf(p.cb, f.x, v[j]);
+                    v[j + 1] = fmaf(p.cb, f.y, v[j + 1]);
                 }
             }
         }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col = col0 + 32 * k, row = row0 + lane;
             if (row0 >= c.side || col >= c.side) return;
-            const __half* own = a + (int64_t)row * c.ld_a + col;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= p.cc;
-            add_row(own, row, col, v);
-            if (c.low) add_row(own + (int64_t)c.low * c.side * c.ld_a, row, col, v);
+            add_block(0, col, v);
+            if (c.low) add_block((int64_t)c.low * c.side * c.ld_a, col, v);
             if ((unsigned)(row - col) < 32u) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -447,18 +520,20 @@ struct Poly {
 struct Apply {
     static constexpr unsigned int kStatus = 0x2000u;
     Batch b;
+    Schedule s;
     int from;
 
-    struct Deal {};
-    __device__ __forceinline__ Deal deal(int) const { return Deal{}; }
-    __device__ __forceinline__ bool piece(const Deal&, int i, Piece* q) const {
-        if (i >= b.out_pieces) return false;
-        const int k = class_of<&Class::out_before>(b, i);
+    using Deal = Turns;
+    __device__ __forceinline__ Deal deal(int pair, int) const { return Turns{pair, 0, 0}; }
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        int group, place;
+        if (!next_piece(s, d, &group, &place)) return false;
+        const int k = group / 2, tiles = s.tiles[group], z = place / tiles, t = place % tiles;
         const Class& c = b.c[k];
-        const int z = (i - c.out_before) / c.out_tiles, t = (i - c.out_before) % c.out_tiles;
-        const int row_tiles = (c.rows + kTile - 1) / kTile;
+        const int rows = row_tiles_of(c.rows);
         const Operand x{&c.x[from], z, !c.wide()}, poly{&c.b, z, true};
-        *q = piece_of(c, b.width, c.wide() ? poly : x, c.wide() ? x : poly, t % row_tiles, t / row_tiles, c.cols, c.side, z << 3 | k);
+        *q = piece_of(c, b.width, c.wide() ? poly : x, c.wide() ? x : poly, t % rows,
+                      group & 1 ? whole_columns(c.cols, b.width) : t / rows, c.cols, c.side, z << 3 | k);
         return true;
     }
 };
@@ -588,8 +663,95 @@ std::vector<std::vector<Group>> batches_of(const int64_t* rows, const int64_t* c
 // is done sooner in twice as many (384 x 1536: 124 us with 128, 148 with 256).
 int width_of(const std::vector<Group>& shapes, int sms) {
     int64_t gram = 0;
-    for (const Group& s : shapes) gram += triangle_tiles((int)std::min(s.rows, s.cols), kTile) * (int64_t)s.which.size();
+    for (const Group& s : shapes) {
+        const int64_t t = row_tiles_of((int)std::min(s.rows, s.cols));
+        gram += t * (t + 1) / 2 * (int64_t)s.which.size();
+    }
     return gram * 4 <= sms ? 128 : kTile;
+}
+
+// A group's pieces and how long each takes, in stages of 256 columns.
+struct Work {
+    int group, pieces, cost;
+};
+
+// Deals the groups, longest pieces first, each piece to the pair that has least so far.
+void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
+    std::stable_sort(work.begin(), work.end(), [](const Work& a, const Work& b) { return a.cost > b.cost; });
+    std::vector<int64_t> load(pairs, 0);
+    std::vector<int> order(pairs);
+    s->rounds = 0;
+    for (size_t w = 0; w < work.size(); ++w) {
+        int left = work[w].pieces, done = 0;
+        while (left > 0) {
+            Round& r = s->rows[s->rounds++];
+            r = Round{};
+            r.first = done;
+            r.group = (short)work[w].group;
+            r.repeat = 1;
+            // those that the next pieces go to before anyone gets two of them, least first; all, where rounds run short
+            const bool plain = s->rounds + 2 * (int)(work.size() - w) >= kRounds;
+            const int64_t least = *std::min_element(load.begin(), load.end());
+            order.clear();
+            for (int p = 0; p < pairs; ++p)
+                if (plain || load[p] < least + work[w].cost) order.push_back(p);
+            if ((int)order.size() > left) {
+                std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return load[a] < load[b]; });
+                order.resize(left);
+            }
+            if ((int)order.size() == pairs) r.repeat = (short)std::min(left / pairs, 32767);
+            for (int p : order) {
+                r.pairs[p / 32] |= 1u << p % 32;
+                load[p] += (int64_t)r.repeat * work[w].cost;
+            }
+            left -= r.repeat * (int)order.size();
+            done += r.repeat * (int)order.size();
+        }
+    }
+}
+
+// A piece of `columns` columns: two thirds of the rate at 128 of them, and what a tile's ends take.
+int cost_of(const Class& c, int depth, int columns) {
+    const int stages = (depth + kDepth - 1) / kDepth * (c.low ? 3 : 1);
+    return stages * (kTile + columns) / (2 * kTile) + 6;
+}
+
+int most_pairs(int sms) { return std::max(1, std::min(sms / 2, kMostPairs)); }
+
+template <typename Tiles, typename Depth>
+void schedule(const Batch& b, int sms, Tiles tiles, Depth depth, Schedule* s, int* pieces) {
+    std::vector<Work> work;
+    *pieces = 0;
+    for (int k = 0; k < b.classes; ++k) {
+        const Class& c = b.c[k];
+        for (int narrow = 0; narrow < 2; ++narrow) {
+            int columns;
+            const int n = tiles(c, narrow != 0, &columns);
+            s->tiles[2 * k + narrow] = n;
+            if (n) work.push_back(Work{2 * k + narrow, n * c.count, cost_of(c, depth(c), columns)});
+            *pieces += n * c.count;
+        }
+    }
+    deal_out(std::move(work), std::min(most_pairs(sms), *pieces), s);
+}
+
+// The pieces of the three products.
+struct Schedules {
+    Schedule gram, poly, apply;
+    int symmetric_pieces, apply_pieces;
+};
+void schedules(const Batch& b, int sms, Schedules* s) {
+    const auto triangle = [&](const Class& c, bool narrow, int* columns) {
+        *columns = narrow ? columns_of(c.side % b.width, b.width) : b.width;
+        return narrow ? (has_narrow(c.side, b.width) ? row_tiles_of(c.side) : 0) : triangle_tiles(c.side, b.width);
+    };
+    const auto all = [&](const Class& c, bool narrow, int* columns) {
+        *columns = narrow ? columns_of(c.cols % b.width, b.width) : b.width;
+        return row_tiles_of(c.rows) * (narrow ? has_narrow(c.cols, b.width) : whole_columns(c.cols, b.width));
+    };
+    schedule(b, sms, triangle, [](const Class& c) { return std::max(c.rows, c.cols); }, &s->gram, &s->symmetric_pieces);
+    schedule(b, sms, triangle, [](const Class& c) { return c.side; }, &s->poly, &s->symmetric_pieces);
+    schedule(b, sms, all, [](const Class& c) { return c.side; }, &s->apply, &s->apply_pieces);
 }
 
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
@@ -615,17 +777,11 @@ int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* bas
         for (int i = 0; i < 2; ++i) c.px[i] = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.rows * c.ld_x * 2));
         c.pa = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
         c.pb = reinterpret_cast<__half*>(take((int64_t)(c.count + c.low) * c.side * c.ld_a * 2));
-        c.gram_tiles = triangle_tiles(c.side, b->width);
-        c.out_tiles = ((c.rows + kTile - 1) / kTile) * ((c.cols + b->width - 1) / b->width);
-        c.gram_before = b->gram_pieces;
-        c.out_before = b->out_pieces;
         const int64_t n = s.rows * s.cols;
         c.item = round_up(std::max<int64_t>(kItem, (n + kMostItems - 1) / kMostItems), kItem);
         c.items = (int)((n + c.item - 1) / c.item);
         c.items_before = b->items;
         b->matrices += c.count;
-        b->gram_pieces += c.count * c.gram_tiles;
-        b->out_pieces += c.count * c.out_tiles;
         b->items += c.count * c.items;
     }
     *squares = reinterpret_cast<double*>(take((int64_t)b->items * sizeof(double)));
@@ -653,33 +809,24 @@ bool maps(Batch* b) {
 
 template <typename T, bool kMuon>
 cudaError_t first(const Batch& b, const Streams& s, const Update& u, double* squares, double eps, void* stream) {
-    int from = 0, to = 0;
-    int64_t elements = 0;
-    for (int k = 0; k < b.classes; ++k)
-        for (int z = 0; z < b.c[k].count; ++z) {
-            to += b.c[k].items;
-            elements += (int64_t)b.c[k].rows * b.c[k].cols;
-            if (elements < kGroupElements && to < b.items) continue;
-            MICA_STEP(launch_after(momentum_kernel<T, kMuon>, to - from, 256, 0, stream, b, s, u, from, squares));
-            MICA_STEP(launch_after(first_kernel<T, kMuon>, to - from, 256, 0, stream, b, s, u, from, (const double*)squares, eps));
-            from = to;
-            elements = 0;
-        }
-    return cudaSuccess;
+    MICA_STEP(launch_after(momentum_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, squares));
+    return launch_after(first_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, (const double*)squares, eps);
 }
 
 template <typename O, bool kMuon>
-cudaError_t last(const Muon& call, const Batch& b, const std::vector<Group>& shapes, int from, int sms, void* stream) {
+cudaError_t last(const Muon& call, const Batch& b, const Schedules& s, const std::vector<Group>& shapes, int from, int sms,
+                 void* stream) {
     ApplyLast<O, kMuon> p{};
     p.b = b;
+    p.s = s.apply;
     p.from = from;
     int k = 0;
-    for (const Group& s : shapes)
-        for (int32_t i : s.which) p.out[k++] = static_cast<O*>(call.out[i]);
+    for (const Group& shape : shapes)
+        for (int32_t i : shape.which) p.out[k++] = static_cast<O*>(call.out[i]);
     p.decay = (float)(1.0 - call.hp.lr * call.hp.weight_decay);
     p.skip = (call.hp.flags & MICA_STEP_SKIP_NONFINITE) != 0;
     p.factor = call.d_factor;
-    return launch_gemm<__half>(p, b.out_pieces, sms, stream);
+    return launch_gemm<__half>(p, s.apply_pieces, 2 * most_pairs(sms), stream);
 }
 
 cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* workspace, int sms, void* stream) {
@@ -687,6 +834,8 @@ cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* worksp
     double* squares;
     place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, sms, workspace, &b, &squares);
     if (!maps(&b)) return cudaErrorInvalidValue;
+    Schedules deals;
+    schedules(b, sms, &deals);
     Streams s{};
     int k = 0;
     for (const Group& shape : shapes)
@@ -715,23 +864,26 @@ cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* worksp
         const int from = step & 1;
         Gram g{};
         g.b = b;
+        g.s = deals.gram;
         g.from = from;
-        MICA_STEP(launch_gemm<__half>(g, b.gram_pieces, sms, stream));
+        MICA_STEP(launch_gemm<__half>(g, deals.symmetric_pieces, 2 * most_pairs(sms), stream));
         Poly p{};
         p.b = b;
+        p.s = deals.poly;
         p.ca = (float)(c[0] * kScale);
         p.cb = (float)c[1];
         p.cc = (float)(c[2] / kScale);
-        MICA_STEP(launch_gemm<__half>(p, b.gram_pieces, sms, stream));
+        MICA_STEP(launch_gemm<__half>(p, deals.symmetric_pieces, 2 * most_pairs(sms), stream));
         if (step + 1 < call.ns->steps) {
             ApplyMiddle a{};
             a.b = b;
+            a.s = deals.apply;
             a.from = from;
-            MICA_STEP(launch_gemm<__half>(a, b.out_pieces, sms, stream));
+            MICA_STEP(launch_gemm<__half>(a, deals.apply_pieces, 2 * most_pairs(sms), stream));
         } else {
-            MICA_STEP((call.m                         ? last<float, true>(call, b, shapes, from, sms, stream)
-                       : call.out_dtype == MICA_F16 ? last<__half, false>(call, b, shapes, from, sms, stream)
-                                                      : last<__nv_bfloat16, false>(call, b, shapes, from, sms, stream)));
+            MICA_STEP((call.m                         ? last<float, true>(call, b, deals, shapes, from, sms, stream)
+                       : call.out_dtype == MICA_F16 ? last<__half, false>(call, b, deals, shapes, from, sms, stream)
+                                                      : last<__nv_bfloat16, false>(call, b, deals, shapes, from, sms, stream)));
         }
     }
     return cudaSuccess;
