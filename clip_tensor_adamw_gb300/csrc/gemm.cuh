@@ -13,6 +13,8 @@
 // A policy P is the kernel's parameter, with
 //   Deal deal(int pair, int pairs) const            how the work is dealt to one of the pairs; computed once a thread
 //   bool piece(Deal&, Piece*) const                 the pair's next piece of work; false when there are no more
+//   kAhead                                          the work is known from the parameter alone, and the first piece is looked
+//                                                   up while the kernel before still runs (1 to 2 us, most of it misses)
 //   struct Epilogue                                 what becomes of a piece's sums, made for each piece by each of its threads:
 //     Epilogue(const P&, const Deal&, const Piece&, const Place&)
 //     void chunk(int c, float (&v)[32])             columns [32 c, 32 c + 32) of the thread's row of its half, in order
@@ -74,6 +76,9 @@ struct GemmBarriers {
     uint32_t tmem;
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void load_box3_for_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 at;\n\t"
@@ -154,16 +159,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     cluster_sync();
     fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bar.tmem);
+    typename P::Deal deal;
+    Piece q;
+    bool ok = true, more = false;
+    if constexpr (P::kAhead) {
+        deal = p.deal(pair, pairs);
+        more = p.piece(deal, &q);
+        if (warp == kLoader && lane == 0 && more) {
+            prefetch_map(q.a.map);
+            prefetch_map(q.b.map);
+        }
+    }
     wait_prerequisite();
     allow_dependents();
+    if constexpr (!P::kAhead) {
+        deal = p.deal(pair, pairs);
+        more = p.piece(deal, &q);
+    }
 
-    typename P::Deal deal = p.deal(pair, pairs);
-    bool ok = true;
-    Piece q;
     if (warp == kLoader) {
         if (lane == 0) {
             Turn<kStages> turn;
-            while (ok && p.piece(deal, &q))
+            for (; ok && more; more = p.piece(deal, &q))
                 for (int k = q.from; k < q.to; ++k, turn.next()) {
                     const int s = turn.at;
                     if (!(ok = mbar_wait_idle(&bar.used[s], turn.round ^ 1))) break;
@@ -187,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             const uint64_t a0 = operand_descriptor(smem_u32(a_stage)), b0 = operand_descriptor(smem_u32(b_stage));
             Turn<kStages> turn;
             Turn<2> sums;
-            while (ok && p.piece(deal, &q)) {
+            for (; ok && more; more = p.piece(deal, &q)) {
                 const int b = sums.at;
                 const uint32_t how = instruction<T>(q.a.k_major, q.b.k_major, q.columns);
                 const uint32_t a_step = (q.a.k_major ? 32 : 2048) >> 4, b_step = (q.b.k_major ? 32 : 2048) >> 4;
@@ -213,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int quarter = warp % 4, half = warp / 4;
         Place place{rank * kHalf + quarter * 32 + lane, 0, lane, staging + warp * kStagingBytes};
         Turn<2> sums;
-        while (p.piece(deal, &q)) {
+        for (; more; more = p.piece(deal, &q)) {
             const int b = sums.at, chunks = q.columns / 64;
             place.first_column = half * (q.columns / 2);
             const uint32_t own = tmem + ((uint32_t)quarter << 21) + b * kTile + place.first_column;

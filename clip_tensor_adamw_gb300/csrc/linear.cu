@@ -218,6 +218,7 @@ struct RowSum {
 
 struct Logits {
     static constexpr unsigned int kStatus = 0x100u;
+    static constexpr bool kAhead = false;
     CUtensorMap h, w;
     const Meta* meta;
     const int* target;
@@ -414,6 +415,7 @@ struct LogitGrad : Logits {
 template <typename T>
 struct HiddenGrad {
     static constexpr unsigned int kStatus = 0x200u;
+    static constexpr bool kAhead = false;
     CUtensorMap d, w;
     const Meta* meta;
     const int* index;
@@ -484,6 +486,7 @@ struct HiddenGrad {
 template <typename O>
 struct WeightGrad {
     static constexpr unsigned int kStatus = 0x400u;
+    static constexpr bool kAhead = false;
     CUtensorMap d, h;
     const Meta* meta;
     int most, piece_index, vocab, features;

@@ -31,7 +31,7 @@ constexpr int kMostClasses = 8;      // of a batch
 constexpr int kMostMatrices = 256;
 constexpr int64_t kBatchElements = (int64_t)128 << 20;
 constexpr int kItem = 8192;          // elements that a CTA of the streaming kernels has in registers
-constexpr int kMostItems = 1024;     // parts of a matrix's square sum
+constexpr int kMostItems = 512;      // parts of a matrix's square sum
 constexpr float kScale = 1024.0f;
 // Matrices whose smaller side is at most this are held in pairs: a small matrix's elements are large beside a weight's, so the
 // error would show in a float32 weight (a step of rate r changes the weights' norm by r / 0.02 sqrt(side) of it or so), and
@@ -180,6 +180,25 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
     const bool skip = kMuon && u.skip && !(f > 0.0f);
     const bool wide = aligned16(in) && aligned16(m);
     const bool even = c.cols % 4 == 0;
+    __half* x = c.px[0] + (int64_t)it.z * c.rows * c.ld_x;
+    const int64_t low = (int64_t)c.low * c.rows * c.ld_x;
+    // the row and column of the thread's elements, which go on by 1,024
+    int64_t at = it.from + threadIdx.x * 4;
+    int64_t row = at / c.cols;
+    int col = (int)(at - row * c.cols);
+    const int rows_on = 1024 / c.cols, cols_on = 1024 - rows_on * c.cols;
+    float4 g[4], now[4];
+    int there[4];
+    auto load = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t a = at + j * 1024;
+            there[j] = a >= it.to ? 0 : it.to - a < 4 ? (int)(it.to - a) : 4;
+            g[j] = load4(in + a, there[j], wide);
+            if (kMuon) now[j] = load4(m + a, there[j], wide);
+        }
+    };
+    load();  // (before the norm is known: its sum takes a while)
     if (!skip) {
         const double* mine = squares + c.items_before + it.z * c.items;
         double sum = 0.0;
@@ -192,28 +211,11 @@ __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batc
             sum = 0.0;
             for (int i = 0; i < 8; ++i) sum += part[i];
             const float q = (float)sum;
-            const double norm = q > 1e-30f && q < 1e30f ? (double)sqrtf(q) : sqrt(sum);
-            scale = (float)((double)kScale / (norm + eps));
+            scale = q > 1e-30f && q < 1e30f ? kScale / (sqrtf(q) + (float)eps) : (float)((double)kScale / (sqrt(sum) + eps));
         }
         __syncthreads();
     }
-    __half* x = c.px[0] + (int64_t)it.z * c.rows * c.ld_x;
-    const int64_t low = (int64_t)c.low * c.rows * c.ld_x;
-    // the row and column of the thread's elements, which go on by 1,024
-    int64_t at = it.from + threadIdx.x * 4;
-    int64_t row = at / c.cols;
-    int col = (int)(at - row * c.cols);
-    const int rows_on = 1024 / c.cols, cols_on = 1024 - rows_on * c.cols;
-    for (; at < it.to; at += 4 * 1024) {
-        float4 g[4], now[4];
-        int there[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t a = at + j * 1024;
-            there[j] = a >= it.to ? 0 : it.to - a < 4 ? (int)(it.to - a) : 4;
-            g[j] = load4(in + a, there[j], wide);
-            if (kMuon) now[j] = load4(m + a, there[j], wide);
-        }
+    for (; at < it.to; at += 4 * 1024, load()) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (!skip) {
@@ -404,6 +406,7 @@ __device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, in
 // A = x x^T or x^T x
 struct Gram : Symmetric {
     static constexpr unsigned int kStatus = 0x800u;
+    static constexpr bool kAhead = true;
     int from;  // the buffer that x is in
 
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
@@ -441,6 +444,7 @@ struct Gram : Symmetric {
 // B = a I + b A + c A^2
 struct Poly : Symmetric {
     static constexpr unsigned int kStatus = 0x1000u;
+    static constexpr bool kAhead = true;
     float ca, cb, cc;
 
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
@@ -459,6 +463,7 @@ struct Poly : Symmetric {
         int row0, col0, lane;
         unsigned char* staging;
         bool mirror;
+        uint4 next[4];  // of A, for the next chunk
         __device__ __forceinline__ Epilogue(const Poly& p, const Deal&, const Piece& q, const Place& at)
             : p(p), c(p.b.c[unpack(q.tile).c]), lane(at.lane), staging(at.staging) {
             const int64_t first = (int64_t)unpack(q.tile).z * c.side * c.ld_a;
@@ -467,17 +472,21 @@ struct Poly : Symmetric {
             row0 = q.m0 + at.row - at.lane;
             col0 = q.n0 + at.first_column;
             mirror = q.n0 >= q.m0 + kTile;
+            load_block(0, col0, next);
         }
-        // v += b times the warp's 32 x 32 of A (or of its low half, `low` elements further on): four lanes to a row, and through
-        // the staging buffer to a row to a lane
-        __device__ __forceinline__ void add_block(int64_t low, int col, float (&v)[32]) const {
-            uint4* s = reinterpret_cast<uint4*>(staging);
+        // The warp's 32 x 32 of A (or of its low half, `low` elements further on), four lanes to a row
+        __device__ __forceinline__ void load_block(int64_t low, int col, uint4 (&u)[4]) const {
             const __half* from = a + low + (int64_t)(row0 + lane / 4) * c.ld_a + col + lane % 4 * 8;
-            uint4 u[4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                u[i] = uint4{};
                 if (row0 + lane / 4 + 8 * i < c.side && col + lane % 4 * 8 < c.side)
                     u[i] = __ldcg(reinterpret_cast<const uint4*>(from + (int64_t)(8 * i) * c.ld_a));
+            }
+        }
+        // v += b times that, through the staging buffer to a row to a lane
+        __device__ __forceinline__ void add_block(const uint4 (&u)[4], float (&v)[32]) const {
+            uint4* s = reinterpret_cast<uint4*>(staging);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -503,8 +512,14 @@ struct Poly : Symmetric {
             if (row0 >= c.side || col >= c.side) return;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= p.cc;
-            add_block(0, col, v);
-            if (c.low) add_block((int64_t)c.low * c.side * c.ld_a, col, v);
+            const uint4 now[4] = {next[0], next[1], next[2], next[3]};
+            load_block(0, col + 32, next);  // (a tile's end reads a little on: the loads' latency is most of a chunk's time)
+            add_block(now, v);
+            if (c.low) {
+                uint4 rest[4];
+                load_block((int64_t)c.low * c.side * c.ld_a, col, rest);
+                add_block(rest, v);
+            }
             if ((unsigned)(row - col) < 32u) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -519,6 +534,7 @@ struct Poly : Symmetric {
 // x = B x or x B: what the middle steps and the last one share
 struct Apply {
     static constexpr unsigned int kStatus = 0x2000u;
+    static constexpr bool kAhead = true;
     Batch b;
     Schedule s;
     int from;
