@@ -274,7 +274,7 @@ struct SplitDeal {
 // The number of parts is the one that makes the rest shortest by this count, in stages: rounds of parts, each with a part's
 // stages and kPartCost for filling and emptying it; and what joining takes, kJoinCost and a quarter of a stage for each part
 // (512 KB written and read). 48 tiles of 786 stages on 76 pairs: 1 part 221 us, 3 parts (2 rounds) 150 us.
-constexpr int kPartCost = 6, kJoinCost = 12, kLeastStages = 4, kMostRounds = 3;
+constexpr int kPartCost = 6, kJoinCost = 12, kLeastStages = 4, kMostRounds = 2;
 __host__ __device__ inline SplitDeal split_deal(int tiles, int stages, int pair, int pairs) {
     SplitDeal d{tiles, stages, tiles / pairs * pairs, 1, tiles, pair, pairs};
     const int rest = tiles - d.whole;

@@ -6,8 +6,13 @@
 //
 // The rows that count are gathered first, so that unscored rows (prompts) cost nothing, and taken in pieces of at most
 // kGradBytes of d. The forward pass is one product over all of the vocabulary whose epilogue keeps a running maximum and sum
-// for each row; the gradient takes the product again (a third more of the operations; keeping the logits would take memory
-// that grows with rows x vocabulary), rounds d to 16 bits once, in its epilogue, and multiplies it with W and with h.
+// for each row. The gradient takes the product again: keeping the logits would take memory that grows with rows x vocabulary.
+// d is rounded to 16 bits once, in that product's epilogue, and multiplied with W and with h in one launch.
+//
+// Cross entropy, where both are wanted, needs the product once (bfloat16 and large enough, kOnceProducts): its epilogue leaves
+// q_ij = exp(z_ij - z_i,target), which needs no maximum (the sum is at least 1) and has bfloat16's range, and sums it up. The
+// rest is a factor 1 / sum_j q_ij for each row: in dh's epilogue, and on h's rows for dW. The few rows whose sum leaves the
+// range, whose targets are less likely than some e^-44, are taken again, counted from lse.
 //
 // Logits, maxima, sums and gradients' sums are float32. d is rounded to the operands' type because the tensor cores multiply
 // what they are given in 16 bits: relative 2^-9 (bfloat16) or 2^-12 of each of its elements on average. binary16 has not the
@@ -21,11 +26,14 @@
 namespace mica {
 namespace {
 
-constexpr int kScanThreads = 1024, kScanItems = 8;
-constexpr int64_t kGradBytes = (int64_t)1 << 30;   // of d, that a piece of the rows takes
+constexpr int64_t kGradBytes = (int64_t)1 << 30;    // of d, that a piece of the rows takes
 constexpr int64_t kStatBytes = (int64_t)256 << 20;  // of the forward pass's maxima and sums
 constexpr int kMostRows = 16384;                    // of a piece in the forward pass
+// Products of rows x features x vocabulary from which cross entropy takes the logits once: below, the product that it saves
+// is shorter than the launch that looks for rows to take again.
+constexpr double kOnceProducts = 1e10;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMostSum = 0x1p64f;                 // of exp(z - z_target) over 32 columns
 
 // What the scan of the targets leaves for the kernels after it.
 struct Meta {
@@ -33,6 +41,7 @@ struct Meta {
     float coef;       // cross entropy: every row's coefficient, with the scale of d in it
     float scale;      // of d
     float inv_scale;
+    unsigned int ticket;  // CTAs of the rows' joins that have ended
 };
 
 // Rows [from, from + rows) of those that count.
@@ -56,154 +65,157 @@ __device__ __forceinline__ int64_t target_at(const void* targets, bool wide, int
 }
 
 // ------------------------------------------------------------------------------------------------------------------------
-// which rows count
+// the rows that count, side by side
 // ------------------------------------------------------------------------------------------------------------------------
 
-struct Scan {
+struct Gather {
     const void* targets;
-    int wide, rows;
-    const float* dlogps;  // or null: a row whose dlogps is 0 does not count
-    float* logps;         // or null; logps and lse of rows that do not count are 0
-    float* lse;           // or null
-    int* index;           // the rows that count, in order, and after them, backwards, the others
-    Meta* meta;
+    const unsigned short* h;
+    int64_t ld_h;
+    int rows, features, vocab, wide, aligned;
+    const float* dlogps;   // or null: a row whose dlogps is 0 does not count
+    const float* lse;      // with dlogps
     float inv_t;
-    float ce_factor;      // cross entropy: -grad_scale / T, divided by `denom` or, where that is 0, by the count
+    float ce_factor;       // cross entropy: -grad_scale / T, divided by `denom` or, where that is 0, by the count
     float denom;
-    int scaled;           // d is scaled
+    int scaled;            // d is scaled
+    int most, piece;
+    Meta* meta;            // written by the first piece
+    int* index;            // the rows that count
+    unsigned short* out;   // [most][ld]
+    int ld;
+    int* target;           // [most] -1: past the vocabulary
+    float* coef;           // [most] c * scale, or null
+    float* origin;         // [most] lse * log2(e), or z_target a (below), or null
+    const unsigned short* w;  // where z_target is wanted, or null
+    int64_t ld_w;
+    float a;               // log2(e) / T
+    int* again;            // [1 + most / 256] or null: zeroed
+    float* logps;          // or null; logps and lse_out of rows that do not count are 0
+    float* lse_out;        // or null
+    unsigned short* zero;  // rows that do not count get zeros here, or null
+    int64_t ld_zero;
 };
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// One CTA: a few microseconds for 8,192 rows.
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(Scan s) {
-    __shared__ int sums[32];
-    __shared__ float tops[32];
+__device__ __forceinline__ bool row_counts(const Gather& g, int i, float* c) {
+    if (target_at(g.targets, g.wide, i) < 0) return false;
+    *c = g.dlogps ? g.dlogps[i] : 1.0f;
+    return *c != 0.0f;
+}
+
+// A CTA takes neighbouring rows. Each looks through all of the targets, for the rows that count before its own and altogether
+// (64 KB for 8,192 rows): a launch less than with a scan of its own. Rows past a piece's up to the next multiple of 64 are
+// zeros: the weight gradient adds them up.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_kernel(Gather g) {
+    __shared__ int sums[2][8];
+    __shared__ float tops[8];
+    __shared__ uint32_t flags[8];
     wait_prerequisite();
     allow_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int before = 0;
+    const int each = (g.rows + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int64_t from = (int64_t)blockIdx.x * each, to = from + each < g.rows ? from + each : g.rows;
+    int before = 0, count = 0;
     float top = 0.0f;
-    for (int base = 0; base < s.rows; base += kScanThreads * kScanItems) {
-        const int first = base + threadIdx.x * kScanItems;
-        uint32_t on = 0;
-#pragma unroll
-        for (int k = 0; k < kScanItems; ++k) {
-            const int i = first + k;
-            if (i >= s.rows || target_at(s.targets, s.wide, i) < 0) continue;
-            const float c = s.dlogps ? s.dlogps[i] : 1.0f;
-            if (c == 0.0f) continue;
-            on |= 1u << k;
-            if (fabsf(c) > top || c != c) top = fabsf(c);  // (a NaN stays: nothing is larger)
-        }
-        const int mine = __popc(on);
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int v = __shfl_up_sync(~0u, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) sums[warp] = upto;
-        __syncthreads();
-        int at = before + upto - mine, all = 0;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) at += sums[i];
-            all += sums[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kScanItems; ++k) {
-            const int i = first + k;
-            if (i >= s.rows) break;
-            if (on >> k & 1) {
-                s.index[at++] = i;
-            } else {
-                s.index[s.rows - 1 - (i - at)] = i;
-                if (s.logps) s.logps[i] = 0.0f;
-                if (s.lse) s.lse[i] = 0.0f;
-            }
-        }
-        before += all;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < g.rows; i += 256) {
+        float c;
+        if (!row_counts(g, (int)i, &c)) continue;
+        ++count;
+        before += i < from;
+        if (fabsf(c) > top || c != c) top = fabsf(c);  // (a NaN stays: nothing is larger)
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
+        before += __shfl_xor_sync(~0u, before, d);
+        count += __shfl_xor_sync(~0u, count, d);
         const float v = __shfl_xor_sync(~0u, top, d);
         if (v > top || v != v) top = v;
     }
-    if (lane == 0) tops[warp] = top;
+    if (lane == 0) {
+        sums[0][warp] = before;
+        sums[1][warp] = count;
+        tops[warp] = top;
+    }
     __syncthreads();
-    if (threadIdx.x) return;
-    for (int i = 0; i < 32; ++i)
+    before = count = 0;
+    for (int i = 0; i < 8; ++i) {
+        before += sums[0][i];
+        count += sums[1][i];
         if (tops[i] > top || tops[i] != tops[i]) top = tops[i];
-    Meta m{before, 0.0f, 1.0f, 1.0f};
-    const float ce = s.ce_factor / (s.denom > 0.0f ? s.denom : (float)before);
-    const float most = s.dlogps ? top * s.inv_t : fabsf(ce);
-    if (s.scaled && most > 0.0f && most < INFINITY) {
-        int e = (int)(__float_as_uint(most) >> 23) - 127;  // most < 2^(e + 1); a subnormal counts as 2^-127
+    }
+    Meta m{count, 0.0f, 1.0f, 1.0f, 0u};
+    const float ce = g.ce_factor / (g.denom > 0.0f ? g.denom : (float)count);
+    const float largest = g.dlogps ? top * g.inv_t : fabsf(ce);
+    if (g.scaled && largest > 0.0f && largest < INFINITY) {
+        int e = (int)(__float_as_uint(largest) >> 23) - 127;  // largest < 2^(e + 1); a subnormal counts as 2^-127
         e = 14 - (e < -100 ? -100 : e);
         m.scale = power_of_two(e);
         m.inv_scale = power_of_two(-e);
     }
     m.coef = ce * m.scale;
-    *s.meta = m;
-}
-
-// ------------------------------------------------------------------------------------------------------------------------
-// the rows that count, side by side
-// ------------------------------------------------------------------------------------------------------------------------
-
-struct Gather {
-    const unsigned short* h;
-    const void* targets;
-    int64_t ld_h;
-    int rows, features, vocab, wide, aligned;
-    const int* index;
-    const Meta* meta;
-    int most, piece;
-    const float* lse;      // or null
-    const float* dlogps;   // or null
-    float inv_t;
-    unsigned short* out;   // [most][ld]
-    int ld;
-    int* target;           // [most] -1: past the vocabulary
-    float* coef;           // [most] c * scale, or null
-    float* origin;         // [most] lse * log2(e)
-    unsigned short* zero;  // rows that do not count get zeros here, or null
-    int64_t ld_zero;
-};
-
-// A warp to a row. Rows up to the next multiple of 64 are zeros: the weight gradient adds them up.
-__global__ void __launch_bounds__(256) gather_kernel(Gather g) {
-    wait_prerequisite();
-    allow_dependents();
-    const Meta m = *g.meta;
-    const Span span = span_of(m.count, g.most, g.piece);
-    const int lane = threadIdx.x % 32, padded = (span.rows + 63) / 64 * 64;
-    const int others = g.zero && g.piece == 0 ? g.rows - m.count : 0;
-    for (int64_t r = blockIdx.x * 8ll + threadIdx.x / 32; r < padded + others; r += gridDim.x * 8ll) {
-        if (r >= padded) {
-            unsigned short* to = g.zero + (int64_t)g.index[g.rows - 1 - (r - padded)] * g.ld_zero;
-            for (int c = lane; c < g.features; c += 32) to[c] = 0;
-            continue;
-        }
-        unsigned short* to = g.out + r * g.ld;
-        if (r >= span.rows) {
-            for (int c = lane; c < g.ld / 8; c += 32) reinterpret_cast<uint4*>(to)[c] = uint4{};
-            continue;
-        }
-        const int64_t i = g.index[span.from + r];
-        const unsigned short* from = g.h + i * g.ld_h;
-        const int whole = g.aligned ? g.features / 8 : 0;
-        for (int c = lane; c < whole; c += 32) reinterpret_cast<uint4*>(to)[c] = reinterpret_cast<const uint4*>(from)[c];
-        for (int c = whole * 8 + lane; c < g.features; c += 32) to[c] = from[c];
-        if (lane == 0) {
-            const int64_t y = target_at(g.targets, g.wide, i);
-            g.target[r] = y < g.vocab ? (int)y : -1;
-            if (g.coef) {
-                g.coef[r] = y >= g.vocab ? NAN : g.dlogps ? g.dlogps[i] * g.inv_t * m.scale : m.coef;
-                g.origin[r] = g.lse[i] * kLog2E;
+    const Span span = span_of(count, g.most, g.piece);
+    if (blockIdx.x == 0) {
+        if (g.piece == 0 && threadIdx.x == 0) *g.meta = m;
+        if (g.again)
+            for (int i = threadIdx.x; i < 1 + g.most / kTile; i += 256) g.again[i] = 0;
+        for (int r = span.rows + warp; r < (span.rows + 63) / 64 * 64; r += 8)
+            for (int c = lane; c < g.ld / 8; c += 32) reinterpret_cast<uint4*>(g.out + (int64_t)r * g.ld)[c] = uint4{};
+    }
+    // 256 rows at a time: their flags, and then a warp to a row
+    for (int64_t base = from; base < to; base += 256) {
+        const int64_t own = base + threadIdx.x;
+        float c;
+        const uint32_t word = __ballot_sync(~0u, own < to && row_counts(g, (int)own, &c));
+        if (lane == 0) flags[warp] = word;
+        __syncthreads();
+        int rank0 = before;
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t f = flags[k];
+            // rows 32 k + warp, + 8, ...
+            for (int j = warp; j < 32 && base + 32 * k + j < to; j += 8) {
+                const int64_t i = base + 32 * k + j;
+                if (!(f >> j & 1)) {
+                    if (g.piece) continue;
+                    if (g.zero) {
+                        unsigned short* z = g.zero + i * g.ld_zero;
+                        for (int x = lane; x < g.features; x += 32) z[x] = 0;
+                    }
+                    if (lane == 0 && g.logps) g.logps[i] = 0.0f;
+                    if (lane == 0 && g.lse_out) g.lse_out[i] = 0.0f;
+                    continue;
+                }
+                const int rank = rank0 + __popc(f & ((1u << j) - 1)), r = rank - span.from;
+                if (r < 0 || r >= span.rows) continue;
+                const unsigned short* in = g.h + i * g.ld_h;
+                unsigned short* out = g.out + (int64_t)r * g.ld;
+                const int whole = g.aligned ? g.features / 8 : 0;
+                for (int x = lane; x < whole; x += 32) reinterpret_cast<uint4*>(out)[x] = reinterpret_cast<const uint4*>(in)[x];
+                for (int x = whole * 8 + lane; x < g.features; x += 32) out[x] = in[x];
+                const int64_t y = target_at(g.targets, g.wide, i);
+                float z = 0.0f;  // the target's logit
+                if (g.w && y < g.vocab) {
+                    const T* a = reinterpret_cast<const T*>(in);
+                    const T* b = reinterpret_cast<const T*>(g.w + y * g.ld_w);
+#pragma unroll 4
+                    for (int x = lane; x < g.features; x += 32) z = fmaf(widen(a[x]), widen(b[x]), z);
+#pragma unroll
+                    for (int d = 16; d; d /= 2) z += __shfl_xor_sync(~0u, z, d);
+                }
+                if (lane) continue;
+                g.index[rank] = (int)i;
+                g.target[r] = y < g.vocab ? (int)y : -1;
+                if (g.coef) g.coef[r] = y >= g.vocab ? NAN : g.dlogps ? g.dlogps[i] * g.inv_t * m.scale : m.coef;
+                if (g.dlogps) g.origin[r] = g.lse[i] * kLog2E;
+                else if (g.w) g.origin[r] = y >= g.vocab ? NAN : z * g.a;
             }
+            rank0 += __popc(f);
         }
+        before = rank0;
+        __syncthreads();
     }
 }
 
@@ -291,43 +303,94 @@ struct LogitSums : Logits {
     };
 };
 
-struct Join {
-    const Meta* meta;
-    const int* index;
-    const int* target;
-    const RowSum* sums;
-    const float* at;
-    int most, piece, parts;
-    float a;
-    float* logps;
-    float* lse;  // or null
-};
+// The product that cross entropy takes once: q = 2^(z a - origin), 0 at the target, and its sum. A sum counts from the
+// target's logit; where 32 columns leave the range (kMostSum), from the largest so far, and the row is taken again.
+template <typename T>
+struct LogitOnce : Logits {
+    RowSum* sums;         // [most][vocabulary / 128]; null the second time
+    int parts;
+    const float* origin;  // the target's logit times a; lse, in rows taken again
+    const float* at;      // the second time: the targets' elements
+    const int* again;     // the second time: whether there are any such rows, and in which tiles; or null
+    T* d;                 // [most][ld]
+    int ld;
 
-__device__ __forceinline__ RowSum operator+(RowSum x, RowSum y) {
-    const float o = fmaxf(x.origin, y.origin);
-    return RowSum{o, x.sum * exp2_fast(x.origin - o) + y.sum * exp2_fast(y.origin - o)};
-}
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        if (!again) return Logits::piece(d, q);
+        if (!again[0]) return false;
+        while (Logits::piece(d, q))
+            if (again[1 + q->m0 / kTile]) return true;
+        return false;
+    }
 
-// A warp to a row; joined in a fixed order.
-__global__ void __launch_bounds__(256) join_rows_kernel(Join j) {
-    wait_prerequisite();
-    allow_dependents();
-    const Span span = span_of(j.meta->count, j.most, j.piece);
-    const int lane = threadIdx.x % 32, row = blockIdx.x * 8 + threadIdx.x / 32;
-    if (row >= span.rows) return;
-    RowSum s{-1e38f, 0.0f};
-    const RowSum* own = j.sums + (int64_t)row * j.parts;
-#pragma unroll 4
-    for (int k = lane; k < j.parts; k += 32) s = s + own[k];
+    struct Epilogue {
+        const LogitOnce& p;
+        int row, column, target, lane, stored;
+        bool live;
+        float c, at_target;
+        RowSum s;
+        unsigned char* staging;
+        unsigned short* to;
+        __device__ __forceinline__ Epilogue(const LogitOnce& p, const Deal& d, const Piece& q, const Place& at)
+            : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), lane(at.lane), staging(at.staging) {
+            live = row < d.rows;
+            target = live ? p.target[row] : -1;
+            c = live ? p.origin[row] : INFINITY;
+            at_target = live && p.again ? p.at[row] : 0.0f;
+            s = RowSum{c, 0.0f};
+            stored = (d.rows + 63) / 64 * 64 - (row - lane);  // rows of the warp's 32 that the weight gradient reads
+            to = reinterpret_cast<unsigned short*>(p.d) + (int64_t)(row - lane) * p.ld;
+        }
+        __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
+            const int first = column + 32 * k;
+            if (first >= p.ld || stored <= 0) return;
+            if (first + 32 > p.vocab) {
 #pragma unroll
-    for (int d = 16; d; d /= 2)
-        s = s + RowSum{__shfl_xor_sync(~0u, s.origin, d), __shfl_xor_sync(~0u, s.sum, d)};
-    if (lane) return;
-    const int64_t i = j.index[span.from + row];
-    const float l = log2f(s.sum);
-    j.logps[i] = j.target[row] < 0 ? NAN : (fmaf(j.at[row], j.a, -s.origin) - l) * kLn2;
-    if (j.lse) j.lse[i] = (s.origin + l) * kLn2;
-}
+                for (int i = 0; i < 32; ++i)
+                    if (first + i >= p.vocab) v[i] = -INFINITY;
+            }
+            const bool here = (unsigned)(target - first) < 32u;
+            if (here) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (target == first + i) v[i] = -INFINITY;
+            }
+            float part[4] = {};
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float q0 = exp2_fast(fmaf(v[i], p.a, -c)), q1 = exp2_fast(fmaf(v[i + 1], p.a, -c));
+                part[i % 4] += q0;
+                part[i % 4 + 1] += q1;
+                if (here) {
+                    if (target == first + i) q0 = at_target;
+                    if (target == first + i + 1) q1 = at_target;
+                }
+                w[i / 2] = live ? pack2<T>(q0, q1) : 0u;  // (whatever z was)
+            }
+            const float sum = (part[0] + part[1]) + (part[2] + part[3]);
+            if (!live) {
+            } else if (s.origin == c && sum < kMostSum) {
+                s.sum += sum;
+            } else {
+                float top = v[0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+                top *= p.a;
+                if (top > s.origin) {
+                    s.sum *= exp2_fast(s.origin - top);
+                    s.origin = top;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s.sum += exp2_fast(fmaf(v[i], p.a, -s.origin));
+            }
+            store_block(to, p.ld, stored, p.ld, 0, first, lane, true, staging, w);
+        }
+        __device__ __forceinline__ void done() {
+            if (p.sums && live && column < p.vocab) p.sums[(int64_t)row * p.parts + column / kHalf] = s;
+        }
+    };
+};
 
 // A float32 sum with what its rounding left out.
 struct Exact {
@@ -337,29 +400,152 @@ struct Exact {
         lo += (hi - (s - b)) + (x - b);
         hi = s;
     }
+    __device__ __forceinline__ void add(Exact x) {
+        add(x.hi);
+        lo += x.lo;
+    }
+    __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
 };
 
-// loss = -sum logps / denom, or / the scored rows' number; rows that do not count hold zeros
-__global__ void __launch_bounds__(1024) loss_kernel(const float* logps, int rows, const Meta* meta, float denom, float* loss) {
-    __shared__ Exact part[1024];
+struct Join {
+    Meta* meta;
+    const int* index;
+    const int* target;
+    const RowSum* sums;
+    int most, piece, parts;
+    float a;
+    float* logps;
+    float* lse;            // or null
+    // the logits' sums
+    const float* at;       // the targets' logits
+    float* origin;         // or null: lse * log2(e)
+    // the sums of the product taken once
+    int once;
+    float* at_target;      // what d holds at the target
+    float* factor;         // of a row of d
+    int* again;
+    unsigned short* d;
+    int ld_d;
+    const unsigned short* h;
+    unsigned short* scaled_h;
+    int ld_h, features;
+    // cross entropy's loss, or null
+    float* loss;
+    float denom;
+    Exact* partial;        // [CTAs of all pieces]
+    int all;               // of those
+};
+
+__device__ __forceinline__ RowSum operator+(RowSum x, RowSum y) {
+    const float o = fmaxf(x.origin, y.origin);
+    return RowSum{o, x.sum * exp2_fast(x.origin - o) + y.sum * exp2_fast(y.origin - o)};
+}
+
+// A row's sum, by a warp, in a fixed order.
+__device__ __forceinline__ RowSum row_sum(const Join& j, int row, int lane) {
+    RowSum s{-1e38f, 0.0f};
+    const RowSum* own = j.sums + (int64_t)row * j.parts;
+#pragma unroll 4
+    for (int k = lane; k < j.parts; k += 32) s = s + own[k];
+#pragma unroll
+    for (int d = 16; d; d /= 2) s = s + RowSum{__shfl_xor_sync(~0u, s.origin, d), __shfl_xor_sync(~0u, s.sum, d)};
+    return s;
+}
+
+// A row of the product taken once: the target's logit is the origin c that its sum (over the others) counts from, unless
+// it left the range. d's element at the target is that of p - 1: minus the others' sum. Returns the log-probability.
+template <typename T>
+__device__ __forceinline__ float join_once(const Join& j, const Meta& m, RowSum s, int row, int lane) {
+    const float c = j.origin[row], k = -m.coef;
+    __syncwarp();
+    float logp, factor, at;
+    if (!(c < INFINITY)) {  // inf - inf, or no target
+        logp = factor = at = NAN;
+    } else if (!(s.origin > c)) {
+        logp = -log1pf(s.sum);
+        factor = k / (1.0f + s.sum);
+        at = -s.sum;
+    } else {  // counted from lse the second time
+        const float lse = s.origin + log2f(s.sum + exp2_fast(c - s.origin));
+        logp = (c - lse) * kLn2;
+        factor = k;
+        at = expm1f(logp);
+        if (lane == 0) {
+            j.origin[row] = lse;
+            j.again[0] = 1;
+            j.again[1 + row / kTile] = 1;
+        }
+    }
+    const int y = j.target[row];
+    if (lane == 0) {
+        j.factor[row] = factor;
+        j.at_target[row] = at;
+        if (y >= 0) reinterpret_cast<T*>(j.d)[(int64_t)row * j.ld_d + y] = narrow<T>(at);
+    }
+    const T* in = reinterpret_cast<const T*>(j.h) + (int64_t)row * j.ld_h;
+    T* out = reinterpret_cast<T*>(j.scaled_h) + (int64_t)row * j.ld_h;
+    for (int x = lane * 4; x < j.features; x += 128) {  // (ld_h is a multiple of 8)
+        const float4 v = load4(in + x, 4, true);
+        store4(out + x, make_float4(v.x * factor, v.y * factor, v.z * factor, v.w * factor), 4, true);
+    }
+    return logp;
+}
+
+// A warp to a row; and cross entropy's loss, whose parts the CTA that ends last adds up in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_rows_kernel(Join j) {
+    __shared__ Exact part[256];
+    __shared__ bool last;
     wait_prerequisite();
     allow_dependents();
+    const Meta m = *j.meta;
+    const Span span = span_of(m.count, j.most, j.piece);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row = blockIdx.x * 8 + warp;
+    float logp = 0.0f;
+    if (row < span.rows) {
+        const RowSum s = row_sum(j, row, lane);
+        const int64_t i = j.index[span.from + row];
+        if (j.once) {
+            logp = join_once<T>(j, m, s, row, lane);
+        } else {
+            const float l = log2f(s.sum);
+            logp = j.target[row] < 0 ? NAN : (fmaf(j.at[row], j.a, -s.origin) - l) * kLn2;
+            if (lane == 0 && j.lse) j.lse[i] = (s.origin + l) * kLn2;
+            if (lane == 0 && j.origin) j.origin[row] = s.origin + l;
+        }
+        if (lane == 0) j.logps[i] = logp;
+    } else if (j.once && row < (span.rows + 63) / 64 * 64) {
+        unsigned short* out = j.scaled_h + (int64_t)row * j.ld_h;
+        for (int x = lane; x < j.ld_h / 8; x += 32) reinterpret_cast<uint4*>(out)[x] = uint4{};
+    }
+    if (!j.loss) return;
+    if (lane == 0) part[warp] = Exact{logp, 0.0f};
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        Exact e;
+        for (int i = 0; i < 8; ++i) e.add(part[i]);
+        j.partial[j.piece * (int)gridDim.x + blockIdx.x] = e;
+        __threadfence();
+        last = atomicAdd(&j.meta->ticket, 1u) == (unsigned)j.all - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
     Exact e;
-    for (int i = threadIdx.x; i < rows; i += 1024) e.add(logps[i]);
+    for (int i = threadIdx.x; i < j.all; i += 256) {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(j.partial + i));
+        e.add(Exact{f.x, f.y});
+    }
     part[threadIdx.x] = e;
-    for (int n = 512; n; n /= 2) {
+    for (int n = 128; n; n /= 2) {
         __syncthreads();
         if (threadIdx.x < n) {
             Exact x = part[threadIdx.x];
-            x.add(part[threadIdx.x + n].hi);
-            x.lo += part[threadIdx.x + n].lo;
+            x.add(part[threadIdx.x + n]);
             part[threadIdx.x] = x;
         }
     }
-    if (threadIdx.x) return;
-    const int count = meta->count;
-    const float sum = part[0].hi == part[0].hi && fabsf(part[0].hi) < INFINITY ? part[0].hi + part[0].lo : part[0].hi;
-    *loss = count ? -sum / (denom > 0.0f ? denom : (float)count) : 0.0f;
+    if (threadIdx.x == 0) *j.loss = m.count ? -part[0].value() / (j.denom > 0.0f ? j.denom : (float)m.count) : 0.0f;
 }
 
 // ------------------------------------------------------------------------------------------------------------------------
@@ -412,15 +598,15 @@ struct LogitGrad : Logits {
 // the gradients of the hidden states and of the embedding
 // ------------------------------------------------------------------------------------------------------------------------
 
+// dh = factor * d W, to the rows' places
 template <typename T>
 struct HiddenGrad {
-    static constexpr unsigned int kStatus = 0x200u;
-    static constexpr bool kAhead = false;
     CUtensorMap d, w;
     const Meta* meta;
     const int* index;
     int most, piece_index, vocab, features;
-    T* dh;
+    const float* factor;  // of a row, or null
+    T* dh;                // or null
     int64_t ld;
     int wide, wide16;  // rows aligned for stores of four elements, of eight
     float* parts;
@@ -435,8 +621,8 @@ struct HiddenGrad {
         const Span span = span_of(m.count, most, piece_index);
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
-        static_cast<SplitDeal&>(r) = split_deal((span.rows + kTile - 1) / kTile * column_tiles, (vocab + kDepth - 1) / kDepth,
-                                                pair, pairs);
+        static_cast<SplitDeal&>(r) = split_deal(dh ? (span.rows + kTile - 1) / kTile * column_tiles : 0,
+                                                (vocab + kDepth - 1) / kDepth, pair, pairs);
         r.span = span;
         r.column_tiles = column_tiles;
         r.scale = m.inv_scale;
@@ -452,19 +638,21 @@ struct HiddenGrad {
         return true;
     }
     __device__ __forceinline__ int rows_of(const Deal& r) const { return r.span.rows; }
+    __device__ __forceinline__ float scale_of(const Deal& r, int row) const { return factor ? factor[row] : r.scale; }
     // four sums of a row
     __device__ __forceinline__ void put(const Deal& r, int row, int col, float4 v) const {
         if (row >= r.span.rows || col >= features) return;
-        const float s = r.scale;
+        const float s = scale_of(r, row);
         store4<T>(dh + index[r.span.from + row] * ld + col, make_float4(v.x * s, v.y * s, v.z * s, v.w * s), features - col,
                   wide);
     }
     // a warp's 32 x 32 of them
     __device__ __forceinline__ void block(const Deal& r, int row0, int col0, const Place& at, float (&v)[32]) const {
         if (row0 >= r.span.rows || col0 >= features) return;
+        const float s = row0 + at.lane < r.span.rows ? scale_of(r, row0 + at.lane) : 0.0f;
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * r.scale, v[2 * i + 1] * r.scale);
+        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * s, v[2 * i + 1] * s);
         uint4 x[4];
         by_columns16(at.staging, at.lane, w, x);
         const int row = row0 + at.lane / 4, col = col0 + at.lane % 4 * 8;
@@ -485,12 +673,10 @@ struct HiddenGrad {
 // float32).
 template <typename O>
 struct WeightGrad {
-    static constexpr unsigned int kStatus = 0x400u;
-    static constexpr bool kAhead = false;
     CUtensorMap d, h;
     const Meta* meta;
     int most, piece_index, vocab, features;
-    O* dw;
+    O* dw;         // or null
     int64_t ld;
     const O* add;  // or null
     int64_t ld_add;
@@ -510,7 +696,7 @@ struct WeightGrad {
         const int column_tiles = (features + kTile - 1) / kTile;
         Deal r;
         const int stages = (span.rows + kDepth - 1) / kDepth;
-        r.none = span.rows == 0 && piece_index > 0;
+        r.none = !dw || (span.rows == 0 && piece_index > 0);
         static_cast<SplitDeal&>(r) = split_deal(r.none ? 0 : (vocab + kTile - 1) / kTile * column_tiles, stages ? stages : 1, pair, pairs);
         r.first_stage = stages ? 0 : most / kDepth;  // without rows: past the matrices, where zeros are read
         r.column_tiles = column_tiles;
@@ -586,26 +772,50 @@ struct WeightGrad {
     }
 };
 
-// The epilogue of both: whole tiles to where they belong, parts of split ones to the workspace.
-template <typename G>
-struct Split : G {
+// Both in one launch, dh's pieces first: dW's, which are more and shorter, fill what these leave of the pairs' time.
+template <typename T, typename O>
+struct Gradients {
+    static constexpr unsigned int kStatus = 0x200u;
+    static constexpr bool kAhead = false;
+    HiddenGrad<T> dh;
+    WeightGrad<O> dw;
+
+    struct Deal {
+        typename HiddenGrad<T>::Deal dh;
+        typename WeightGrad<O>::Deal dw;
+    };
+    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
+        Deal d{dh.deal(pair, pairs), dw.deal(pair, pairs)};
+        d.dw.next = (pair + pairs - d.dh.pieces % pairs) % pairs;  // dh's last round goes on with dw's first pieces
+        return d;
+    }
+    __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
+        if (dh.piece(d.dh, q)) return true;
+        if (!dw.piece(d.dw, q)) return false;
+        q->tile = -1 - q->tile;
+        return true;
+    }
+    // whole tiles to where they belong, parts of split ones to the workspace
     struct Epilogue {
-        const Split& p;
-        const typename G::Deal& deal;
+        const Gradients& p;
+        const Deal& deal;
         const Piece& q;
         Place at;
-        __device__ __forceinline__ Epilogue(const Split& p, const typename G::Deal& deal, const Piece& q, const Place& at)
+        __device__ __forceinline__ Epilogue(const Gradients& p, const Deal& deal, const Piece& q, const Place& at)
             : p(p), deal(deal), q(q), at(at) {}
         __device__ __forceinline__ void chunk(int c, float (&v)[32]) {
+            const bool hidden = q.tile >= 0;
             const int row0 = at.row - at.lane, col0 = at.first_column + 32 * c;
             if (q.part < 0) {
-                p.block(deal, q.m0 + row0, q.n0 + col0, at, v);
+                if (hidden) p.dh.block(deal.dh, q.m0 + row0, q.n0 + col0, at, v);
+                else p.dw.block(deal.dw, q.m0 + row0, q.n0 + col0, at, v);
                 return;
             }
-            if (q.m0 + row0 >= p.rows_of(deal) || q.n0 + col0 >= p.features) return;
+            if (q.m0 + row0 >= (hidden ? p.dh.rows_of(deal.dh) : p.dw.vocab) || q.n0 + col0 >= p.dw.features) return;
             float4 x[8];
             by_columns(at.staging, at.lane, v, x);
-            float* to = p.parts + q.part * kPartFloats + (row0 + at.lane / 8) * kTile + col0 + at.lane % 8 * 4;
+            float* to = (hidden ? p.dh.parts : p.dw.parts) + q.part * kPartFloats + (row0 + at.lane / 8) * kTile + col0 +
+                        at.lane % 8 * 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(to + i * 4 * kTile) = x[i];
         }
@@ -616,27 +826,32 @@ struct Split : G {
 // Joins the parts of split tiles, 4 rows to a CTA at a time.
 constexpr int kJoinRows = 4;
 template <typename G>
-__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Split<G> p, int pairs) {
-    wait_prerequisite();
-    allow_dependents();
-    const typename G::Deal deal = p.deal(0, pairs);
+__device__ __forceinline__ void join_split(const G& g, const typename G::Deal& deal, int rows, int features) {
     if (deal.parts == 1) return;
     const int64_t all = (int64_t)(deal.tiles - deal.whole) * (kTile / kJoinRows);
     const int col = threadIdx.x % 64 * 4;
     for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
         const int k = (int)(u / (kTile / kJoinRows)), row = (int)(u % (kTile / kJoinRows)) * kJoinRows + threadIdx.x / 64;
         int m0, n0;
-        p.tile_at(deal, deal.whole + k, &m0, &n0);
-        if (m0 + row >= p.rows_of(deal) || n0 + col >= p.features) continue;
-        const float* from = p.parts + (int64_t)k * deal.parts * kPartFloats + row * kTile + col;
+        g.tile_at(deal, deal.whole + k, &m0, &n0);
+        if (m0 + row >= rows || n0 + col >= features) continue;
+        const float* from = g.parts + (int64_t)k * deal.parts * kPartFloats + row * kTile + col;
         float4 s{};
 #pragma unroll 8
         for (int part = 0; part < deal.parts; ++part) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(from + part * kPartFloats));
             s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
         }
-        p.put(deal, m0 + row, n0 + col, s);
+        g.put(deal, m0 + row, n0 + col, s);
     }
+}
+template <typename T, typename O>
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Gradients<T, O> p, int pairs) {
+    wait_prerequisite();
+    allow_dependents();
+    const typename Gradients<T, O>::Deal deal = p.deal(0, pairs);
+    join_split(p.dh, deal.dh, deal.dh.span.rows, p.dh.features);
+    join_split(p.dw, deal.dw, p.dw.vocab, p.dw.features);
 }
 
 // ------------------------------------------------------------------------------------------------------------------------
@@ -671,7 +886,9 @@ int rows_of_piece(int64_t rows, int64_t bytes_a_row, int64_t bytes, int64_t most
     return (int)(n < need ? n : need);
 }
 
-struct Common {
+struct Room {
+    int most;       // rows of a piece
+    int pieces;
     Meta* meta;
     int* index;
     unsigned short* w;  // a copy with aligned rows, or null
@@ -679,293 +896,337 @@ struct Common {
     int* target;
     unsigned short* h;
     int ld_h;
-};
-struct ForwardPlaces {
-    int most, parts;
+    // the logits' sums
+    int parts;
     RowSum* sums;
     float* at;
-};
-struct GradPlaces {
-    int most, ld;
+    // gradients
+    int ld_d;
     float* coef;
     float* origin;
     unsigned short* d;
-    float* parts;
-    float* sums;
+    float *dh_parts, *dw_parts;
+    float* dw_sums;
     int64_t ld_sums;
+    // cross entropy
+    bool once;
+    Exact* partial;
+    float* factor;
+    unsigned short* scaled_h;
+    int* again;
 };
 
 // TMA reads rows that begin at multiples of 16 bytes and whose stride fits 40 bits.
 bool readable(const Linear& L) { return rows_aligned(L.w, L.ld_w) && L.ld_w >= L.features && L.ld_w < (int64_t)1 << 39; }
 
-int forward_rows(const Linear& L) { return rows_of_piece(L.rows, tiles_of(L.vocab) * 16, kStatBytes, kMostRows); }
-int grad_rows(const Linear& L) { return rows_of_piece(L.rows, round_up(L.vocab, 64) * 2, kGradBytes, (int64_t)1 << 30); }
-
-Common place_common(const Linear& L, int most, Places* p) {
-    Common c{};
+// What a call needs: the forward pass's sums, or gradients, or (cross entropy) both.
+Room places_of(const Linear& L, bool sums, const LinearGrad* G, bool ce, int sms, Places* p) {
+    Room c{};
+    const int grad_rows = rows_of_piece(L.rows, round_up(L.vocab, 64) * 2, kGradBytes, (int64_t)1 << 30);
+    const int sum_rows = rows_of_piece(L.rows, tiles_of(L.vocab) * 16, kStatBytes, kMostRows);
+    c.most = G && (!sums || grad_rows < sum_rows) ? grad_rows : sum_rows;
+    c.pieces = (int)((L.rows + c.most - 1) / c.most);
+    if (c.pieces < 1) c.pieces = 1;  // (without rows too: dw is add, the loss 0)
     c.meta = p->take<Meta>(1);
     c.index = p->take<int>(L.rows);
-    c.target = p->take<int>(most);
+    c.target = p->take<int>(c.most);
     c.ld_h = (int)round_up(L.features, 8);
-    c.h = p->take<unsigned short>((int64_t)most * c.ld_h);
+    c.h = p->take<unsigned short>((int64_t)c.most * c.ld_h);
     c.ld_w = L.ld_w;
     if (!readable(L)) {
         c.ld_w = round_up(L.features, 8);
         c.w = p->take<unsigned short>(L.vocab * c.ld_w);
     }
-    return c;
-}
-ForwardPlaces place_forward(const Linear& L, Places* p) {
-    ForwardPlaces f{};
-    f.most = forward_rows(L);
-    f.parts = (int)((L.vocab + kHalf - 1) / kHalf);
-    f.sums = p->take<RowSum>((int64_t)f.parts * f.most);
-    f.at = p->take<float>(f.most);
-    return f;
-}
-GradPlaces place_grad(const Linear& L, const LinearGrad& G, int sms, Places* p) {
-    GradPlaces g{};
-    g.most = grad_rows(L);
-    g.ld = (int)round_up(L.vocab, 64);
-    g.coef = p->take<float>(g.most);
-    g.origin = p->take<float>(g.most);
-    g.d = p->take<unsigned short>((int64_t)g.most * g.ld);
-    const int pairs = sms / 2 < 1 ? 1 : sms / 2;
-    g.parts = p->take<float>(kMostRounds * pairs * kPartFloats);
-    if (G.dw && L.rows > g.most && G.dw_dtype != MICA_F32) {
-        g.ld_sums = round_up(L.features, 4);
-        g.sums = p->take<float>(L.vocab * g.ld_sums);
+    c.origin = p->take<float>(c.most);
+    if (sums) {
+        c.parts = (int)((L.vocab + kHalf - 1) / kHalf);
+        c.sums = p->take<RowSum>((int64_t)c.parts * c.most);
+        c.at = p->take<float>(c.most);
     }
-    return g;
+    if (ce) c.partial = p->take<Exact>((int64_t)c.pieces * (c.most / 8));
+    if (!G) return c;
+    const int pairs = sms / 2 < 1 ? 1 : sms / 2;
+    c.ld_d = (int)round_up(L.vocab, 64);
+    c.coef = p->take<float>(c.most);
+    c.d = p->take<unsigned short>((int64_t)c.most * c.ld_d);
+    if (G->dh) c.dh_parts = p->take<float>(kMostRounds * pairs * kPartFloats);
+    if (G->dw) c.dw_parts = p->take<float>(kMostRounds * pairs * kPartFloats);
+    if (G->dw && c.pieces > 1 && G->dw_dtype != MICA_F32) {
+        c.ld_sums = round_up(L.features, 4);
+        c.dw_sums = p->take<float>(L.vocab * c.ld_sums);
+    }
+    c.once = ce && L.dtype == MICA_BF16 && (double)L.rows * L.features * L.vocab >= kOnceProducts;
+    if (c.once) {
+        c.factor = p->take<float>(c.most);
+        c.scaled_h = p->take<unsigned short>((int64_t)c.most * c.ld_h);
+        c.again = p->take<int>(1 + c.most / kTile);
+    }
+    return c;
 }
 
 CUtensorMapDataType map_type(int32_t dtype) {
     return dtype == MICA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-#define MICA_STEP(x)                             \
-    do {                                         \
-        const cudaError_t step_e = (x);          \
+#define MICA_STEP(x)                              \
+    do {                                          \
+        const cudaError_t step_e = (x);           \
         if (step_e != cudaSuccess) return step_e; \
     } while (0)
 
-cudaError_t copy_w(const Linear& L, const Common& c, void* stream) {
+cudaError_t copy_w(const Linear& L, const Room& c, void* stream) {
     if (!c.w) return cudaSuccess;
     const int64_t ctas = (L.vocab * (c.ld_w / 8) + 255) / 256;
     return launch_after(align_rows_kernel, ctas < (1 << 16) ? ctas : (1 << 16), 256, 0, stream,
                         static_cast<const unsigned short*>(L.w), L.ld_w, (int64_t)L.vocab, (int64_t)L.features, c.w, c.ld_w);
 }
 
-cudaError_t gather(const Linear& L, const Common& c, int most, int piece, const float* lse, const float* dlogps,
-                   const GradPlaces* g, const LinearGrad* G, void* stream) {
-    Gather a{};
-    a.h = static_cast<const unsigned short*>(L.h);
-    a.targets = L.targets;
-    a.ld_h = L.ld_h;
-    a.rows = (int)L.rows;
-    a.features = L.features;
-    a.vocab = L.vocab;
-    a.wide = L.wide_targets;
-    a.aligned = reinterpret_cast<uintptr_t>(L.h) % 16 == 0 && L.ld_h % 8 == 0;
-    a.index = c.index;
-    a.meta = c.meta;
-    a.most = most;
-    a.piece = piece;
-    a.lse = lse;
-    a.dlogps = dlogps;
-    a.inv_t = (float)(1.0 / L.temperature);
-    a.out = c.h;
-    a.ld = c.ld_h;
-    a.target = c.target;
-    if (g) {
-        a.coef = g->coef;
-        a.origin = g->origin;
+// One call: logps and lse where given (with sums), gradients where G is, from dlogps and lse_in or as cross entropy's.
+struct Call {
+    const Linear& L;
+    const LinearGrad* G;
+    const float* lse_in;
+    const float* dlogps;
+    float* logps;
+    float* lse;
+    float* loss;  // null: not cross entropy
+    double denom, grad_scale;
+    int sms;
+    void* stream;
+};
+
+template <typename T>
+cudaError_t gather(const Call& call, const Room& c, int piece) {
+    const Linear& L = call.L;
+    Gather g{};
+    g.targets = L.targets;
+    g.h = static_cast<const unsigned short*>(L.h);
+    g.ld_h = L.ld_h;
+    g.rows = (int)L.rows;
+    g.features = L.features;
+    g.vocab = L.vocab;
+    g.wide = L.wide_targets;
+    g.aligned = reinterpret_cast<uintptr_t>(L.h) % 16 == 0 && L.ld_h % 8 == 0;
+    g.dlogps = call.dlogps;
+    g.lse = call.lse_in;
+    g.inv_t = (float)(1.0 / L.temperature);
+    g.ce_factor = (float)(-call.grad_scale / L.temperature);
+    g.denom = (float)call.denom;
+    g.scaled = L.dtype == MICA_F16;
+    g.most = c.most;
+    g.piece = piece;
+    g.meta = c.meta;
+    g.index = c.index;
+    g.out = c.h;
+    g.ld = c.ld_h;
+    g.target = c.target;
+    g.coef = c.coef;
+    g.origin = c.origin;
+    g.a = (float)(1.4426950408889634074 / L.temperature);
+    if (c.once) {
+        g.w = c.w ? c.w : static_cast<const unsigned short*>(L.w);
+        g.ld_w = c.ld_w;
+        g.again = c.again;
     }
-    if (G && G->dh && piece == 0) {
-        a.zero = static_cast<unsigned short*>(G->dh);
-        a.ld_zero = G->ld_dh;
+    g.logps = call.logps;
+    g.lse_out = call.lse;
+    if (call.G) {
+        g.zero = static_cast<unsigned short*>(call.G->dh);
+        g.ld_zero = call.G->ld_dh;
     }
-    const int64_t ctas = ((a.zero ? L.rows + 64 : most) + 7) / 8;
-    return launch_after(gather_kernel, ctas < 4096 ? ctas : 4096, 256, 0, stream, a);
+    const int64_t ctas = (L.rows + 7) / 8, most = 4 * (int64_t)call.sms;
+    return launch_after(gather_kernel<T>, ctas < 1 ? 1 : ctas < most ? ctas : most, 256, 0, call.stream, g);
 }
 
-// What both products over the vocabulary share.
-bool fill(Logits* p, const Linear& L, const Common& c, int most, int piece) {
+// What the products over the vocabulary share.
+bool fill(Logits* p, const Linear& L, const Room& c, int piece) {
     p->meta = c.meta;
     p->target = c.target;
-    p->most = most;
+    p->most = c.most;
     p->piece_index = piece;
     p->vocab = L.vocab;
     p->stages = (L.features + kDepth - 1) / kDepth;
     p->a = (float)(1.4426950408889634074 / L.temperature);
-    return matrix_map(&p->h, map_type(L.dtype), c.h, L.features, most, c.ld_h, 1) &&
+    return matrix_map(&p->h, map_type(L.dtype), c.h, L.features, c.most, c.ld_h, 1) &&
            matrix_map(&p->w, map_type(L.dtype), c.w ? c.w : L.w, L.features, L.vocab, c.ld_w, 1);
 }
 
 template <typename T>
-cudaError_t forward(const Linear& L, const Common& c, const ForwardPlaces& f, float* logps, float* lse, int sms, void* stream) {
-    for (int64_t at = 0, piece = 0; at < L.rows; at += f.most, ++piece) {
-        MICA_STEP(gather(L, c, f.most, (int)piece, nullptr, nullptr, nullptr, nullptr, stream));
-        LogitSums p{};
-        if (!fill(&p, L, c, f.most, (int)piece)) return cudaErrorInvalidValue;
-        p.sums = f.sums;
-        p.parts = f.parts;
-        p.at = f.at;
-        MICA_STEP((launch_gemm<T>(p, f.most / kTile * tiles_of(L.vocab), sms, stream)));
-        const Join j{c.meta, c.index, c.target, f.sums, f.at, f.most, (int)piece, f.parts, p.a, logps, lse};
-        MICA_STEP(launch_after(join_rows_kernel, f.most / 8, 256, 0, stream, j));
-    }
-    return cudaSuccess;
-}
-
-// stages: how many there can be at most
-template <typename T, typename G>
-cudaError_t split_product(const Split<G>& p, int64_t tiles, int64_t stages, int sms, void* stream) {
-    const int pairs = sms / 2 < 1 ? 1 : sms / 2;
-    MICA_STEP((launch_gemm<T>(p, pairs, sms, stream)));
-    if (stages < 2 * kLeastStages) return cudaSuccess;  // no tile is split
-    const int64_t ctas = (tiles < pairs ? tiles : pairs) * (kTile / kJoinRows);
-    return launch_after(join_parts_kernel<G>, ctas, 256, 0, stream, p, pairs);
+cudaError_t join_rows(const Call& call, const Room& c, int piece) {
+    Join j{};
+    j.meta = c.meta;
+    j.index = c.index;
+    j.target = c.target;
+    j.sums = c.sums;
+    j.most = c.most;
+    j.piece = piece;
+    j.parts = c.parts;
+    j.a = (float)(1.4426950408889634074 / call.L.temperature);
+    j.logps = call.logps;
+    j.lse = call.lse;
+    j.at = c.at;
+    j.origin = call.G ? c.origin : nullptr;
+    j.once = c.once;
+    j.at_target = c.at;
+    j.factor = c.factor;
+    j.again = c.again;
+    j.d = c.d;
+    j.ld_d = c.ld_d;
+    j.h = c.h;
+    j.scaled_h = c.scaled_h;
+    j.ld_h = c.ld_h;
+    j.features = call.L.features;
+    j.loss = call.loss;
+    j.denom = (float)call.denom;
+    j.partial = c.partial;
+    j.all = c.pieces * (c.most / 8);
+    return launch_after(join_rows_kernel<T>, c.most / 8, 256, 0, call.stream, j);
 }
 
 template <typename T, typename O>
-cudaError_t weight_grad(const Linear& L, const Common& c, const GradPlaces& g, const LinearGrad& G, int piece, int sms,
-                        void* stream) {
-    Split<WeightGrad<O>> p{};
-    p.meta = c.meta;
-    p.most = g.most;
-    p.piece_index = piece;
-    p.vocab = L.vocab;
-    p.features = L.features;
-    p.dw = static_cast<O*>(G.dw);
-    p.ld = G.ld_dw;
-    p.add = static_cast<const O*>(G.add);
-    p.ld_add = G.ld_add;
-    p.sums = sizeof(O) == 4 ? static_cast<float*>(G.dw) : g.sums;
-    p.ld_sums = sizeof(O) == 4 ? G.ld_dw : g.ld_sums;
+cudaError_t gradients(const Call& call, const Room& c, int piece) {
+    const Linear& L = call.L;
+    const LinearGrad& G = *call.G;
+    Gradients<T, O> p{};
+    const auto type = map_type(L.dtype);
+    CUtensorMap d;
+    if (!matrix_map(&d, type, c.d, L.vocab, c.most, c.ld_d, 1)) return cudaErrorInvalidValue;
+    HiddenGrad<T>& x = p.dh;
+    x.d = d;
+    x.meta = c.meta;
+    x.index = c.index;
+    x.most = c.most;
+    x.piece_index = piece;
+    x.vocab = L.vocab;
+    x.features = L.features;
+    x.factor = c.factor;
+    x.dh = static_cast<T*>(G.dh);
+    x.ld = G.ld_dh;
+    x.wide = reinterpret_cast<uintptr_t>(G.dh) % 8 == 0 && G.ld_dh % 4 == 0;
+    x.wide16 = reinterpret_cast<uintptr_t>(G.dh) % 16 == 0 && G.ld_dh % 8 == 0;
+    x.parts = c.dh_parts;
+    if (!matrix_map(&x.w, type, c.w ? c.w : L.w, L.features, L.vocab, c.ld_w, 1)) return cudaErrorInvalidValue;
+    WeightGrad<O>& y = p.dw;
+    y.d = d;
+    y.meta = c.meta;
+    y.most = c.most;
+    y.piece_index = piece;
+    y.vocab = L.vocab;
+    y.features = L.features;
+    y.dw = static_cast<O*>(G.dw);
+    y.ld = G.ld_dw;
+    y.add = static_cast<const O*>(G.add);
+    y.ld_add = G.ld_add;
+    y.sums = sizeof(O) == 4 ? static_cast<float*>(G.dw) : c.dw_sums;
+    y.ld_sums = sizeof(O) == 4 ? G.ld_dw : c.ld_sums;
     const size_t four = 4 * sizeof(O);
-    p.wide = reinterpret_cast<uintptr_t>(G.dw) % four == 0 && G.ld_dw % 4 == 0;
-    p.wide16 = reinterpret_cast<uintptr_t>(G.dw) % 16 == 0 && G.ld_dw % 8 == 0;
-    p.wide_add = reinterpret_cast<uintptr_t>(G.add) % four == 0 && G.ld_add % 4 == 0;
-    p.wide_sums = sizeof(O) == 4 ? p.wide : 1;
-    p.parts = g.parts;
-    if (!matrix_map(&p.d, map_type(L.dtype), g.d, L.vocab, g.most, g.ld, 1) ||
-        !matrix_map(&p.h, map_type(L.dtype), c.h, L.features, g.most, c.ld_h, 1))
-        return cudaErrorInvalidValue;
-    return split_product<T>(p, tiles_of(L.vocab) * tiles_of(L.features), (L.rows + kDepth - 1) / kDepth, sms, stream);
+    y.wide = reinterpret_cast<uintptr_t>(G.dw) % four == 0 && G.ld_dw % 4 == 0;
+    y.wide16 = reinterpret_cast<uintptr_t>(G.dw) % 16 == 0 && G.ld_dw % 8 == 0;
+    y.wide_add = reinterpret_cast<uintptr_t>(G.add) % four == 0 && G.ld_add % 4 == 0;
+    y.wide_sums = sizeof(O) == 4 ? y.wide : 1;
+    y.parts = c.dw_parts;
+    if (!matrix_map(&y.h, type, c.once ? c.scaled_h : c.h, L.features, c.most, c.ld_h, 1)) return cudaErrorInvalidValue;
+    const int pairs = call.sms / 2 < 1 ? 1 : call.sms / 2;
+    MICA_STEP((launch_gemm<T>(p, pairs, call.sms, call.stream)));
+    // no tile of a sum this short is split
+    const bool short_dh = !G.dh || (L.vocab + kDepth - 1) / kDepth < 2 * kLeastStages;
+    const bool short_dw = !G.dw || (L.rows + kDepth - 1) / kDepth < 2 * kLeastStages;
+    if (short_dh && short_dw) return cudaSuccess;
+    return launch_after(join_parts_kernel<T, O>, 8 * (int64_t)call.sms, 256, 0, call.stream, p, pairs);
 }
 
-// lse: as the forward pass leaves it; dlogps null: cross entropy
 template <typename T>
-cudaError_t backward(const Linear& L, const Common& c, const GradPlaces& g, const LinearGrad& G, const float* lse,
-                     const float* dlogps, int sms, void* stream) {
-    // (without rows too: dw is add)
-    for (int64_t at = 0, piece = 0; piece == 0 || at < L.rows; at += g.most, ++piece) {
-        MICA_STEP(gather(L, c, g.most, (int)piece, lse, dlogps, &g, &G, stream));
-        LogitGrad<T> p{};
-        if (!fill(&p, L, c, g.most, (int)piece)) return cudaErrorInvalidValue;
-        p.coef = g.coef;
-        p.origin = g.origin;
-        p.d = reinterpret_cast<T*>(g.d);
-        p.ld = g.ld;
-        MICA_STEP((launch_gemm<T>(p, g.most / kTile * tiles_of(L.vocab), sms, stream)));
-        if (G.dh) {
-            Split<HiddenGrad<T>> q{};
-            q.meta = c.meta;
-            q.index = c.index;
-            q.most = g.most;
-            q.piece_index = (int)piece;
-            q.vocab = L.vocab;
-            q.features = L.features;
-            q.dh = static_cast<T*>(G.dh);
-            q.ld = G.ld_dh;
-            q.wide = reinterpret_cast<uintptr_t>(G.dh) % 8 == 0 && G.ld_dh % 4 == 0;
-            q.wide16 = reinterpret_cast<uintptr_t>(G.dh) % 16 == 0 && G.ld_dh % 8 == 0;
-            q.parts = g.parts;
-            q.w = p.w;
-            if (!matrix_map(&q.d, map_type(L.dtype), g.d, L.vocab, g.most, g.ld, 1)) return cudaErrorInvalidValue;
-            MICA_STEP((split_product<T>(q, g.most / kTile * tiles_of(L.features), (L.vocab + kDepth - 1) / kDepth, sms, stream)));
+cudaError_t run(const Call& call, const Room& c) {
+    const Linear& L = call.L;
+    const bool forward = call.logps || call.loss;
+    const int64_t tiles = c.most / kTile * tiles_of(L.vocab);
+    MICA_STEP(copy_w(L, c, call.stream));
+    for (int piece = 0; piece < c.pieces; ++piece) {
+        MICA_STEP(gather<T>(call, c, piece));
+        if (c.once) {
+            LogitOnce<T> p{};
+            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            p.sums = c.sums;
+            p.parts = c.parts;
+            p.origin = c.origin;
+            p.d = reinterpret_cast<T*>(c.d);
+            p.ld = c.ld_d;
+            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
+            MICA_STEP(join_rows<T>(call, c, piece));
+            p.sums = nullptr;
+            p.at = c.at;
+            p.again = c.again;
+            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
+        } else if (forward) {
+            LogitSums p{};
+            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            p.sums = c.sums;
+            p.parts = c.parts;
+            p.at = c.at;
+            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
+            MICA_STEP(join_rows<T>(call, c, piece));
         }
-        if (G.dw)
-            MICA_STEP((G.dw_dtype == MICA_F32   ? weight_grad<T, float>(L, c, g, G, (int)piece, sms, stream)
-                       : G.dw_dtype == MICA_F16 ? weight_grad<T, __half>(L, c, g, G, (int)piece, sms, stream)
-                                                : weight_grad<T, __nv_bfloat16>(L, c, g, G, (int)piece, sms, stream)));
+        if (!call.G) continue;
+        if (!c.once) {
+            LogitGrad<T> p{};
+            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            p.coef = c.coef;
+            p.origin = c.origin;
+            p.d = reinterpret_cast<T*>(c.d);
+            p.ld = c.ld_d;
+            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
+        }
+        const int32_t type = call.G->dw ? call.G->dw_dtype : L.dtype;
+        MICA_STEP((type == MICA_F32   ? gradients<T, float>(call, c, piece)
+                   : type == MICA_F16 ? gradients<T, __half>(call, c, piece)
+                                      : gradients<T, __nv_bfloat16>(call, c, piece)));
     }
     return cudaSuccess;
 }
 
-cudaError_t scan(const Linear& L, const Common& c, const float* dlogps, float* logps, float* lse, double denom,
-                 double grad_scale, void* stream) {
-    const Scan s{L.targets, L.wide_targets, (int)L.rows, dlogps, logps, lse, c.index, c.meta, (float)(1.0 / L.temperature),
-                 (float)(-grad_scale / L.temperature), (float)denom, L.dtype == MICA_F16};
-    return launch_after(scan_kernel, 1, kScanThreads, 0, stream, s);
+int run_typed(const Call& call, const Room& c) {
+    return (int)(call.L.dtype == MICA_BF16 ? run<__nv_bfloat16>(call, c) : run<__half>(call, c));
 }
 
 }  // namespace
 
 int64_t linear_logps_workspace(const Linear& L) {
-    if (L.rows == 0) return 0;
     Places p(nullptr);
-    place_common(L, forward_rows(L), &p);
-    place_forward(L, &p);
+    places_of(L, true, nullptr, false, 1, &p);
     return p.bytes();
 }
 
 int launch_linear_logps(const Linear& L, float* logps, float* lse, void* workspace, int sms, void* stream) {
     Places p(workspace);
-    const Common c = place_common(L, forward_rows(L), &p);
-    const ForwardPlaces f = place_forward(L, &p);
-    MICA_STEP(scan(L, c, nullptr, logps, lse, 0.0, 0.0, stream));
-    MICA_STEP(copy_w(L, c, stream));
-    return L.dtype == MICA_BF16 ? forward<__nv_bfloat16>(L, c, f, logps, lse, sms, stream)
-                                : forward<__half>(L, c, f, logps, lse, sms, stream);
+    const Room c = places_of(L, true, nullptr, false, sms, &p);
+    return run_typed(Call{L, nullptr, nullptr, nullptr, logps, lse, nullptr, 0.0, 0.0, sms, stream}, c);
 }
 
 int64_t linear_grad_workspace(const Linear& L, const LinearGrad& G, int sms) {
     Places p(nullptr);
-    place_common(L, grad_rows(L), &p);
-    place_grad(L, G, sms, &p);
+    places_of(L, false, &G, false, sms, &p);
     return p.bytes();
 }
 
 int launch_linear_grad(const Linear& L, const float* lse, const float* dlogps, const LinearGrad& G, void* workspace, int sms,
                        void* stream) {
     Places p(workspace);
-    const Common c = place_common(L, grad_rows(L), &p);
-    const GradPlaces g = place_grad(L, G, sms, &p);
-    MICA_STEP(scan(L, c, dlogps, nullptr, nullptr, 0.0, 0.0, stream));
-    MICA_STEP(copy_w(L, c, stream));
-    return L.dtype == MICA_BF16 ? backward<__nv_bfloat16>(L, c, g, G, lse, dlogps, sms, stream)
-                                : backward<__half>(L, c, g, G, lse, dlogps, sms, stream);
+    const Room c = places_of(L, false, &G, false, sms, &p);
+    return run_typed(Call{L, &G, lse, dlogps, nullptr, nullptr, nullptr, 0.0, 0.0, sms, stream}, c);
 }
-
-static int ce_rows(const Linear& L) { return forward_rows(L) > grad_rows(L) ? forward_rows(L) : grad_rows(L); }
 
 int64_t linear_ce_workspace(const Linear& L, const LinearGrad& G, int sms) {
     Places p(nullptr);
-    place_common(L, ce_rows(L), &p);
-    p.take<float>(L.rows);
-    place_forward(L, &p);
-    if (G.dh || G.dw) place_grad(L, G, sms, &p);
+    places_of(L, true, G.dh || G.dw ? &G : nullptr, true, sms, &p);
     return p.bytes();
 }
 
 int launch_linear_ce(const Linear& L, double denom, double grad_scale, float* loss, float* logps, const LinearGrad& G,
                      void* workspace, int sms, void* stream) {
     Places p(workspace);
-    const Common c = place_common(L, ce_rows(L), &p);
-    float* lse = p.take<float>(L.rows);
-    const ForwardPlaces f = place_forward(L, &p);
-    MICA_STEP(scan(L, c, nullptr, logps, lse, denom, grad_scale, stream));
-    MICA_STEP(copy_w(L, c, stream));
-    MICA_STEP(L.dtype == MICA_BF16 ? forward<__nv_bfloat16>(L, c, f, logps, lse, sms, stream)
-                                   : forward<__half>(L, c, f, logps, lse, sms, stream));
-    MICA_STEP(launch_after(loss_kernel, 1, 1024, 0, stream, (const float*)logps, (int)L.rows, (const Meta*)c.meta, (float)denom,
-                           loss));
-    if (!G.dh && !G.dw) return cudaSuccess;
-    const GradPlaces g = place_grad(L, G, sms, &p);
-    return L.dtype == MICA_BF16 ? backward<__nv_bfloat16>(L, c, g, G, lse, nullptr, sms, stream)
-                                : backward<__half>(L, c, g, G, lse, nullptr, sms, stream);
+    const LinearGrad* g = G.dh || G.dw ? &G : nullptr;
+    const Room c = places_of(L, true, g, true, sms, &p);
+    return run_typed(Call{L, g, nullptr, nullptr, logps, nullptr, loss, denom, grad_scale, sms, stream}, c);
 }
 
 int read_linear_status(unsigned int* status) { return (int)read_gemm_status(status); }

@@ -269,7 +269,7 @@ typedef struct {
  * d[t][j] = dlogps[t] / temperature * ((j == target) - exp(z[t][j] - lse[t])), dh = d w and dw = add + d^T h. A row whose
  * target is negative or whose dlogps is 0 does not count: its dh is zeros. workspace: mica_linear_grad_workspace bytes for
  * the same arguments, 16-byte aligned: 2 bytes x rows x vocab but no more than some 1 GB (larger batches are taken in pieces),
- * 60 MB, and where there are pieces and dw is of 16 bits, 4 bytes x vocab x features.
+ * 80 MB, and where there are pieces and dw is of 16 bits, 4 bytes x vocab x features.
  * Errors: as mica_linear_logps.
  */
 MICA_API mica_status mica_linear_logps_grad(const mica_linear* l, const float* lse, const float* dlogps,

@@ -65,14 +65,17 @@ class Want:
         self.err = self.t_err + 6 * U * (top + 1) + 2.0 ** -22 + (vocab / 1024 + 64) * U
         self.p = torch.exp(self.z - self.lse[:, None])
 
-    def grads(self, dlogps, dtype, add=None):
-        """(dh, its bound, dw, its bound), before the last rounding"""
+    def grads(self, dlogps, dtype, add=None, once=False):
+        """(dh, its bound, dw, its bound), before the last rounding. once: with h's rows scaled by the rest of the softmax, and
+        rounded once more, and d counted from another origin"""
         c = torch.where(self.on, dlogps.double() / self.t, 0.0)[:, None]
         one = torch.zeros_like(self.p).scatter_(1, self.y.clamp(min=0)[:, None], 1.0)
         d = c * (one - self.p)
         err = c.abs() * (2 * self.err[:, None] * self.p + 4 * U) + ROUND[dtype] * d.abs()
         if dtype == torch.float16:
             err += 2.0 ** -25 * 2.0 ** -13 * c.abs().amax() * (c != 0)
+        if once and dtype == torch.bfloat16:
+            err += ROUND[dtype] * d.abs() * 1.01 + c.abs() * 2 * self.err[:, None] * self.p
         rows, vocab = d.shape
         long = lambda n: (n / 16 + 4) * 2.0 ** -22  # noqa: E731
         dh, dw = d @ self.w, d.t() @ self.h
@@ -144,3 +147,257 @@ def test_cross_entropy(rows, features, vocab, dtype):
         rounded(r.dw, dw, dw_err)
     r2 = mica.mica_linear_cross_entropy(h, w, y, denom=5.0, grad=False)
     assert r2.dh is None and r2.dw is None and torch.equal(r2.loss, r.loss) and torch.equal(r2.logps, r.logps)
+
+
+# large enough for cross entropy to take the logits once in bfloat16, and a little less
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+@pytest.mark.parametrize("rows,features,vocab,skip", [(300, 517, 70001, 0.3), (1100, 256, 40003, 0.5), (513, 1000, 20011, 0.0),
+                                                      (90, 520, 213001, 0.2)])
+def test_cross_entropy_of_many(rows, features, vocab, skip, dtype):
+    h, w, y = make(rows, features, vocab, dtype, seed=rows, skip=skip)
+    for scale, t in ((64.0, 1.0), (-3.0, 0.8)):
+        want = Want(h, w, y, t)
+        n = max(1, int(want.on.sum()))
+        r = mica.mica_linear_cross_entropy(h, w, y, grad_scale=scale, temperature=t)
+        close(r.logps, want.logps, 2 * want.err)
+        close(r.loss[0], -want.logps.sum() / n, 2 * want.err.sum() / n + 4 * U * want.logps.abs().sum() / n)
+        c = torch.full((rows,), -scale / n, device="cuda")
+        dh, dh_err, dw, dw_err = want.grads(c, dtype, once=True)
+        rounded(r.dh, dh, dh_err)
+        rounded(r.dw, dw, dw_err)
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_unlikely_targets(dtype):
+    """Rows whose target is e^-30 to e^-400 likely, among ordinary ones: the sum of exp(z - z_target) leaves its range."""
+    rows, features, vocab = 520, 512, 50021
+    h, w, y = make(rows, features, vocab, dtype, seed=11, skip=0.1)
+    g = gen(12)
+    far = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    some = torch.arange(rows, device="cuda") % 7 == 3
+    some &= torch.arange(rows, device="cuda") < 300  # the second tile of rows has a few, the third none
+    row, at = w[far].float(), w[y.clamp(min=0)].float()
+    size = 15.0 + 190.0 * torch.rand(rows, 1, generator=g, device="cuda")
+    push = size * (row / row.square().sum(1, keepdim=True) - at / at.square().sum(1, keepdim=True))
+    h = torch.where(some[:, None], (h.float() + push).to(dtype), h)
+    want = Want(h, w, y)
+    assert float(want.logps.min()) < -200 and int((want.logps < -45).sum()) > 20
+    n = int(want.on.sum())
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    close(r.logps, want.logps, 2 * want.err)
+    dh, dh_err, dw, dw_err = want.grads(torch.full((rows,), -1.0 / n, device="cuda"), dtype, once=True)
+    rounded(r.dh, dh, dh_err)
+    rounded(r.dw, dw, dw_err)
+
+
+@pytest.mark.parametrize("rows,vocab", [(70, 200), (300, 70001)])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_what_does_not_count_is_not_read(dtype, rows, vocab):
+    """Rows without a target may hold anything; their gradients are zeros, and the others' as if they were not there."""
+    h, w, y = make(rows, 512, vocab, dtype, seed=3, skip=0.4)
+    off = y < 0
+    clean = mica.mica_linear_cross_entropy(h, w, y)
+    dirty = torch.where(off[:, None], torch.full_like(h, math.nan), h)
+    r = mica.mica_linear_cross_entropy(dirty, w, y)
+    for a, b in zip(r, clean):
+        assert torch.equal(a, b)
+    assert not r.dh[off].any() and not r.logps[off].any()
+    lp, lse = mica.mica_linear_logps(dirty, w, y, lse=True)
+    assert not lp[off].any() and not lse[off].any() and lp.isfinite().all()
+    c = torch.randn(rows, generator=gen(4), device="cuda")
+    g1 = mica.mica_linear_logps_grad(h, w, y, lse, c)
+    g2 = mica.mica_linear_logps_grad(dirty, w, y, torch.where(off, math.nan, lse), torch.where(off, math.nan, c))
+    assert torch.equal(g1[0], g2[0]) and torch.equal(g1[1], g2[1])
+
+
+@pytest.mark.parametrize("vocab", [300, 70001])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_targets_past_the_vocabulary(dtype, vocab):
+    """NaN, in the row's log-probability and gradients and in all of dw; not where its coefficient is 0."""
+    rows = 300
+    h, w, y = make(rows, 512, vocab, dtype, seed=5, skip=0.2)
+    y[7], y[11] = vocab, 1 << 40
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    bad = (y >= vocab).nonzero()[:, 0]
+    assert r.logps[bad].isnan().all() and r.loss.isnan() and r.dh[bad].isnan().all() and r.dw.isnan().all()
+    rest = y < vocab
+    assert r.logps[rest].isfinite().all() and r.dh[rest].isfinite().all()
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    assert lp[bad].isnan().all() and lp[rest].isfinite().all()
+    c = torch.ones(rows, device="cuda")
+    c[bad] = 0.0
+    dh, dw = mica.mica_linear_logps_grad(h, w, y, lse, c)
+    assert dh.isfinite().all() and dw.isfinite().all() and not dh[bad].any()
+    c[7] = 1.0
+    dh, dw = mica.mica_linear_logps_grad(h, w, y, lse, c)
+    assert dh[7].isnan().all() and dw.isnan().all() and not dh[11].any()
+
+
+@pytest.mark.parametrize("vocab", [300, 70001])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_infinities(dtype, vocab):
+    """A row with an infinity in h or w: what the formula gives, infinities and NaNs, and the other rows as ever."""
+    h, w, y = make(300, 512, vocab, dtype, seed=6, skip=0.0)
+    h[5, 3] = math.inf
+    h[9, 0] = math.nan
+    want = torch.log_softmax(h.double() @ w.double().t(), 1).gather(1, y[:, None])[:, 0]
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    ok = want.isfinite()
+    assert int(ok.sum()) == 298
+    close(r.logps[ok], want[ok], 2 * Want(h[ok], w, y[ok]).err)
+    assert not r.logps[~ok].isfinite().any() and not r.loss.isfinite().any() and r.dh[~ok].isnan().any(1).all()
+    assert r.dh[ok].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+@pytest.mark.parametrize("features,ld_h,ld_w,offset", [(64, 64, 64, 1), (63, 70, 65, 0), (72, 80, 96, 8), (72, 0, 72, 0), (40, 41, 48, 3),
+                                                       (64, 64, 0, 0)])
+def test_strides_and_offsets(features, ld_h, ld_w, offset, dtype):
+    """Rows at every alignment, of h, w, the gradients and what these are added to; and matrices whose rows are all the same."""
+    rows, vocab = 130, 517
+    h, w, y = make(rows, features, vocab, dtype, seed=features, ld_h=ld_h or 1, ld_w=ld_w or 1, offset=offset)
+    if ld_h == 0:
+        h = h[:1].expand(rows, features)
+    if ld_w == 0:
+        w = w[:1].expand(vocab, features)
+    want = Want(h, w, y)
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    close(lp, want.logps, 2 * want.err)
+    c = torch.randn(rows, generator=gen(8), device="cuda")
+    for first, extra, out in ((0, 0, dtype), (1, 3, dtype), (8, 8, torch.float32), (3, 1, torch.float32), (0, 16, torch.bfloat16)):
+        g = gen(9)
+        base_h = torch.full((first + rows * (features + extra) + 9,), 7.0, dtype=dtype, device="cuda")
+        base_w = torch.full((first + vocab * (features + extra) + 9,), 7.0, dtype=out, device="cuda")
+        dh = base_h[first:].as_strided((rows, features), (features + extra, 1))
+        dw = base_w[first:].as_strided((vocab, features), (features + extra, 1))
+        add = strided(g, vocab, features, features + 5, 1, out)
+        exact = want.grads(c, dtype, add=add)
+        a, b = mica.mica_linear_logps_grad(h, w, y, lse, c, dh=dh, dw=dw, add=add)
+        assert a.data_ptr() == dh.data_ptr() and b.data_ptr() == dw.data_ptr()
+        rounded(dh, exact[0], exact[1])
+        rounded(dw, exact[2], exact[3])
+        kept = dw.clone()
+        mica.mica_linear_logps_grad(h, w, y, lse, c, want_dh=False, dw=dw, add=dw)
+        exact = want.grads(c, dtype, add=kept)
+        rounded(dw, exact[2], exact[3])
+        for base, t in ((base_h, dh), (base_w, dw)):  # nothing beside the rows was written
+            t.fill_(7.0)
+            assert (base == 7.0).all()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=str)
+def test_more_rows_than_a_piece(out):
+    """A vocabulary so large that the rows are taken in pieces, whose sums wait for one another."""
+    rows, features, vocab = 1500, 40, 600_007
+    h, w, y = make(rows, features, vocab, torch.bfloat16, seed=2, skip=0.1)
+    add = torch.randn(vocab, features, generator=gen(3), device="cuda").to(out)
+    want = Want(h, w, y)
+    n = int(want.on.sum())
+    r = mica.mica_linear_cross_entropy(h, w, y, add=add)
+    close(r.logps, want.logps, 2 * want.err)
+    close(r.loss[0], -want.logps.sum() / n, 2 * want.err.sum() / n + 4 * U * want.logps.abs().sum() / n)
+    dh, dh_err, dw, dw_err = want.grads(torch.full((rows,), -1.0 / n, device="cuda"), torch.bfloat16, add=add, once=True)
+    rounded(r.dh, dh, dh_err)
+    rounded(r.dw, dw, dw_err)
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    close(lp, want.logps, 2 * want.err)
+    a, b = mica.mica_linear_logps_grad(h, w, y, lse, torch.where(want.on, -1.0 / n, 0.0).float(), add=add)
+    rounded(a, dh, dh_err)
+    rounded(b, dw, dw_err)
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_no_rows(dtype):
+    """Without rows, or with none that counts: the loss is 0, dw is add."""
+    w = torch.randn(300, 72, generator=gen(1), device="cuda").to(dtype)
+    add = torch.randn(300, 72, generator=gen(2), device="cuda")
+    for rows in (0, 5, 700):
+        h = torch.full((rows, 72), math.nan, dtype=dtype, device="cuda")
+        y = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
+        r = mica.mica_linear_cross_entropy(h, w, y, add=add)
+        assert float(r.loss) == 0.0 and not r.logps.any() and not r.dh.any() and torch.equal(r.dw, add)
+        r = mica.mica_linear_cross_entropy(h, w, y, denom=3.0)
+        assert float(r.loss) == 0.0 and not r.dw.any()
+        lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+        assert not lp.any() and not lse.any()
+        c = torch.ones(rows, device="cuda")
+        a, b = mica.mica_linear_logps_grad(h, w, y, lse, c, add=add)
+        assert not a.any() and torch.equal(b, add)
+        a, b = mica.mica_linear_logps_grad(h, w, y, lse, c)
+        assert not b.any() and b.dtype == dtype
+
+
+def test_one_gradient_alone():
+    h, w, y = make(200, 128, 3001, torch.bfloat16, seed=4)
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    a = mica.mica_linear_cross_entropy(h, w, y, want_dw=False)
+    b = mica.mica_linear_cross_entropy(h, w, y, want_dh=False)
+    assert a.dw is None and b.dh is None and torch.equal(a.dh, r.dh) and torch.equal(b.dw, r.dw)
+    assert torch.equal(a.loss, r.loss)
+
+
+@pytest.mark.parametrize("rows,features,vocab", [(40, 100, 1000), (400, 512, 60007)])
+def test_streams_graphs_and_repeats(rows, features, vocab):
+    """The same bits on another stream, twice at once on two, and captured into a graph and replayed on new inputs."""
+    h, w, y = make(rows, features, vocab, torch.bfloat16, seed=9)
+    first = mica.mica_linear_cross_entropy(h, w, y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [mica.mica_linear_cross_entropy(h, w, y, stream=s) for s in streams for _ in range(3)]
+    torch.cuda.synchronize()
+    for r in both:
+        assert all(torch.equal(a, b) for a, b in zip(r, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = mica.mica_linear_cross_entropy(h, w, y)
+        lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+        g = mica.mica_linear_logps_grad(h, w, y, lse, lp)
+    for seed in (10, 11):
+        h2, w2, y2 = make(rows, features, vocab, torch.bfloat16, seed=seed, skip=0.1 * (seed - 9))
+        for a, b in ((h, h2), (w, w2), (y, y2)):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = mica.mica_linear_cross_entropy(h2, w2, y2)
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+        lp2, lse2 = mica.mica_linear_logps(h2, w2, y2, lse=True)
+        g2 = mica.mica_linear_logps_grad(h2, w2, y2, lse2, lp2)
+        assert torch.equal(lp, lp2) and torch.equal(g[0], g2[0]) and torch.equal(g[1], g2[1])
+
+
+def test_gradients_against_differences():
+    """The loss's change along a direction of h, and of w, against the gradients: the loss is exact to 1e-6 or so, the step is
+    small and the second difference is taken off by going both ways."""
+    h, w, y = make(64, 128, 900, torch.float16, seed=21, skip=0.2)
+    r = mica.mica_linear_cross_entropy(h, w, y, dw_dtype=torch.float32)
+    g = gen(22)
+    for x, d in ((h, r.dh), (w, r.dw)):
+        step = (0.02 * torch.randn(x.shape, generator=g, device="cuda")).half()
+        up, down = (x + step), (x - step)
+        a = mica.mica_linear_cross_entropy(up if x is h else h, up if x is w else w, y, grad=False).loss.double()
+        b = mica.mica_linear_cross_entropy(down if x is h else h, down if x is w else w, y, grad=False).loss.double()
+        change = ((up.double() - down.double()) * d.double()).sum()
+        # third differences: (|step| |row|)^3 / 6 or so of 0.2^3; and the gradients' own rounding
+        assert abs(float(a - b - change)) <= 2e-3 * float(((up.double() - down.double()).abs() * d.double().abs()).sum()) + 1e-5
+
+
+def test_refusals():
+    h, w, y = make(8, 64, 100, torch.bfloat16)
+    lse, c = torch.zeros(8, device="cuda"), torch.ones(8, device="cuda")
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        mica.mica_linear_cross_entropy(h, w, y, dh=h)
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        mica.mica_linear_logps_grad(h, w, y, lse, c, dw=w)
+    with pytest.raises(mica.MicaError, match="HYPER"):
+        mica.mica_linear_logps(h, w, y, temperature=0.0)
+    with pytest.raises(mica.MicaError, match="HYPER"):
+        mica.mica_linear_cross_entropy(h, w, y, grad_scale=math.inf)
+    with pytest.raises(mica.MicaError, match="ADDRESS"):
+        mica.mica_linear_logps(h.cpu(), w, y)
+    with pytest.raises(mica.MicaError, match="ADDRESS"):
+        mica.mica_linear_logps(h, w, y.cpu())
+    dw = torch.zeros(100, 64, device="cuda")
+    with pytest.raises(mica.MicaError, match="OVERLAP"):  # what is added to overlaps the result at another place
+        both = torch.zeros(101, 64, device="cuda")
+        mica.mica_linear_logps_grad(h, w, y, lse, c, dw=both[1:], add=both[:-1])
+    mica.mica_linear_logps_grad(h, w, y, lse, c, dw=dw, add=dw)
