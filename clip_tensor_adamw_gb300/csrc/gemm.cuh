@@ -14,7 +14,13 @@
 //   Deal deal(int pair, int pairs) const            how the work is dealt to one of the pairs; computed once a thread
 //   bool piece(Deal&, Piece*) const                 the pair's next piece of work; false when there are no more
 //   kAhead                                          the work is known from the parameter alone, and the first piece is looked
-//                                                   up while the kernel before still runs (1 to 2 us, most of it misses)
+//                                                   up while the kernel before still runs (1 to 2 us, most of it misses);
+//                                                   otherwise void prefetch() const does what it can
+//   kJoins                                          tiles may be split, and the kernel joins their sums itself: each warp
+//                                                   leaves its part's in `part_sums` (kPartFloats for each part), and the one
+//                                                   that comes last, by `tickets` (16 for each tile, zeros before and after),
+//                                                   adds them up in their order; the epilogue's bool wants(int c) says which
+//                                                   chunks are worth it
 //   struct Epilogue                                 what becomes of a piece's sums, made for each piece by each of its threads:
 //     Epilogue(const P&, const Deal&, const Piece&, const Place&)
 //     void chunk(int c, float (&v)[32])             columns [32 c, 32 c + 32) of the thread's row of its half, in order
@@ -59,6 +65,9 @@ struct Piece {
     int from, to;
     int tile;   // for the epilogue, as the policy likes
     int part;   // >= 0: part of a split tile
+    int parts;  // kJoins: how many it has (then `part` counts from 0), from `first` on among all parts
+    int first;
+    int slot;   // the tile's place among all
     int low;    // > 0: both operands are sums of two matrices, the second (the rounding's rest) `low` further on in z: the
     int depth;  // products of stages [0, depth) of high and high, high and low, low and high follow one another
 };
@@ -129,6 +138,27 @@ __device__ __forceinline__ void load_sums32(uint32_t at, float (&f)[32]) {
     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
 }
 
+constexpr int64_t kPartFloats = (int64_t)kTile * kTile;  // of a part's sums
+
+// Where a warp leaves its share of a part's sums.
+template <typename P>
+__device__ __forceinline__ float* part_of(const P& p, const Piece& q, int part, int rank, int warp) {
+    return p.part_sums + (int64_t)(q.first + part) * kPartFloats + (rank * kTakers + warp) * (kPartFloats / (2 * kTakers));
+}
+// Whether the warp is the last of `parts` to get here; it leaves the ticket at 0.
+__device__ __forceinline__ bool comes_last(unsigned int* ticket, int parts, int lane) {
+    __threadfence();
+    __syncwarp();
+    unsigned int before = 0;
+    if (lane == 0) {
+        before = atomicAdd(ticket, 1u);
+        if (before == (unsigned)parts - 1) *ticket = 0u;
+    }
+    before = __shfl_sync(~0u, before, 0);
+    __threadfence();
+    return before == (unsigned)parts - 1;
+}
+
 template <typename T, typename P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ P p) {
     extern __shared__ unsigned char raw[];
@@ -169,6 +199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             prefetch_map(q.a.map);
             prefetch_map(q.b.map);
         }
+    }
+    if constexpr (!P::kAhead) {
+        if (warp == kLoader && lane == 0) p.prefetch();
     }
     wait_prerequisite();
     allow_dependents();
@@ -246,7 +279,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     __syncwarp();
                     if (lane == 0) arrive_leader(&bar.sum_empty[b]);
                 }
+                if constexpr (P::kJoins) {
+                    if (q.parts > 1) {
+                        if (!epilogue.wants(c)) continue;
+                        float* out = part_of(p, q, q.part, rank, warp) + c * 1024 + lane;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) out[e * 32] = v[e];
+                        continue;
+                    }
+                }
                 epilogue.chunk(c, v);
+            }
+            if constexpr (P::kJoins) {
+                if (q.parts > 1) {
+                    if (epilogue.wants(0) && comes_last(p.tickets + (q.slot * 2 + rank) * kTakers + warp, q.parts, lane))
+#pragma unroll 1
+                        for (int c = 0; c < chunks && epilogue.wants(c); ++c) {
+                            float v[32] = {};
+                            for (int part = 0; part < q.parts; ++part) {
+                                const float* in = part_of(p, q, part, rank, warp) + c * 1024 + lane;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] += __ldcg(in + e * 32);
+                            }
+                            epilogue.chunk(c, v);
+                        }
+                    sums.next();
+                    continue;
+                }
             }
             epilogue.done();
             sums.next();
@@ -300,15 +359,14 @@ __device__ __forceinline__ bool split_piece(SplitDeal& d, Piece* q) {
     if (i >= d.pieces) return false;
     d.next += d.pairs;
     if (i < d.whole || d.parts == 1) {
-        *q = Piece{{}, {}, 0, 0, kTile, 0, d.stages, i, -1, 0, 0};
+        *q = Piece{{}, {}, 0, 0, kTile, 0, d.stages, i, -1, 1, 0, 0, 0, 0};
         return true;
     }
     const int k = i - d.whole, part = k % d.parts;
     *q = Piece{{}, {}, 0, 0, kTile, (int)((int64_t)d.stages * part / d.parts), (int)((int64_t)d.stages * (part + 1) / d.parts),
-               d.whole + k / d.parts, k, 0, 0};
+               d.whole + k / d.parts, k, 1, 0, 0, 0, 0};
     return true;
 }
-constexpr int64_t kPartFloats = (int64_t)kTile * kTile;  // of a part's sums, row by row
 
 // ------------------------------------------------------------------------------------------------------------------------
 // from a row to a thread, to coalesced accesses
@@ -386,8 +444,15 @@ __device__ __forceinline__ void store_block(unsigned short* to, int64_t ld, int 
         const unsigned short* s = reinterpret_cast<const unsigned short*>(staging);
         if (col0 + lane >= cols) return;
         at = to + row0 * ld + col0 + lane;
-        for (int r = 0; r < 32 && row0 + r < rows; ++r)
-            at[r * ld] = s[r * 32 + ((lane / 8 ^ ((r >> 1) & 3)) * 8) + lane % 8];
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += 16) {
+            unsigned short e[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) e[r] = s[(r0 + r) * 32 + ((lane / 8 ^ ((r >> 1) & 3)) * 8) + lane % 8];
+#pragma unroll
+            for (int r = 0; r < 16; ++r, at += ld)
+                if (row0 + r0 + r < rows) *at = e[r];
+        }
         return;
     }
 #pragma unroll
@@ -448,8 +513,17 @@ template <typename T, typename P>
 cudaError_t launch_gemm(const P& p, int64_t pieces, int sms, void* stream) {
     const auto kernel = gemm_kernel<T, P>;
     g_gemm_launched = true;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmShared);
+    // once for each device (a kernel's attributes are the device's, and the call takes as long as a third of a launch)
+    static std::atomic<uint64_t> set{0};
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+    if (!(set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmShared);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
     const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
     return launch_after(kernel, 2 * (pieces < pairs ? pieces : pairs), kGemmThreads, kGemmShared, stream, p);
 }

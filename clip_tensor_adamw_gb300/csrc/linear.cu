@@ -60,6 +60,16 @@ __device__ __forceinline__ Span span_of(int count, int most, int j) {
 // Whether the j-th piece is the last with rows in it.
 __device__ __forceinline__ bool last_span(int count, int most, int j) { return span_of(count, most, j + 1).rows == 0; }
 
+// How a piece of the rows is dealt, which the gather works out for the products: their divisions would take each of them
+// some 2 us before its first load.
+struct Dealt {
+    Span span;
+    int first, last;    // piece
+    SplitDeal dh, dw;   // of pair 0
+    int dh_left;        // dh's pieces in their last round
+    float inv_scale;    // of d
+};
+
 __device__ __forceinline__ int64_t target_at(const void* targets, bool wide, int64_t i) {
     return wide ? static_cast<const int64_t*>(targets)[i] : static_cast<const int32_t*>(targets)[i];
 }
@@ -81,6 +91,8 @@ struct Gather {
     int scaled;            // d is scaled
     int most, piece;
     Meta* meta;            // written by the first piece
+    Dealt* dealt;          // by each
+    int pairs, has_dh, has_dw;
     int* index;            // the rows that count
     unsigned short* out;   // [most][ld]
     int ld;
@@ -120,13 +132,23 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather g) {
     const int64_t from = (int64_t)blockIdx.x * each, to = from + each < g.rows ? from + each : g.rows;
     int before = 0, count = 0;
     float top = 0.0f;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < g.rows; i += 256) {
-        float c;
-        if (!row_counts(g, (int)i, &c)) continue;
-        ++count;
-        before += i < from;
-        if (fabsf(c) > top || c != c) top = fabsf(c);  // (a NaN stays: nothing is larger)
+    constexpr int kAtOnce = 16;  // loads of a thread in flight
+    for (int64_t i0 = threadIdx.x; i0 < g.rows; i0 += 256 * kAtOnce) {
+        bool scored[kAtOnce];
+        float c[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t i = i0 + 256 * k;
+            scored[k] = i < g.rows && target_at(g.targets, g.wide, i) >= 0;
+            c[k] = g.dlogps && i < g.rows ? g.dlogps[i] : 1.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (!scored[k] || c[k] == 0.0f) continue;
+            ++count;
+            before += i0 + 256 * k < from;
+            if (fabsf(c[k]) > top || c[k] != c[k]) top = fabsf(c[k]);  // (a NaN stays: nothing is larger)
+        }
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
@@ -160,6 +182,19 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather g) {
     const Span span = span_of(count, g.most, g.piece);
     if (blockIdx.x == 0) {
         if (g.piece == 0 && threadIdx.x == 0) *g.meta = m;
+        if (threadIdx.x == 32) {
+            const int across = (g.features + kTile - 1) / kTile, stages = (span.rows + kDepth - 1) / kDepth;
+            Dealt d;
+            d.span = span;
+            d.first = g.piece == 0;
+            d.last = last_span(count, g.most, g.piece);
+            d.dh = split_deal(g.has_dh ? (span.rows + kTile - 1) / kTile * across : 0, (g.vocab + kDepth - 1) / kDepth, 0, g.pairs);
+            d.dw = split_deal(g.has_dw && (span.rows || d.first) ? (g.vocab + kTile - 1) / kTile * across : 0,
+                              stages ? stages : 1, 0, g.pairs);
+            d.dh_left = d.dh.pieces % g.pairs;
+            d.inv_scale = m.inv_scale;
+            *g.dealt = d;
+        }
         if (g.again)
             for (int i = threadIdx.x; i < 1 + g.most / kTile; i += 256) g.again[i] = 0;
         for (int r = span.rows + warp; r < (span.rows + 63) / 64 * 64; r += 8)
@@ -192,16 +227,26 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather g) {
                 if (r < 0 || r >= span.rows) continue;
                 const unsigned short* in = g.h + i * g.ld_h;
                 unsigned short* out = g.out + (int64_t)r * g.ld;
-                const int whole = g.aligned ? g.features / 8 : 0;
-                for (int x = lane; x < whole; x += 32) reinterpret_cast<uint4*>(out)[x] = reinterpret_cast<const uint4*>(in)[x];
-                for (int x = whole * 8 + lane; x < g.features; x += 32) out[x] = in[x];
                 const int64_t y = target_at(g.targets, g.wide, i);
+                const unsigned short* own = g.w && y < g.vocab ? g.w + y * g.ld_w : nullptr;  // (16-byte aligned)
+                const int whole = g.aligned ? g.features / 8 : 0;
                 float z = 0.0f;  // the target's logit
-                if (g.w && y < g.vocab) {
-                    const T* a = reinterpret_cast<const T*>(in);
-                    const T* b = reinterpret_cast<const T*>(g.w + y * g.ld_w);
-#pragma unroll 4
-                    for (int x = lane; x < g.features; x += 32) z = fmaf(widen(a[x]), widen(b[x]), z);
+#pragma unroll 2
+                for (int x = lane; x < whole; x += 32) {
+                    const uint4 u = reinterpret_cast<const uint4*>(in)[x];
+                    reinterpret_cast<uint4*>(out)[x] = u;
+                    if (!own) continue;
+                    const uint4 v = reinterpret_cast<const uint4*>(own)[x];
+                    const T *a = reinterpret_cast<const T*>(&u), *b = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z = fmaf(widen(a[e]), widen(b[e]), z);
+                }
+                for (int x = whole * 8 + lane; x < g.features; x += 32) {
+                    const unsigned short u = in[x];
+                    out[x] = u;
+                    if (own) z = fmaf(widen(reinterpret_cast<const T&>(u)), widen(reinterpret_cast<const T*>(own)[x]), z);
+                }
+                if (own) {
 #pragma unroll
                     for (int d = 16; d; d /= 2) z += __shfl_xor_sync(~0u, z, d);
                 }
@@ -230,26 +275,31 @@ struct RowSum {
 
 struct Logits {
     static constexpr unsigned int kStatus = 0x100u;
-    static constexpr bool kAhead = false;
+    static constexpr bool kAhead = false, kJoins = false;
     CUtensorMap h, w;
-    const Meta* meta;
+    const Dealt* dealt;
     const int* target;
-    int most, piece_index, vocab, stages;
+    int vocab, stages, across;  // across: tiles
     float a;  // log2(e) / T
+
+    __device__ __forceinline__ void prefetch() const {
+        prefetch_map(&h);
+        prefetch_map(&w);
+    }
 
     struct Deal {
         int rows, row_tiles, pieces, next, pairs;
     };
     __device__ __forceinline__ Deal deal(int pair, int pairs) const {
-        const int rows = span_of(meta->count, most, piece_index).rows, row_tiles = (rows + kTile - 1) / kTile;
-        return Deal{rows, row_tiles, row_tiles * ((vocab + kTile - 1) / kTile), pair, pairs};
+        const int rows = dealt->span.rows, row_tiles = (rows + kTile - 1) / kTile;
+        return Deal{rows, row_tiles, row_tiles * across, pair, pairs};
     }
     // rows first: h stays in L2 while W passes once
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
         const int i = d.next;
         if (i >= d.pieces) return false;
         d.next += d.pairs;
-        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile, 0, stages, i, -1, 0, 0};
+        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile, 0, stages, i, -1, 1, 0, 0, 0, 0};
         return true;
     }
 };
@@ -602,9 +652,9 @@ struct LogitGrad : Logits {
 template <typename T>
 struct HiddenGrad {
     CUtensorMap d, w;
-    const Meta* meta;
+    const Dealt* dealt;
     const int* index;
-    int most, piece_index, vocab, features;
+    int features;
     const float* factor;  // of a row, or null
     T* dh;                // or null
     int64_t ld;
@@ -616,16 +666,13 @@ struct HiddenGrad {
         int column_tiles;
         float scale;
     };
-    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
-        const Meta m = *meta;
-        const Span span = span_of(m.count, most, piece_index);
-        const int column_tiles = (features + kTile - 1) / kTile;
+    __device__ __forceinline__ Deal deal(const Dealt& t, int pair) const {
         Deal r;
-        static_cast<SplitDeal&>(r) = split_deal(dh ? (span.rows + kTile - 1) / kTile * column_tiles : 0,
-                                                (vocab + kDepth - 1) / kDepth, pair, pairs);
-        r.span = span;
-        r.column_tiles = column_tiles;
-        r.scale = m.inv_scale;
+        static_cast<SplitDeal&>(r) = t.dh;
+        r.next = pair;
+        r.span = t.span;
+        r.column_tiles = (features + kTile - 1) / kTile;
+        r.scale = t.inv_scale;
         return r;
     }
     __device__ __forceinline__ bool piece(Deal& r, Piece* q) const {
@@ -674,8 +721,7 @@ struct HiddenGrad {
 template <typename O>
 struct WeightGrad {
     CUtensorMap d, h;
-    const Meta* meta;
-    int most, piece_index, vocab, features;
+    int most, vocab, features;
     O* dw;         // or null
     int64_t ld;
     const O* add;  // or null
@@ -687,22 +733,19 @@ struct WeightGrad {
 
     struct Deal : SplitDeal {
         int column_tiles, first_stage;
-        bool first, last, none;
+        bool first, last;
         float scale;
     };
-    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
-        const Meta m = *meta;
-        const Span span = span_of(m.count, most, piece_index);
-        const int column_tiles = (features + kTile - 1) / kTile;
+    __device__ __forceinline__ Deal deal(const Dealt& t, int pair) const {
         Deal r;
-        const int stages = (span.rows + kDepth - 1) / kDepth;
-        r.none = !dw || (span.rows == 0 && piece_index > 0);
-        static_cast<SplitDeal&>(r) = split_deal(r.none ? 0 : (vocab + kTile - 1) / kTile * column_tiles, stages ? stages : 1, pair, pairs);
-        r.first_stage = stages ? 0 : most / kDepth;  // without rows: past the matrices, where zeros are read
-        r.column_tiles = column_tiles;
-        r.first = piece_index == 0;
-        r.last = last_span(m.count, most, piece_index);
-        r.scale = m.inv_scale;
+        static_cast<SplitDeal&>(r) = t.dw;
+        // dh's last round goes on with dw's first pieces
+        r.next = pair >= t.dh_left ? pair - t.dh_left : pair - t.dh_left + r.pairs;
+        r.column_tiles = (features + kTile - 1) / kTile;
+        r.first_stage = t.span.rows ? 0 : most / kDepth;  // without rows: past the matrices, where zeros are read
+        r.first = t.first;
+        r.last = t.last;
+        r.scale = t.inv_scale;
         return r;
     }
     __device__ __forceinline__ bool piece(Deal& r, Piece* q) const {
@@ -776,7 +819,7 @@ struct WeightGrad {
 template <typename T, typename O>
 struct Gradients {
     static constexpr unsigned int kStatus = 0x200u;
-    static constexpr bool kAhead = false;
+    static constexpr bool kAhead = false, kJoins = false;
     HiddenGrad<T> dh;
     WeightGrad<O> dw;
 
@@ -784,10 +827,15 @@ struct Gradients {
         typename HiddenGrad<T>::Deal dh;
         typename WeightGrad<O>::Deal dw;
     };
-    __device__ __forceinline__ Deal deal(int pair, int pairs) const {
-        Deal d{dh.deal(pair, pairs), dw.deal(pair, pairs)};
-        d.dw.next = (pair + pairs - d.dh.pieces % pairs) % pairs;  // dh's last round goes on with dw's first pieces
-        return d;
+    __device__ __forceinline__ void prefetch() const {
+        prefetch_map(&dh.d);
+        prefetch_map(&dh.w);
+        prefetch_map(&dw.d);
+        prefetch_map(&dw.h);
+    }
+    __device__ __forceinline__ Deal deal(int pair, int) const {
+        const Dealt t = *dh.dealt;
+        return Deal{dh.deal(t, pair), dw.deal(t, pair)};
     }
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
         if (dh.piece(d.dh, q)) return true;
@@ -846,10 +894,10 @@ __device__ __forceinline__ void join_split(const G& g, const typename G::Deal& d
     }
 }
 template <typename T, typename O>
-__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Gradients<T, O> p, int pairs) {
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Gradients<T, O> p) {
     wait_prerequisite();
     allow_dependents();
-    const typename Gradients<T, O>::Deal deal = p.deal(0, pairs);
+    const typename Gradients<T, O>::Deal deal = p.deal(0, 0);
     join_split(p.dh, deal.dh, deal.dh.span.rows, p.dh.features);
     join_split(p.dw, deal.dw, p.dw.vocab, p.dw.features);
 }
@@ -890,6 +938,7 @@ struct Room {
     int most;       // rows of a piece
     int pieces;
     Meta* meta;
+    Dealt* dealt;
     int* index;
     unsigned short* w;  // a copy with aligned rows, or null
     int64_t ld_w;       // of what is used
@@ -928,6 +977,7 @@ Room places_of(const Linear& L, bool sums, const LinearGrad* G, bool ce, int sms
     c.pieces = (int)((L.rows + c.most - 1) / c.most);
     if (c.pieces < 1) c.pieces = 1;  // (without rows too: dw is add, the loss 0)
     c.meta = p->take<Meta>(1);
+    c.dealt = p->take<Dealt>(1);
     c.index = p->take<int>(L.rows);
     c.target = p->take<int>(c.most);
     c.ld_h = (int)round_up(L.features, 8);
@@ -1016,6 +1066,10 @@ cudaError_t gather(const Call& call, const Room& c, int piece) {
     g.most = c.most;
     g.piece = piece;
     g.meta = c.meta;
+    g.dealt = c.dealt;
+    g.pairs = call.sms / 2 < 1 ? 1 : call.sms / 2;
+    g.has_dh = call.G && call.G->dh;
+    g.has_dw = call.G && call.G->dw;
     g.index = c.index;
     g.out = c.h;
     g.ld = c.ld_h;
@@ -1039,12 +1093,11 @@ cudaError_t gather(const Call& call, const Room& c, int piece) {
 }
 
 // What the products over the vocabulary share.
-bool fill(Logits* p, const Linear& L, const Room& c, int piece) {
-    p->meta = c.meta;
+bool fill(Logits* p, const Linear& L, const Room& c) {
+    p->dealt = c.dealt;
     p->target = c.target;
-    p->most = c.most;
-    p->piece_index = piece;
     p->vocab = L.vocab;
+    p->across = (int)tiles_of(L.vocab);
     p->stages = (L.features + kDepth - 1) / kDepth;
     p->a = (float)(1.4426950408889634074 / L.temperature);
     return matrix_map(&p->h, map_type(L.dtype), c.h, L.features, c.most, c.ld_h, 1) &&
@@ -1084,7 +1137,7 @@ cudaError_t join_rows(const Call& call, const Room& c, int piece) {
 }
 
 template <typename T, typename O>
-cudaError_t gradients(const Call& call, const Room& c, int piece) {
+cudaError_t gradients(const Call& call, const Room& c) {
     const Linear& L = call.L;
     const LinearGrad& G = *call.G;
     Gradients<T, O> p{};
@@ -1093,11 +1146,8 @@ cudaError_t gradients(const Call& call, const Room& c, int piece) {
     if (!matrix_map(&d, type, c.d, L.vocab, c.most, c.ld_d, 1)) return cudaErrorInvalidValue;
     HiddenGrad<T>& x = p.dh;
     x.d = d;
-    x.meta = c.meta;
+    x.dealt = c.dealt;
     x.index = c.index;
-    x.most = c.most;
-    x.piece_index = piece;
-    x.vocab = L.vocab;
     x.features = L.features;
     x.factor = c.factor;
     x.dh = static_cast<T*>(G.dh);
@@ -1108,9 +1158,7 @@ cudaError_t gradients(const Call& call, const Room& c, int piece) {
     if (!matrix_map(&x.w, type, c.w ? c.w : L.w, L.features, L.vocab, c.ld_w, 1)) return cudaErrorInvalidValue;
     WeightGrad<O>& y = p.dw;
     y.d = d;
-    y.meta = c.meta;
     y.most = c.most;
-    y.piece_index = piece;
     y.vocab = L.vocab;
     y.features = L.features;
     y.dw = static_cast<O*>(G.dw);
@@ -1132,7 +1180,7 @@ cudaError_t gradients(const Call& call, const Room& c, int piece) {
     const bool short_dh = !G.dh || (L.vocab + kDepth - 1) / kDepth < 2 * kLeastStages;
     const bool short_dw = !G.dw || (L.rows + kDepth - 1) / kDepth < 2 * kLeastStages;
     if (short_dh && short_dw) return cudaSuccess;
-    return launch_after(join_parts_kernel<T, O>, 8 * (int64_t)call.sms, 256, 0, call.stream, p, pairs);
+    return launch_after(join_parts_kernel<T, O>, 8 * (int64_t)call.sms, 256, 0, call.stream, p);
 }
 
 template <typename T>
@@ -1145,7 +1193,7 @@ cudaError_t run(const Call& call, const Room& c) {
         MICA_STEP(gather<T>(call, c, piece));
         if (c.once) {
             LogitOnce<T> p{};
-            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            if (!fill(&p, L, c)) return cudaErrorInvalidValue;
             p.sums = c.sums;
             p.parts = c.parts;
             p.origin = c.origin;
@@ -1159,7 +1207,7 @@ cudaError_t run(const Call& call, const Room& c) {
             MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
         } else if (forward) {
             LogitSums p{};
-            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            if (!fill(&p, L, c)) return cudaErrorInvalidValue;
             p.sums = c.sums;
             p.parts = c.parts;
             p.at = c.at;
@@ -1169,7 +1217,7 @@ cudaError_t run(const Call& call, const Room& c) {
         if (!call.G) continue;
         if (!c.once) {
             LogitGrad<T> p{};
-            if (!fill(&p, L, c, piece)) return cudaErrorInvalidValue;
+            if (!fill(&p, L, c)) return cudaErrorInvalidValue;
             p.coef = c.coef;
             p.origin = c.origin;
             p.d = reinterpret_cast<T*>(c.d);
@@ -1177,9 +1225,9 @@ cudaError_t run(const Call& call, const Room& c) {
             MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
         }
         const int32_t type = call.G->dw ? call.G->dw_dtype : L.dtype;
-        MICA_STEP((type == MICA_F32   ? gradients<T, float>(call, c, piece)
-                   : type == MICA_F16 ? gradients<T, __half>(call, c, piece)
-                                      : gradients<T, __nv_bfloat16>(call, c, piece)));
+        MICA_STEP((type == MICA_F32   ? gradients<T, float>(call, c)
+                   : type == MICA_F16 ? gradients<T, __half>(call, c)
+                                      : gradients<T, __nv_bfloat16>(call, c)));
     }
     return cudaSuccess;
 }

@@ -166,11 +166,14 @@ __device__ __forceinline__ float rest_of(float x) { return x - __half2float(__fl
 // x = 2^10 u / (|u| + eps) in binary16, rows ld_x apart.
 template <typename T, bool kMuon>
 __global__ void __launch_bounds__(256) first_kernel(const __grid_constant__ Batch b, const __grid_constant__ Streams s,
-                                                    Update u, const double* squares, double eps) {
+                                                    Update u, const double* squares, double eps, unsigned int* tickets,
+                                                    int count) {
     __shared__ double part[8];
     __shared__ float scale;
     wait_prerequisite();
     allow_dependents();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < count; i += 256) tickets[i] = 0u;
     const Item it = item_at(b, blockIdx.x);
     const Class& c = b.c[it.c];
     const int k = c.first + it.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -272,14 +275,17 @@ static_assert(kMostClasses <= 8, "a piece's class has three bits");
 constexpr int kMostPairs = 96, kMostGroups = 2 * kMostClasses, kRounds = 64;
 struct Round {
     uint32_t pairs[kMostPairs / 32];
-    int first;     // piece of the group
-    short repeat;  // rounds like this one, one after the other
-    short group;
+    int first;   // piece of the group
+    int repeat;  // rounds like this one, one after the other
+    int group;
 };
 struct Schedule {
     Round rows[kRounds];
     int rounds;
     int tiles[kMostGroups];  // of a matrix; group 2 k: class k's whole tiles, 2 k + 1: its narrow ones
+    int slot[kMostGroups];   // tiles of the groups before,
+    int first[kMostGroups];  // and their parts
+    int parts[kMostClasses]; // of a tile
 };
 struct Turns {
     int pair, at, repeat;
@@ -306,7 +312,7 @@ __device__ __forceinline__ bool next_piece(const Schedule& s, Turns& t, int* gro
 __device__ __forceinline__ Piece piece_of(const Class& c, int width, const Operand& a, const Operand& b, int m, int n, int cols,
                                           int depth, int tile) {
     const int stages = (depth + kDepth - 1) / kDepth;
-    return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages, tile, -1, c.low, stages};
+    return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages, tile, -1, 1, 0, 0, c.low, stages};
 }
 
 // Whole columns of tiles, and whether there is a narrow one.
@@ -341,10 +347,18 @@ struct Symmetric {
 
     using Deal = Turns;
     __device__ __forceinline__ Deal deal(int pair, int) const { return Turns{pair, 0, 0}; }
-    __device__ __forceinline__ bool tile(Deal& d, int* k, int* z, int* m, int* n) const {
+    // the next piece's class, matrix, tile, and with its parts the tile's place among all
+    __device__ __forceinline__ bool tile(Deal& d, int* k, int* z, int* m, int* n, int* part, int* slot, int* first) const {
         int group, place;
         if (!next_piece(s, d, &group, &place)) return false;
         *k = group / 2;
+        *part = 0;
+        if (s.parts[*k] > 1) {
+            *part = place % s.parts[*k];
+            place /= s.parts[*k];
+        }
+        *slot = s.slot[group] + place;
+        *first = s.first[group] + place * s.parts[*k];
         const int tiles = s.tiles[group], side = b.c[*k].side, t = place % tiles;
         *z = place / tiles;
         if (group & 1) *m = t, *n = whole_columns(side, b.width);
@@ -405,16 +419,27 @@ __device__ __forceinline__ void store_symmetric(__half* to, int ld, int side, in
 
 // A = x x^T or x^T x
 struct Gram : Symmetric {
+    float* part_sums;
+    unsigned int* tickets;
     static constexpr unsigned int kStatus = 0x800u;
-    static constexpr bool kAhead = true;
+    static constexpr bool kAhead = true, kJoins = true;
     int from;  // the buffer that x is in
 
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
-        int k, z, m, n;
-        if (!tile(d, &k, &z, &m, &n)) return false;
+        int k, z, m, n, part, slot, first;
+        if (!tile(d, &k, &z, &m, &n, &part, &slot, &first)) return false;
         const Class& c = b.c[k];
         const Operand x{&c.x[from], z, c.wide()};
         *q = piece_of(c, b.width, x, x, m, n, c.side, c.wide() ? c.cols : c.rows, z << 3 | k);
+        if (s.parts[k] > 1) {
+            const int stages = q->to;
+            q->part = part;
+            q->parts = s.parts[k];
+            q->slot = slot;
+            q->first = first;
+            q->from = stages * part / q->parts;
+            q->to = stages * (part + 1) / q->parts;
+        }
         return true;
     }
     struct Epilogue {
@@ -430,9 +455,10 @@ struct Gram : Symmetric {
             col0 = q.n0 + at.first_column;
             mirror = q.n0 >= q.m0 + kTile;
         }
+        __device__ __forceinline__ bool wants(int k) const { return row0 < c.side && col0 + 32 * k < c.side; }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col = col0 + 32 * k;
-            if (row0 >= c.side || col >= c.side) return;
+            if (!wants(k)) return;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kScale;
             store_symmetric(to, c.ld_a, c.side, row0, col, lane, staging, v, mirror, (int64_t)c.low * c.side * c.ld_a);
@@ -444,12 +470,12 @@ struct Gram : Symmetric {
 // B = a I + b A + c A^2
 struct Poly : Symmetric {
     static constexpr unsigned int kStatus = 0x1000u;
-    static constexpr bool kAhead = true;
+    static constexpr bool kAhead = true, kJoins = false;
     float ca, cb, cc;
 
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
-        int k, z, m, n;
-        if (!tile(d, &k, &z, &m, &n)) return false;
+        int k, z, m, n, part, slot, first;
+        if (!tile(d, &k, &z, &m, &n, &part, &slot, &first)) return false;
         const Class& c = b.c[k];
         const Operand a{&c.a, z, true};
         *q = piece_of(c, b.width, a, a, m, n, c.side, c.side, z << 3 | k);
@@ -534,7 +560,7 @@ struct Poly : Symmetric {
 // x = B x or x B: what the middle steps and the last one share
 struct Apply {
     static constexpr unsigned int kStatus = 0x2000u;
-    static constexpr bool kAhead = true;
+    static constexpr bool kAhead = true, kJoins = false;
     Batch b;
     Schedule s;
     int from;
@@ -703,7 +729,7 @@ void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
             Round& r = s->rows[s->rounds++];
             r = Round{};
             r.first = done;
-            r.group = (short)work[w].group;
+            r.group = work[w].group;
             r.repeat = 1;
             // those that the next pieces go to before anyone gets two of them, least first; all, where rounds run short
             const bool plain = s->rounds + 2 * (int)(work.size() - w) >= kRounds;
@@ -715,13 +741,21 @@ void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
                 std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return load[a] < load[b]; });
                 order.resize(left);
             }
-            if ((int)order.size() == pairs) r.repeat = (short)std::min(left / pairs, 32767);
+            const int each = (int)order.size();
+            if (each == pairs) {
+                r.repeat = left / pairs;
+            } else if (each < left) {  // as often as it takes them to come near the others
+                int64_t next = INT64_MAX;
+                for (int p = 0; p < pairs; ++p)
+                    if (load[p] >= least + work[w].cost) next = std::min(next, load[p]);
+                r.repeat = (int)std::max<int64_t>(1, std::min<int64_t>(left / each, (next - least) / work[w].cost));
+            }
             for (int p : order) {
                 r.pairs[p / 32] |= 1u << p % 32;
                 load[p] += (int64_t)r.repeat * work[w].cost;
             }
-            left -= r.repeat * (int)order.size();
-            done += r.repeat * (int)order.size();
+            left -= r.repeat * each;
+            done += r.repeat * each;
         }
     }
 }
@@ -734,27 +768,53 @@ int cost_of(const Class& c, int depth, int columns) {
 
 int most_pairs(int sms) { return std::max(1, std::min(sms / 2, kMostPairs)); }
 
+// The parts that a tile's sum is split in, where pairs are idle. A part saves its share of the stages, a quarter of a
+// microsecond each; joining costs two, and half of one for each part and 32 columns, which the last to come adds up alone. So
+// 16 x 1,600 in pairs of binary16, a sum of 75 stages, is split in 6 (19 us without, 8 with), and 384 x 1,536, of 24, is not
+// (12.7 us without, 14.5 in 4).
+int parts_of(int stages, int columns) {
+    const int chunks = (columns + 63) / 64, parts = (int)std::sqrt(stages / (2.0 * chunks));
+    return parts > 1 && 0.25 * stages > 0.25 * stages / parts + 0.5 * parts * chunks + 2.0 ? parts : 1;
+}
 template <typename Tiles, typename Depth>
-void schedule(const Batch& b, int sms, Tiles tiles, Depth depth, Schedule* s, int* pieces) {
+void schedule(const Batch& b, int sms, bool split, Tiles tiles, Depth depth, Schedule* s, int* pieces) {
     std::vector<Work> work;
-    *pieces = 0;
+    const int pairs = most_pairs(sms);
+    int n[kMostGroups], columns[kMostGroups], stages[kMostClasses], slots = 0;
     for (int k = 0; k < b.classes; ++k) {
         const Class& c = b.c[k];
-        for (int narrow = 0; narrow < 2; ++narrow) {
-            int columns;
-            const int n = tiles(c, narrow != 0, &columns);
-            s->tiles[2 * k + narrow] = n;
-            if (n) work.push_back(Work{2 * k + narrow, n * c.count, cost_of(c, depth(c), columns)});
-            *pieces += n * c.count;
+        stages[k] = (depth(c) + kDepth - 1) / kDepth * (c.low ? 3 : 1);
+        s->parts[k] = 1;
+        for (int g = 2 * k; g < 2 * k + 2; ++g) {
+            n[g] = s->tiles[g] = tiles(c, (g & 1) != 0, &columns[g]);
+            n[g] *= c.count;
+            s->slot[g] = slots;
+            slots += n[g];
         }
     }
-    deal_out(std::move(work), std::min(most_pairs(sms), *pieces), s);
+    if (split && b.width == 128 && slots <= pairs / 2) {
+        int all = 0;
+        for (int k = 0; k < b.classes; ++k) {
+            s->parts[k] = parts_of(stages[k], std::min(b.c[k].side, 128));
+            all += s->parts[k] * (n[2 * k] + n[2 * k + 1]);
+        }
+        if (all > pairs) std::fill(s->parts, s->parts + kMostClasses, 1);
+    }
+    *pieces = 0;
+    for (int g = 0; g < 2 * b.classes; ++g) {
+        const Class& c = b.c[g / 2];
+        const int parts = s->parts[g / 2], count = n[g] * parts;
+        s->first[g] = *pieces;
+        if (count) work.push_back(Work{g, count, cost_of(c, depth(c), columns[g]) / parts + 3});
+        *pieces += count;
+    }
+    deal_out(std::move(work), std::min(pairs, *pieces), s);
 }
 
 // The pieces of the three products.
 struct Schedules {
     Schedule gram, poly, apply;
-    int symmetric_pieces, apply_pieces;
+    int gram_pieces, poly_pieces, apply_pieces;
 };
 void schedules(const Batch& b, int sms, Schedules* s) {
     const auto triangle = [&](const Class& c, bool narrow, int* columns) {
@@ -765,13 +825,21 @@ void schedules(const Batch& b, int sms, Schedules* s) {
         *columns = narrow ? columns_of(c.cols % b.width, b.width) : b.width;
         return row_tiles_of(c.rows) * (narrow ? has_narrow(c.cols, b.width) : whole_columns(c.cols, b.width));
     };
-    schedule(b, sms, triangle, [](const Class& c) { return std::max(c.rows, c.cols); }, &s->gram, &s->symmetric_pieces);
-    schedule(b, sms, triangle, [](const Class& c) { return c.side; }, &s->poly, &s->symmetric_pieces);
-    schedule(b, sms, all, [](const Class& c) { return c.side; }, &s->apply, &s->apply_pieces);
+    schedule(b, sms, true, triangle, [](const Class& c) { return std::max(c.rows, c.cols); }, &s->gram, &s->gram_pieces);
+    schedule(b, sms, false, triangle, [](const Class& c) { return c.side; }, &s->poly, &s->poly_pieces);
+    schedule(b, sms, false, all, [](const Class& c) { return c.side; }, &s->apply, &s->apply_pieces);
 }
 
+// The rest of a batch's workspace.
+constexpr int kTickets = kMostPairs / 2 * 2 * kTakers;  // of all tiles of a list that has split ones
+struct Extra {
+    double* squares;
+    unsigned int* tickets;
+    float* part_sums;  // of at most as many parts as there are pairs
+};
+
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
-int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* base, Batch* b, double** squares) {
+int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* base, Batch* b, Extra* extra) {
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* p = base ? base + at : nullptr;
@@ -800,7 +868,13 @@ int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* bas
         b->matrices += c.count;
         b->items += c.count * c.items;
     }
-    *squares = reinterpret_cast<double*>(take((int64_t)b->items * sizeof(double)));
+    extra->squares = reinterpret_cast<double*>(take((int64_t)b->items * sizeof(double)));
+    extra->tickets = reinterpret_cast<unsigned int*>(take(kTickets * sizeof(unsigned int)));
+    int64_t tiles = 0;  // of the narrow kind, which lists have that are split
+    for (int k = 0; k < b->classes; ++k)
+        tiles += (triangle_tiles(b->c[k].side, 128) + (has_narrow(b->c[k].side, 128) ? row_tiles_of(b->c[k].side) : 0)) * (int64_t)b->c[k].count;
+    if (tiles <= kMostPairs / 2)
+        extra->part_sums = reinterpret_cast<float*>(take(kMostPairs * kPartFloats * sizeof(float)));
     return at;
 }
 
@@ -824,9 +898,10 @@ bool maps(Batch* b) {
     } while (0)
 
 template <typename T, bool kMuon>
-cudaError_t first(const Batch& b, const Streams& s, const Update& u, double* squares, double eps, void* stream) {
-    MICA_STEP(launch_after(momentum_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, squares));
-    return launch_after(first_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, (const double*)squares, eps);
+cudaError_t first(const Batch& b, const Streams& s, const Update& u, const Extra& extra, double eps, void* stream) {
+    MICA_STEP(launch_after(momentum_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, extra.squares));
+    return launch_after(first_kernel<T, kMuon>, b.items, 256, 0, stream, b, s, u, (const double*)extra.squares, eps,
+                        extra.tickets, kTickets);
 }
 
 template <typename O, bool kMuon>
@@ -847,8 +922,8 @@ cudaError_t last(const Muon& call, const Batch& b, const Schedules& s, const std
 
 cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* workspace, int sms, void* stream) {
     Batch b;
-    double* squares;
-    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, sms, workspace, &b, &squares);
+    Extra extra;
+    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, sms, workspace, &b, &extra);
     if (!maps(&b)) return cudaErrorInvalidValue;
     Schedules deals;
     schedules(b, sms, &deals);
@@ -869,27 +944,29 @@ cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* worksp
                    (call.hp.flags & MICA_STEP_SKIP_NONFINITE) != 0, call.d_factor};
     const double eps = call.ns->eps;
     if (call.m)
-        MICA_STEP((call.in_dtype == MICA_F16 ? first<__half, true>(b, s, u, squares, eps, stream)
-                                             : first<float, true>(b, s, u, squares, eps, stream)));
+        MICA_STEP((call.in_dtype == MICA_F16 ? first<__half, true>(b, s, u, extra, eps, stream)
+                                             : first<float, true>(b, s, u, extra, eps, stream)));
     else
-        MICA_STEP((call.in_dtype == MICA_F16   ? first<__half, false>(b, s, u, squares, eps, stream)
-                   : call.in_dtype == MICA_BF16 ? first<__nv_bfloat16, false>(b, s, u, squares, eps, stream)
-                                                : first<float, false>(b, s, u, squares, eps, stream)));
+        MICA_STEP((call.in_dtype == MICA_F16   ? first<__half, false>(b, s, u, extra, eps, stream)
+                   : call.in_dtype == MICA_BF16 ? first<__nv_bfloat16, false>(b, s, u, extra, eps, stream)
+                                                : first<float, false>(b, s, u, extra, eps, stream)));
     for (int step = 0; step < call.ns->steps; ++step) {
         const double* c = call.ns->coefficients + 3 * step;
         const int from = step & 1;
         Gram g{};
         g.b = b;
         g.s = deals.gram;
+        g.part_sums = extra.part_sums;
+        g.tickets = extra.tickets;
         g.from = from;
-        MICA_STEP(launch_gemm<__half>(g, deals.symmetric_pieces, 2 * most_pairs(sms), stream));
+        MICA_STEP(launch_gemm<__half>(g, deals.gram_pieces, 2 * most_pairs(sms), stream));
         Poly p{};
         p.b = b;
         p.s = deals.poly;
         p.ca = (float)(c[0] * kScale);
         p.cb = (float)c[1];
         p.cc = (float)(c[2] / kScale);
-        MICA_STEP(launch_gemm<__half>(p, deals.symmetric_pieces, 2 * most_pairs(sms), stream));
+        MICA_STEP(launch_gemm<__half>(p, deals.poly_pieces, 2 * most_pairs(sms), stream));
         if (step + 1 < call.ns->steps) {
             ApplyMiddle a{};
             a.b = b;
@@ -911,8 +988,8 @@ int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint
     int64_t most = 0;
     for (const auto& shapes : batches_of(rows, cols, T)) {
         Batch b;
-        double* squares;
-        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, 1, nullptr, &b, &squares));
+        Extra extra;
+        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, 1, nullptr, &b, &extra));
     }
     return most;
 }
