@@ -1239,6 +1239,7 @@ int run_typed(const Call& call, const Room& c) {
 }  // namespace
 
 int64_t linear_logps_workspace(const Linear& L) {
+    if (L.rows == 0) return 0;
     Places p(nullptr);
     places_of(L, true, nullptr, false, 1, &p);
     return p.bytes();

@@ -61,6 +61,8 @@ def _sizes(L: TensorList, what: str, precise: bool):
 
 def _iteration(steps: int, coefficients, eps: float, precise: bool) -> _NewtonSchulz:
     rows = list(coefficients)
+    if not rows or steps < 1:
+        raise ValueError("at least one step is needed")
     if not hasattr(rows[0], "__len__"):
         rows = [rows] * steps
     if len(rows) != steps or any(len(r) != 3 for r in rows):

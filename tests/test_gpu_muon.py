@@ -143,3 +143,157 @@ def test_steps(adjust, precise, gdt, nesterov):
             most = rate * off(u, o, precise) + 8 * U * float(before_w[k].double().norm() + rate * o.norm()) + 1e-6 * rate
             assert distance(w[k], want) <= most, (k, distance(w[k], want), most)
             assert not grads[k].any() if zero else torch.equal(grads[k], kept[k])
+
+
+def test_zeros_infinities_and_nans():
+    """A zero matrix gives zeros, one with an infinity or a NaN gives NaNs; the others of the list are as they would be alone."""
+    g = gen(11)
+    x = [torch.randn(s, generator=g, device="cuda") for s in [(300, 400), (300, 400), (300, 400), (40, 20), (40, 20), (40, 20)]]
+    x[0].zero_()
+    x[3].zero_()
+    x[1][17, 5] = math.inf
+    x[4][3, 3] = math.nan
+    r = mica.mica_orthogonalize(x).tensors
+    assert not r[0].any() and not r[3].any() and r[1].isnan().all() and r[4].isnan().all()
+    for i in (2, 5):
+        assert torch.equal(r[i], mica.mica_orthogonalize([x[i]]).tensors[0])
+        check(r[i], x[i])
+
+
+@pytest.mark.parametrize("scale", [1e-25, 1e-18, 1e15, 1e34])
+@pytest.mark.parametrize("shape", [(60, 90), (300, 280)], ids=str)
+def test_any_scale(shape, scale):
+    """Squares that float32 cannot hold: the result does not depend on the matrix's size (eps apart)."""
+    x = torch.randn(shape, generator=gen(12), device="cuda") * scale
+    check(mica.mica_orthogonalize([x], eps=1e-30).tensors[0], x, eps=1e-30)
+    one = torch.zeros_like(x)  # a single element: the square sum is one square
+    one[7, 3] = scale
+    r = mica.mica_orthogonalize([one], eps=1e-30, out_dtype=torch.float16).tensors[0]
+    want = 1.0
+    for _ in range(5):
+        a, b, c = COEFFICIENTS
+        want = a * want + b * want ** 3 + c * want ** 5
+    assert abs(float(r[7, 3]) - want) <= 0.01 and int((r != 0).sum()) == 1
+
+
+def test_eps_counts():
+    x = torch.randn(50, 70, generator=gen(13), device="cuda") * 1e-3
+    for eps in (1e-7, 0.05, 1.0):
+        check(mica.mica_orthogonalize([x], eps=eps).tensors[0], x, eps=eps)
+
+
+def test_in_place_and_alignment():
+    """Results over the inputs; matrices that begin at any element."""
+    g = gen(14)
+    for dtype in (torch.float16, torch.bfloat16):
+        for offset in (0, 1, 3, 4):
+            flat = torch.randn(offset + 130 * 77 + 300 * 8, generator=g, device="cuda").to(dtype)
+            views = [flat[offset:offset + 130 * 77].view(130, 77), flat[offset + 130 * 77:offset + 130 * 77 + 2400].view(300, 8)]
+            want = mica.mica_orthogonalize([v.clone() for v in views])
+            tail = flat[offset + 130 * 77 + 2400:].clone()
+            mica.mica_orthogonalize(views, views)
+            for a, b in zip(views, want.tensors):
+                assert torch.equal(a, b)
+            assert torch.equal(flat[offset + 130 * 77 + 2400:], tail)
+    w = torch.randn(1 + 65 * 33, generator=g, device="cuda")[1:].view(65, 33)
+    grad = torch.randn(3 + 65 * 33, generator=g, device="cuda")[3:].view(65, 33)
+    m = torch.randn(2 + 65 * 33, generator=g, device="cuda")[2:].view(65, 33)
+    copies = [t.clone() for t in (w, grad, m)]
+    mica.mica_muon_steps([w], [grad], [m], lr=0.1)
+    mica.mica_muon_steps(*[[t] for t in copies], lr=0.1)
+    assert torch.equal(w, copies[0]) and torch.equal(m, copies[2])
+
+
+@pytest.mark.parametrize("coefficients,steps", [((1.5, -0.5, 0.0), 10), ((1.875, -1.25, 0.375), 7), ((2.0, -1.5, 0.5), 1)])
+def test_other_polynomials(coefficients, steps):
+    x = torch.randn(90, 300, generator=gen(15), device="cuda")
+    check(mica.mica_orthogonalize([x], coefficients=coefficients, steps=steps).tensors[0], x, coefficients=coefficients, steps=steps)
+    rows = [coefficients] * (steps - 1) + [(3.0, -3.2, 1.2)]
+    check(mica.mica_orthogonalize([x], coefficients=rows, steps=steps).tensors[0], x, coefficients=rows)
+
+
+def test_long_sides():
+    g = gen(16)
+    for shape in [(3, 100_003), (70_001, 5), (260, 20_000), (20_000, 260)]:
+        x = torch.randn(shape, generator=g, device="cuda")
+        check(mica.mica_orthogonalize([x], out_dtype=torch.float16).tensors[0], x)
+
+
+@pytest.mark.parametrize("gdt", [torch.float32, torch.float16], ids=str)
+@pytest.mark.parametrize("factor", [0.0, math.nan, math.inf, -1.0])
+def test_skip_nonfinite(factor, gdt):
+    """A factor that is not > 0 leaves w and m as they are, and still zeroes g when asked; without the flag it counts."""
+    g = gen(17)
+    shapes = [(40, 30), (300, 310)]
+    w, m = ([torch.randn(s, generator=g, device="cuda") for s in shapes] for _ in range(2))
+    grads = [torch.randn(s, generator=g, device="cuda").to(gdt) for s in shapes]
+    f = torch.full((1,), factor, device="cuda")
+    kept = [[t.clone() for t in x] for x in (w, m)]
+    mica.mica_muon_steps(w, grads, m, lr=0.1, factor=f, skip_nonfinite=True, zero_grad=True)
+    went = factor == math.inf  # > 0
+    for a, b in zip((w, m), kept):
+        for s, t in zip(a, b):
+            assert torch.equal(s, t) != went
+    assert not any(t.any() for t in grads)
+    if factor == 0.0:
+        mica.mica_muon_steps(w, grads, m, lr=0.1, factor=f)
+        assert not torch.equal(w[0], kept[0][0])
+
+
+def test_lists_without_elements():
+    assert mica.mica_orthogonalize([]).T == 0
+    e = torch.empty(0, 5, device="cuda")
+    r = mica.mica_orthogonalize([e, e.t().contiguous()])
+    assert [tuple(t.shape) for t in r.tensors] == [(0, 5), (5, 0)]
+    mica.mica_muon_steps([], [], [], lr=0.1)
+    mica.mica_muon_steps([e], [e.clone()], [e.clone()], lr=0.1)
+
+
+def test_streams_graphs_and_repeats():
+    g = gen(18)
+    shapes = [(384, 384), (384, 1536), (16, 1600), (513, 2048)]
+    x = mica.TensorList([torch.randn(s, generator=g, device="cuda") for s in shapes])
+    first = mica.mica_orthogonalize(x)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    both = [mica.mica_orthogonalize(x, stream=s) for s in streams for _ in range(3)]
+    torch.cuda.synchronize()
+    for r in both:
+        assert all(torch.equal(a, b) for a, b in zip(r.tensors, first.tensors))
+    w, m = ([torch.randn(s, generator=g, device="cuda") for s in shapes] for _ in range(2))
+    copies = [[t.clone() for t in y] for y in (w, m)]
+    factor = torch.full((1,), 0.5, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    mica.mica_muon_steps(*[[t.clone() for t in y] for y in (w, x.tensors, m)], lr=0.01, factor=factor)  # loads the library
+    with torch.cuda.graph(graph):
+        mica.mica_muon_steps(w, x, m, lr=0.01, factor=factor)
+    for step in range(3):
+        for t in x.tensors:
+            t.normal_(generator=g)
+        factor.fill_(0.3 + step)
+        graph.replay()
+        mica.mica_muon_steps(copies[0], x, copies[1], lr=0.01, factor=factor)
+        for a, b in zip((w, m), copies):
+            assert all(torch.equal(s, t) for s, t in zip(a, b)), step
+
+
+def test_refusals():
+    x = torch.randn(64, 64, device="cuda")
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        mica.mica_muon_steps([x], [x], [torch.zeros_like(x)], lr=0.1)
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        mica.mica_muon_steps([x, x], [x.clone(), x.clone()], [x.clone(), x.clone()], lr=0.1)
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        half = torch.randn(65, 64, device="cuda").half()
+        mica.mica_orthogonalize([half[:64]], [half[1:]])
+    y = torch.randn(64, 64, device="cuda").half()
+    with pytest.raises(mica.MicaError, match="OVERLAP"):
+        mica.mica_orthogonalize([y, y], [y, torch.empty_like(y)])
+    with pytest.raises(mica.MicaError, match="ADDRESS"):
+        mica.mica_orthogonalize([x.cpu()], [torch.empty(64, 64, dtype=torch.float16, device="cuda")])
+    for bad in (dict(coefficients=(3.4445, 4.775, 2.0315)), dict(coefficients=(7.0, 0.0, 0.0)), dict(eps=0.0), dict(eps=2.0)):
+        with pytest.raises(mica.MicaError, match="HYPER"):
+            mica.mica_orthogonalize([x], **bad)
+    with pytest.raises(ValueError):
+        mica.mica_orthogonalize([x], steps=0, coefficients=[])
+    mica.mica_orthogonalize([x, x])  # one matrix read twice is fine
