@@ -746,9 +746,11 @@ void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
                 r.repeat = left / pairs;
             } else if (each < left) {  // as often as it takes them to come near the others
                 int64_t next = INT64_MAX;
+                int64_t most = least;
                 for (int p = 0; p < pairs; ++p)
                     if (load[p] >= least + work[w].cost) next = std::min(next, load[p]);
-                r.repeat = (int)std::max<int64_t>(1, std::min<int64_t>(left / each, (next - least) / work[w].cost));
+                    else most = std::max(most, load[p]);
+                r.repeat = (int)std::max<int64_t>(1, std::min<int64_t>(left / each, (next - most) / work[w].cost));
             }
             for (int p : order) {
                 r.pairs[p / 32] |= 1u << p % 32;

@@ -306,12 +306,36 @@ def test_more_rows_than_a_piece(out):
     rounded(b, dw, dw_err)
 
 
+@pytest.mark.parametrize("rows,skip", [(2048, 0.5), (2049, 0.5), (20_000, 0.1), (40_000, 0.9), (70_001, 0.02)])
+def test_many_rows(rows, skip):
+    """Rows that are looked through by a kernel of its own, more than a piece of the forward pass, and over the boundary."""
+    h, w, y = make(rows, 40, 301, torch.float16, seed=rows, skip=skip)
+    dirty = torch.where((y < 0)[:, None], torch.full_like(h, math.nan), h)
+    want = Want(h, w, y)
+    lp, lse = mica.mica_linear_logps(dirty, w, y, lse=True)
+    close(lp, want.logps, 2 * want.err)
+    close(lse, torch.where(want.on, want.lse, 0.0), want.err + U * want.lse.abs())
+    c = torch.randn(rows, generator=gen(1), device="cuda")
+    c[::5] = 0.0
+    got = mica.mica_linear_logps_grad(dirty, w, y, lse, c)
+    dh, dh_err, dw, dw_err = want.grads(c, torch.float16)
+    rounded(got[0], dh, dh_err)
+    rounded(got[1], dw, dw_err)
+    assert not got[0][(y < 0) | (c == 0)].any()
+    r = mica.mica_linear_cross_entropy(dirty, w, y, grad_scale=256.0)
+    n = int(want.on.sum())
+    close(r.loss[0], -want.logps.sum() / n, 2 * want.err.sum() / n + 4 * U * want.logps.abs().sum() / n)
+    dh, dh_err, dw, dw_err = want.grads(torch.full((rows,), -256.0 / n, device="cuda"), torch.float16)
+    rounded(r.dh, dh, dh_err)
+    rounded(r.dw, dw, dw_err)
+
+
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
 def test_no_rows(dtype):
     """Without rows, or with none that counts: the loss is 0, dw is add."""
     w = torch.randn(300, 72, generator=gen(1), device="cuda").to(dtype)
     add = torch.randn(300, 72, generator=gen(2), device="cuda")
-    for rows in (0, 5, 700):
+    for rows in (0, 5, 700, 3000):
         h = torch.full((rows, 72), math.nan, dtype=dtype, device="cuda")
         y = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
         r = mica.mica_linear_cross_entropy(h, w, y, add=add)
@@ -327,8 +351,9 @@ def test_no_rows(dtype):
         assert not b.any() and b.dtype == dtype
 
 
-def test_one_gradient_alone():
-    h, w, y = make(200, 128, 3001, torch.bfloat16, seed=4)
+@pytest.mark.parametrize("rows,features,vocab", [(200, 128, 3001), (400, 512, 60007)])
+def test_one_gradient_alone(rows, features, vocab):
+    h, w, y = make(rows, features, vocab, torch.bfloat16, seed=4)
     r = mica.mica_linear_cross_entropy(h, w, y)
     a = mica.mica_linear_cross_entropy(h, w, y, want_dw=False)
     b = mica.mica_linear_cross_entropy(h, w, y, want_dh=False)
