@@ -1,7 +1,8 @@
 """clip + AdamW optimizer step on one GB300 (sm_103a): ScaleTensors, ClipGradNorms and AdamWSteps (also over
 parameter groups, and both as one fused step), ClipGradNorms fused into the gradients' last write when that write is
-an add, and SGD / SGD with momentum over the same lists; and, before the step, losses over logits with their gradient
-and activation checkpoints in 8 bits with the backward passes that read them (train.py).
+an add, and SGD / SGD with momentum over the same lists; the step whose update is orthogonalised by Newton-Schulz products
+(muon.py); and, before the step, losses over logits and from hidden states with their gradients, and activation checkpoints
+in 8 bits with the backward passes that read them (train.py).
 
 The compute lives in libmica_optim.so (hand-written CUDA kernels behind the C ABI of include/mica_optim.h); this
 package is its Python binding. Build the library with ``python -m clip_tensor_adamw_gb300.build``.
