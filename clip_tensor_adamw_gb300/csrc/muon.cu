@@ -56,7 +56,6 @@ struct Class {
 struct Batch {
     Class c[kMostClasses];
     int classes, matrices, items;
-    int width;  // a tile's columns
 };
 
 // ------------------------------------------------------------------------------------------------------------------------
@@ -282,6 +281,8 @@ struct Round {
 struct Schedule {
     Round rows[kRounds];
     int rounds;
+    int pieces;
+    int width;               // a tile's columns
     int tiles[kMostGroups];  // of a matrix; group 2 k: class k's whole tiles, 2 k + 1: its narrow ones
     int slot[kMostGroups];   // tiles of the groups before,
     int first[kMostGroups];  // and their parts
@@ -361,8 +362,8 @@ struct Symmetric {
         *first = s.first[group] + place * s.parts[*k];
         const int tiles = s.tiles[group], side = b.c[*k].side, t = place % tiles;
         *z = place / tiles;
-        if (group & 1) *m = t, *n = whole_columns(side, b.width);
-        else triangle(t, side, b.width, m, n);
+        if (group & 1) *m = t, *n = whole_columns(side, s.width);
+        else triangle(t, side, s.width, m, n);
         return true;
     }
 };
@@ -430,7 +431,7 @@ struct Gram : Symmetric {
         if (!tile(d, &k, &z, &m, &n, &part, &slot, &first)) return false;
         const Class& c = b.c[k];
         const Operand x{&c.x[from], z, c.wide()};
-        *q = piece_of(c, b.width, x, x, m, n, c.side, c.wide() ? c.cols : c.rows, z << 3 | k);
+        *q = piece_of(c, s.width, x, x, m, n, c.side, c.wide() ? c.cols : c.rows, z << 3 | k);
         if (s.parts[k] > 1) {
             const int stages = q->to;
             q->part = part;
@@ -478,7 +479,7 @@ struct Poly : Symmetric {
         if (!tile(d, &k, &z, &m, &n, &part, &slot, &first)) return false;
         const Class& c = b.c[k];
         const Operand a{&c.a, z, true};
-        *q = piece_of(c, b.width, a, a, m, n, c.side, c.side, z << 3 | k);
+        *q = piece_of(c, s.width, a, a, m, n, c.side, c.side, z << 3 | k);
         return true;
     }
     struct Epilogue {
@@ -574,8 +575,8 @@ struct Apply {
         const Class& c = b.c[k];
         const int rows = row_tiles_of(c.rows);
         const Operand x{&c.x[from], z, !c.wide()}, poly{&c.b, z, true};
-        *q = piece_of(c, b.width, c.wide() ? poly : x, c.wide() ? x : poly, t % rows,
-                      group & 1 ? whole_columns(c.cols, b.width) : t / rows, c.cols, c.side, z << 3 | k);
+        *q = piece_of(c, s.width, c.wide() ? poly : x, c.wide() ? x : poly, t % rows,
+                      group & 1 ? whole_columns(c.cols, s.width) : t / rows, c.cols, c.side, z << 3 | k);
         return true;
     }
 };
@@ -623,21 +624,25 @@ struct ApplyLast : Apply {
             to = p.out[c.first + unpack(q.tile).z];
             row0 = q.m0 + at.row - at.lane;
             col0 = q.n0 + at.first_column;
-            wide = aligned16(to) && c.cols % 4 == 0;
+            wide = aligned16(to) && c.cols % (16 / (int)sizeof(O)) == 0;
             if (kMuon && p.skip && p.factor && !(*p.factor > 0.0f)) row0 = c.rows;
         }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int col0 = this->col0 + 32 * k;
             if (row0 >= c.rows || col0 >= c.cols) return;
-            float4 x[8];
-            by_columns(staging, lane, v, x);
-            const int row = row0 + lane / 8, col = col0 + lane % 8 * 4, there = c.cols - col;
-            if (col >= c.cols) return;
-            O* at = to + (int64_t)row * c.cols + col;
-            const int64_t step = 4 * (int64_t)c.cols;
             constexpr float kOne = 1.0f / (kScale * kScale);
-            if constexpr (kMuon) {
-                float4 w[8];
+            if constexpr (!kMuon) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack2<O>(v[2 * i] * kOne, v[2 * i + 1] * kOne);
+                store_block(reinterpret_cast<unsigned short*>(to), c.cols, c.rows, c.cols, row0, col0, lane, wide, staging, w);
+            } else {
+                float4 x[8], w[8];
+                by_columns(staging, lane, v, x);
+                const int row = row0 + lane / 8, col = col0 + lane % 8 * 4, there = c.cols - col;
+                if (col >= c.cols) return;
+                O* at = to + (int64_t)row * c.cols + col;
+                const int64_t step = 4 * (int64_t)c.cols;
                 const float rate = c.rate * kOne;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -646,13 +651,10 @@ struct ApplyLast : Apply {
                 for (int i = 0; i < 8; ++i)
                     x[i] = make_float4(w[i].x * p.decay - x[i].x * rate, w[i].y * p.decay - x[i].y * rate,
                                        w[i].z * p.decay - x[i].z * rate, w[i].w * p.decay - x[i].w * rate);
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = make_float4(x[i].x * kOne, x[i].y * kOne, x[i].z * kOne, x[i].w * kOne);
+                for (int i = 0; i < 8; ++i)
+                    if (row + 4 * i < c.rows) store4(at + i * step, x[i], there, wide);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (row + 4 * i < c.rows) store4(at + i * step, x[i], there, wide);
         }
         __device__ __forceinline__ void done() {}
     };
@@ -700,25 +702,13 @@ std::vector<std::vector<Group>> batches_of(const int64_t* rows, const int64_t* c
     return out;
 }
 
-// A tile's columns: 256, or 128 where tiles of 256 would leave pairs without one. Products of 256 x 128 run at two thirds of
-// the rate of 256 x 256 (four layers of GPT-2 XL: 3.93 ms with 128 columns, 3.24 with 256), but a list too small for the GPU
-// is done sooner in twice as many (384 x 1536: 124 us with 128, 148 with 256).
-int width_of(const std::vector<Group>& shapes, int sms) {
-    int64_t gram = 0;
-    for (const Group& s : shapes) {
-        const int64_t t = row_tiles_of((int)std::min(s.rows, s.cols));
-        gram += t * (t + 1) / 2 * (int64_t)s.which.size();
-    }
-    return gram * 4 <= sms ? 128 : kTile;
-}
-
-// A group's pieces and how long each takes, in stages of 256 columns.
+// A group's pieces and how long each takes, in nanoseconds.
 struct Work {
     int group, pieces, cost;
 };
 
-// Deals the groups, longest pieces first, each piece to the pair that has least so far.
-void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
+// Deals the groups, longest pieces first, each piece to the pair that has least so far; what the busiest pair has.
+int64_t deal_out(std::vector<Work> work, int pairs, Schedule* s) {
     std::stable_sort(work.begin(), work.end(), [](const Work& a, const Work& b) { return a.cost > b.cost; });
     std::vector<int64_t> load(pairs, 0);
     std::vector<int> order(pairs);
@@ -760,13 +750,14 @@ void deal_out(std::vector<Work> work, int pairs, Schedule* s) {
             done += r.repeat * each;
         }
     }
+    return *std::max_element(load.begin(), load.end());
 }
 
-// A piece of `columns` columns, in stages of 256. What a stage takes is what it loads, some 58 bytes a clock and SM: 0.285 us
-// for 32 KB, 0.25 to 0.27 for the 24 KB of up to 128 columns. And what a tile's ends take.
+// A piece of `columns` columns: what its stages load (some 58 bytes a clock and SM: 285 ns for 32 KB, 250 to 270 for the 24 KB
+// of up to 128 columns), and a part of its epilogue, which the next piece's products do not hide.
 int cost_of(const Class& c, int depth, int columns) {
     const int stages = (depth + kDepth - 1) / kDepth * (c.low ? 3 : 1);
-    return (columns > 128 ? stages : stages * 15 / 16) + 6;
+    return columns > 128 ? stages * 285 + 1000 : stages * 255 + 600;
 }
 
 int most_pairs(int sms) { return std::max(1, std::min(sms / 2, kMostPairs)); }
@@ -779,58 +770,67 @@ int parts_of(int stages, int columns) {
     const int chunks = (columns + 63) / 64, parts = (int)std::sqrt(stages / (2.0 * chunks));
     return parts > 1 && 0.25 * stages > 0.25 * stages / parts + 0.5 * parts * chunks + 2.0 ? parts : 1;
 }
+// tiles(class, narrow, width, &columns): a matrix's whole or narrow tiles. Returns how long the product takes.
 template <typename Tiles, typename Depth>
-void schedule(const Batch& b, int sms, bool split, Tiles tiles, Depth depth, Schedule* s, int* pieces) {
+int64_t schedule(const Batch& b, int sms, int width, bool split, Tiles tiles, Depth depth, Schedule* s) {
     std::vector<Work> work;
     const int pairs = most_pairs(sms);
-    int n[kMostGroups], columns[kMostGroups], stages[kMostClasses], slots = 0;
-    for (int k = 0; k < b.classes; ++k) {
-        const Class& c = b.c[k];
-        stages[k] = (depth(c) + kDepth - 1) / kDepth * (c.low ? 3 : 1);
-        s->parts[k] = 1;
-        for (int g = 2 * k; g < 2 * k + 2; ++g) {
-            n[g] = s->tiles[g] = tiles(c, (g & 1) != 0, &columns[g]);
-            n[g] *= c.count;
-            s->slot[g] = slots;
-            slots += n[g];
-        }
+    int n[kMostGroups], columns[kMostGroups], slots = 0;
+    s->width = width;
+    for (int g = 0; g < 2 * b.classes; ++g) {
+        const Class& c = b.c[g / 2];
+        n[g] = s->tiles[g] = tiles(c, (g & 1) != 0, width, &columns[g]);
+        n[g] *= c.count;
+        s->slot[g] = slots;
+        s->parts[g / 2] = 1;
+        slots += n[g];
     }
-    if (split && b.width == 128 && slots <= pairs / 2) {
+    if (split && width == 128 && slots <= pairs / 2) {
         int all = 0;
         for (int k = 0; k < b.classes; ++k) {
-            s->parts[k] = parts_of(stages[k], std::min(b.c[k].side, 128));
+            const Class& c = b.c[k];
+            s->parts[k] = parts_of((depth(c) + kDepth - 1) / kDepth * (c.low ? 3 : 1), std::min(c.side, 128));
             all += s->parts[k] * (n[2 * k] + n[2 * k + 1]);
         }
         if (all > pairs) std::fill(s->parts, s->parts + kMostClasses, 1);
     }
-    *pieces = 0;
+    s->pieces = 0;
     for (int g = 0; g < 2 * b.classes; ++g) {
         const Class& c = b.c[g / 2];
         const int parts = s->parts[g / 2], count = n[g] * parts;
-        s->first[g] = *pieces;
-        if (count) work.push_back(Work{g, count, cost_of(c, depth(c), columns[g]) / parts + 3});
-        *pieces += count;
+        s->first[g] = s->pieces;
+        if (count) work.push_back(Work{g, count, cost_of(c, depth(c), columns[g]) / parts + (parts > 1 ? 1000 : 0)});
+        s->pieces += count;
     }
-    deal_out(std::move(work), std::min(pairs, *pieces), s);
+    return deal_out(std::move(work), std::min(pairs, s->pieces), s) + (width > 128 ? 2500 : 1200);  // and the last epilogue
+}
+
+// Tiles of 256 columns, or of 128 where the product is done sooner so: their rate is two thirds (four layers of GPT-2 XL:
+// 3.93 ms with 128 columns, 3.16 with 256), but a list too small for the GPU takes twice as many (384 x 1,536: 124 us with
+// 128, 148 with 256).
+template <typename Tiles, typename Depth>
+void best_schedule(const Batch& b, int sms, bool split, Tiles tiles, Depth depth, Schedule* s) {
+    Schedule narrow{};
+    const int64_t wide = schedule(b, sms, kTile, split, tiles, depth, s);
+    if (s->pieces < 2 * most_pairs(sms) && schedule(b, sms, 128, split, tiles, depth, &narrow) < wide) *s = narrow;
 }
 
 // The pieces of the three products.
 struct Schedules {
     Schedule gram, poly, apply;
-    int gram_pieces, poly_pieces, apply_pieces;
 };
 void schedules(const Batch& b, int sms, Schedules* s) {
-    const auto triangle = [&](const Class& c, bool narrow, int* columns) {
-        *columns = narrow ? columns_of(c.side % b.width, b.width) : b.width;
-        return narrow ? (has_narrow(c.side, b.width) ? row_tiles_of(c.side) : 0) : triangle_tiles(c.side, b.width);
+    const auto triangle = [](const Class& c, bool narrow, int width, int* columns) {
+        *columns = narrow ? columns_of(c.side % width, width) : width;
+        return narrow ? (has_narrow(c.side, width) ? row_tiles_of(c.side) : 0) : triangle_tiles(c.side, width);
     };
-    const auto all = [&](const Class& c, bool narrow, int* columns) {
-        *columns = narrow ? columns_of(c.cols % b.width, b.width) : b.width;
-        return row_tiles_of(c.rows) * (narrow ? has_narrow(c.cols, b.width) : whole_columns(c.cols, b.width));
+    const auto all = [](const Class& c, bool narrow, int width, int* columns) {
+        *columns = narrow ? columns_of(c.cols % width, width) : width;
+        return row_tiles_of(c.rows) * (narrow ? has_narrow(c.cols, width) : whole_columns(c.cols, width));
     };
-    schedule(b, sms, true, triangle, [](const Class& c) { return std::max(c.rows, c.cols); }, &s->gram, &s->gram_pieces);
-    schedule(b, sms, false, triangle, [](const Class& c) { return c.side; }, &s->poly, &s->poly_pieces);
-    schedule(b, sms, false, all, [](const Class& c) { return c.side; }, &s->apply, &s->apply_pieces);
+    best_schedule(b, sms, true, triangle, [](const Class& c) { return std::max(c.rows, c.cols); }, &s->gram);
+    best_schedule(b, sms, false, triangle, [](const Class& c) { return c.side; }, &s->poly);
+    best_schedule(b, sms, false, all, [](const Class& c) { return c.side; }, &s->apply);
 }
 
 // The rest of a batch's workspace.
@@ -842,7 +842,7 @@ struct Extra {
 };
 
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
-int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* base, Batch* b, Extra* extra) {
+int64_t place(const std::vector<Group>& shapes, bool precise, char* base, Batch* b, Extra* extra) {
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* p = base ? base + at : nullptr;
@@ -850,7 +850,6 @@ int64_t place(const std::vector<Group>& shapes, bool precise, int sms, char* bas
         return p;
     };
     *b = Batch{};
-    b->width = width_of(shapes, sms);
     for (const Group& s : shapes) {
         Class& c = b->c[b->classes++];
         c.rows = (int)s.rows;
@@ -920,15 +919,15 @@ cudaError_t last(const Muon& call, const Batch& b, const Schedules& s, const std
     p.decay = (float)(1.0 - call.hp.lr * call.hp.weight_decay);
     p.skip = (call.hp.flags & MICA_STEP_SKIP_NONFINITE) != 0;
     p.factor = call.d_factor;
-    return launch_gemm<__half>(p, s.apply_pieces, 2 * most_pairs(sms), stream);
+    return launch_gemm<__half>(p, s.apply.pieces, 2 * most_pairs(sms), stream);
 }
 
 cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* workspace, int sms, void* stream) {
     Batch b;
     Extra extra;
-    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, sms, workspace, &b, &extra);
+    place(shapes, (call.ns->flags & MICA_NS_PRECISE) != 0, workspace, &b, &extra);
     if (!maps(&b)) return cudaErrorInvalidValue;
-    Schedules deals;
+    Schedules deals{};
     schedules(b, sms, &deals);
     Streams s{};
     int k = 0;
@@ -962,20 +961,20 @@ cudaError_t run(const Muon& call, const std::vector<Group>& shapes, char* worksp
         g.part_sums = extra.part_sums;
         g.tickets = extra.tickets;
         g.from = from;
-        MICA_STEP(launch_gemm<__half>(g, deals.gram_pieces, 2 * most_pairs(sms), stream));
+        MICA_STEP(launch_gemm<__half>(g, deals.gram.pieces, 2 * most_pairs(sms), stream));
         Poly p{};
         p.b = b;
         p.s = deals.poly;
         p.ca = (float)(c[0] * kScale);
         p.cb = (float)c[1];
         p.cc = (float)(c[2] / kScale);
-        MICA_STEP(launch_gemm<__half>(p, deals.poly_pieces, 2 * most_pairs(sms), stream));
+        MICA_STEP(launch_gemm<__half>(p, deals.poly.pieces, 2 * most_pairs(sms), stream));
         if (step + 1 < call.ns->steps) {
             ApplyMiddle a{};
             a.b = b;
             a.s = deals.apply;
             a.from = from;
-            MICA_STEP(launch_gemm<__half>(a, deals.apply_pieces, 2 * most_pairs(sms), stream));
+            MICA_STEP(launch_gemm<__half>(a, deals.apply.pieces, 2 * most_pairs(sms), stream));
         } else {
             MICA_STEP((call.m                         ? last<float, true>(call, b, deals, shapes, from, sms, stream)
                        : call.out_dtype == MICA_F16 ? last<__half, false>(call, b, deals, shapes, from, sms, stream)
@@ -992,7 +991,7 @@ int64_t muon_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint
     for (const auto& shapes : batches_of(rows, cols, T)) {
         Batch b;
         Extra extra;
-        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, 1, nullptr, &b, &extra));
+        most = std::max(most, place(shapes, (flags & MICA_NS_PRECISE) != 0, nullptr, &b, &extra));
     }
     return most;
 }
