@@ -167,6 +167,68 @@ def test_cross_entropy_of_many(rows, features, vocab, skip, dtype):
         rounded(r.dw, dw, dw_err)
 
 
+@pytest.mark.parametrize("rows,features,vocab", [(2500, 300, 5000), (4000, 520, 9000), (700, 800, 40_000), (5200, 100, 700), (2100, 2000, 3000)])
+def test_work_of_both_gradients(rows, features, vocab):
+    """How both gradients' tiles are dealt: dh's split along the vocabulary or not, dw's going on in turn."""
+    h, w, y = make(rows, features, vocab, torch.bfloat16, seed=rows, skip=0.05)
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    c = torch.randn(rows, generator=gen(2), device="cuda")
+    got = mica.mica_linear_logps_grad(h, w, y, lse, c)
+    dh, dh_err, dw, dw_err = Want(h, w, y).grads(c, torch.bfloat16)
+    rounded(got[0], dh, dh_err)
+    rounded(got[1], dw, dw_err)
+    one = mica.mica_linear_logps_grad(h, w, y, lse, c, want_dh=False)[1]
+    two = mica.mica_linear_logps_grad(h, w, y, lse, c, want_dw=False)[0]
+    rounded(one, dw, dw_err)
+    rounded(two, dh, dh_err)
+
+
+def test_offsets_past_32_bits():
+    """An embedding, its gradient and hidden states of more than 2^31 elements; the rows at their ends against float64."""
+    rows, features, vocab = 40, 40_000, 60_000
+    g = gen(31)
+    w = torch.empty(vocab, features, dtype=torch.bfloat16, device="cuda").normal_(0.0, features ** -0.5, generator=g)
+    h = torch.empty(70_000, features, dtype=torch.bfloat16, device="cuda")[::1790]  # 40 rows, the last past 2^31 elements
+    h.normal_(generator=g)
+    assert h.shape[0] == rows and w.numel() > 2 ** 31 and h.stride(0) * (rows - 1) > 2 ** 31
+    y = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    y[0], y[1], y[2] = 0, vocab - 1, vocab - 2
+    z = torch.cat([h.double() @ w[a:a + 5000].double().t() for a in range(0, vocab, 5000)], 1)
+    lse = torch.logsumexp(z, 1)
+    want = z.gather(1, y[:, None])[:, 0] - lse
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    # the longest sum: 2,500 additions of 16 products each, truncated; 2 (features / 16 + 2) 2^-23 sum |h w| as above
+    err = 2 * (features / 16 + 2) * 2.0 ** -23 * float((h.double().abs() @ w[:1000].double().abs().t()).max()) * 1.5 + 1e-4
+    close(r.logps, want, err)
+    d = (torch.exp(z - lse[:, None]) - torch.nn.functional.one_hot(y, vocab)) / rows
+    for at in (slice(0, 3), slice(vocab - 3, vocab), slice(int(y[5]), int(y[5]) + 1)):
+        dw = d[:, at].t() @ h.double()
+        assert float((r.dw[at].double() - dw).norm()) <= 0.02 * float(dw.norm())
+    for i in (0, rows - 1):
+        dh = sum(d[i, a:a + 5000] @ w[a:a + 5000].double() for a in range(0, vocab, 5000))
+        assert float((r.dh[i].double() - dh).norm()) <= 0.02 * float(dh.norm())
+
+
+def test_largest_vocabulary():
+    """2^24 tokens: more than 2^32 elements of d, 65,536 tiles across, a row's sum of 131,072 parts."""
+    rows, features, vocab = 300, 16, 1 << 24
+    g = gen(32)
+    h = torch.randn(rows, features, generator=g, device="cuda").half()
+    w = torch.randn(vocab, features, generator=g, device="cuda").half()
+    y = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    y[0], y[1] = vocab - 1, 0
+    lse = torch.logsumexp(torch.stack([torch.logsumexp(h.double() @ w[a:a + (1 << 20)].double().t(), 1)
+                                       for a in range(0, vocab, 1 << 20)]), 0)
+    want = (h.double() * w[y].double()).sum(1) - lse
+    r = mica.mica_linear_cross_entropy(h, w, y, grad_scale=2.0 ** 20)
+    close(r.logps, want, (vocab / 1024 / 32 + 64) * U + 1e-5)  # a lane joins 4,096 of a row's parts, five joins follow
+    for at in (0, vocab - 1, int(y[7])):
+        p = torch.exp(h.double() @ w[at].double() - lse)
+        d = (p - (y == at).double()) / rows * 2.0 ** 20
+        dw = d @ h.double()
+        assert float((r.dw[at].double() - dw).abs().max()) <= 2.0 ** -10 * float((d.abs() @ h.double().abs()).max())
+
+
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
 def test_unlikely_targets(dtype):
     """Rows whose target is e^-30 to e^-400 likely, among ordinary ones: the sum of exp(z - z_target) leaves its range."""

@@ -219,6 +219,26 @@ def test_long_sides():
         check(mica.mica_orthogonalize([x], out_dtype=torch.float16).tensors[0], x)
 
 
+def test_offsets_past_32_bits():
+    """A matrix of more than 2^31 elements, one step: its last rows against the formula in float32 (whose own error, 1e-5 or
+    so, counts for nothing beside binary16's 2^-11 per rounding)."""
+    rows, cols = 131_072, 16_392
+    assert rows * cols > 2 ** 31
+    x = torch.empty(rows, cols, dtype=torch.float16, device="cuda").normal_(generator=gen(19))
+    r = mica.mica_orthogonalize([x], steps=1, out_dtype=torch.float16).tensors[0]
+    norm = math.sqrt(sum(float(x[a:a + 8192].float().square().sum(dtype=torch.float64)) for a in range(0, rows, 8192)))
+    gram = torch.zeros(cols, cols, device="cuda")
+    for a in range(0, rows, 8192):
+        part = x[a:a + 8192].float() / norm
+        gram += part.t() @ part
+    a, b, c = COEFFICIENTS
+    for at in (slice(0, 4), slice(rows - 4, rows)):
+        u = x[at].float() / norm
+        ug = u @ gram
+        want = a * u + b * ug + c * (ug @ gram)
+        assert float((r[at].float() - want).norm()) <= 4 * 2.0 ** -11 * float(want.norm())
+
+
 @pytest.mark.parametrize("gdt", [torch.float32, torch.float16], ids=str)
 @pytest.mark.parametrize("factor", [0.0, math.nan, math.inf, -1.0])
 def test_skip_nonfinite(factor, gdt):
