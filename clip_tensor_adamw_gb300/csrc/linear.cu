@@ -9,10 +9,11 @@
 // for each row. The gradient takes the product again: keeping the logits would take memory that grows with rows x vocabulary.
 // d is rounded to 16 bits once, in that product's epilogue, and multiplied with W and with h in one launch.
 //
-// Cross entropy, where both are wanted, needs the product once (bfloat16 and large enough, kOnceProducts): its epilogue leaves
-// q_ij = exp(z_ij - z_i,target), which needs no maximum (the sum is at least 1) and has bfloat16's range, and sums it up. The
-// rest is a factor 1 / sum_j q_ij for each row: in dh's epilogue, and on h's rows for dW. The few rows whose sum leaves the
-// range, whose targets are less likely than some e^-44, are taken again, counted from lse.
+// Cross entropy, which has the forward pass and the gradient in one call, needs the product once in bfloat16: its epilogue
+// leaves q_ij = exp(z_ij - z_i,target), which needs no maximum (the sum is at least 1) and has bfloat16's range, and sums it
+// up. The rest is a factor 1 / sum_j q_ij for each row: in dh's epilogue, and on h's rows for dW. The few rows whose sum leaves
+// the range, whose targets are less likely than some e^-44, are taken again, counted from lse. Against taking the product
+// twice: 16 x 256 x 5,000 42 us and 44, 1,024 x 768 x 50,257 176 and 211, 8,192 x 768 x 50,257 1,254 and 1,564.
 //
 // Logits, maxima, sums and gradients' sums are float32. d is rounded to the operands' type because the tensor cores multiply
 // what they are given in 16 bits: relative 2^-9 (bfloat16) or 2^-12 of each of its elements on average. binary16 has not the
@@ -29,10 +30,9 @@ namespace {
 constexpr int64_t kGradBytes = (int64_t)1 << 30;    // of d, that a piece of the rows takes
 constexpr int64_t kStatBytes = (int64_t)256 << 20;  // of the forward pass's maxima and sums
 constexpr int kMostRows = 16384;                    // of a piece in the forward pass
-constexpr int kLookRows = 2048;                     // up to which every CTA of the gather looks through all targets
-// Products of rows x features x vocabulary from which cross entropy takes the logits once: below, the product that it saves
-// is shorter than the launch that looks for rows to take again.
-constexpr double kOnceProducts = 1e10;
+// Rows up to which every CTA of the gather looks through all targets, which saves a launch: log-probabilities of 1,024 rows 22.0
+// us so and 23.5 with a scan before, of 2,048 27.9 and 26.9, of 16,384 131 and 103.
+constexpr int kLookRows = 1024;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMostSum = 0x1p64f;                 // of exp(z - z_target) over 32 columns
 
@@ -201,7 +201,7 @@ __device__ __forceinline__ void begin_piece(const Gather& g, const Meta& m, cons
         for (int c = lane; c < g.ld / 8; c += 32) reinterpret_cast<uint4*>(g.out + (int64_t)r * g.ld)[c] = uint4{};
 }
 
-// Many rows (kLookRows): one CTA looks through the targets and writes down which count, in order, and behind them, backwards,
+// Many rows (over kLookRows): one CTA looks through the targets and writes down which count, in order, and behind them, backwards,
 // the others; gather_kernel takes a piece of them. 8,192 rows: 12 us and 8; 1 M rows: 0.2 ms.
 __global__ void __launch_bounds__(1024) scan_kernel(Gather g) {
     __shared__ int sums[32];
@@ -446,7 +446,7 @@ struct LogitSums : Logits {
     };
 };
 
-// The product that cross entropy takes once: q = 2^(z a - origin), 0 at the target, and its sum. A sum counts from the
+// The product that cross entropy takes once (and, so that its loss is the same, without gradients too): q = 2^(z a - origin), 0 at the target, and its sum. A sum counts from the
 // target's logit; where 32 columns leave the range (kMostSum), from the largest so far, and the row is taken again.
 template <typename T>
 struct LogitOnce : Logits {
@@ -455,7 +455,7 @@ struct LogitOnce : Logits {
     const float* origin;  // the target's logit times a; lse, in rows taken again
     const float* at;      // the second time: the targets' elements
     const int* again;     // the second time: whether there are any such rows, and in which tiles; or null
-    T* d;                 // [most][ld]
+    T* d;                 // [most][ld], or null for the sums alone
     int ld;
 
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
@@ -486,7 +486,7 @@ struct LogitOnce : Logits {
         }
         __device__ __forceinline__ void chunk(int k, float (&v)[32]) {
             const int first = column + 32 * k;
-            if (first >= p.ld || stored <= 0) return;
+            if (first >= p.ld || stored <= 0) return;  // (ld: the vocabulary, rounded up)
             if (first + 32 > p.vocab) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -527,7 +527,7 @@ struct LogitOnce : Logits {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s.sum += exp2_fast(fmaf(v[i], p.a, -s.origin));
             }
-            store_block(to, p.ld, stored, p.ld, 0, first, lane, true, staging, w);
+            if (p.d) store_block(to, p.ld, stored, p.ld, 0, first, lane, true, staging, w);
         }
         __device__ __forceinline__ void done() {
             if (p.sums && live && column < p.vocab) p.sums[(int64_t)row * p.parts + column / kHalf] = s;
@@ -567,7 +567,7 @@ struct Join {
     float* at_target;      // what d holds at the target
     float* factor;         // of a row of d
     int* again;
-    unsigned short* d;
+    unsigned short* d;     // null: no gradients
     int ld_d;
     const unsigned short* h;
     unsigned short* scaled_h;
@@ -613,12 +613,13 @@ __device__ __forceinline__ float join_once(const Join& j, const Meta& m, RowSum 
         logp = (c - lse) * kLn2;
         factor = k;
         at = expm1f(logp);
-        if (lane == 0) {
+        if (lane == 0 && j.d) {
             j.origin[row] = lse;
             j.again[0] = 1;
             j.again[1 + row / kTile] = 1;
         }
     }
+    if (!j.d) return logp;
     const int y = j.target[row];
     if (lane == 0) {
         j.factor[row] = factor;
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(Join j) {
             if (lane == 0 && j.origin) j.origin[row] = s.origin + l;
         }
         if (lane == 0) j.logps[i] = logp;
-    } else if (j.once && row < (span.rows + 63) / 64 * 64) {
+    } else if (j.scaled_h && row < (span.rows + 63) / 64 * 64) {
         unsigned short* out = j.scaled_h + (int64_t)row * j.ld_h;
         for (int x = lane; x < j.ld_h / 8; x += 32) reinterpret_cast<uint4*>(out)[x] = uint4{};
     }
@@ -1087,9 +1088,10 @@ Room places_of(const Linear& L, bool sums, const LinearGrad* G, bool ce, int sms
         c.at = p->take<float>(c.most);
     }
     if (ce) c.partial = p->take<Exact>((int64_t)c.pieces * (c.most / 8));
+    c.once = ce && L.dtype == MICA_BF16;
+    c.ld_d = (int)round_up(L.vocab, 64);
     if (!G) return c;
     const int pairs = sms / 2 < 1 ? 1 : sms / 2;
-    c.ld_d = (int)round_up(L.vocab, 64);
     c.coef = p->take<float>(c.most);
     c.d = p->take<unsigned short>((int64_t)c.most * c.ld_d);
     if (G->dh) c.dh_parts = p->take<float>(kMostRounds * pairs * kPartFloats);
@@ -1098,7 +1100,6 @@ Room places_of(const Linear& L, bool sums, const LinearGrad* G, bool ce, int sms
         c.ld_sums = round_up(L.features, 4);
         c.dw_sums = p->take<float>(L.vocab * c.ld_sums);
     }
-    c.once = ce && L.dtype == MICA_BF16 && (double)L.rows * L.features * L.vocab >= kOnceProducts;
     if (c.once) {
         c.factor = p->take<float>(c.most);
         c.scaled_h = p->take<unsigned short>((int64_t)c.most * c.ld_h);
@@ -1213,7 +1214,7 @@ cudaError_t join_rows(const Call& call, const Room& c, int piece) {
     j.logps = call.logps;
     j.lse = call.lse;
     j.at = c.at;
-    j.origin = call.G ? c.origin : nullptr;
+    j.origin = call.G || c.once ? c.origin : nullptr;
     j.once = c.once;
     j.at_target = c.at;
     j.factor = c.factor;
@@ -1299,7 +1300,7 @@ cudaError_t run(const Call& call, const Room& c) {
             p.sums = nullptr;
             p.at = c.at;
             p.again = c.again;
-            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
+            if (call.G) MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
         } else if (forward) {
             LogitSums p{};
             if (!fill(&p, L, c)) return cudaErrorInvalidValue;
