@@ -392,7 +392,8 @@ struct Logits {
         const int i = d.next;
         if (i >= d.pieces) return false;
         d.next += d.pairs;
-        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile, 0, stages, i, -1, 1, 0, 0, 0, 0};
+        *q = Piece{{&h, 0, true}, {&w, 0, true}, i % d.row_tiles * kTile, i / d.row_tiles * kTile, kTile,
+                   0, stages, i, -1, 1, 0, 0, 0, 0};
         return true;
     }
 };
@@ -446,8 +447,9 @@ struct LogitSums : Logits {
     };
 };
 
-// The product that cross entropy takes once (and, so that its loss is the same, without gradients too): q = 2^(z a - origin), 0 at the target, and its sum. A sum counts from the
-// target's logit; where 32 columns leave the range (kMostSum), from the largest so far, and the row is taken again.
+// The product that cross entropy takes once (and, so that its loss is the same, without gradients too): q = 2^(z a - origin), 0
+// at the target, and its sum. A sum counts from the target's logit; where 32 columns leave the range (kMostSum), from the
+// largest so far, and the row is taken again.
 template <typename T>
 struct LogitOnce : Logits {
     RowSum* sums;         // [most][vocabulary / 128]; null the second time

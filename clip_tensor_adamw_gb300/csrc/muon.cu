@@ -313,7 +313,8 @@ __device__ __forceinline__ bool next_piece(const Schedule& s, Turns& t, int* gro
 __device__ __forceinline__ Piece piece_of(const Class& c, int width, const Operand& a, const Operand& b, int m, int n, int cols,
                                           int depth, int tile) {
     const int stages = (depth + kDepth - 1) / kDepth;
-    return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages, tile, -1, 1, 0, 0, c.low, stages};
+    return Piece{a, b, m * kTile, n * width, columns_of(cols - n * width, width), 0, c.low ? 3 * stages : stages,
+                 tile, -1, 1, 0, 0, c.low, stages};
 }
 
 // Whole columns of tiles, and whether there is a narrow one.
@@ -874,7 +875,8 @@ int64_t place(const std::vector<Group>& shapes, bool precise, char* base, Batch*
     extra->tickets = reinterpret_cast<unsigned int*>(take(kTickets * sizeof(unsigned int)));
     int64_t tiles = 0;  // of the narrow kind, which lists have that are split
     for (int k = 0; k < b->classes; ++k)
-        tiles += (triangle_tiles(b->c[k].side, 128) + (has_narrow(b->c[k].side, 128) ? row_tiles_of(b->c[k].side) : 0)) * (int64_t)b->c[k].count;
+        tiles += (triangle_tiles(b->c[k].side, 128) + (has_narrow(b->c[k].side, 128) ? row_tiles_of(b->c[k].side) : 0)) *
+                 (int64_t)b->c[k].count;
     if (tiles <= kMostPairs / 2)
         extra->part_sums = reinterpret_cast<float*>(take(kMostPairs * kPartFloats * sizeof(float)));
     return at;

@@ -248,6 +248,8 @@ def test_unlikely_targets(dtype):
     n = int(want.on.sum())
     r = mica.mica_linear_cross_entropy(h, w, y)
     close(r.logps, want.logps, 2 * want.err)
+    alone = mica.mica_linear_cross_entropy(h, w, y, grad=False)
+    assert torch.equal(alone.logps, r.logps) and torch.equal(alone.loss, r.loss)
     dh, dh_err, dw, dw_err = want.grads(torch.full((rows,), -1.0 / n, device="cuda"), dtype, once=True)
     rounded(r.dh, dh, dh_err)
     rounded(r.dw, dw, dw_err)
