@@ -82,8 +82,9 @@ def mica_orthogonalize(x, out=None, *, steps: int = 5, coefficients=COEFFICIENTS
     the nearest one with orthogonal rows or columns, in one go for the whole list: the direction of a Muon update.
     ``coefficients``: (a, b, c) of the polynomial a t + b t^3 + c t^5 that each singular value goes through in a step, or
     one such triple for each step. ``precise`` holds what is stored between the products in pairs of float16 (three times
-    the work), as matrices whose smaller side is at most 256 always are. ``out`` takes the results (float16 or bfloat16; it may be ``x`` itself); otherwise
-    they are new matrices of ``out_dtype`` (by default x's, or bfloat16 for float32). Returns the list of results."""
+    the work), as matrices whose smaller side is at most 256 always are. ``out`` takes the results (float16 or bfloat16; it
+    may be ``x`` itself); otherwise they are new matrices of ``out_dtype`` (by default x's, or bfloat16 for float32).
+    Returns the list of results."""
     X = _as_list(x)
     rows, cols, size = _sizes(X, "x", precise)
     ns = _iteration(steps, coefficients, eps, precise)
@@ -121,6 +122,8 @@ def mica_muon_steps(w, g, m, *, lr: float, momentum: float = 0.95, weight_decay:
         raise TypeError(f"m must be float32, not {M.dtype}")
     _same(W, G, "w and g")
     _same(W, M, "w and m")
+    if factor is not None and (factor.dtype != torch.float32 or factor.numel() != 1):
+        raise ValueError("factor must be one float32 on the device")
     if adjust not in _ADJUST:
         raise ValueError(f"adjust {adjust!r} is none of {sorted(_ADJUST)}")
     rows, cols, size = _sizes(W, "w", precise)

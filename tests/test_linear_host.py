@@ -164,7 +164,9 @@ def test_muon_binding_checks():
               lambda: mica.mica_orthogonalize([x], steps=3, coefficients=[(1.0, 0.0, 0.0)] * 2),
               lambda: mica.mica_muon_steps([x], [x.t().contiguous()], [x], lr=0.1),
               lambda: mica.mica_muon_steps([x], [x], [x, x], lr=0.1),
-              lambda: mica.mica_muon_steps([x], [x], [x], lr=0.1, adjust="other")):
+              lambda: mica.mica_muon_steps([x], [x], [x], lr=0.1, adjust="other"),
+              lambda: mica.mica_muon_steps([x], [x], [x], lr=0.1, factor=torch.ones(1).half()),
+              lambda: mica.mica_muon_steps([x], [x], [x], lr=0.1, factor=torch.ones(2))):
         with pytest.raises(ValueError):
             f()
     with pytest.raises(TypeError):
