@@ -13,7 +13,9 @@
 // leaves q_ij = exp(z_ij - z_i,target), which needs no maximum (the sum is at least 1) and has bfloat16's range, and sums it
 // up. The rest is a factor 1 / sum_j q_ij for each row: in dh's epilogue, and on h's rows for dW. The few rows whose sum leaves
 // the range, whose targets are less likely than some e^-44, are taken again, counted from lse. Against taking the product
-// twice: 16 x 256 x 5,000 42 us and 44, 1,024 x 768 x 50,257 176 and 211, 8,192 x 768 x 50,257 1,254 and 1,564.
+// twice: 16 x 256 x 5,000 42 us and 44, 1,024 x 768 x 50,257 176 and 211, 8,192 x 768 x 50,257 1,254 and 1,564. The sum of a
+// row may be 2^80 and its coefficient 2^-100: the coefficient is brought to 2^-1 by a power of two, which the gradients'
+// epilogues take out again.
 //
 // Logits, maxima, sums and gradients' sums are float32. d is rounded to the operands' type because the tensor cores multiply
 // what they are given in 16 bits: relative 2^-9 (bfloat16) or 2^-12 of each of its elements on average. binary16 has not the
@@ -89,7 +91,8 @@ struct Gather {
     float inv_t;
     float ce_factor;       // cross entropy: -grad_scale / T, divided by `denom` or, where that is 0, by the count
     float denom;
-    int scaled;            // d is scaled
+    int scaled;            // d is scaled (bfloat16, the logits taken once: what its rows are multiplied by)
+    int scaled_to;         // and the largest |c| brought to [2^scaled_to, 2^(scaled_to + 1))
     int most, piece;
     Meta* meta;            // written by the first piece
     Dealt* dealt;          // by each
@@ -125,7 +128,7 @@ __device__ __forceinline__ Meta meta_of(const Gather& g, int count, float top) {
     const float largest = g.dlogps ? top * g.inv_t : fabsf(ce);
     if (g.scaled && largest > 0.0f && largest < INFINITY) {
         int e = (int)(__float_as_uint(largest) >> 23) - 127;  // largest < 2^(e + 1); a subnormal counts as 2^-127
-        e = 14 - (e < -100 ? -100 : e);
+        e = g.scaled_to - (e < -100 ? -100 : e > 124 ? 124 : e);
         m.scale = power_of_two(e);
         m.inv_scale = power_of_two(-e);
     }
@@ -744,7 +747,7 @@ struct LogitGrad : Logits {
 // the gradients of the hidden states and of the embedding
 // ------------------------------------------------------------------------------------------------------------------------
 
-// dh = factor * d W, to the rows' places
+// dh = scale * factor * d W, to the rows' places
 template <typename T>
 struct HiddenGrad {
     CUtensorMap d, w;
@@ -781,21 +784,21 @@ struct HiddenGrad {
         return true;
     }
     __device__ __forceinline__ int rows_of(const Deal& r) const { return r.span.rows; }
-    __device__ __forceinline__ float scale_of(const Deal& r, int row) const { return factor ? factor[row] : r.scale; }
+    __device__ __forceinline__ float factor_of(int row) const { return factor ? factor[row] : 1.0f; }
     // four sums of a row
     __device__ __forceinline__ void put(const Deal& r, int row, int col, float4 v) const {
         if (row >= r.span.rows || col >= features) return;
-        const float s = scale_of(r, row);
-        store4<T>(dh + index[r.span.from + row] * ld + col, make_float4(v.x * s, v.y * s, v.z * s, v.w * s), features - col,
-                  wide);
+        const float f = factor_of(row), s = r.scale;  // (one after the other: their product may leave float32's range)
+        store4<T>(dh + index[r.span.from + row] * ld + col,
+                  make_float4(v.x * f * s, v.y * f * s, v.z * f * s, v.w * f * s), features - col, wide);
     }
     // a warp's 32 x 32 of them
     __device__ __forceinline__ void block(const Deal& r, int row0, int col0, const Place& at, float (&v)[32]) const {
         if (row0 >= r.span.rows || col0 >= features) return;
-        const float s = row0 + at.lane < r.span.rows ? scale_of(r, row0 + at.lane) : 0.0f;
+        const float f = row0 + at.lane < r.span.rows ? factor_of(row0 + at.lane) : 0.0f, s = r.scale;
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * s, v[2 * i + 1] * s);
+        for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i] * f * s, v[2 * i + 1] * f * s);
         uint4 x[4];
         by_columns16(at.staging, at.lane, w, x);
         const int row = row0 + at.lane / 4, col = col0 + at.lane % 4 * 8;
@@ -1158,7 +1161,8 @@ cudaError_t gather(const Call& call, const Room& c, int piece) {
     g.inv_t = (float)(1.0 / L.temperature);
     g.ce_factor = (float)(-call.grad_scale / L.temperature);
     g.denom = (float)call.denom;
-    g.scaled = L.dtype == MICA_F16;
+    g.scaled = L.dtype == MICA_F16 || c.once;
+    g.scaled_to = c.once ? -1 : 14;
     g.most = c.most;
     g.piece = piece;
     g.meta = c.meta;

@@ -493,3 +493,25 @@ def test_refusals():
         both = torch.zeros(101, 64, device="cuda")
         mica.mica_linear_logps_grad(h, w, y, lse, c, dw=both[1:], add=both[:-1])
     mica.mica_linear_logps_grad(h, w, y, lse, c, dw=dw, add=dw)
+
+
+@pytest.mark.parametrize("denom,scale", [(1e30, 1.0), (1.0, 1e-30), (1e20, 1e-10), (1e-20, 1.0)])
+def test_small_and_large_coefficients(denom, scale):
+    """A coefficient far from 1 with targets from ordinary to e^-70 likely: what multiplies d's rows, the coefficient over the
+    sum of exp(z - z_target), is smaller than any normal float32, the gradients are not."""
+    rows, features, vocab = 300, 512, 5003
+    h, w, y = make(rows, features, vocab, torch.bfloat16, seed=41, skip=0.1)
+    g = gen(42)
+    far = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    row, at = w[far].float(), w[y.clamp(min=0)].float()
+    size = torch.arange(rows, device="cuda")[:, None] % 4 * 6.0 * (1.0 + torch.rand(rows, 1, generator=g, device="cuda"))
+    push = size * (row / row.square().sum(1, keepdim=True) - at / at.square().sum(1, keepdim=True))
+    h = (h.float() + push).bfloat16()
+    want = Want(h, w, y)
+    assert int(((want.logps < -18) & (want.logps > -44)).sum()) > 50 and float(want.logps.min()) < -50
+    c = torch.full((rows,), -scale / denom, device="cuda")
+    dh, dh_err, dw, dw_err = want.grads(c, torch.bfloat16, once=True)
+    for out in (torch.float32, torch.bfloat16):
+        r = mica.mica_linear_cross_entropy(h, w, y, denom=denom, grad_scale=scale, dw_dtype=out)
+        rounded(r.dh, dh, dh_err)
+        rounded(r.dw, dw, dw_err)
