@@ -71,6 +71,7 @@ struct Dealt {
     SplitDeal dh, dw;   // of pair 0
     int dh_left;        // dh's pieces in their last round
     float inv_scale;    // of d
+    int no_grad;        // every row's coefficient is 0: d is zeros, whatever the logits are
 };
 
 __device__ __forceinline__ int64_t target_at(const void* targets, bool wide, int64_t i) {
@@ -196,6 +197,7 @@ __device__ __forceinline__ void begin_piece(const Gather& g, const Meta& m, cons
                           g.pairs);
         d.dh_left = d.dh.pieces % g.pairs;
         d.inv_scale = m.inv_scale;
+        d.no_grad = !g.dlogps && m.coef == 0.0f;
         *g.dealt = d;
     }
     if (g.again)
@@ -385,10 +387,11 @@ struct Logits {
 
     struct Deal {
         int rows, row_tiles, pieces, next, pairs;
+        bool no_grad;
     };
     __device__ __forceinline__ Deal deal(int pair, int pairs) const {
         const int rows = dealt->span.rows, row_tiles = (rows + kTile - 1) / kTile;
-        return Deal{rows, row_tiles, row_tiles * across, pair, pairs};
+        return Deal{rows, row_tiles, row_tiles * across, pair, pairs, dealt->no_grad != 0};
     }
     // rows first: h stays in L2 while W passes once
     __device__ __forceinline__ bool piece(Deal& d, Piece* q) const {
@@ -474,7 +477,7 @@ struct LogitOnce : Logits {
     struct Epilogue {
         const LogitOnce& p;
         int row, column, target, lane, stored;
-        bool live;
+        bool live, kept;
         float c, at_target;
         RowSum s;
         unsigned char* staging;
@@ -482,6 +485,7 @@ struct LogitOnce : Logits {
         __device__ __forceinline__ Epilogue(const LogitOnce& p, const Deal& d, const Piece& q, const Place& at)
             : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), lane(at.lane), staging(at.staging) {
             live = row < d.rows;
+            kept = live && !d.no_grad;
             target = live ? p.target[row] : -1;
             c = live ? p.origin[row] : INFINITY;
             at_target = live && p.again ? p.at[row] : 0.0f;
@@ -514,7 +518,7 @@ struct LogitOnce : Logits {
                     if (target == first + i) q0 = at_target;
                     if (target == first + i + 1) q1 = at_target;
                 }
-                w[i / 2] = live ? pack2<T>(q0, q1) : 0u;  // (whatever z was)
+                w[i / 2] = kept ? pack2<T>(q0, q1) : 0u;  // (whatever z was)
             }
             const float sum = (part[0] + part[1]) + (part[2] + part[3]);
             if (!live) {
@@ -625,6 +629,7 @@ __device__ __forceinline__ float join_once(const Join& j, const Meta& m, RowSum 
         }
     }
     if (!j.d) return logp;
+    if (k == 0.0f) factor = at = 0.0f;
     const int y = j.target[row];
     if (lane == 0) {
         j.factor[row] = factor;
@@ -717,7 +722,7 @@ struct LogitGrad : Logits {
         unsigned short* to;
         __device__ __forceinline__ Epilogue(const LogitGrad& p, const Deal& d, const Piece& q, const Place& at)
             : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), lane(at.lane), staging(at.staging) {
-            live = row < d.rows;
+            live = row < d.rows && !d.no_grad;
             target = live ? p.target[row] : -1;
             c = live ? p.coef[row] : 0.0f;
             origin = live ? p.origin[row] : 0.0f;

@@ -279,7 +279,7 @@ MICA_API int64_t mica_linear_grad_workspace(const mica_linear* l, const mica_lin
 
 typedef struct {
     double denom;      /* >= 0, finite: what the sum over rows is divided by; 0: the number of rows that count */
-    double grad_scale; /* finite */
+    double grad_scale; /* finite; 0: every row's coefficient is 0, its logits' gradient zeros whatever its target is */
 } mica_cross_entropy_hp;
 
 /*

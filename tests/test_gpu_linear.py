@@ -515,3 +515,21 @@ def test_small_and_large_coefficients(denom, scale):
         r = mica.mica_linear_cross_entropy(h, w, y, denom=denom, grad_scale=scale, dw_dtype=out)
         rounded(r.dh, dh, dh_err)
         rounded(r.dw, dw, dw_err)
+
+
+@pytest.mark.parametrize("vocab", [300, 70001])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_no_coefficient(dtype, vocab):
+    """With a gradient scale of 0 every row's coefficient is 0: zeros, whatever the targets are, and the loss as ever."""
+    rows = 300
+    h, w, y = make(rows, 512, vocab, dtype, seed=43, skip=0.2)
+    row, at = w[torch.arange(rows, device="cuda") % vocab].float(), w[y.clamp(min=0)].float()
+    push = 100.0 * (row / row.square().sum(1, keepdim=True) - at / at.square().sum(1, keepdim=True))
+    h[40:60] = (h.float() + push).to(dtype)[40:60]  # targets less likely than e^-100
+    add = torch.randn(vocab, 512, generator=gen(44), device="cuda")
+    r = mica.mica_linear_cross_entropy(h, w, y, grad_scale=0.0, add=add)
+    assert not r.dh.any() and torch.equal(r.dw, add) and r.loss.isfinite()
+    y[7], y[11] = vocab, 1 << 40
+    r = mica.mica_linear_cross_entropy(h, w, y, grad_scale=0.0, add=add)
+    assert r.logps[7].isnan() and r.logps[11].isnan() and r.loss.isnan()
+    assert not r.dh.any() and torch.equal(r.dw, add)
