@@ -122,11 +122,18 @@ __device__ __forceinline__ bool row_counts(const Gather& g, int i, float* c) {
     return *c != 0.0f;
 }
 
-// What the first look at the targets leaves: how many rows count, and the largest of their |dlogps|.
+// Of a row's coefficient, what the scale of d goes by: nothing where it is an infinity or a NaN, which shows in its row's d
+// under any scale and must not take the other rows' bits.
+__device__ __forceinline__ float size_of(const Gather& g, float c) {
+    const float size = fabsf(c * g.inv_t);
+    return size < INFINITY ? size : 0.0f;
+}
+
+// What the first look at the targets leaves: how many rows count, and the largest of their coefficients' sizes.
 __device__ __forceinline__ Meta meta_of(const Gather& g, int count, float top) {
     Meta m{count, 0.0f, 1.0f, 1.0f, 0u};
     const float ce = g.ce_factor / (g.denom > 0.0f ? g.denom : (float)count);
-    const float largest = g.dlogps ? top * g.inv_t : fabsf(ce);
+    const float largest = g.dlogps ? top : fabsf(ce);
     if (g.scaled && largest > 0.0f && largest < INFINITY) {
         int e = (int)(__float_as_uint(largest) >> 23) - 127;  // largest < 2^(e + 1); a subnormal counts as 2^-127
         e = g.scaled_to - (e < -100 ? -100 : e > 124 ? 124 : e);
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Gather g) {
             float c;
             if (first + k >= g.rows || !row_counts(g, first + k, &c)) continue;
             on |= 1u << k;
-            if (fabsf(c) > top || c != c) top = fabsf(c);  // (a NaN stays: nothing is larger)
+            top = fmaxf(top, size_of(g, c));
         }
         const int mine = __popc(on);
         int upto = mine;
@@ -252,15 +259,11 @@ __global__ void __launch_bounds__(1024) scan_kernel(Gather g) {
         before += all;
     }
 #pragma unroll
-    for (int d = 16; d; d /= 2) {
-        const float v = __shfl_xor_sync(~0u, top, d);
-        if (v > top || v != v) top = v;
-    }
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     if (lane == 0) tops[warp] = top;
     __syncthreads();
     if (threadIdx.x) return;
-    for (int i = 0; i < 32; ++i)
-        if (tops[i] > top || tops[i] != tops[i]) top = tops[i];
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, tops[i]);
     *g.meta = meta_of(g, before, top);
 }
 
@@ -308,15 +311,14 @@ __global__ void __launch_bounds__(256) look_kernel(Gather g) {
             if (!scored[k] || c[k] == 0.0f) continue;
             ++count;
             before += i0 + 256 * k < from;
-            if (fabsf(c[k]) > top || c[k] != c[k]) top = fabsf(c[k]);
+            top = fmaxf(top, size_of(g, c[k]));
         }
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         before += __shfl_xor_sync(~0u, before, d);
         count += __shfl_xor_sync(~0u, count, d);
-        const float v = __shfl_xor_sync(~0u, top, d);
-        if (v > top || v != v) top = v;
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     }
     if (lane == 0) {
         sums[0][warp] = before;
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(256) look_kernel(Gather g) {
     for (int i = 0; i < 8; ++i) {
         before += sums[0][i];
         count += sums[1][i];
-        if (tops[i] > top || tops[i] != tops[i]) top = tops[i];
+        top = fmaxf(top, tops[i]);
     }
     const Meta m = meta_of(g, count, top);
     const Span span = span_of(count, g.most, g.piece);

@@ -533,3 +533,23 @@ def test_no_coefficient(dtype, vocab):
     r = mica.mica_linear_cross_entropy(h, w, y, grad_scale=0.0, add=add)
     assert r.logps[7].isnan() and r.logps[11].isnan() and r.loss.isnan()
     assert not r.dh.any() and torch.equal(r.dw, add)
+
+
+@pytest.mark.parametrize("rows", [300, 1500])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan, 3e38])
+def test_one_coefficient_that_is_no_number(bad, rows):
+    """An infinity or a NaN among small coefficients: its row's gradient and dw show it, the other rows' have the bits that they
+    have without it. 3e38 leaves float32 when it is divided by the temperature."""
+    h, w, y = make(rows, 200, 900, torch.float16, seed=45, skip=0.2)
+    y[3] = 5
+    lp, lse = mica.mica_linear_logps(h, w, y, temperature=0.5, lse=True)
+    c = 1e-7 * torch.randn(rows, generator=gen(46), device="cuda")
+    c[3] = 1e-9
+    dh, _ = mica.mica_linear_logps_grad(h, w, y, lse, c, temperature=0.5, dw_dtype=torch.float32)
+    exact = Want(h, w, y, 0.5).grads(c, torch.float16)
+    rounded(dh, exact[0], exact[1])
+    c[3] = bad
+    got, dw = mica.mica_linear_logps_grad(h, w, y, lse, c, temperature=0.5, dw_dtype=torch.float32)
+    assert not got[3].isfinite().any() and not dw.isfinite().all()
+    rest = torch.arange(rows, device="cuda") != 3
+    assert torch.equal(got[rest], dh[rest])
