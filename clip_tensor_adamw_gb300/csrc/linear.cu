@@ -372,6 +372,8 @@ __global__ void __launch_bounds__(256) look_kernel(Gather g) {
 struct RowSum {
     float origin, sum;
 };
+// The origin of a part without a logit so far: finite, so that minus infinity counts from it as 0.
+constexpr float kLeastOrigin = -1e38f;
 
 struct Logits {
     static constexpr unsigned int kStatus = 0x100u;
@@ -417,7 +419,7 @@ struct LogitSums : Logits {
         bool live;
         RowSum s;
         __device__ __forceinline__ Epilogue(const LogitSums& p, const Deal& d, const Piece& q, const Place& at)
-            : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), s{-1e38f, 0.0f} {
+            : p(p), row(q.m0 + at.row), column(q.n0 + at.first_column), s{kLeastOrigin, 0.0f} {
             live = row < d.rows;
             target = live ? p.target[row] : -1;
         }
@@ -490,6 +492,7 @@ struct LogitOnce : Logits {
             kept = live && !d.no_grad;
             target = live ? p.target[row] : -1;
             c = live ? p.origin[row] : INFINITY;
+            if (c < kLeastOrigin) c = kLeastOrigin;  // a banned target, whose origin no banned token may be counted from
             at_target = live && p.again ? p.at[row] : 0.0f;
             s = RowSum{c, 0.0f};
             stored = (d.rows + 63) / 64 * 64 - (row - lane);  // rows of the warp's 32 that the weight gradient reads
@@ -597,7 +600,7 @@ __device__ __forceinline__ RowSum operator+(RowSum x, RowSum y) {
 
 // A row's sum, by a warp, in a fixed order.
 __device__ __forceinline__ RowSum row_sum(const Join& j, int row, int lane) {
-    RowSum s{-1e38f, 0.0f};
+    RowSum s{kLeastOrigin, 0.0f};
     const RowSum* own = j.sums + (int64_t)row * j.parts;
 #pragma unroll 4
     for (int k = lane; k < j.parts; k += 32) s = s + own[k];

@@ -553,3 +553,48 @@ def test_one_coefficient_that_is_no_number(bad, rows):
     assert not got[3].isfinite().any() and not dw.isfinite().all()
     rest = torch.arange(rows, device="cuda") != 3
     assert torch.equal(got[rest], dh[rest])
+
+
+@pytest.mark.parametrize("vocab", [129, 200, 257, 70017])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_banned_target(dtype, vocab):
+    """A token whose embedding makes every logit minus infinity, the last of the vocabulary, as a target and not: a
+    log-probability of minus infinity, and the gradients of a probability of 0."""
+    rows, features = 70, 72
+    h, w, y = make(rows, features, vocab, dtype, seed=vocab, skip=0.2)
+    h[:, 0] = h[:, 0].abs() + 1.0
+    y[y == vocab - 1] = 0
+    y[5], y[64] = vocab - 1, vocab - 1
+    w[-1, 0] = -2000.0
+    want = Want(h, w, y)  # (a probability of exp(-2000): 0 in float64 too)
+    want.err = Want(h, w[:-1], y.clamp(max=vocab - 2)).err
+    w[-1, 0] = -math.inf
+    last = y == vocab - 1
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    close(lse, torch.where(want.on, want.lse, 0.0), want.err + U * want.lse.abs())
+    n = int(want.on.sum())
+    r = mica.mica_linear_cross_entropy(h, w, y, dw_dtype=torch.float32)
+    for got in (lp, r.logps):
+        assert (got[last] == -math.inf).all()
+        close(got[~last], want.logps[~last], 2 * want.err[~last])
+    assert float(r.loss) == math.inf
+    c = torch.full((rows,), -1.0 / n, device="cuda")
+    dh, dh_err, dw, dw_err = want.grads(c, dtype, once=True)
+    two = mica.mica_linear_logps_grad(h, w, y, want.lse.float(), c, dw_dtype=torch.float32)
+    for got_h, got_w in (r[2:], two):
+        rounded(got_h[:, 1:], dh[:, 1:], dh_err[:, 1:])  # (the first feature's is 0 times an infinity)
+        rounded(got_w, dw, dw_err)
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_only_banned_tokens(dtype):
+    """A row with nothing but minus infinities gives NaN, as 0 / 0 does; the others are as they were."""
+    h, w, y = make(40, 64, 100, dtype, seed=47, skip=0.0)
+    h[:, 0], w[:, 0] = 0.0, -1.0
+    lp = mica.mica_linear_logps(h, w, y)
+    h[3, 0] = math.inf
+    got, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    r = mica.mica_linear_cross_entropy(h, w, y)
+    assert got[3].isnan() and lse[3] == -math.inf and r.logps[3].isnan() and r.dh[3].isnan().all()
+    rest = torch.arange(40, device="cuda") != 3
+    assert torch.equal(got[rest], lp[rest]) and r.dh[rest].isfinite().all()
