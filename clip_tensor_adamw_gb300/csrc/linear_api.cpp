@@ -29,7 +29,8 @@ mica_status check_linear(const mica_linear* l, Linear* L) {
 
 mica_status check_grads(const mica_linear* l, const mica_linear_grads* g, LinearGrad* G) {
     *G = LinearGrad{g->dh, g->ld_dh, g->dw, g->ld_dw, g->dw_dtype, g->add, g->ld_add};
-    if (!g->dh && !g->dw) return fail(MICA_ERR_NULL, "neither dh nor dw is given");
+    // (without rows dh has no elements, and may be NULL for that)
+    if (!g->dh && !g->dw && l->rows > 0) return fail(MICA_ERR_NULL, "neither dh nor dw is given");
     if (g->dh) MICA_TRY(check_stride(g->ld_dh, l->features, l->rows, l->features, "dh"));
     if (!g->dw) {
         if (g->add) return fail(MICA_ERR_NULL, "add is given without dw");
@@ -95,7 +96,8 @@ extern "C" int64_t mica_linear_grad_workspace(const mica_linear* l, const mica_l
     Linear L;
     LinearGrad G;
     int dev = 0;
-    if (check_linear(l, &L) != MICA_OK || !g || check_grads(l, g, &G) != MICA_OK || current_device(&dev) != MICA_OK) return 0;
+    if (check_linear(l, &L) != MICA_OK || !g || check_grads(l, g, &G) != MICA_OK || (!G.dh && !G.dw)) return 0;
+    if (current_device(&dev) != MICA_OK) return 0;
     return linear_grad_workspace(L, G, sm_count(dev));
 }
 
@@ -107,6 +109,7 @@ extern "C" mica_status mica_linear_logps_grad(const mica_linear* l, const float*
     MICA_TRY(check_linear(l, &L));
     if (!g) return fail(MICA_ERR_NULL, "the gradients are NULL");
     MICA_TRY(check_grads(l, g, &G));
+    if (!G.dh && !G.dw) return ok();
     int dev = 0;
     MICA_TRY(current_device(&dev));
     const int sms = sm_count(dev);

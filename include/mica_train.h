@@ -249,8 +249,9 @@ MICA_API mica_status mica_linear_logps(const mica_linear* l, float* logps, float
 MICA_API int64_t mica_linear_logps_workspace(const mica_linear* l);
 
 /*
- * Where the gradients go: dh (rows x features, of h's type) and dw (vocab x features, MICA_F32, MICA_F16 or MICA_BF16), each
- * or neither NULL; dw = add + the gradient, where add is of dw's type, NULL for zeros, or dw itself (accumulation in place).
+ * Where the gradients go: dh (rows x features, of h's type) and dw (vocab x features, MICA_F32, MICA_F16 or MICA_BF16), one
+ * or both (without rows dh may be NULL too); dw = add + the gradient, where add is of dw's type, NULL for zeros, or dw itself
+ * (accumulation in place).
  * The gradient of the logits is rounded to h's type (scaled, in binary16, so that its largest row uses the whole range), as
  * the tensor cores take it: so dh and dw are off by some 2^-9 (bfloat16) or 2^-12 (binary16) of their norm, whatever dw's
  * type; sums are float32 and rounded once.

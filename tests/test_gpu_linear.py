@@ -598,3 +598,16 @@ def test_only_banned_tokens(dtype):
     assert got[3].isnan() and lse[3] == -math.inf and r.logps[3].isnan() and r.dh[3].isnan().all()
     rest = torch.arange(40, device="cuda") != 3
     assert torch.equal(got[rest], lp[rest]) and r.dh[rest].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_one_gradient_of_no_rows(dtype):
+    """Without rows there is nothing in dh, whose pointer is null, and the call is none the worse for it."""
+    h, w = torch.empty(0, 72, dtype=dtype, device="cuda"), torch.ones(300, 72, dtype=dtype, device="cuda")
+    y, none = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    r = mica.mica_linear_cross_entropy(h, w, y, want_dw=False)
+    assert float(r.loss) == 0.0 and r.dh.shape == (0, 72) and r.dw is None
+    dh, dw = mica.mica_linear_logps_grad(h, w, y, none, none, want_dw=False)
+    assert dh.shape == (0, 72) and dw is None
+    r = mica.mica_linear_cross_entropy(h, w, y, want_dh=False)
+    assert r.dh is None and not r.dw.any()

@@ -175,3 +175,13 @@ def test_muon_binding_checks():
         mica.mica_muon_steps([x.half()], [x], [x], lr=0.1)
     with pytest.raises(TypeError):
         mica.mica_muon_steps([x], [x], [x.half()], lr=0.1)
+
+
+def test_no_rows_and_no_gradients():
+    """Without rows dh has no elements and its pointer may be null; with rows a gradient has to go somewhere."""
+    L = train._train()
+    none = grads(dh=None, dw=None)
+    assert L.mica_linear_logps_grad(linear(rows=0), None, None, none, None, 0, None) == OK
+    assert L.mica_linear_grad_workspace(linear(rows=0), none) == 0
+    assert L.mica_linear_logps_grad(linear(rows=0), None, None, grads(dh=None, dw=None, add=0x8000), None, 0, None) == NULL
+    assert L.mica_linear_cross_entropy(linear(), hp(), 0x6000, 0x6100, none, 0x7000, 1 << 40, None) == NULL
