@@ -403,6 +403,13 @@ def _linear(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, temperature
                    targets.element_size())
 
 
+def _wanted(want_dh: bool, want_dw: bool, dh, dw, add) -> None:
+    """A buffer of a gradient that is not wanted would keep what it holds, unnoticed: refused."""
+    for name, given, wanted, of in (("dh", dh, want_dh, "dh"), ("dw", dw, want_dw, "dw"), ("add", add, want_dw, "dw")):
+        if given is not None and not wanted:
+            raise ValueError(f"{name} is given, but {of} is not wanted")
+
+
 def _linear_grads(h: torch.Tensor, w: torch.Tensor, want_dh: bool, want_dw: bool, dh: torch.Tensor | None,
                   dw: torch.Tensor | None, add: torch.Tensor | None, dw_dtype: torch.dtype | None):
     """(dh, dw, the call's argument, or None where no gradient is wanted)"""
@@ -415,10 +422,6 @@ def _linear_grads(h: torch.Tensor, w: torch.Tensor, want_dh: bool, want_dw: bool
         if add is not None and (add.shape != w.shape or add.dtype != dw_dtype):
             raise ValueError(f"add must be {dw_dtype} of shape {tuple(w.shape)}, not {add.dtype} of {tuple(add.shape)}")
         dw = _output(dw, tuple(w.shape), dw_dtype, "dw", w)
-    elif add is not None:
-        raise ValueError("add is given without dw")
-    else:
-        dw = None
     g = _LinearGrads(None if dh is None else dh.data_ptr(), None if dw is None else dw.data_ptr(),
                      None if add is None else add.data_ptr(), 0 if dh is None else _matrix(dh, "dh"),
                      0 if dw is None else _matrix(dw, "dw"), 0 if add is None else _matrix(add, "add"),
@@ -450,7 +453,8 @@ def mica_linear_logps_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tens
     """The gradients ``(dh, dw)`` of hidden states and embedding given that of mica_linear_logps's result, for any loss
     over log-probabilities. ``dh`` has h's dtype, ``dw`` ``dw_dtype`` (by default that of ``dw``, then of ``add``, then
     of w); ``dw`` is ``add`` plus the gradient, and ``add`` may be ``dw`` itself. ``want_dh`` and ``want_dw`` leave one
-    out (None)."""
+    out (None), whose buffers must then not be given."""
+    _wanted(want_dh, want_dw, dh, dw, add)
     l = _linear(h, w, targets, temperature)
     z, d = _vector(lse, l.rows, "lse"), _vector(dlogps, l.rows, "dlogps")
     L = _train()
@@ -472,6 +476,7 @@ def mica_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.T
     """Softmax cross entropy of ``targets`` under ``h @ w.T / temperature``, summed over the scored rows and divided by
     ``denom`` (None: their number), and the gradients of ``grad_scale`` times it, without keeping the logits. Arguments
     as mica_linear_logps and mica_linear_logps_grad; ``grad=False`` leaves both gradients out."""
+    _wanted(grad and want_dh, grad and want_dw, dh, dw, add)
     l = _linear(h, w, targets, temperature)
     if denom is not None and not denom > 0.0:
         raise ValueError(f"denom must be > 0, not {denom}")

@@ -185,3 +185,16 @@ def test_no_rows_and_no_gradients():
     assert L.mica_linear_grad_workspace(linear(rows=0), none) == 0
     assert L.mica_linear_logps_grad(linear(rows=0), None, None, grads(dh=None, dw=None, add=0x8000), None, 0, None) == NULL
     assert L.mica_linear_cross_entropy(linear(), hp(), 0x6000, 0x6100, none, 0x7000, 1 << 40, None) == NULL
+
+
+def test_dropped_arguments():
+    """What cannot be filled is refused, not dropped: a gradient's buffer, or what is added to it, where none is wanted."""
+    h, w, y = torch.zeros(4, 64).bfloat16(), torch.zeros(100, 64).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    z, dw, dh = torch.zeros(4), torch.zeros(100, 64), torch.zeros(4, 64).bfloat16()
+    for kw in (dict(grad=False, dw=dw), dict(grad=False, add=dw), dict(grad=False, dh=dh), dict(want_dw=False, dw=dw),
+               dict(want_dw=False, add=dw), dict(want_dh=False, dh=dh), dict(want_dh=False, want_dw=False, dw=dw)):
+        with pytest.raises(ValueError, match="given"):
+            mica.mica_linear_cross_entropy(h, w, y, **kw)
+        if "grad" not in kw:
+            with pytest.raises(ValueError, match="given"):
+                mica.mica_linear_logps_grad(h, w, y, z, z, **kw)
