@@ -86,6 +86,10 @@ def mica_orthogonalize(x, out=None, *, steps: int = 5, coefficients=COEFFICIENTS
     may be ``x`` itself); otherwise they are new matrices of ``out_dtype`` (by default x's, or bfloat16 for float32).
     Returns the list of results."""
     X = _as_list(x)
+    if out is not None:
+        out = _as_list(out)
+        if out_dtype is not None and out.T and out.dtype != out_dtype:
+            raise TypeError(f"out_dtype is {out_dtype}, but out is {out.dtype}")
     rows, cols, size = _sizes(X, "x", precise)
     ns = _iteration(steps, coefficients, eps, precise)
     code = _TYPES.get(X.dtype, 0 if X.dtype is None else None)

@@ -198,3 +198,10 @@ def test_dropped_arguments():
         if "grad" not in kw:
             with pytest.raises(ValueError, match="given"):
                 mica.mica_linear_logps_grad(h, w, y, z, z, **kw)
+
+
+def test_output_of_another_type():
+    """out_dtype beside out has to be out's."""
+    x = torch.zeros(4, 5)
+    with pytest.raises(TypeError, match="out_dtype"):
+        mica.mica_orthogonalize([x], [x.half()], out_dtype=torch.bfloat16)
