@@ -24,6 +24,32 @@ mica_status check_sizes(const int64_t* rows, const int64_t* cols, int32_t T) {
     return MICA_OK;
 }
 
+// The largest that |q(u)| and sqrt(u) |q(u)|, q = a + b u + c u^2, come to over u in [0, top^2]: at an end, or where the
+// derivative is 0, b + 2 c u = 0 for the one and a + 3 b u + 5 c u^2 = 0 for the other.
+struct Peaks {
+    double factor = 0.0, value = 0.0;
+};
+Peaks peaks_of(const double* coefficients, double top) {
+    const double a = coefficients[0], b = coefficients[1], c = coefficients[2], end = top * top;
+    Peaks p;
+    const auto at = [&](double u) {
+        if (!(u >= 0.0 && u <= end)) return;  // (or no number: the derivative has no such root)
+        const double q = std::fabs(a + u * (b + u * c));
+        p.factor = std::max(p.factor, q);
+        p.value = std::max(p.value, std::sqrt(u) * q);
+    };
+    at(0.0);
+    at(end);
+    at(-b / (2.0 * c));
+    const double square = 9.0 * b * b - 20.0 * a * c;
+    if (square >= 0.0) {
+        const double w = -0.5 * (3.0 * b + std::copysign(std::sqrt(square), b));
+        at(w / (5.0 * c));
+        at(a / w);
+    }
+    return p;
+}
+
 // Follows the largest singular value that each step can leave: what the products hold in binary16 (x, x x^T and the
 // polynomial of it, 2^10 times) must stay within its range.
 mica_status check_iteration(const mica_newton_schulz* ns) {
@@ -33,23 +59,18 @@ mica_status check_iteration(const mica_newton_schulz* ns) {
     if (ns->steps < 1 || ns->steps > MICA_MAX_NS_STEPS)
         return fail(MICA_ERR_HYPER, "steps = %d is outside [1, %d]", ns->steps, MICA_MAX_NS_STEPS);
     if (!ns->coefficients) return fail(MICA_ERR_NULL, "coefficients is NULL");
-    constexpr double kMost = 32.0;
-    constexpr int kSamples = 4096;
+    constexpr double kMost = 32.0, kMostCoefficient = 1e30;
     double top = 1.0;
     for (int s = 0; s < ns->steps; ++s) {
-        const double *c = ns->coefficients + 3 * s, a = c[0], b = c[1], d = c[2];
-        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(d))
-            return fail(MICA_ERR_HYPER, "step %d's coefficients are not finite", s);
-        double next = 0.0, poly = 0.0;
-        for (int i = 0; i <= kSamples; ++i) {
-            const double t = top * i / kSamples, q = std::fabs(a + t * t * (b + t * t * d));
-            poly = std::max(poly, q);
-            next = std::max(next, t * q);
-        }
-        if (!(poly <= kMost && next <= kMost && next * next <= kMost))
+        const double* c = ns->coefficients + 3 * s;
+        for (int i = 0; i < 3; ++i)
+            if (!(std::fabs(c[i]) <= kMostCoefficient))
+                return fail(MICA_ERR_HYPER, "step %d's coefficient %g is not within 1e30", s, c[i]);
+        const Peaks p = peaks_of(c, top);
+        if (!(p.factor <= kMost && p.value * p.value <= kMost))
             return fail(MICA_ERR_HYPER, "step %d's polynomial reaches %g: it must stay below %g", s,
-                        std::max(poly, next * next), kMost);
-        top = next;
+                        std::max(p.factor, p.value * p.value), kMost);
+        top = p.value;
     }
     return MICA_OK;
 }

@@ -30,8 +30,8 @@ extern "C" {
  * The iteration: x = u / (|u| + eps), |u| the Frobenius norm; then, `steps` times, with G the smaller of x x^T and x^T x,
  *   x = a x + (b G + c G^2) x     (G on the side that it fits)
  * where step s takes (a, b, c) = coefficients[3 s .. 3 s + 2]. So each singular value t of x becomes a t + b t^3 + c t^5, and
- * the singular vectors stay. The polynomials' values, and those of a + b t^2 + c t^4, must stay below 32 in size for all
- * singular values that can occur (MICA_ERR_HYPER otherwise).
+ * the singular vectors stay. For all singular values that can occur, |u| being 1 at first, the polynomials'
+ * values must be at most sqrt(32) in size, and those of a + b t^2 + c t^4 at most 32 (MICA_ERR_HYPER otherwise).
  * x, G and the polynomial of G are held in binary16 between the products (scaled by 2^10; products are exact and summed in
  * float32), which takes a result some 2^-9 to 2^-10 of its norm off; directions whose singular values in u are a thousand
  * times below the largest get correspondingly less accurate. With MICA_NS_PRECISE, and always for matrices whose smaller side
@@ -40,7 +40,7 @@ extern "C" {
  */
 #define MICA_NS_PRECISE 1u
 typedef struct {
-    const double* coefficients; /* host, 3 * steps, finite */
+    const double* coefficients; /* host, 3 * steps, at most 1e30 in size */
     double eps;                 /* [1e-30, 1] */
     int32_t steps;              /* [1, MICA_MAX_NS_STEPS] */
     uint32_t flags;             /* MICA_NS_PRECISE or 0 */

@@ -2,6 +2,7 @@
 anything reaches a device, with the documented status; workspace sizes; and the binding's own checks."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -205,3 +206,38 @@ def test_output_of_another_type():
     x = torch.zeros(4, 5)
     with pytest.raises(TypeError, match="out_dtype"):
         mica.mica_orthogonalize([x], [x.half()], out_dtype=torch.bfloat16)
+
+
+def test_polynomials_are_bounded_between_samples_too():
+    """The second step's factor 32 + e - c (t^2 - u)^2 passes 32 at t^2 = u alone, by less than its curvature takes off within a
+    four-thousandth of the range of t; and one that touches 32 from below is taken (and fails for want of a device)."""
+    u, c = (0.1 * 2048.5 / 4096) ** 2, 1e6
+
+    def rows(e):
+        return (0.1, 0.0, 0.0, 32.0 + e - c * u * u, 2.0 * c * u, -c)
+
+    assert orthogonalize(ns=iteration(rows(7e-7), steps=2)) == HYPER
+    assert orthogonalize(ns=iteration(rows(-7e-7), steps=2)) not in (OK, HYPER)
+    # t (a + b t^2 + c t^4) at its own peak, where neither end nor the factor's peak is: 1.5 t - 0.5 t^3 ... scaled to pass sqrt(32)
+    top = 32.0 ** 0.5
+    for scale, want in ((1.0 + 1e-9, True), (1.0 - 1e-9, False)):
+        a = top * scale * 1.5 * 3.0 ** 0.5  # a t (1 - t^2) peaks at t = 3^-1/2 with a 2 / (3 3^1/2) a
+        got = orthogonalize(ns=iteration((a, -a, 0.0), steps=1))
+        assert (got == HYPER) == want
+    # a step after one that leaves nothing takes whatever is finite
+    assert orthogonalize(ns=iteration((0.0, 0.0, 0.0, 1.0, -0.5, 0.0), steps=2)) not in (OK, HYPER)
+    # what float32 does not hold is refused, also where it would be multiplied by 0
+    assert orthogonalize(ns=iteration((0.0, 0.0, 0.0, 1.0, 1e39, 0.0), steps=2)) == HYPER
+
+
+def test_polynomials_at_their_limits():
+    """Random polynomials scaled to where they reach the limits, by 20,001 samples (off by less than 1e-5 of the peak)."""
+    r = random.Random(5)
+    for _ in range(60):
+        a, b, c = (r.uniform(-1, 1) * 4.0 ** r.uniform(-1, 2) for _ in range(3))
+        t = [i / 20000 for i in range(20001)]
+        q = [abs(a + x * x * (b + x * x * c)) for x in t]
+        s = min(32.0 / max(q), 32.0 ** 0.5 / max(x * y for x, y in zip(t, q)))
+        for e, refused in ((1e-4, True), (-1e-4, False)):
+            got = orthogonalize(ns=iteration([v * s * (1 + e) for v in (a, b, c)], steps=1))
+            assert (got == HYPER) == refused, (a, b, c, e)
