@@ -771,7 +771,31 @@ int parts_of(int stages, int columns) {
     const int chunks = (columns + 63) / 64, parts = (int)std::sqrt(stages / (2.0 * chunks));
     return parts > 1 && 0.25 * stages > 0.25 * stages / parts + 0.5 * parts * chunks + 2.0 ? parts : 1;
 }
-// tiles(class, narrow, width, &columns): a matrix's whole or narrow tiles. Returns how long the product takes.
+// The parts of each class's Gram sums, in tiles of 128 columns. Returns the pieces of all classes together where any is split,
+// and 0 where none is.
+int split_gram(const Batch& b, int pairs, int* parts) {
+    int64_t tiles[kMostClasses], all = 0;
+    std::fill(parts, parts + kMostClasses, 1);
+    for (int k = 0; k < b.classes; ++k) {
+        const Class& c = b.c[k];
+        tiles[k] = (triangle_tiles(c.side, 128) + (has_narrow(c.side, 128) ? row_tiles_of(c.side) : 0)) * (int64_t)c.count;
+        all += tiles[k];
+    }
+    if (all > pairs / 2) return 0;
+    all = 0;
+    bool any = false;
+    for (int k = 0; k < b.classes; ++k) {
+        const Class& c = b.c[k];
+        parts[k] = parts_of((std::max(c.rows, c.cols) + kDepth - 1) / kDepth * (c.low ? 3 : 1), std::min(c.side, 128));
+        all += parts[k] * tiles[k];
+        any = any || parts[k] > 1;
+    }
+    if (any && all <= pairs) return (int)all;
+    std::fill(parts, parts + kMostClasses, 1);
+    return 0;
+}
+// tiles(class, narrow, width, &columns): a matrix's whole or narrow tiles; split: the product is Gram's, whose sums may be split.
+// Returns how long the product takes.
 template <typename Tiles, typename Depth>
 int64_t schedule(const Batch& b, int sms, int width, bool split, Tiles tiles, Depth depth, Schedule* s) {
     std::vector<Work> work;
@@ -786,15 +810,7 @@ int64_t schedule(const Batch& b, int sms, int width, bool split, Tiles tiles, De
         s->parts[g / 2] = 1;
         slots += n[g];
     }
-    if (split && width == 128 && slots <= pairs / 2) {
-        int all = 0;
-        for (int k = 0; k < b.classes; ++k) {
-            const Class& c = b.c[k];
-            s->parts[k] = parts_of((depth(c) + kDepth - 1) / kDepth * (c.low ? 3 : 1), std::min(c.side, 128));
-            all += s->parts[k] * (n[2 * k] + n[2 * k + 1]);
-        }
-        if (all > pairs) std::fill(s->parts, s->parts + kMostClasses, 1);
-    }
+    if (split && width == 128) split_gram(b, pairs, s->parts);
     s->pieces = 0;
     for (int g = 0; g < 2 * b.classes; ++g) {
         const Class& c = b.c[g / 2];
@@ -839,7 +855,7 @@ constexpr int kTickets = kMostPairs / 2 * 2 * kTakers;  // of all tiles of a lis
 struct Extra {
     double* squares;
     unsigned int* tickets;
-    float* part_sums;  // of at most as many parts as there are pairs
+    float* part_sums;  // where sums are split, of at most as many parts as there are pairs
 };
 
 // Fills a batch, with places in the workspace (null: sizes only); the bytes it takes.
@@ -873,12 +889,9 @@ int64_t place(const std::vector<Group>& shapes, bool precise, char* base, Batch*
     }
     extra->squares = reinterpret_cast<double*>(take((int64_t)b->items * sizeof(double)));
     extra->tickets = reinterpret_cast<unsigned int*>(take(kTickets * sizeof(unsigned int)));
-    int64_t tiles = 0;  // of the narrow kind, which lists have that are split
-    for (int k = 0; k < b->classes; ++k)
-        tiles += (triangle_tiles(b->c[k].side, 128) + (has_narrow(b->c[k].side, 128) ? row_tiles_of(b->c[k].side) : 0)) *
-                 (int64_t)b->c[k].count;
-    if (tiles <= kMostPairs / 2)
-        extra->part_sums = reinterpret_cast<float*>(take(kMostPairs * kPartFloats * sizeof(float)));
+    int parts[kMostClasses];
+    const int64_t pieces = split_gram(*b, kMostPairs, parts);  // (no fewer than where there are fewer pairs)
+    extra->part_sums = reinterpret_cast<float*>(take(pieces * kPartFloats * sizeof(float)));
     return at;
 }
 

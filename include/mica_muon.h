@@ -46,9 +46,10 @@ typedef struct {
     uint32_t flags;             /* MICA_NS_PRECISE or 0 */
 } mica_newton_schulz;
 
-/* The workspace of both calls for a list of these sizes and the iteration's flags, in bytes (the pointer 16-byte aligned):
- * some 4 bytes an element, of at most 128 M elements or the largest matrix at a time, and 4 bytes x the smaller side
- * squared; twice that for matrices held in pairs. */
+/* The workspace of both calls for a list of these sizes and the iteration's flags, in bytes (the pointer 16-byte aligned).
+ * A list is taken in batches of at most 8 shapes, 256 matrices and 128 M elements (or one larger matrix), and the largest
+ * batch's is needed: some 4 bytes an element and 4 bytes x the smaller side squared, twice that for matrices held in pairs,
+ * and, for lists so small that long sums are split, 256 KB for each part, at most 24 MB. */
 MICA_API int64_t mica_newton_schulz_workspace(const int64_t* rows, const int64_t* cols, int32_t T, uint32_t flags);
 
 /*

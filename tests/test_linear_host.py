@@ -241,3 +241,17 @@ def test_polynomials_at_their_limits():
         for e, refused in ((1e-4, True), (-1e-4, False)):
             got = orthogonalize(ns=iteration([v * s * (1 + e) for v in (a, b, c)], steps=1))
             assert (got == HYPER) == refused, (a, b, c, e)
+
+
+def test_small_lists_take_small_workspaces():
+    """Room for parts of sums only where the list has sums that are split."""
+    M = muon._muon()
+
+    def size(*shapes):
+        return M.mica_newton_schulz_workspace(*sizes(*shapes), 0)
+
+    assert size((1, 1)) < 1 << 16 and size((64, 64)) < 1 << 18
+    exact = 4 * 384 * 1536 + 4 * 384 * 384
+    assert exact <= size((384, 1536)) < exact + (1 << 14)
+    part = 256 * 256 * 4
+    assert 2 * part < size((16, 1600)) < 24 << 20  # a sum of 75 stages in pairs
