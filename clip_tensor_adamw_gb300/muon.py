@@ -84,7 +84,8 @@ def mica_orthogonalize(x, out=None, *, steps: int = 5, coefficients=COEFFICIENTS
     one such triple for each step. ``precise`` holds what is stored between the products in pairs of float16 (three times
     the work), as matrices whose smaller side is at most 256 always are. ``out`` takes the results (float16 or bfloat16; it
     may be ``x`` itself); otherwise they are new matrices of ``out_dtype`` (by default x's, or bfloat16 for float32).
-    Returns the list of results."""
+    Returns the list of results. The same list gives the same bits; beside other matrices one's may differ in the last places
+    of its sums, which are split where the list is small."""
     X = _as_list(x)
     if out is not None:
         out = _as_list(out)

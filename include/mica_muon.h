@@ -11,7 +11,9 @@
  *   - A matrix is rows[k] x cols[k] contiguous elements; sides in [0, MICA_MAX_SIDE] (one with a side of 0 is skipped).
  *   - Nothing is allocated and no table is cached: what a call needs is the caller's workspace, whose contents need not be
  *     set and are not read by a later call. Every call can be captured into a CUDA graph.
- *   - Results do not depend on the order in which CTAs run: no floating-point atomics.
+ *   - Results do not depend on the order in which CTAs run: no floating-point atomics. The same list gives the same bits. In
+ *     another list a matrix's may differ in the last places of its float32 sums: where a list has too few tiles for the GPU,
+ *     a long sum is split in parts, by the list's sizes and the number of SMs.
  */
 #ifndef MICA_MUON_H
 #define MICA_MUON_H

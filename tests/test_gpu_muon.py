@@ -317,3 +317,21 @@ def test_refusals():
     with pytest.raises(ValueError):
         mica.mica_orthogonalize([x], steps=0, coefficients=[])
     mica.mica_orthogonalize([x, x])  # one matrix read twice is fine
+
+
+@pytest.mark.parametrize("shape", [(16, 1600), (260, 20_000), (1600, 16)], ids=str)
+def test_split_sums(shape):
+    """A sum that is split where the list leaves pairs of CTAs idle and is not beside larger matrices: other bits perhaps, the
+    same error; and the same bits whenever the list is the same."""
+    g = gen(20)
+    x = torch.randn(shape, generator=g, device="cuda")
+    others = [torch.randn(s, generator=g, device="cuda") for s in [(1600, 1600), (1201, 777)] + [shape] * 20]
+    alone = [mica.mica_orthogonalize([x], out_dtype=torch.float16).tensors[0] for _ in range(3)]
+    beside = [mica.mica_orthogonalize([x] + others, out_dtype=torch.float16).tensors[0] for _ in range(3)]
+    for r in (alone, beside):
+        check(r[0], x)
+        assert torch.equal(r[0], r[1]) and torch.equal(r[0], r[2])
+    w, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    mica.mica_muon_steps([w], [x], [m], lr=1.0, momentum=0.0, adjust="none")
+    want = iterate(x)
+    assert distance(-w, want) <= off(x, want) + 8 * U * float(want.norm()) + 1e-6
