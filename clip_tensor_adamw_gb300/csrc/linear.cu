@@ -1,12 +1,13 @@
 // Losses from hidden states h (rows x features) and an output embedding W (vocabulary x features): log-probabilities of given
-// tokens under the softmax of z = h W^T / T, and their gradients, without a matrix of logits.
+// tokens under the softmax of z = h W^T / T, and their gradients. The logits are not stored. The gradients do store a matrix of
+// the logits' size: theirs, d, in 16 bits, of as many rows at a time as 1 GB holds (but no fewer than a tile's 256).
 //
 //   forward   lse_i = log sum_j exp z_ij, logp_i = z_i,target - lse_i
 //   gradient  d_ij = c_i (1[j = target] - exp(z_ij - lse_i)), c_i = dlogps_i / T; dh = d W, dW = d^T h
 //
 // The rows that count are gathered first, so that unscored rows (prompts) cost nothing, and taken in pieces of at most
 // kGradBytes of d. The forward pass is one product over all of the vocabulary whose epilogue keeps a running maximum and sum
-// for each row. The gradient takes the product again: keeping the logits would take memory that grows with rows x vocabulary.
+// for each row. The gradient takes the product again, since float32 logits would take twice d's room.
 // d is rounded to 16 bits once, in that product's epilogue, and multiplied with W and with h in one launch.
 //
 // Cross entropy, which has the forward pass and the gradient in one call, needs the product once in bfloat16: its epilogue
@@ -29,7 +30,7 @@
 namespace mica {
 namespace {
 
-constexpr int64_t kGradBytes = (int64_t)1 << 30;    // of d, that a piece of the rows takes
+constexpr int64_t kGradBytes = (int64_t)1 << 30;    // of d, that a piece of the rows takes (or 256 rows, if that is more)
 constexpr int64_t kStatBytes = (int64_t)256 << 20;  // of the forward pass's maxima and sums
 constexpr int kMostRows = 16384;                    // of a piece in the forward pass
 // Rows up to which every CTA of the gather looks through all targets, which saves a launch: log-probabilities of 1,024 rows 22.0

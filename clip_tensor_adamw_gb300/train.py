@@ -432,7 +432,7 @@ def _linear_grads(h: torch.Tensor, w: torch.Tensor, want_dh: bool, want_dw: bool
 def mica_linear_logps(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, *, temperature: float = 1.0,
                       lse: bool = False, stream=None):
     """Log-probabilities of ``targets`` (int32 or int64, [rows]; negative: not scored, 0) under the softmax of
-    ``h @ w.T / temperature``, float32 [rows], without keeping the logits. ``h``: hidden states [rows, features], ``w``:
+    ``h @ w.T / temperature``, float32 [rows], without storing the logits. ``h``: hidden states [rows, features], ``w``:
     the output embedding [vocabulary, features], both float16 or bfloat16, any row stride. With ``lse`` also the
     logarithms of the sums of exp of the logits, which mica_linear_logps_grad takes: ``(logps, lse)``."""
     l = _linear(h, w, targets, temperature)
@@ -474,7 +474,8 @@ def mica_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.T
                               dw: torch.Tensor | None = None, add: torch.Tensor | None = None,
                               dw_dtype: torch.dtype | None = None, stream=None) -> LinearCrossEntropy:
     """Softmax cross entropy of ``targets`` under ``h @ w.T / temperature``, summed over the scored rows and divided by
-    ``denom`` (None: their number), and the gradients of ``grad_scale`` times it, without keeping the logits. Arguments
+    ``denom`` (None: their number), and the gradients of ``grad_scale`` times it, without storing the logits. The
+    workspace holds their gradient in 16 bits, for as many rows at a time as 1 GB takes (at least 256). Arguments
     as mica_linear_logps and mica_linear_logps_grad; ``grad=False`` leaves both gradients out."""
     _wanted(grad and want_dh, grad and want_dw, dh, dw, add)
     l = _linear(h, w, targets, temperature)

@@ -1,4 +1,4 @@
-"""Pre-training steps with this package's kernels and plain matrix products: hidden states -> cross entropy without logits,
+"""Pre-training steps with this package's kernels and plain matrix products: hidden states -> cross entropy without stored logits,
 with both gradients -> one clip over all gradients -> Muon for the hidden matrices, AdamW for the tied embedding and the gains.
 
 The model is a stack of residual MLP blocks between an embedding and the same embedding as output layer, in bfloat16 with

@@ -12,7 +12,7 @@
  *   mica_act_unpack         the values a checkpoint stands for
  *   mica_act_grad           an activation function's backward pass from a checkpoint
  *   mica_packed_wgrad       a linear layer's weight gradient from its input's checkpoint
- *   mica_linear_logps       log-probabilities of given tokens from hidden states and an output embedding, no logits kept
+ *   mica_linear_logps       log-probabilities of given tokens from hidden states and an output embedding, logits not stored
  *   mica_linear_logps_grad  the gradients of both, given that of the log-probabilities (any loss over them)
  *   mica_linear_cross_entropy  softmax cross entropy from hidden states, with both gradients
  *
@@ -214,15 +214,25 @@ MICA_API int64_t mica_packed_wgrad_workspace(const mica_packed* x, const void* d
 
 /*
  * Hidden states, an output embedding and the token scored in each row: row t's logits are
- * z[j] = sum_k h[t*ld_h + k] * w[j*ld_w + k] / temperature, j < vocab. They are not kept: no buffer grows with
- * rows * vocab, only with rows and with vocab.
+ * z[j] = sum_k h[t*ld_h + k] * w[j*ld_w + k] / temperature, j < vocab. They are never stored. Rows are taken in pieces, and
+ * the workspaces hold, for a piece of P rows:
+ *   - 2 P vocab bytes with gradients: the logits' gradient in 16 bits (or, in cross entropy, what it is a multiple of). P is
+ *     at most 2^29 / vocab, rounded down to a multiple of 256, but no fewer than 256: so all rows up to 1 GB of it (8,192 rows
+ *     of 50,257 tokens: 824 MB), pieces of up to 1 GB beyond, and 256 rows where those take more (8.6 GB at 2^24 tokens)
+ *   - P vocab / 16 bytes in the forward pass (mica_linear_logps, cross entropy): maxima and sums. There P is at most 16,384
+ *     and 2^32 / vocab, rounded as above: 256 MB
+ *   - 2 P features bytes, the rows that count gathered; as much again in cross entropy with gradients of MICA_BF16
+ * and further
+ *   - 2 vocab features bytes, a copy of w, where its rows do not begin at multiples of 16 bytes or overlap
+ *   - 40 MB for each of dh and dw, sums of parts; 4 vocab features bytes more where there are several pieces and dw is of 16 bits
+ *   - some 4 bytes a row and 40 a row of a piece
+ *
  *   - the products are exact and summed in float32; maxima and sums over the vocabulary are float32
  *   - target < 0: the row does not count. It is not read; its log-probability is 0 and its gradient zeros, whatever it
  *     holds. Rows that do not count cost next to nothing
  *   - target >= vocab: the log-probability is NaN (nothing out of range is read), and so are the gradients that the row
  *     takes part in, unless its coefficient is 0
- *   - h and w have the same type, MICA_F16 or MICA_BF16, any alignment and row stride (rows that are not 16-byte aligned
- *     are copied into the workspace first)
+ *   - h and w have the same type, MICA_F16 or MICA_BF16, any alignment and row stride
  */
 typedef struct {
     const void* h;        /* rows x features */
@@ -269,8 +279,7 @@ typedef struct {
  * The gradients given that of the log-probabilities, dlogps[rows] float32, and lse[rows] as mica_linear_logps gives it: with
  * d[t][j] = dlogps[t] / temperature * ((j == target) - exp(z[t][j] - lse[t])), dh = d w and dw = add + d^T h. A row whose
  * target is negative or whose dlogps is 0 does not count: its dh is zeros. workspace: mica_linear_grad_workspace bytes for
- * the same arguments, 16-byte aligned: 2 bytes x rows x vocab but no more than some 1 GB (larger batches are taken in pieces),
- * 80 MB, and where there are pieces and dw is of 16 bits, 4 bytes x vocab x features.
+ * the same arguments, 16-byte aligned.
  * Errors: as mica_linear_logps.
  */
 MICA_API mica_status mica_linear_logps_grad(const mica_linear* l, const float* lse, const float* dlogps,

@@ -611,3 +611,37 @@ def test_one_gradient_of_no_rows(dtype):
     assert dh.shape == (0, 72) and dw is None
     r = mica.mica_linear_cross_entropy(h, w, y, want_dh=False)
     assert r.dh is None and not r.dw.any()
+
+
+def test_workspace_sizes():
+    """The documented sum, of which the matrix of d is the largest part: up to 1 GB of it, and never fewer than 256 rows."""
+    L = mica.train._train()
+
+    def size(rows, features, vocab, sums, dw_dtype=0, ld_w=None):
+        l = mica.train._Linear(None, 0x1000, None, rows, features, vocab, features, ld_w or features, 1.0, 4, 8)
+        g = mica.train._LinearGrads(0x1000, 0x1000, None, features, features, 0, dw_dtype, 0)
+        return L.mica_linear_cross_entropy_workspace(l, g) if sums else L.mica_linear_grad_workspace(l, g)
+
+    def documented(rows, features, vocab, sums, dw_dtype=0, copied=False):
+        up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+        piece = max(256, (1 << 30) // (2 * vocab) // 256 * 256)
+        if sums:
+            piece = min(piece, 16384, max(256, (256 << 20) // (vocab // 16) // 256 * 256))
+        piece = min(up(rows), piece)
+        total = 2 * piece * vocab + 2 * piece * features + (80 << 20) + 4 * rows
+        if sums:
+            total += piece * vocab // 16 + 2 * piece * features
+        if copied:
+            total += 2 * vocab * features
+        if piece < rows and dw_dtype:
+            total += 4 * vocab * features
+        return total
+
+    for args in ((8192, 768, 50257), (100, 64, 1000), (4096, 1600, 131072), (1500, 40, 600_007), (300, 16, 1 << 24), (40, 40_000, 60_000)):
+        for sums in (False, True):
+            for dt in (0, 4):
+                got, want = size(*args, sums, dt), documented(*args, sums, dt)
+                assert 0.9 * want <= got <= 1.1 * want + (1 << 20), (args, sums, dt, got, want)
+    assert size(300, 16, 1 << 24, True) > 8 << 30  # 256 rows of 2^24
+    got, want = size(512, 1001, 30_000, False, ld_w=1001), documented(512, 1001, 30_000, False, copied=True)
+    assert 0.9 * want <= got <= 1.1 * want + (1 << 20)
