@@ -24,6 +24,8 @@
 // gradients' epilogues take out again.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "linear.h"
 
@@ -38,6 +40,9 @@ constexpr int kMostRows = 16384;                    // of a piece in the forward
 constexpr int kLookRows = 1024;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMostSum = 0x1p64f;                 // of exp(z - z_target) over 32 columns
+// Whether cross entropy takes the product once: binary16 has not the range.
+template <typename T>
+constexpr bool kTakenOnce = std::is_same<T, __nv_bfloat16>::value;
 
 // What the scan of the targets leaves for the kernels after it.
 struct Meta {
@@ -161,7 +166,7 @@ __device__ __forceinline__ void take_row(const Gather& g, const Meta& m, int64_t
     const unsigned short* in = g.h + i * g.ld_h;
     unsigned short* out = g.out + (int64_t)r * g.ld;
     const int64_t y = target_at(g.targets, g.wide, i);
-    const unsigned short* own = g.w && y < g.vocab ? g.w + y * g.ld_w : nullptr;  // (16-byte aligned)
+    const unsigned short* own = kTakenOnce<T> && g.w && y < g.vocab ? g.w + y * g.ld_w : nullptr;  // (16-byte aligned)
     const int whole = g.aligned ? g.features / 8 : 0;
     float z = 0.0f;  // the target's logit
 #pragma unroll 2
@@ -461,8 +466,8 @@ struct LogitSums : Logits {
 // The product that cross entropy takes once (and, so that its loss is the same, without gradients too): q = 2^(z a - origin), 0
 // at the target, and its sum. A sum counts from the target's logit; where 32 columns leave the range (kMostSum), from the
 // largest so far, and the row is taken again.
-template <typename T>
 struct LogitOnce : Logits {
+    using T = __nv_bfloat16;
     RowSum* sums;         // [most][vocabulary / 128]; null the second time
     int parts;
     const float* origin;  // the target's logit times a; lse, in rows taken again
@@ -612,8 +617,8 @@ __device__ __forceinline__ RowSum row_sum(const Join& j, int row, int lane) {
 
 // A row of the product taken once: the target's logit is the origin c that its sum (over the others) counts from, unless
 // it left the range. d's element at the target is that of p - 1: minus the others' sum. Returns the log-probability.
-template <typename T>
 __device__ __forceinline__ float join_once(const Join& j, const Meta& m, RowSum s, int row, int lane) {
+    using T = __nv_bfloat16;
     const float c = j.origin[row], k = -m.coef;
     __syncwarp();
     float logp, factor, at;
@@ -665,9 +670,10 @@ __global__ void __launch_bounds__(256) join_rows_kernel(Join j) {
     if (row < span.rows) {
         const RowSum s = row_sum(j, row, lane);
         const int64_t i = j.index[span.from + row];
-        if (j.once) {
-            logp = join_once<T>(j, m, s, row, lane);
-        } else {
+        if constexpr (kTakenOnce<T>) {
+            if (j.once) logp = join_once(j, m, s, row, lane);
+        }
+        if (!kTakenOnce<T> || !j.once) {
             const float l = log2f(s.sum);
             logp = j.target[row] < 0 ? NAN : (fmaf(j.at[row], j.a, -s.origin) - l) * kLn2;
             if (lane == 0 && j.lse) j.lse[i] = (s.origin + l) * kLn2;
@@ -1104,7 +1110,7 @@ Room places_of(const Linear& L, bool sums, const LinearGrad* G, bool ce, int sms
         c.at = p->take<float>(c.most);
     }
     if (ce) c.partial = p->take<Exact>((int64_t)c.pieces * (c.most / 8));
-    c.once = ce && L.dtype == MICA_BF16;
+    c.once = ce && L.dtype == MICA_BF16;  // (kTakenOnce)
     c.ld_d = (int)round_up(L.vocab, 64);
     if (!G) return c;
     const int pairs = sms / 2 < 1 ? 1 : sms / 2;
@@ -1296,29 +1302,39 @@ cudaError_t gradients(const Call& call, const Room& c) {
     return launch_after(join_parts_kernel<T, O>, 8 * (int64_t)call.sms, 256, 0, call.stream, p);
 }
 
+// Tiles of the product over the vocabulary, of a whole piece.
+int64_t logit_tiles(const Linear& L, const Room& c) { return c.most / kTile * tiles_of(L.vocab); }
+
+// Cross entropy's product taken once, and again for rows whose sum has left its range.
+cudaError_t logits_once(const Call& call, const Room& c, int piece) {
+    LogitOnce p{};
+    if (!fill(&p, call.L, c)) return cudaErrorInvalidValue;
+    p.sums = c.sums;
+    p.parts = c.parts;
+    p.origin = c.origin;
+    p.d = reinterpret_cast<LogitOnce::T*>(c.d);
+    p.ld = c.ld_d;
+    MICA_STEP((launch_gemm<LogitOnce::T>(p, logit_tiles(call.L, c), call.sms, call.stream)));
+    MICA_STEP(join_rows<LogitOnce::T>(call, c, piece));
+    if (!call.G) return cudaSuccess;
+    p.sums = nullptr;
+    p.at = c.at;
+    p.again = c.again;
+    return launch_gemm<LogitOnce::T>(p, logit_tiles(call.L, c), call.sms, call.stream);
+}
+
 template <typename T>
 cudaError_t run(const Call& call, const Room& c) {
     const Linear& L = call.L;
     const bool forward = call.logps || call.loss;
-    const int64_t tiles = c.most / kTile * tiles_of(L.vocab);
+    const int64_t tiles = logit_tiles(L, c);
     MICA_STEP(copy_w(L, c, call.stream));
     for (int piece = 0; piece < c.pieces; ++piece) {
         MICA_STEP(gather<T>(call, c, piece));
-        if (c.once) {
-            LogitOnce<T> p{};
-            if (!fill(&p, L, c)) return cudaErrorInvalidValue;
-            p.sums = c.sums;
-            p.parts = c.parts;
-            p.origin = c.origin;
-            p.d = reinterpret_cast<T*>(c.d);
-            p.ld = c.ld_d;
-            MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
-            MICA_STEP(join_rows<T>(call, c, piece));
-            p.sums = nullptr;
-            p.at = c.at;
-            p.again = c.again;
-            if (call.G) MICA_STEP((launch_gemm<T>(p, tiles, call.sms, call.stream)));
-        } else if (forward) {
+        if constexpr (kTakenOnce<T>) {
+            if (c.once) MICA_STEP(logits_once(call, c, piece));
+        }
+        if (forward && !c.once) {
             LogitSums p{};
             if (!fill(&p, L, c)) return cudaErrorInvalidValue;
             p.sums = c.sums;
