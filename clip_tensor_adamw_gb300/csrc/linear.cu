@@ -16,7 +16,11 @@
 // the range, whose targets are less likely than some e^-44, are taken again, counted from lse. Against taking the product
 // twice: 16 x 256 x 5,000 42 us and 44, 1,024 x 768 x 50,257 176 and 211, 8,192 x 768 x 50,257 1,254 and 1,564. The sum of a
 // row may be 2^80 and its coefficient 2^-100: the coefficient is brought to 2^-1 by a power of two, which the gradients'
-// epilogues take out again.
+// epilogues take out again. Scaling h's rows rounds them once more, and the target's element of q, most of a row, is rounded
+// with the rest: a float32 dW is off by 2.4e-3 of its norm, and dh, with its own rounding of 1.7e-3, as well. The product taken
+// twice (mica_linear_logps and its gradient) comes to 0.9e-3 and 1.9e-3 (2,048 x 768 x 20,011). A factor that makes up for the
+// target's rounding (1.7e-3 for both) was not kept: it shifts the other elements by as much, three roundings where two are
+// stated.
 //
 // Logits, maxima, sums and gradients' sums are float32. d is rounded to the operands' type because the tensor cores multiply
 // what they are given in 16 bits: relative 2^-9 (bfloat16) or 2^-12 of each of its elements on average. binary16 has not the
