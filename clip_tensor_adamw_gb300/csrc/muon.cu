@@ -3,10 +3,11 @@
 //   x = u / (|u| + eps);  A = x x^T (wide) or x^T x (tall);  B = a I + b A + c A^2;  x = B x (wide) or x B (tall);  and again
 //
 // A list goes through every product together: matrices of the same shape are a class, which lies in the workspace as one
-// array with one tensor map, and a launch takes the tiles of all classes. So a step of the iteration is three launches
-// whatever the list holds, and small matrices fill the GPU between them. Nothing is transposed: a tall matrix's A takes x as
-// MN-major operands, and A and B are symmetric. Of A and B only the tiles on and above the diagonal are computed; the
-// others are written as their mirror image, which is a thread's column and so coalesced too.
+// array with one tensor map, and a launch takes the tiles of all classes. So a step of the iteration is three launches for up
+// to 8 shapes, 256 matrices and 128 M elements (a batch; longer lists go through the whole iteration batch by batch), and
+// small matrices fill the GPU between them. Nothing is transposed: a tall matrix's A takes x as MN-major operands, and A and B
+// are symmetric. Of A and B only the tiles on and above the diagonal are computed; the others are written as their mirror
+// image, which is a thread's column and so coalesced too.
 //
 // x, A and B are stored in binary16: 11 bits where bfloat16 has 8, at the same rate, and the range is known, since the
 // singular values stay of order 1. They are scaled by 2^10, so that elements down to 2^-24 are normal. With a x folded into
@@ -34,8 +35,11 @@ constexpr int kItem = 8192;          // elements that a CTA of the streaming ker
 constexpr int kMostItems = 512;      // parts of a matrix's square sum
 constexpr float kScale = 1024.0f;
 // Matrices whose smaller side is at most this are held in pairs: a small matrix's elements are large beside a weight's, so the
-// error would show in a float32 weight (a step of rate r changes the weights' norm by r / 0.02 sqrt(side) of it or so), and
-// its products, a tile or a few for each matrix, are short.
+// error would show in a float32 weight (a step of rate r changes the weights' norm by r / 0.02 sqrt(side) of it or so; 256 x
+// 300 is off by 5e-8 so, 257 x 300 by 4e-6), and its products, a tile or a few for each matrix, are short. mica_orthogonalize,
+// which rounds its result to 16 bits, gets binary16's own rounding and no more (2.0e-4 of the norm, where single binary16 comes
+// to 1.1e-3 to 1.7e-3) and the bits that a step takes; it costs next to nothing there: six small and odd matrices take 188 us,
+// and 184 with all of them single.
 constexpr int kPreciseSide = 256;
 
 struct Class {
@@ -754,8 +758,9 @@ int64_t deal_out(std::vector<Work> work, int pairs, Schedule* s) {
     return *std::max_element(load.begin(), load.end());
 }
 
-// A piece of `columns` columns: what its stages load (some 58 bytes a clock and SM: 285 ns for 32 KB, 250 to 270 for the 24 KB
-// of up to 128 columns), and a part of its epilogue, which the next piece's products do not hide.
+// A piece of `columns` columns: its stages, as measured (285 ns for a whole tile's; 250 to 270 for up to 128 columns, which have
+// half the products and three quarters of the loads: what holds those up is not known), and a part of its epilogue, which the
+// next piece's products do not hide.
 int cost_of(const Class& c, int depth, int columns) {
     const int stages = (depth + kDepth - 1) / kDepth * (c.low ? 3 : 1);
     return columns > 128 ? stages * 285 + 1000 : stages * 255 + 600;

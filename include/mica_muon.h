@@ -37,8 +37,8 @@ extern "C" {
  * x, G and the polynomial of G are held in binary16 between the products (scaled by 2^10; products are exact and summed in
  * float32), which takes a result some 2^-9 to 2^-10 of its norm off; directions whose singular values in u are a thousand
  * times below the largest get correspondingly less accurate. With MICA_NS_PRECISE, and always for matrices whose smaller side
- * is at most 256, they are held in pairs of binary16, at three times the operations, for results some 2^-19 off before they
- * are rounded to out's type. A zero matrix gives zeros; a matrix with an infinity or a NaN gives NaNs.
+ * is at most 256 (whose products are short), they are held in pairs of binary16, at three times the operations, for results
+ * some 2^-19 off before they are rounded to out's type. A zero matrix gives zeros; a matrix with an infinity or a NaN gives NaNs.
  */
 #define MICA_NS_PRECISE 1u
 typedef struct {
