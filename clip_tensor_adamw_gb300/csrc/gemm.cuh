@@ -273,6 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 float v[32];
+                __syncwarp();  // (TMEM is read by the whole warp at once, whose lanes an epilogue's edges part)
                 load_sums32(own + c * 32, v);
                 if (c == chunks - 1) {
                     fence_before();
