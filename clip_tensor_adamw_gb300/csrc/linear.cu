@@ -146,7 +146,8 @@ __device__ __forceinline__ Meta meta_of(const Gather& g, int count, float top) {
     const float largest = g.dlogps ? top : fabsf(ce);
     if (g.scaled && largest > 0.0f && largest < INFINITY) {
         int e = (int)(__float_as_uint(largest) >> 23) - 127;  // largest < 2^(e + 1); a subnormal counts as 2^-127
-        e = g.scaled_to - (e < -100 ? -100 : e > 124 ? 124 : e);
+        e = g.scaled_to - (e < -100 ? -100 : e);
+        if (e < -126) e = -126;  // (bfloat16 only, whose range holds what is left)
         m.scale = power_of_two(e);
         m.inv_scale = power_of_two(-e);
     }

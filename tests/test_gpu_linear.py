@@ -645,3 +645,26 @@ def test_workspace_sizes():
     assert size(300, 16, 1 << 24, True) > 8 << 30  # 256 rows of 2^24
     got, want = size(512, 1001, 30_000, False, ld_w=1001), documented(512, 1001, 30_000, False, copied=True)
     assert 0.9 * want <= got <= 1.1 * want + (1 << 20)
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_coefficients_at_the_end_of_float32(dtype):
+    """Coefficients of up to 2.8e38, whose gradients float32 still holds: small hidden states, one row to a token."""
+    rows, features, vocab = 120, 64, 900
+    h, w, y = make(rows, features, vocab, dtype, seed=48, skip=0.1)
+    h = (h.float() * 2.0 ** -6).to(dtype)
+    y = torch.where(y < 0, y, torch.arange(rows, device="cuda"))
+    lp, lse = mica.mica_linear_logps(h, w, y, lse=True)
+    c = 2.8e38 * (2.0 * torch.rand(rows, generator=gen(49), device="cuda") - 1.0)
+    c[1], c[2] = 2.8e38, -2.8e38
+    want = Want(h, w, y)
+    _, _, dw, dw_err = want.grads(c, dtype)
+    assert float(dw.abs().max()) < 3e38
+    got = mica.mica_linear_logps_grad(h, w, y, lse, c, want_dh=False, dw_dtype=torch.float32)[1]
+    rounded(got, dw, dw_err)
+    n = int(want.on.sum())
+    for scale in (1e38, 2.8e38):
+        r = mica.mica_linear_cross_entropy(h, w, y, denom=1.0, grad_scale=scale, want_dh=False, dw_dtype=torch.float32)
+        _, _, dw, dw_err = want.grads(torch.full((rows,), -scale, device="cuda"), dtype, once=True)
+        assert float(dw.abs().max()) < 3e38
+        rounded(r.dw, dw, dw_err)
