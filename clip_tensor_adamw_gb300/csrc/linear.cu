@@ -16,11 +16,11 @@
 // the range, whose targets are less likely than some e^-44, are taken again, counted from lse. Against taking the product
 // twice: 16 x 256 x 5,000 42 us and 44, 1,024 x 768 x 50,257 176 and 211, 8,192 x 768 x 50,257 1,254 and 1,564. The sum of a
 // row may be 2^80 and its coefficient 2^-100: the coefficient is brought to 2^-1 by a power of two, which the gradients'
-// epilogues take out again. Scaling h's rows rounds them once more, and the target's element of q, most of a row, is rounded
-// with the rest: a float32 dW is off by 2.4e-3 of its norm, and dh, with its own rounding of 1.7e-3, as well. The product taken
-// twice (mica_linear_logps and its gradient) comes to 0.9e-3 and 1.9e-3 (2,048 x 768 x 20,011). A factor that makes up for the
-// target's rounding (1.7e-3 for both) was not kept: it shifts the other elements by as much, three roundings where two are
-// stated.
+// epilogues take out again. Scaling h's rows rounds them once more. The target's element of q, most of a row, is rounded with the
+// rest, which the factor makes up for: dh comes out with its own rounding and no more (1.7e-3 of its norm), a float32 dW off by
+// 1.7e-3 (without: 2.4e-3 both; 2,048 x 768 x 20,011). The product taken twice (mica_linear_logps and its gradient) comes to
+// 1.9e-3 and 0.9e-3 where the coefficients are a power of two, which leaves d's target elements exact, and to 2.4e-3 and 1.7e-3
+// elsewhere.
 //
 // Logits, maxima, sums and gradients' sums are float32. d is rounded to the operands' type because the tensor cores multiply
 // what they are given in 16 bits: relative 2^-9 (bfloat16) or 2^-12 of each of its elements on average. binary16 has not the
@@ -633,6 +633,9 @@ __device__ __forceinline__ float join_once(const Join& j, const Meta& m, RowSum 
         logp = -log1pf(s.sum);
         factor = k / (1.0f + s.sum);
         at = -s.sum;
+        // The target's element, most of the row, is rounded to T: the factor makes up for that, and shifts the others, whose own
+        // roundings are as large, by as much. (Below 2^-100 it counts for nothing, and near 2^-126 T has fewer bits.)
+        if (s.sum > 0x1p-100f) factor *= s.sum / widen(narrow<T>(s.sum));
     } else {  // counted from lse the second time
         const float lse = s.origin + log2f(s.sum + exp2_fast(c - s.origin));
         logp = (c - lse) * kLn2;

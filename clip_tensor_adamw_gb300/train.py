@@ -475,10 +475,8 @@ def mica_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.T
                               dw_dtype: torch.dtype | None = None, stream=None) -> LinearCrossEntropy:
     """Softmax cross entropy of ``targets`` under ``h @ w.T / temperature``, summed over the scored rows and divided by
     ``denom`` (None: their number), and the gradients of ``grad_scale`` times it, without storing the logits. The
-    workspace holds their gradient in 16 bits, for as many rows at a time as 1 GB takes (at least 256). In bfloat16 ``dw`` is
-    off by some 2.4e-3 of its norm before its own rounding; by less where mica_linear_logps and mica_linear_logps_grad are
-    called instead, which take a quarter more time. Arguments as mica_linear_logps and mica_linear_logps_grad; ``grad=False``
-    leaves both gradients out."""
+    workspace holds their gradient in 16 bits, for as many rows at a time as 1 GB takes (at least 256). Arguments
+    as mica_linear_logps and mica_linear_logps_grad; ``grad=False`` leaves both gradients out."""
     _wanted(grad and want_dh, grad and want_dw, dh, dw, add)
     l = _linear(h, w, targets, temperature)
     if denom is not None and not denom > 0.0:

@@ -265,8 +265,8 @@ MICA_API int64_t mica_linear_logps_workspace(const mica_linear* l);
  * The gradient of the logits is rounded to h's type (scaled, in binary16, so that its largest finite row uses the whole
  * range), as the tensor cores take it; sums are float32 and rounded once. So before its own rounding an element is off by up
  * to 2^-8 (bfloat16) or 2^-11 (binary16) of the terms that it sums up, whatever dw's type: dw by 0.9e-3 to 1.7e-3, or 1.3e-4
- * to 2.1e-4, of its norm. mica_linear_cross_entropy rounds twice for dw in bfloat16: up to 2^-7, some 2.4e-3 of the norm. Who
- * wants less there takes mica_linear_logps and mica_linear_logps_grad, at a quarter more time.
+ * to 2.1e-4, of its norm. mica_linear_cross_entropy rounds up to three times in bfloat16, but once where a row's target is, so
+ * that it comes to 1.7e-3 of the norm as well, and up to 3 x 2^-8 of an element's terms.
  */
 typedef struct {
     void* dh;

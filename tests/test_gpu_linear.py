@@ -511,6 +511,10 @@ def test_small_and_large_coefficients(denom, scale):
     assert int(((want.logps < -18) & (want.logps > -44)).sum()) > 50 and float(want.logps.min()) < -50
     c = torch.full((rows,), -scale / denom, device="cuda")
     dh, dh_err, dw, dw_err = want.grads(c, torch.bfloat16, once=True)
+    # The factor of a row makes up for the rounding of its target's element, and shifts the others by that rounding: in dw, where
+    # h's rows are rounded too, theirs is a third, e(d), which counts where one other token has nearly all of a row's probability.
+    d = c[:, None].double() * (want.p - torch.zeros_like(want.p).scatter_(1, y.clamp(min=0)[:, None], 1.0)) * want.on[:, None]
+    dw_err = dw_err + ROUND[torch.bfloat16] * (d.abs().t() @ want.h.abs())
     for out in (torch.float32, torch.bfloat16):
         r = mica.mica_linear_cross_entropy(h, w, y, denom=denom, grad_scale=scale, dw_dtype=out)
         rounded(r.dh, dh, dh_err)
@@ -668,3 +672,16 @@ def test_coefficients_at_the_end_of_float32(dtype):
         _, _, dw, dw_err = want.grads(torch.full((rows,), -scale, device="cuda"), dtype, once=True)
         assert float(dw.abs().max()) < 3e38
         rounded(r.dw, dw, dw_err)
+
+
+def test_cross_entropy_is_as_exact_as_its_roundings():
+    """In the norm: dh is off by its own rounding, a float32 dw by one rounding of its rows. A rounding to bfloat16 is off by
+    2^-8 / 3^1/2 (2^-2 <= u < 2^-1 in size: a root mean square of 2^-9 3^-1/2 / u, between 1.1e-3 and 2.3e-3, 1.66e-3 over all),
+    and two of them by 2^1/2 as much: 2.35e-3. 2.0e-3 lies between one and two."""
+    h, w, y = make(700, 256, 5000, torch.bfloat16, seed=50, skip=0.1)
+    want = Want(h, w, y)
+    n = int(want.on.sum())
+    dh, _, dw, _ = want.grads(torch.full((700,), -1.0 / n, device="cuda"), torch.bfloat16)
+    r = mica.mica_linear_cross_entropy(h, w, y, dw_dtype=torch.float32)
+    for got, exact in ((r.dh, dh), (r.dw, dw)):
+        assert float((got.double() - exact).norm()) <= 2.0e-3 * float(exact.norm())
