@@ -152,6 +152,13 @@ __device__ __forceinline__ Meta meta_of(const Gather& g, int count, float top) {
         m.inv_scale = power_of_two(-e);
     }
     m.coef = ce * m.scale;
+    // Cross entropy in binary16: every row's coefficient is the same, so that what it has beside a power of two can wait for the
+    // epilogues, and d's target elements, most of a row, are exact where p is small. (An infinite one stays as it is.)
+    const float size = fabsf(m.coef);
+    if (!g.dlogps && g.scaled && !g.w && size >= 0x1p14f && size < 0x1p15f) {
+        m.inv_scale *= size * 0x1p-14f;
+        m.coef = copysignf(0x1p14f, m.coef);
+    }
     return m;
 }
 
@@ -889,7 +896,7 @@ struct WeightGrad {
         float4 a{};
         if (!r.first) a = load4(sums + row * ld_sums + col, there, wide_sums);
         else if (add) a = load4(add + row * ld_add + col, there, wide_add);
-        v = make_float4(fmaf(v.x, s, a.x), fmaf(v.y, s, a.y), fmaf(v.z, s, a.z), fmaf(v.w, s, a.w));  // (s: a power of two)
+        v = make_float4(fmaf(v.x, s, a.x), fmaf(v.y, s, a.y), fmaf(v.z, s, a.z), fmaf(v.w, s, a.w));
         if (r.last) store4<O>(dw + row * ld + col, v, there, wide);
         else store4<float>(sums + row * ld_sums + col, v, there, wide_sums);
     }

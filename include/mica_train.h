@@ -266,7 +266,8 @@ MICA_API int64_t mica_linear_logps_workspace(const mica_linear* l);
  * range), as the tensor cores take it; sums are float32 and rounded once. So before its own rounding an element is off by up
  * to 2^-8 (bfloat16) or 2^-11 (binary16) of the terms that it sums up, whatever dw's type: dw by 0.9e-3 to 1.7e-3, or 1.3e-4
  * to 2.1e-4, of its norm. mica_linear_cross_entropy rounds up to three times in bfloat16, but once where a row's target is, so
- * that it comes to 1.7e-3 of the norm as well, and up to 3 x 2^-8 of an element's terms.
+ * that it comes to 1.7e-3 of the norm as well, and up to 3 x 2^-8 of an element's terms; in binary16 its target's elements are
+ * exact where the target is unlikely (1.4e-4).
  */
 typedef struct {
     void* dh;

@@ -685,3 +685,25 @@ def test_cross_entropy_is_as_exact_as_its_roundings():
     r = mica.mica_linear_cross_entropy(h, w, y, dw_dtype=torch.float32)
     for got, exact in ((r.dh, dh), (r.dw, dw)):
         assert float((got.double() - exact).norm()) <= 2.0e-3 * float(exact.norm())
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_cross_entropy_rounds_what_it_says(dtype):
+    """A float32 dw against a model in float64: binary16 rounds 2^14 (1[target] - p) and nothing else, whatever the number of
+    rows; bfloat16 h's rows times a factor, and p where the target is not. Half as much again is allowed for p's own error (a few
+    2^-22 against 2^-11) and for which way the roundings fall."""
+    h, w, y = make(601, 256, 5000, dtype, seed=51, skip=0.1)
+    want = Want(h, w, y)
+    n = int(want.on.sum())
+    c = torch.full((601,), -1.0 / n, device="cuda")
+    _, _, dw, _ = want.grads(c, dtype)
+    one = torch.zeros_like(want.p).scatter_(1, y.clamp(min=0)[:, None], 1.0)
+    f = -want.on.double()[:, None] / n
+    if dtype is torch.float16:
+        model = ((one - want.p) * 2.0 ** 14).half().double().t() @ (want.h * f * 2.0 ** -14)
+    else:
+        p = torch.where(one > 0, want.p, want.p.bfloat16().double())
+        model = (one - p).t() @ (want.h * f).bfloat16().double()
+    r = mica.mica_linear_cross_entropy(h, w, y, dw_dtype=torch.float32)
+    off = float((r.dw.double() - dw).norm())
+    assert off <= 1.5 * float((model - dw).norm()), (off, float((model - dw).norm()), float(dw.norm()))
